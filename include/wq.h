@@ -235,6 +235,177 @@ wq_status qembed_gather(const int32_t* ids, int64_t T, const uint32_t* Wpacked,
                         const wq_bf16* scales, int64_t V, int64_t D, int bits, int group,
                         wq_bf16* out, int32_t* bad_count, void* stream);
 
+/* ---- serving operators around the quantized layers ---------------------------
+ *
+ * What a served model runs between its linear layers: attention of the new
+ * token over the stored keys and values, the pages these live in, and the
+ * numbers of the answer from the logits of the lm_head. The source pages name
+ * the layers only; these calls have no counterpart there.
+ *
+ * The cache. One layer's cache is kv [P, 2, Hkv, S, D]: P pages of S tokens,
+ * keys then values, Hkv key heads of D values. The page calls take L layers at
+ * once, kv [L, P, page], a page being the same 2 * Hkv * S * D values in every
+ * layer; one page id names it in all of them. Sequence b's tokens
+ * j*S .. j*S + S - 1 lie on page block_table[b, j] ([B, W] int32); entries at
+ * or beyond ceil(lens[b] / S) are not read. Values are bf16 (WQ_KV_BF16) or
+ * e4m3 (WQ_KV_E4M3: 4 exponent and 3 fraction bits, no infinity, largest
+ * finite 448) standing for code * scale[h], one positive float32 scale per key
+ * head for the keys and one for the values (NULL with bf16).
+ * 1 <= S, D in {64, 96, 128, 192, 256}.
+ *
+ * No device data can make these calls read or write out of range: a sequence,
+ * position or page id outside its range is left out, and counted (added to
+ * *bad_count) where the call has a bad_count that is not NULL.
+ */
+#define WQ_KV_BF16 0
+#define WQ_KV_E4M3 1
+
+/* Writes new keys and values into their pages.
+ *  k, v        [T, Hkv, D] bf16, rows k_stride and v_stride elements apart
+ *              (multiples of 8, at least Hkv * D): they may be slices of a
+ *              fused projection's output.
+ *  seq, pos    [T] int32: token t is token pos[t] (from 0) of sequence seq[t];
+ *              seq NULL means that token t belongs to sequence t (T <= B).
+ *  kv          the cache; e4m3 codes are RN(clamp(x / scale, -448, 448)) with
+ *              an IEEE float32 division, NaN stays NaN.
+ * T >= 0 (T = 0 enqueues nothing). Two tokens of one call with the same place
+ * leave either one's values. bad_count: tokens left out. */
+wq_status kv_append(const wq_bf16* k, const wq_bf16* v, int64_t k_stride, int64_t v_stride, int64_t T,
+                    const int32_t* seq, const int32_t* pos, const int32_t* block_table, int64_t B, int64_t W,
+                    void* kv, int kv_type, int64_t P, int64_t Hkv, int64_t S, int64_t D, const float* k_scale,
+                    const float* v_scale, int32_t* bad_count, void* stream);
+
+/* Bytes of workspace kv_attn_decode needs (whatever the lengths). */
+size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+
+/* Attention of one new token per sequence over its stored ones, query head h
+ * reading key head h / (Hq / Hkv):
+ *   x[t] = sm_scale * <q[b, h], k[t]>,  t in [max(0, len - window), len),
+ *   out[b, h] = sum_t exp(x[t] - m) v[t] / l,  m = max_t x[t],
+ *   l = sum_t exp(x[t] - m),  lse[b, h] = m + ln l,
+ * all in float32, out rounded to bf16 once. A sequence without tokens (length
+ * 0 or less, or every page id out of range) gives zeros and lse = -inf, as do
+ * scores that are all -inf.
+ *  q           [B, Hq, D] bf16, rows q_stride elements apart (a multiple of 8,
+ *              at least Hq * D).
+ *  lens        [B] int32: tokens of each sequence, the new one among them (its
+ *              key and value are in the cache already); values above W * S
+ *              count as W * S.
+ *  window      0: all of them; otherwise the last `window` tokens.
+ *  out         [B, Hq, D] bf16;  lse [B, Hq] float32 or NULL.
+ *  workspace   at least kv_attn_workspace_bytes(); zero-filled before its
+ *              first use and then left to this call alone (what it keeps there
+ *              between calls is not zero). Not shared by calls that may run
+ *              concurrently; zeroed again after a call that failed.
+ * The result's bits do not depend on timing. B >= 0; Hq a multiple of Hkv.
+ * bad_count: pages left out. Tokens on a page beyond the length are never
+ * used, whatever they hold. */
+wq_status kv_attn_decode(const wq_bf16* q, int64_t q_stride, const void* kv, int kv_type,
+                         const int32_t* block_table, const int32_t* lens, int64_t B, int64_t W, int64_t P,
+                         int64_t Hq, int64_t Hkv, int64_t S, int64_t D, const float* k_scale, const float* v_scale,
+                         float sm_scale, int64_t window, wq_bf16* out, float* lse, int32_t* bad_count,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/* Page management. ref [P] int32 counts the sequences that hold each page; a
+ * page is free when its count is 0, and free pages are handed out in ascending
+ * order, so every result is the same whatever the timing. The calls read the
+ * tables, lengths and counts from their inputs and write the new ones to the
+ * *_out arrays; an output may be the input of the same name (an update in
+ * place) but must not overlap any other array. Nothing is handed back to the
+ * host: page ids, grants and counts stay on the device.
+ * page_bytes is a multiple of 16; 1 <= P, W, B. */
+
+/* Bytes of scratch (contents undefined between calls) for kv_pages_fork,
+ * kv_pages_reserve (n = B) and kv_pages_compact (n = 0). */
+size_t kv_pages_scratch_bytes(int64_t n, int64_t B, int64_t W, int64_t P);
+
+/* Copies page src[i] to page dst[i], i < n, in all L layers. No page may be a
+ * destination twice, or both a source and a destination of one call.
+ * bad_count: pairs left out. */
+wq_status kv_pages_copy(void* kv, int64_t L, int64_t P, int64_t page_bytes, const int32_t* src, const int32_t* dst,
+                        int64_t n, int32_t* bad_count, void* stream);
+
+/* Starts sequence child[i] as a copy of sequence parent[i], i < n: it shares
+ * the parent's full pages (their counts rise by one), and a last page that is
+ * not full is copied in all L layers to a free page, which the child holds
+ * alone. granted[i] = 1, and lens_out[child] = lens[parent]. Pairs are served
+ * in order; one for which the free pages that the pairs up to it ask for do
+ * not suffice (and which needs one), or whose sequence ids are out of range or
+ * equal, has granted[i] = 0, and its child is left without tokens
+ * (lens_out = 0, where the id is in range). Row entries beyond the child's
+ * pages keep what block_table has there. The child must hold no pages before
+ * the call, no sequence is a child twice and, for an update in place, none is
+ * both child and parent. */
+wq_status kv_pages_fork(void* kv, int64_t L, int64_t P, int64_t page_bytes, const int32_t* block_table,
+                        const int32_t* lens, const int32_t* ref, int64_t B, int64_t W, int64_t S,
+                        const int32_t* parent, const int32_t* child, int64_t n, int32_t* table_out,
+                        int32_t* lens_out, int32_t* ref_out, int32_t* granted, void* scratch, size_t scratch_bytes,
+                        void* stream);
+
+/* Gives every sequence the free pages that new_lens[b] tokens need beyond the
+ * ceil(lens[b] / S) that it has (none if it needs no more), counts 1 each, in
+ * the order of b. granted[b] = 1, or 0 for a sequence that needs pages when
+ * the free ones do not cover what the sequences up to it ask for, or that wants
+ * more than W: its row stays as it is. lens is not changed: the caller's next
+ * lengths are new_lens where granted. */
+wq_status kv_pages_reserve(const int32_t* block_table, const int32_t* lens, const int32_t* new_lens,
+                           const int32_t* ref, int64_t B, int64_t W, int64_t S, int64_t P, int32_t* table_out,
+                           int32_t* ref_out, int32_t* granted, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Gives back the pages of sequences seqs[i], i < n, each at most once a call:
+ * their counts fall by one and lens_out[seqs[i]] = 0. block_table stays as it
+ * is. A count never falls below 0. bad_count: sequence ids and page ids out of
+ * range, and pages that were free already. */
+wq_status kv_pages_free(const int32_t* block_table, const int32_t* lens, const int32_t* ref, int64_t B, int64_t W,
+                        int64_t S, int64_t P, const int32_t* seqs, int64_t n, int32_t* lens_out, int32_t* ref_out,
+                        int32_t* bad_count, void* stream);
+
+/* Moves the pages in use to the front of the pool: with n pages in use, those
+ * at or above n go to the free ones below n, the lowest to the lowest and so
+ * on, in all L layers; afterwards pages 0 .. n-1 are in use and the others are
+ * free. n_live [1] receives n, remap [P] each old page's new id (-1 for a free
+ * one), table_out the rows with their first ceil(lens[b] / S) entries renamed
+ * (an id out of range becomes -1) and the others as they were, ref_out the
+ * counts. */
+wq_status kv_pages_compact(void* kv, int64_t L, int64_t P, int64_t page_bytes, const int32_t* block_table,
+                           const int32_t* lens, const int32_t* ref, int64_t B, int64_t W, int64_t S,
+                           int32_t* table_out, int32_t* ref_out, int32_t* remap, int32_t* n_live, void* scratch,
+                           size_t scratch_bytes, void* stream);
+
+#define WQ_LOGITS_BF16 0
+#define WQ_LOGITS_F32 1
+
+/* Bytes of workspace token_logprobs needs. */
+size_t token_logprobs_workspace_bytes(int64_t T, int64_t V, int top_k);
+
+/* Log probabilities from logits, per row with y = logits[t, :] / temperature,
+ * m = max y and l = sum exp(y - m), in float32:
+ *   logprob[t]  = y[ids[t]] - m - ln l,
+ *   rank[t]     = 1 + the number of tokens that come before ids[t] (larger
+ *                 logit, or an equal one and a smaller id),
+ *   entropy[t]  = ln l - sum exp(y - m) (y - m) / l  (nats),
+ *   top_ids[t], top_logprobs[t]: the first top_k tokens of that order and
+ *                 their log probabilities.
+ *  logits      [T, V] bf16 or float32 (logits_type), rows `ld` elements apart
+ *              (ld >= V, any alignment of the rows; the array itself 16-byte
+ *              aligned).
+ *  ids         [T] int32 or NULL (then logprob and rank are not written and
+ *              may be NULL). An id outside [0, V) has log probability -inf and
+ *              rank 0, and is counted.
+ *  logprob, entropy [T] float32; rank [T] int32; top_logprobs [T, top_k]
+ *              float32, top_ids [T, top_k] int32 (not NULL when top_k > 0);
+ *              entropy may be NULL.
+ *  top_k       0 .. min(32, V);  temperature > 0 and finite.
+ *  workspace   as kv_attn_decode's, its own.
+ * -inf logits have no probability and add nothing; a row of nothing but -inf
+ * has log probabilities -inf and entropy 0. A row with NaN or +inf has NaN for
+ * its numbers; NaN comes first in the order, all NaN being equal, as are 0.0
+ * and -0.0. The result's bits do not depend on timing. T >= 0. */
+wq_status token_logprobs(const void* logits, int logits_type, int64_t ld, int64_t T, int64_t V, const int32_t* ids,
+                         float temperature, int top_k, float* logprob, int32_t* rank, float* entropy,
+                         float* top_logprobs, int32_t* top_ids, int32_t* bad_count, void* workspace, size_t ws_bytes,
+                         void* stream);
+
 /* ---- test and debug entry points ---------------------------------------- */
 
 /* The launch plan of the CTA-pair decode kernel for a shape (host only, no

@@ -1,0 +1,288 @@
+"""GPU checks of kv_append and kv_attn_decode against the float64 oracle.
+
+Tolerances, from the kernel's arithmetic (float32 scores, weights and sums,
+weights kept to at least 16 bits in the products, one rounding to bf16):
+ - a score is off by at most D 2^-24 A, A the largest sm_scale sum |q k|, and
+   by 2^-22 |x| from the scaling, the exponential's argument and itself, so lse
+   is off by at most e = (D 2^-24 + 2^-21) A + 2^-18;
+ - the output's weights are off by 2 e + 2^-15 in all, its rounding by 2^-8:
+   |out - ref| <= 2^-8 |ref| + (2 e + 2^-15) max |v|.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as R
+from tests.helpers import Guarded
+
+import weight_only_int2_gb300 as wq
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+class Case:
+    """A cache with the tables of sequences of the given lengths, its unused
+    tokens and pages filled with NaN."""
+
+    def __init__(self, lens, Hkv=2, G=4, D=128, S=16, e4m3=False, seed=0, W=None, spare=3, q_scale=1.0):
+        r = np.random.default_rng(seed)
+        self.S, self.e4m3 = S, e4m3
+        pages = [max(0, -(-n // S)) for n in lens]
+        self.W = W or max(1, max(pages, default=1))
+        P = sum(pages) + spare
+        ids = r.permutation(P)
+        self.table = np.full((len(lens), self.W), -1, dtype=np.int32)
+        self.lens = np.array(lens, dtype=np.int32)
+        codes = np.full((P, 2, Hkv, S, D), 0x7F if e4m3 else 0x7FC0, dtype=np.uint8 if e4m3 else np.uint16)
+        at = 0
+        for b, n in enumerate(lens):
+            for j in range(pages[b]):
+                p = ids[at]
+                at += 1
+                self.table[b, j] = p
+                m = min(S, n - j * S)
+                x = r.standard_normal((2, Hkv, m, D))
+                if e4m3:
+                    codes[p, :, :, :m] = R.e4m3_codes(x * 40)
+                else:
+                    codes[p, :, :, :m] = bf16_bits(x)
+        if e4m3:
+            self.kv = R.e4m3_values()[codes]
+            self.kv_dev = torch.from_numpy(codes).cuda().view(E4M3)
+            self.ks, self.vs = ((r.random(Hkv) + 0.5).astype(np.float32) / 40 for _ in range(2))
+        else:
+            self.kv = bf16_values(codes)
+            self.kv_dev = torch.from_numpy(codes.view(np.int16)).cuda().view(torch.bfloat16)
+            self.ks = self.vs = None
+        q = bf16_bits(r.standard_normal((len(lens), Hkv * G, D)) * q_scale)
+        self.q = bf16_values(q)
+        self.q_dev = torch.from_numpy(q.view(np.int16)).cuda().view(torch.bfloat16)
+        self.sm = 1 / math.sqrt(D)
+
+    def scales(self):
+        if not self.e4m3:
+            return {}
+        return {"k_scale": torch.from_numpy(self.ks).cuda(), "v_scale": torch.from_numpy(self.vs).cuda()}
+
+    def call(self, **kw):
+        kw = {"sm_scale": self.sm, "return_lse": True, **self.scales(), **kw}
+        return wq.kv_attn_decode(kw.pop("q", self.q_dev), self.kv_dev, torch.from_numpy(self.table).cuda(),
+                                 torch.from_numpy(self.lens).cuda(), **kw)
+
+    def check(self, out, lse, window=0, bad=None):
+        ref, ref_lse, gone, A = R.attn_decode(self.q, self.kv, self.table, self.lens, self.sm, window, self.ks, self.vs)
+        D = self.q.shape[2]
+        e = (D * 2.0 ** -24 + 2.0 ** -21) * A + 2.0 ** -18
+        top = np.nanmax(np.abs(self.kv[:, 1]), initial=0) * (1 if self.vs is None else self.vs.max())
+        out, lse = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+        assert np.array_equal(np.isinf(lse), np.isinf(ref_lse))
+        fin = np.isfinite(ref_lse)
+        assert np.all(np.abs(lse[fin] - ref_lse[fin]) <= e), np.abs(lse[fin] - ref_lse[fin]).max()
+        off = np.abs(out - ref) - 2.0 ** -8 * np.abs(ref)
+        assert np.all(off <= (2 * e + 2.0 ** -15) * top), (off.max(), (2 * e + 2.0 ** -15) * top)
+        assert np.all(out[~fin] == 0)
+        if bad is not None:
+            assert int(bad.item()) == gone
+
+
+def bf16_bits(x):
+    u = np.asarray(x, dtype=np.float32).view(np.uint32)
+    return ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
+
+
+def bf16_values(b):
+    return (b.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+LENS = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 130, 300, 517]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("G,Hkv", [(1, 3), (5, 2), (8, 1), (12, 2), (16, 1), (23, 2)])
+def test_attn_heads(D, G, Hkv, e4m3):
+    c = Case(LENS, Hkv=Hkv, G=G, D=D, e4m3=e4m3, seed=D + G)
+    c.check(*c.call())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("S", [1, 3, 8, 17, 48, 64, 100, 256])
+def test_attn_page_sizes(S, e4m3):
+    c = Case([1, S - 1, S, S + 1, 3 * S + 2, 700, 0], S=S, e4m3=e4m3, seed=S)
+    c.check(*c.call())
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 64, 100, 1000, 1 << 40])
+def test_attn_window(window):
+    c = Case(LENS, seed=window % 97, e4m3=window == 17)
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.check(*c.call(window=window, bad_count=bad), window=window, bad=bad)
+
+
+@pytest.mark.parametrize("B,n,e4m3", [(1, 1, False), (1, 5000, False), (1, 40000, False), (1, 40001, True),
+                                     (3, 9001, False), (200, 37, False), (400, 3, True)])
+def test_attn_long_and_many(B, n, e4m3):
+    c = Case([max(1, n - 11 * b) for b in range(B)], Hkv=2, G=3, e4m3=e4m3, seed=n)
+    c.check(*c.call())
+
+
+def test_attn_large_scores():
+    """Scores of some hundreds: weights that differ by more than float32 holds."""
+    c = Case([200, 64, 333], q_scale=40.0, seed=9)
+    c.check(*c.call())
+
+
+def test_attn_page_ids_and_lengths_out_of_range():
+    c = Case([40, 64, 33, 100, 16], W=9, seed=3)
+    P = c.kv.shape[0]
+    c.table[0, 1] = -1
+    c.table[1, 0] = P
+    c.table[2, :] = [2 ** 31 - 1, -2 ** 31, -5, -1, -1, -1, -1, -1, -1]  # nothing left
+    c.lens[3] = -7
+    c.lens[4] = 2 ** 31 - 1  # counts as W * S: the other pages are out of range
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.check(*c.call(bad_count=bad), bad=bad)
+
+
+def test_attn_scores_of_minus_infinity():
+    c = Case([50, 20], Hkv=1, G=2, seed=4)
+    c.kv[c.table[0, :4], 0, :, :, :] = -np.inf
+    c.kv_dev[torch.from_numpy(c.table[0, :4].astype(np.int64)).cuda(), 0] = -math.inf
+    c.q[:] = np.abs(c.q) + 1
+    c.q = bf16_values(bf16_bits(c.q))
+    c.q_dev = torch.from_numpy(bf16_bits(c.q).view(np.int16)).cuda().view(torch.bfloat16)
+    out, lse = c.call()
+    assert torch.all(out[0] == 0) and torch.all(lse[0] == -math.inf)
+    ref, ref_lse, _, _ = R.attn_decode(c.q[1:], c.kv, c.table[1:], c.lens[1:], c.sm)
+    assert np.abs(lse[1].cpu().numpy() - ref_lse[0]).max() < 1e-3
+    # NaN in a stored value reaches the result of its sequence and no other's
+    c.kv_dev[c.table[1, 0], 1, 0, 3, 5] = math.nan
+    out2, _ = c.call()
+    assert torch.isnan(out2[1, :, 5]).all() and not torch.isnan(out2[1, :, :5]).any()
+    assert torch.equal(out2[0], out[0])
+
+
+def test_attn_strided_queries_and_guarded_outputs():
+    c = Case([5, 100, 33], Hkv=2, G=4, seed=5)
+    wide = torch.full((3, 8 * 128 + 2 * 2 * 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, :1024] = c.q_dev.view(3, 1024)
+    out, lse = Guarded((3, 8, 128), torch.bfloat16), Guarded((3, 8), torch.float32)
+    c.check(*c.call(q=wide[:, :1024].unflatten(1, (8, 128)), out=out.t, lse=lse.t))
+    out.check("out")
+    lse.check("lse")
+
+
+def test_attn_repeats_and_streams():
+    """The same bits again and again: alone, after other shapes on the same
+    workspace, on another stream, and in a graph."""
+    c = Case([3000, 1, 777, 12000], Hkv=2, G=5, seed=6)
+    out, lse = c.call()
+    other = Case([9, 2000], Hkv=1, G=16, D=256, e4m3=True, seed=7)
+    for _ in range(5):
+        other.check(*other.call())
+        out2, lse2 = c.call()
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        out3, lse3 = c.call()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, out3) and torch.equal(lse, lse3)
+    table, lens = torch.from_numpy(c.table).cuda(), torch.from_numpy(c.lens).cuda()
+    out4, lse4 = torch.empty_like(out), torch.empty_like(lse)
+    need = wq.kv_attn_workspace_bytes(4, 10, 2, 128)
+    ws = torch.zeros(max(16, need), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        wq.kv_attn_decode(c.q_dev, c.kv_dev, table, lens, out=out4, lse=lse4, ws=ws)
+    for n in (c.lens, np.array([5, 4000 - 3001, 1, 0], dtype=np.int32), c.lens):
+        lens.copy_(torch.from_numpy(n))
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, out4) and torch.equal(lse, lse4)
+
+
+def test_attn_offsets_beyond_32_bits():
+    """Pages whose elements lie beyond 2^31 (and bytes beyond 2^32)."""
+    H, S, D = 8, 256, 256
+    P = (1 << 31) // (2 * H * S * D) + 8
+    kv = torch.zeros((P, 2, H, S, D), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kv[P - 3:] = torch.randn((3, 2, H, S, D), generator=g, device="cuda").bfloat16()
+    q = torch.randn((1, 8, D), generator=g, device="cuda").bfloat16()
+    table = torch.tensor([[P - 1, P - 3]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([S + 77], dtype=torch.int32, device="cuda")
+    out, lse = wq.kv_attn_decode(q, kv, table, lens, return_lse=True)
+    small = kv[[P - 1, P - 3]].clone()
+    out2, lse2 = wq.kv_attn_decode(q, small, torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), lens,
+                                   return_lse=True)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    x = torch.randn((1, 8, D), generator=g, device="cuda").bfloat16()
+    wq.kv_append(x, x, torch.tensor([S + 5], dtype=torch.int32, device="cuda"), table, kv)
+    assert torch.equal(kv[P - 3, 0, :, 5], x[0]) and torch.equal(kv[P - 3, 1, :, 5], x[0])
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("D,S,Hkv,T", [(64, 16, 2, 1), (96, 7, 3, 37), (128, 16, 8, 64), (192, 1, 1, 5),
+                                      (256, 100, 4, 211)])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("sliced", [False, True])
+def test_append(D, S, Hkv, T, e4m3, sliced):
+    r = np.random.default_rng(D + T)
+    B, W = 5, -(-2 * T // (5 * S)) + 1
+    P = B * W + 2
+    table = r.permutation(P)[:B * W].reshape(B, W).astype(np.int32)
+    at = r.permutation(B * W * S)[:T]
+    seq, pos = (at // (W * S)).astype(np.int32), (at % (W * S)).astype(np.int32)
+    if T > 8:  # tokens that have no place
+        seq[1], seq[2], pos[3], pos[4] = -1, B, -1, W * S
+        table[seq[5], pos[5] // S] = P
+    bits = bf16_bits(r.standard_normal((T, 2, Hkv, D)) * 3)
+    bits[0, 0, 0, :6] = [0x0000, 0x8000, 0x7F80, 0xFF80, 0x7FC0, 0x4780]  # 0, -0, inf, -inf, NaN, 65536
+    ks, vs = ((r.random(Hkv) + 0.5).astype(np.float32) / 30 for _ in range(2))
+    x = torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16)
+    k, v = (x[:, 0], x[:, 1]) if sliced else (x[:, 0].contiguous(), x[:, 1].contiguous())
+    kv = Guarded((P, 2, Hkv, S, D), E4M3 if e4m3 else torch.bfloat16)
+    want = kv.t.view(torch.uint8 if e4m3 else torch.int16).cpu().numpy().copy()
+    vals = bf16_values(bits)
+    bad = 0
+    for t, (page, slot) in enumerate(R.token_places(table, P, S, seq, pos)):
+        if page < 0:
+            bad += 1
+            continue
+        for i, w in ((0, ks), (1, vs)):
+            if e4m3:
+                y = vals[t, i].astype(np.float32) / w[:, None]  # one IEEE division
+                c = R.e4m3_codes(np.nan_to_num(y.astype(np.float64), nan=0.0))
+                want[page, i, :, slot] = np.where(np.isnan(y), 0x7F, c)
+            else:
+                want[page, i, :, slot] = bits[t, i].view(np.int16)
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = {"k_scale": torch.from_numpy(ks).cuda(), "v_scale": torch.from_numpy(vs).cuda()} if e4m3 else {}
+    wq.kv_append(k, v, torch.from_numpy(pos).cuda(), torch.from_numpy(table).cuda(), kv.t,
+                 seq=torch.from_numpy(seq).cuda(), bad_count=count, **kw)
+    got = kv.t.view(torch.uint8 if e4m3 else torch.int16).cpu().numpy()
+    if e4m3:  # either NaN code is a NaN
+        got, want = (np.where((a & 127) == 127, 127, a) for a in (got, want))
+    assert np.array_equal(got, want)
+    assert int(count.item()) == bad
+    kv.check("cache")
+
+
+def test_append_without_seq_and_empty():
+    kv = torch.zeros((4, 2, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    x = torch.randn((2, 2, 64), device="cuda").bfloat16()
+    pos = torch.tensor([8, 3], dtype=torch.int32, device="cuda")
+    wq.kv_append(x, x * 2, pos, table, kv)
+    assert torch.equal(kv[1, 0, :, 0], x[0]) and torch.equal(kv[2, 1, :, 3], x[1] * 2)
+    before = kv.clone()
+    wq.kv_append(x[:0], x[:0], pos[:0], table, kv)
+    assert torch.equal(kv, before)
+    out = wq.kv_attn_decode(x[:0], kv, table[:0], pos[:0])
+    assert out.shape == (0, 2, 64)

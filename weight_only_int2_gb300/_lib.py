@@ -45,6 +45,25 @@ SIGNATURES = {
                            _c_size, _c_ptr, _c_size, _c_ptr]),
     "qembed_gather": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_int, _c_int, _c_ptr,
                                _c_ptr, _c_ptr]),
+    "kv_append": (_c_int, [_c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_ptr,
+                           _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "kv_attn_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "kv_attn_decode": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64,
+                                _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, ctypes.c_float, _c_i64, _c_ptr, _c_ptr,
+                                _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "kv_pages_scratch_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "kv_pages_copy": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_ptr]),
+    "kv_pages_fork": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64,
+                               _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "kv_pages_reserve": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr,
+                                  _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "kv_pages_free": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_i64, _c_ptr,
+                               _c_ptr, _c_ptr, _c_ptr]),
+    "kv_pages_compact": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64,
+                                  _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "token_logprobs_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_int]),
+    "token_logprobs": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, ctypes.c_float, _c_int, _c_ptr,
+                                _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "wq_debug_decode_plan": (_c_int, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_ptr]),
     "wq_debug_route": (_c_int, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_ptr]),
     "wq_debug_unpack": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_int, _c_ptr, _c_ptr]),
@@ -334,6 +353,277 @@ def qembed_gather(ids: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
     _check(load().qembed_gather(_ptr(ids), T, _ptr(packed), _ptr(scales), V, D, bits, group, _ptr(out),
                                 _ptr(bad_count), _stream()), "qembed_gather")
     return out
+
+
+# ---------------------------------------------------------------- serving operators
+
+_KV_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+_LOGIT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _need_rows(t: torch.Tensor, name: str, shape) -> int:
+    """A bf16 tensor whose rows are contiguous and whose first dimension may
+    have any stride; returns that stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16 (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    row = shape[1] * shape[2]
+    if shape[0] == 0:
+        return row
+    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return row if shape[0] == 1 else t.stride(0)
+
+
+def _need_cache(kv: torch.Tensor, k_scale, v_scale):
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 5 or kv.shape[1] != 2:
+        raise ValueError("kv must be a tensor [P, 2, Hkv, S, D]")
+    if kv.dtype not in _KV_TYPES:
+        raise TypeError(f"kv must be bfloat16 or float8_e4m3fn (got {kv.dtype})")
+    _need(kv, "kv", kv.dtype)
+    if kv.dtype == torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale are for e4m3 caches")
+    else:
+        _need(k_scale, "k_scale", torch.float32, (kv.shape[2],))
+        _need(v_scale, "v_scale", torch.float32, (kv.shape[2],))
+    return _KV_TYPES[kv.dtype]
+
+
+def _need_pool(kv: torch.Tensor):
+    """kv [L, P, 2, Hkv, S, D] or one layer's [P, 2, Hkv, S, D]: (L, P, S, page bytes)."""
+    if not isinstance(kv, torch.Tensor) or kv.dim() not in (5, 6) or kv.shape[-4] != 2:
+        raise ValueError("kv must be a tensor [L, P, 2, Hkv, S, D] or [P, 2, Hkv, S, D]")
+    if kv.dtype not in _KV_TYPES:
+        raise TypeError(f"kv must be bfloat16 or float8_e4m3fn (got {kv.dtype})")
+    _need(kv, "kv", kv.dtype)
+    L, (P, two, H, S, D) = (kv.shape[0] if kv.dim() == 6 else 1), kv.shape[-5:]
+    return L, P, S, two * H * S * D * kv.element_size()
+
+
+def kv_attn_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().kv_attn_workspace_bytes(B, Hq, Hkv, D))
+
+
+def kv_pages_scratch_bytes(n: int, B: int, W: int, P: int) -> int:
+    return int(load().kv_pages_scratch_bytes(n, B, W, P))
+
+
+def token_logprobs_workspace_bytes(T: int, V: int, top_k: int) -> int:
+    return int(load().token_logprobs_workspace_bytes(T, V, top_k))
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, block_table: torch.Tensor, kv: torch.Tensor,
+              seq: torch.Tensor | None = None, k_scale: torch.Tensor | None = None,
+              v_scale: torch.Tensor | None = None, bad_count: torch.Tensor | None = None) -> torch.Tensor:
+    """Writes k, v [T, Hkv, D] bf16 (rows may be strided) into the pages of kv
+    [P, 2, Hkv, S, D]: token t as token pos[t] of sequence seq[t] (of sequence
+    t without seq). Returns kv."""
+    kind = _need_cache(kv, k_scale, v_scale)
+    P, _, H, S, D = kv.shape
+    T, (B, W) = k.shape[0], block_table.shape
+    ks, vs = _need_rows(k, "k", (T, H, D)), _need_rows(v, "v", (T, H, D))
+    _need(pos, "pos", torch.int32, (T,))
+    _need(block_table, "block_table", torch.int32, (B, W))
+    if seq is not None:
+        _need(seq, "seq", torch.int32, (T,))
+    if bad_count is not None:
+        _need(bad_count, "bad_count", torch.int32)
+    _check(load().kv_append(_ptr(k), _ptr(v), ks, vs, T, _ptr(seq), _ptr(pos), _ptr(block_table), B, W, _ptr(kv),
+                            kind, P, H, S, D, _ptr(k_scale), _ptr(v_scale), _ptr(bad_count), _stream()), "kv_append")
+    return kv
+
+
+def kv_attn_decode(q: torch.Tensor, kv: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+                   sm_scale: float | None = None, window: int = 0, k_scale: torch.Tensor | None = None,
+                   v_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, return_lse: bool = False,
+                   bad_count: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Attention of one new token per sequence: q [B, Hq, D] bf16 over the
+    lens[b] tokens of kv [P, 2, Hkv, S, D] that block_table [B, W] names.
+    sm_scale: 1/sqrt(D) if None; window: the last so many tokens (0: all).
+    Returns out [B, Hq, D] bf16, and lse [B, Hq] float32 with return_lse."""
+    kind = _need_cache(kv, k_scale, v_scale)
+    P, _, H, S, D = kv.shape
+    B, Hq = q.shape[0], q.shape[1]
+    W = block_table.shape[1]
+    qs = _need_rows(q, "q", (B, Hq, D))
+    _need(block_table, "block_table", torch.int32, (B, W))
+    _need(lens, "lens", torch.int32, (B,))
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, "out", torch.bfloat16, (B, Hq, D))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, Hq))
+    elif return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if bad_count is not None:
+        _need(bad_count, "bad_count", torch.int32)
+    lib = load()
+    if ws is None:
+        ws = _cached("kv_attn", lib.kv_attn_workspace_bytes(B, Hq, H, D))
+    _check(lib.kv_attn_decode(_ptr(q), qs, _ptr(kv), kind, _ptr(block_table), _ptr(lens), B, W, P, Hq, H, S, D,
+                              _ptr(k_scale), _ptr(v_scale), D ** -0.5 if sm_scale is None else sm_scale, window,
+                              _ptr(out), _ptr(lse), _ptr(bad_count), _ptr(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _stream()), "kv_attn_decode")
+    return (out, lse) if return_lse else out
+
+
+def kv_pages_copy(kv: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+                  bad_count: torch.Tensor | None = None) -> torch.Tensor:
+    """Copies page src[i] to page dst[i] in every layer of kv; returns kv."""
+    L, P, _, size = _need_pool(kv)
+    n = src.shape[0]
+    _need(src, "src", torch.int32, (n,))
+    _need(dst, "dst", torch.int32, (n,))
+    if bad_count is not None:
+        _need(bad_count, "bad_count", torch.int32)
+    _check(load().kv_pages_copy(_ptr(kv), L, P, size, _ptr(src), _ptr(dst), n, _ptr(bad_count), _stream()),
+           "kv_pages_copy")
+    return kv
+
+
+def _need_tables(block_table, lens, ref):
+    B, W = block_table.shape
+    P = ref.shape[0]
+    _need(block_table, "block_table", torch.int32, (B, W))
+    _need(lens, "lens", torch.int32, (B,))
+    _need(ref, "ref", torch.int32, (P,))
+    return B, W, P
+
+
+def _or_in_place(out, given, name):
+    if out is None:
+        return given
+    _need(out, name, torch.int32, given.shape)
+    return out
+
+
+def _out_32(out, shape, name, device):
+    if out is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _need(out, name, torch.int32, shape)
+    return out
+
+
+def kv_pages_fork(kv: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor,
+                  parent: torch.Tensor, child: torch.Tensor, table_out: torch.Tensor | None = None,
+                  lens_out: torch.Tensor | None = None, ref_out: torch.Tensor | None = None,
+                  granted: torch.Tensor | None = None):
+    """Starts sequence child[i] as a copy of parent[i]: full pages are shared,
+    a partial last page is copied to a free one. Updates block_table, lens and
+    ref in place unless given other outputs; returns (block_table, lens, ref,
+    granted)."""
+    L, P, S, size = _need_pool(kv)
+    B, W, _ = _need_tables(block_table, lens, ref)
+    _need(ref, "ref", torch.int32, (P,))
+    n = parent.shape[0]
+    _need(parent, "parent", torch.int32, (n,))
+    _need(child, "child", torch.int32, (n,))
+    table_out = _or_in_place(table_out, block_table, "table_out")
+    lens_out, ref_out = _or_in_place(lens_out, lens, "lens_out"), _or_in_place(ref_out, ref, "ref_out")
+    granted = _out_32(granted, (n,), "granted", kv.device)
+    lib = load()
+    scr = scratch(lib.kv_pages_scratch_bytes(n, B, W, P))
+    _check(lib.kv_pages_fork(_ptr(kv), L, P, size, _ptr(block_table), _ptr(lens), _ptr(ref), B, W, S, _ptr(parent),
+                             _ptr(child), n, _ptr(table_out), _ptr(lens_out), _ptr(ref_out), _ptr(granted),
+                             _ptr(scr), scr.numel(), _stream()), "kv_pages_fork")
+    return table_out, lens_out, ref_out, granted
+
+
+def kv_pages_reserve(block_table: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor, ref: torch.Tensor,
+                     page_size: int, table_out: torch.Tensor | None = None, ref_out: torch.Tensor | None = None,
+                     granted: torch.Tensor | None = None):
+    """Gives every sequence the free pages that new_lens[b] tokens need beyond
+    those of lens[b]. Updates block_table and ref in place unless given other
+    outputs; returns (block_table, ref, granted)."""
+    B, W, P = _need_tables(block_table, lens, ref)
+    _need(new_lens, "new_lens", torch.int32, (B,))
+    table_out, ref_out = _or_in_place(table_out, block_table, "table_out"), _or_in_place(ref_out, ref, "ref_out")
+    granted = _out_32(granted, (B,), "granted", ref.device)
+    lib = load()
+    scr = scratch(lib.kv_pages_scratch_bytes(B, B, W, P))
+    _check(lib.kv_pages_reserve(_ptr(block_table), _ptr(lens), _ptr(new_lens), _ptr(ref), B, W, page_size, P,
+                                _ptr(table_out), _ptr(ref_out), _ptr(granted), _ptr(scr),
+                                0 if scr is None else scr.numel(), _stream()), "kv_pages_reserve")
+    return table_out, ref_out, granted
+
+
+def kv_pages_free(block_table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, seqs: torch.Tensor,
+                  page_size: int, lens_out: torch.Tensor | None = None, ref_out: torch.Tensor | None = None,
+                  bad_count: torch.Tensor | None = None):
+    """Gives back the pages of the sequences seqs. Updates lens and ref in
+    place unless given other outputs; returns (lens, ref)."""
+    B, W, P = _need_tables(block_table, lens, ref)
+    n = seqs.shape[0]
+    _need(seqs, "seqs", torch.int32, (n,))
+    lens_out, ref_out = _or_in_place(lens_out, lens, "lens_out"), _or_in_place(ref_out, ref, "ref_out")
+    if bad_count is not None:
+        _need(bad_count, "bad_count", torch.int32)
+    _check(load().kv_pages_free(_ptr(block_table), _ptr(lens), _ptr(ref), B, W, page_size, P, _ptr(seqs), n,
+                                _ptr(lens_out), _ptr(ref_out), _ptr(bad_count), _stream()), "kv_pages_free")
+    return lens_out, ref_out
+
+
+def kv_pages_compact(kv: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor,
+                     table_out: torch.Tensor | None = None, ref_out: torch.Tensor | None = None,
+                     remap: torch.Tensor | None = None, n_live: torch.Tensor | None = None):
+    """Moves the pages in use to the front of the pool. Updates block_table and
+    ref in place unless given other outputs; returns (block_table, ref, remap,
+    n_live)."""
+    L, P, S, size = _need_pool(kv)
+    B, W, _ = _need_tables(block_table, lens, ref)
+    _need(ref, "ref", torch.int32, (P,))
+    table_out, ref_out = _or_in_place(table_out, block_table, "table_out"), _or_in_place(ref_out, ref, "ref_out")
+    remap, n_live = _out_32(remap, (P,), "remap", kv.device), _out_32(n_live, (1,), "n_live", kv.device)
+    lib = load()
+    scr = scratch(lib.kv_pages_scratch_bytes(0, B, W, P))
+    _check(lib.kv_pages_compact(_ptr(kv), L, P, size, _ptr(block_table), _ptr(lens), _ptr(ref), B, W, S,
+                                _ptr(table_out), _ptr(ref_out), _ptr(remap), _ptr(n_live), _ptr(scr), scr.numel(),
+                                _stream()), "kv_pages_compact")
+    return table_out, ref_out, remap, n_live
+
+
+def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k: int = 0, temperature: float = 1.0,
+                   bad_count: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Per row of logits [T, V] (bf16 or float32, rows may be strided): the log
+    probability and rank of ids[t], the entropy, and the best top_k tokens.
+    Returns (logprob [T], rank [T], entropy [T], top_logprobs [T, top_k],
+    top_ids [T, top_k]); logprob and rank are None without ids."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype not in _LOGIT_TYPES:
+        raise TypeError(f"logits must be bfloat16 or float32 (got {logits.dtype})")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [T, V] with contiguous rows")
+    (T, V), dev = logits.shape, logits.device
+    lp = rank = None
+    if ids is not None:
+        _need(ids, "ids", torch.int32, (T,))
+        lp = torch.empty(T, dtype=torch.float32, device=dev)
+        rank = torch.empty(T, dtype=torch.int32, device=dev)
+    if bad_count is not None:
+        _need(bad_count, "bad_count", torch.int32)
+    k = max(int(top_k), 0)
+    entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    top = torch.empty((T, k), dtype=torch.float32, device=dev)
+    top_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    lib = load()
+    if ws is None:
+        ws = _cached("logprobs", lib.token_logprobs_workspace_bytes(T, V, k))
+    _check(lib.token_logprobs(_ptr(logits), _LOGIT_TYPES[logits.dtype], V if T <= 1 else logits.stride(0), T, V,
+                              _ptr(ids), temperature, top_k, _ptr(lp), _ptr(rank), _ptr(entropy), _ptr(top),
+                              _ptr(top_ids), _ptr(bad_count), _ptr(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _stream()), "token_logprobs")
+    return lp, rank, entropy, top, top_ids
 
 
 _PLAN_KEYS = ("ok", "C", "H", "nchunk", "T", "ksplit", "NS", "G", "Gh", "sbox", "sx0", "NT", "smem",

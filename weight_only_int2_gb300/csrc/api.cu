@@ -37,7 +37,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 EncodeTiledFn g_encode = nullptr;
 std::once_flag g_encode_once;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
 wq_status fail(wq_status s, const char* fmt, ...) {
   va_list ap;
@@ -51,7 +51,8 @@ wq_status cuda_fail(cudaError_t e, const char* where) {
   return fail(WQ_ECUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-// Fills `c` for the current device; sets up the device's state on first use.
+void clear_error() { t_err[0] = 0; }
+
 wq_status get_ctx(void* stream, Ctx* c) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -79,13 +80,13 @@ wq_status get_ctx(void* stream, Ctx* c) {
   return WQ_OK;
 }
 
+namespace {
+
 wq_status check_bits(int bits) {
   if (bits < 2 || bits > 8) return fail(WQ_EINVAL, "bits must be in 2..8 (got %d)", bits);
   return WQ_OK;
 }
 
-// Sizes become grid dimensions and 32-bit TMA coordinates: all below 2^31.
-constexpr int64_t kMaxDim = 0x7FFFFFFF;
 // Experts of one grouped call (each tile looks its expert up in the offsets).
 constexpr int kMaxExperts = 1024;
 
@@ -93,11 +94,6 @@ wq_status check_group_k(int group, int64_t K, const char* kname) {
   if (group != 128) return fail(WQ_EUNSUPPORTED, "group must be 128 (got %d)", group);
   if (K <= 0 || K % 128 != 0 || K > kMaxDim)
     return fail(WQ_EINVAL, "%s must be a positive multiple of 128 below 2^31 (got %lld)", kname, (long long)K);
-  return WQ_OK;
-}
-
-wq_status check_size(int64_t v, const char* name) {
-  if (v < 1 || v > kMaxDim) return fail(WQ_EINVAL, "%s must be in 1..2^31-1 (got %lld)", name, (long long)v);
   return WQ_OK;
 }
 
@@ -117,19 +113,12 @@ wq_status no_route(int64_t M, int64_t N, int64_t K) {
               (long long)M, (long long)N, (long long)K);
 }
 
-#define WQ_TRY(expr)            \
-  do {                          \
-    wq_status _s = (expr);      \
-    if (_s != WQ_OK) return _s; \
-  } while (0)
-
-#define WQ_PTR(p)                                                         \
-  do {                                                                    \
-    if ((p) == nullptr) return fail(WQ_EINVAL, "%s is NULL", #p);          \
-    if (!aligned16(p)) return fail(WQ_EINVAL, "%s is not 16-byte aligned", #p); \
-  } while (0)
-
 }  // namespace
+
+wq_status check_size(int64_t v, const char* name) {
+  if (v < 1 || v > kMaxDim) return fail(WQ_EINVAL, "%s must be in 1..2^31-1 (got %lld)", name, (long long)v);
+  return WQ_OK;
+}
 
 void set_error(const char* fmt, ...) {
   va_list ap;

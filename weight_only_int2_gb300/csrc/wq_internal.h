@@ -23,6 +23,34 @@ struct Ctx {
 // Records a one-line error for wq_last_error() (thread-local).
 void set_error(const char* fmt, ...);
 
+// ---- argument checks of the C-ABI files (defined in api.cu) ------------------
+
+// Records the message and returns s.
+wq_status fail(wq_status s, const char* fmt, ...);
+wq_status cuda_fail(cudaError_t e, const char* where);
+void clear_error();
+
+// Fills `c` for the current device; sets up the device's state on first use.
+wq_status get_ctx(void* stream, Ctx* c);
+
+// Sizes become grid dimensions and 32-bit TMA coordinates: all below 2^31.
+constexpr int64_t kMaxDim = 0x7FFFFFFF;
+wq_status check_size(int64_t v, const char* name);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+#define WQ_TRY(expr)            \
+  do {                          \
+    wq_status _s = (expr);      \
+    if (_s != WQ_OK) return _s; \
+  } while (0)
+
+#define WQ_PTR(p)                                                         \
+  do {                                                                    \
+    if ((p) == nullptr) return fail(WQ_EINVAL, "%s is NULL", #p);          \
+    if (!aligned16(p)) return fail(WQ_EINVAL, "%s is not 16-byte aligned", #p); \
+  } while (0)
+
 // A kernel's dynamic shared-memory limit per device, raised on demand and
 // never lowered, under a lock: host threads that launch concurrently never
 // see a limit below the one they raised (a lowered limit would fail their
@@ -255,5 +283,71 @@ wq_status wna16_route(int64_t M, int64_t N, int64_t K, int bits, void* stream, C
 wq_status wna16_launch(const Ctx& c, Route r, const uint16_t* x, int64_t M, const uint32_t* Wpacked,
                        const uint16_t* scales, int64_t N, int64_t K, int bits, uint16_t* y, void* workspace,
                        const uint8_t* zeros = nullptr);
+
+// ---- serving operators (serve_api.cu; kernels in kv_append.cu, kv_attn.cu,
+// kv_pages.cu and logprobs.cu) -------------------------------------------------
+
+// One layer's paged cache, kv [P, 2, Hkv, S, D] of `type` (WQ_KV_*), with the
+// tables of B sequences.
+struct KvCache {
+  void* kv;
+  int type;
+  int64_t P, Hkv, S, D;
+  const float* k_scale;  // [Hkv], e4m3 only
+  const float* v_scale;
+  const int32_t* table;  // [B, W]
+  int64_t B, W;
+};
+
+cudaError_t launch_kv_append(const Ctx& c, const KvCache& a, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                             int64_t v_stride, int64_t T, const int32_t* seq, const int32_t* pos, int32_t* bad);
+
+size_t kv_attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+cudaError_t launch_kv_attn(const Ctx& c, const KvCache& a, const uint16_t* q, int64_t q_stride, const int32_t* lens,
+                           int64_t Hq, float sm_scale, int64_t window, uint16_t* out, float* lse, int32_t* bad,
+                           void* ws);
+
+// A page pool: L layers of P pages.
+struct PagePool {
+  void* kv;
+  int64_t L, P, page_bytes;
+};
+struct SeqTables {
+  const int32_t* table;  // [B, W]
+  const int32_t* lens;   // [B]
+  const int32_t* ref;    // [P]
+  int64_t B, W, S, P;
+};
+size_t kv_pages_scratch(int64_t n, int64_t B, int64_t W, int64_t P);
+cudaError_t launch_pages_copy(const Ctx& c, const PagePool& p, const int32_t* src, const int32_t* dst, int64_t n,
+                              int32_t* bad);
+cudaError_t launch_pages_fork(const Ctx& c, const PagePool& p, const SeqTables& t, const int32_t* parent,
+                              const int32_t* child, int64_t n, int32_t* table_out, int32_t* lens_out,
+                              int32_t* ref_out, int32_t* granted, void* scratch);
+cudaError_t launch_pages_reserve(const Ctx& c, const SeqTables& t, const int32_t* new_lens, int32_t* table_out,
+                                 int32_t* ref_out, int32_t* granted, void* scratch);
+cudaError_t launch_pages_free(const Ctx& c, const SeqTables& t, const int32_t* seqs, int64_t n, int32_t* lens_out,
+                              int32_t* ref_out, int32_t* bad);
+cudaError_t launch_pages_compact(const Ctx& c, const PagePool& p, const SeqTables& t, int32_t* table_out,
+                                 int32_t* ref_out, int32_t* remap, int32_t* n_live, void* scratch);
+
+struct LogprobArgs {
+  const void* logits;
+  int type;  // WQ_LOGITS_*
+  int64_t ld, T, V;
+  const int32_t* ids;
+  float temperature;
+  int top_k;
+  float* logprob;
+  int32_t* rank;
+  float* entropy;
+  float* top_logprobs;
+  int32_t* top_ids;
+  int32_t* bad;
+  void* ws;
+};
+constexpr int kMaxTopK = 32;
+size_t logprobs_ws_bytes(int64_t T, int64_t V, int top_k);
+cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a);
 
 }  // namespace wq
