@@ -298,6 +298,7 @@ size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
  *              between calls is not zero). Not shared by calls that may run
  *              concurrently; zeroed again after a call that failed.
  * The result's bits do not depend on timing. B >= 0; Hq a multiple of Hkv.
+ * NaN among the tokens used gives NaN, and so may infinite values of v.
  * bad_count: pages left out. Tokens on a page beyond the length are never
  * used, whatever they hold. */
 wq_status kv_attn_decode(const wq_bf16* q, int64_t q_stride, const void* kv, int kv_type,
