@@ -34,16 +34,16 @@
 namespace wq {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;               // tokens a warp takes at a time
-constexpr int kUnit = kStep * kWarps;   // tokens a block takes at a time
+constexpr int kStep = 16;        // tokens a warp takes at a time
 // A (sequence, head) of at most this many units is not cut: a join costs
-// about as much as four units in a row.
-constexpr int kMinShare = 4;
-constexpr int kMaxBlocks = 512;         // shares (the partial results' space)
+// about as much as a few units in a row.
+constexpr int kMinShare = 2;
+// What beginning and ending an item costs, in units: every item takes so many
+// places more in the line, so that shares with many short items take no longer.
+constexpr int kItemCost = 1;
+constexpr int kMaxBlocks = 512;  // shares (the partial results' space)
 
-// Row base of a head chunk: at most 16 query heads of one key head.
+// A head chunk is at most 16 query heads of one key head (kR16), or 8.
 template <int D, bool kE4m3, bool kR16>
 struct Cfg {
   static constexpr int kRows = kR16 ? 16 : 8;
@@ -51,20 +51,28 @@ struct Cfg {
   static constexpr int kPitch = kRowBytes + 16;  // an odd number of 16-byte words: ldmatrix without conflicts
   static constexpr int kSide = kStep * kPitch;   // a step's keys (or values)
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kOPitch = D + 8;          // floats
-  static constexpr int kOBuf = kRows * kOPitch * 4;
-  static constexpr int kMisc = 1024;
-  static constexpr int kFixed = 2 * kOBuf + kMisc;
-  static constexpr int kFit2 = (113 * 1024 - kFixed) / (kWarps * kStage);
-  static constexpr int kFit1 = (226 * 1024 - kFixed) / (kWarps * kStage);
-  static constexpr int kBlocksPerSm = kFit2 >= 3 ? 2 : 1;
-  static constexpr int kFit = kBlocksPerSm == 2 ? kFit2 : kFit1;
+  static constexpr int kMisc = 3072;
+  // Warps of a block and blocks of an SM: as many warps as the registers (a
+  // warp keeps D / 2 or more running sums a thread) and stages allow.
+  static constexpr int kBlocksPerSm = D == 64 ? 2 : 1;
+  static constexpr int kRoom = (kBlocksPerSm == 2 ? 113 : 227) * 1024 - kMisc;
+  static constexpr int kWarps = D <= 128 && D > 64 && kE4m3 ? 12 : (16 * kStage <= kRoom ? 8 : 4);
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kUnit = kStep * kWarps;  // tokens a block takes at a time
+  static constexpr int kFit = kRoom / (kWarps * kStage);
   static constexpr int kStages = kFit < 6 ? kFit : 6;
-  static constexpr int kSmem = kFixed + kWarps * kStages * kStage;
+  static constexpr int kSmem = kMisc + kWarps * kStages * kStage;
+  // A warp's sums on their way to the block's: kOut rows in the stage that was
+  // read last. The pitch keeps 8 rows of a store apart.
+  static constexpr int kOPitch = D + (kE4m3 ? 16 : 8);  // floats
+  static constexpr int kOut = kE4m3 && kR16 ? 8 : kRows;
+  static_assert(kOut * kOPitch * 4 <= kStage, "the sums fit a stage");
   // lanes that load one row (16 bytes each at a time)
   static constexpr int kLanes = kRowBytes % 128 == 0 ? 8 : (kRowBytes % 64 == 0 ? 4 : 2);
   static constexpr int kRowsPerLane = kStep * kLanes / 32;
   static constexpr int kChunks = kRowBytes / (16 * kLanes);
+  // registers of 4 for the queries: 16 columns each, or 32 of e4m3 codes (twice with kR16)
+  static constexpr int kQ = kE4m3 && !kR16 ? D / 32 : D / 16;
   static_assert(kStages >= 2, "at least two stages");
 };
 
@@ -106,16 +114,36 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 template <bool kF16>
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (kF16)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    mma_bf16_16816(c, a0, a1, a2, a3, b0, b1);
+    mma_bf16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four bf16 numbers times `up` as hi + lo, four e4m3 codes each.
+__device__ __forceinline__ void split_e4m3(uint2 w, float up, uint32_t& hi, uint32_t& lo) {
+  hi = lo = 0u;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t p = j ? w.y : w.x;
+    const float x = __uint_as_float(p << 16) * up, y = __uint_as_float(p & 0xFFFF0000u) * up;
+    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+    const __nv_fp8x2_storage_t d = __nv_cvt_float2_to_fp8x2(make_float2(x - f.x, y - f.y), __NV_SATFINITE, __NV_E4M3);
+    hi |= static_cast<uint32_t>(c) << (16 * j);
+    lo |= static_cast<uint32_t>(d) << (16 * j);
+  }
 }
 // Two e4m3 codes (the low or high half of w) as two fp16 numbers, exactly.
 __device__ __forceinline__ uint32_t widen(uint32_t w, bool high) {
@@ -150,6 +178,7 @@ struct Span {
   unsigned first, end;  // below 2^31, but a unit may reach past that
   int units;
 };
+template <int kUnit>
 __device__ __forceinline__ Span span_of(const Args& a, int64_t b) {
   int64_t len = a.lens[b];
   const int64_t cap = a.kv.W * a.kv.S;
@@ -162,33 +191,58 @@ __device__ __forceinline__ Span span_of(const Args& a, int64_t b) {
   return s;
 }
 
-// A place in the line of units: unit `unit` of head chunk `hc` of sequence b.
+// Places of an item in the line: its cost, then its units.
+__device__ __forceinline__ int places(const Span& s) { return s.units == 0 ? 0 : s.units + kItemCost; }
+
+// Unit `unit` of head chunk `hc` of sequence b, at place `at` of the line.
+template <int kUnit>
 struct Cursor {
-  int64_t b;
+  int64_t b, at;
   int hc, unit;
   Span s;
   __device__ void next(const Args& a, int per_seq) {
+    ++at;
     if (++unit < s.units) return;
+    at += kItemCost;
     unit = 0;
     if (++hc < per_seq) return;
     hc = 0;
     do {
       if (++b >= a.kv.B) return;
-      s = span_of(a, b);
+      s = span_of<kUnit>(a, b);
     } while (s.units == 0);
   }
 };
 
+// (m, l) of two parts of a softmax together, into the first.
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2), base = top == -CUDART_INF_F ? 0.0f : top;
+  l = l * exp2_fast(m - base) + l2 * exp2_fast(m2 - base);
+  m = top;
+}
+
+// Four columns of a result.
+template <int D>
+__device__ __forceinline__ void put(const Args& a, int64_t b, int hq, int d, float4 o, float m, float l, float vs) {
+  const float f = l == 0.0f ? 0.0f : vs / l;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * f, o.y * f), y = __floats2bfloat162_rn(o.z * f, o.w * f);
+  *reinterpret_cast<uint2*>(a.out + (b * a.Hq + hq) * D + d) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  if (a.lse != nullptr && d == 0)
+    a.lse[b * a.Hq + hq] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 template <int D, bool kE4m3, bool kR16>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
+__global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, kR16>::kBlocksPerSm)
+    attn_kernel(const Args a) {
   using C = Cfg<D, kE4m3, kR16>;
-  constexpr int kK = D / 16, kN = D / 8;
+  constexpr int kK = D / 16, kN = D / 8, kWarps = C::kWarps, kThreads = C::kThreads, kUnit = C::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* obuf = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStage);
-  float* ml = obuf + 2 * C::kOBuf / 4;                                  // [kWarps][16][2]
-  uint32_t* vmask = reinterpret_cast<uint32_t*>(ml + kWarps * 16 * 2);  // [kWarps][kStages]
-  int64_t* share = reinterpret_cast<int64_t*>(vmask + 32);              // [0] share, [1] b, [2] units before b
-  unsigned* last = reinterpret_cast<unsigned*>(share + 4);
+  float* ml = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStage);  // [kWarps][16][2]
+  uint32_t* vmask = reinterpret_cast<uint32_t*>(ml + kWarps * 16 * 2);           // [kWarps][kStages]
+  int64_t* share = reinterpret_cast<int64_t*>(vmask + 96);  // [0] places of a share, [1] b, [2] those before b, [3] all
+  float* whole_ml = reinterpret_cast<float*>(share + 4);                         // [16][2] of a join
+  unsigned* last = reinterpret_cast<unsigned*>(whole_ml + 32);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = lane >> 2, col = lane & 3;
@@ -196,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
 
   if (warp == 1) {  // sequences without tokens
     for (int64_t b = blockIdx.x; b < a.kv.B; b += gridDim.x) {
-      if (span_of(a, b).units != 0) continue;
+      if (span_of<kUnit>(a, b).units != 0) continue;
       for (int64_t i = lane; i < static_cast<int64_t>(a.Hq) * D / 2; i += 32)
         reinterpret_cast<uint32_t*>(a.out + b * a.Hq * D)[i] = 0;
       if (a.lse != nullptr)
@@ -210,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
     int64_t sum = 0;
     int most = 0;
     for (int64_t b = b0; b < b1; ++b) {
-      const int u = span_of(a, b).units;
+      const int u = places(span_of<kUnit>(a, b));
       sum += u;
       most = u > most ? u : most;
     }
@@ -223,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31) * per_seq;
     int64_t c = (total + gridDim.x - 1) / gridDim.x;
-    const int least = most < kMinShare ? most : kMinShare;
+    const int least = most < kMinShare + kItemCost ? most : kMinShare + kItemCost;
     if (c < least) c = least;
     const int64_t start = c * blockIdx.x;
     if (lane == 0) {
@@ -235,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
     if (start < total && start >= (upto - sum) * per_seq && start < upto * per_seq) {
       int64_t before = upto - sum;
       for (int64_t b = b0; b < b1; ++b) {
-        const int u = span_of(a, b).units;
+        const int u = places(span_of<kUnit>(a, b));
         if (start < (before + u) * per_seq) {
           share[1] = b;
           share[2] = before;
@@ -249,18 +303,22 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
   const int64_t c = share[0], total = share[3];
   if (share[1] < 0) return;
   const int64_t start = c * blockIdx.x, stop = start + c < total ? start + c : total;
-  Cursor cur;
+  Cursor<kUnit> cur;
   cur.b = share[1];
-  cur.s = span_of(a, cur.b);
-  int64_t before = share[2] * per_seq;  // units before sequence cur.b
-  cur.hc = static_cast<int>((start - before) / cur.s.units);
-  cur.unit = static_cast<int>((start - before) % cur.s.units);
+  cur.s = span_of<kUnit>(a, cur.b);
+  {
+    const int64_t rel = start - share[2] * per_seq;
+    cur.hc = static_cast<int>(rel / places(cur.s));
+    const int in = static_cast<int>(rel - static_cast<int64_t>(cur.hc) * places(cur.s));
+    cur.unit = in < kItemCost ? 0 : in - kItemCost;
+    cur.at = start + (in < kItemCost ? kItemCost - in : 0);
+  }
 
   // ---- the loads: a cursor of their own, the page ids one step ahead
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
-  Cursor ld = cur;
-  int64_t to_load = stop - start;
+  Cursor<kUnit> ld = cur;
   const unsigned S = static_cast<unsigned>(a.kv.S);
+  const int64_t to_v = a.kv.Hkv * a.kv.S * C::kRowBytes;
   int ld_slot = 0;
   int32_t ld_page = -1;
   bool ld_in = false;
@@ -272,57 +330,54 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
     ld_page = ld_in ? a.kv.table[ld.b * a.kv.W + j] : -1;
   };
   auto load = [&](int stage) {
-    const int h = ld.hc / a.chunks;
     const bool ok = ld_in && ld_page >= 0 && ld_page < a.kv.P;
     if (ld_in && !ok && a.bad != nullptr && ld.hc == 0 && lane < 16 &&
         (ld_slot == 0 || (ld.unit == 0 && warp == 0 && lane == 0)))
       atomicAdd(a.bad, 1);
-    int64_t off = -1;
-    if (ok) off = ((static_cast<int64_t>(ld_page) * 2 * a.kv.Hkv + h) * a.kv.S + ld_slot) * C::kRowBytes;
+    // a row that is left out reads nothing: its copies have no bytes
+    const int h = ld.hc / a.chunks;
+    uint64_t from = reinterpret_cast<uint64_t>(a.kv.kv);
+    if (ok) from += ((static_cast<int64_t>(ld_page) * 2 * a.kv.Hkv + h) * a.kv.S + ld_slot) * C::kRowBytes;
     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
     if (lane == 0) vmask[warp * C::kStages + stage] = mask;
-    const uint32_t base = ring + stage * C::kStage;
-    const int64_t to_v = a.kv.Hkv * a.kv.S * C::kRowBytes;
-    const uint8_t* kv = static_cast<const uint8_t*>(a.kv.kv);
+    const uint32_t base = ring + stage * C::kStage + (lane / C::kLanes) * C::kPitch + (lane % C::kLanes) * 16;
 #pragma unroll
     for (int i = 0; i < C::kRowsPerLane; ++i) {
       const int r = lane / C::kLanes + i * (32 / C::kLanes);
-      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
-      const uint32_t bytes = o >= 0 ? 16u : 0u;
-      const uint8_t* src = kv + (o >= 0 ? o : 0) + (lane % C::kLanes) * 16;
-      const uint32_t dst = base + r * C::kPitch + (lane % C::kLanes) * 16;
-      const int64_t v = o >= 0 ? to_v : 0;
+      const uint64_t src = __shfl_sync(0xFFFFFFFFu, from, r) + (lane % C::kLanes) * 16;
+      const uint32_t bytes = (mask >> r & 1u) * 16u;
+      const uint32_t dst = base + i * (32 / C::kLanes) * C::kPitch;
 #pragma unroll
       for (int j = 0; j < C::kChunks; ++j) {
-        cp_async16(dst + j * C::kLanes * 16, src + j * C::kLanes * 16, bytes);
-        cp_async16(dst + C::kSide + j * C::kLanes * 16, src + v + j * C::kLanes * 16, bytes);
+        cp_async16(dst + j * C::kLanes * 16, reinterpret_cast<const void*>(src + j * C::kLanes * 16), bytes);
+        cp_async16(dst + C::kSide + j * C::kLanes * 16, reinterpret_cast<const void*>(src + to_v + j * C::kLanes * 16),
+                   bytes);
       }
     }
     ld.next(a, per_seq);
-    --to_load;
-    if (to_load > 0) look_up();
+    if (ld.at < stop) look_up();
   };
-  look_up();
+  if (ld.at < stop) look_up();
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (to_load > 0) load(i);
+    if (ld.at < stop) load(i);
     cp_async_commit();
   }
 
   // ---- the pieces of (sequence, head chunk) items
-  int64_t done = start;
   int stage = 0;
-  while (done < stop) {
+  while (cur.at < stop) {
     const int h = cur.hc / a.chunks, chunk = cur.hc - h * a.chunks;
     const int hq0 = h * a.G + chunk * 16;
     const int rows = a.G - chunk * 16 < 16 ? a.G - chunk * 16 : 16;
-    const int64_t item0 = before + static_cast<int64_t>(cur.hc) * cur.s.units, item1 = item0 + cur.s.units;
-    const int units = static_cast<int>((item1 < stop ? item1 : stop) - done);
+    const int64_t item0 = cur.at - cur.unit, item1 = item0 + cur.s.units;
+    const int units = static_cast<int>((item1 < stop ? item1 : stop) - cur.at);
 
-    // the queries as the MMA's row operand; e4m3: in fp16 behind a power of
-    // two that puts the row's largest at 2^13 (exact but for numbers below
-    // 2^-38 of it)
-    uint32_t qa[kK][kR16 ? 4 : 2];
+    // the queries as the MMA's row operand. For an e4m3 cache they are split
+    // into two e4m3 numbers behind a power of two that puts the row's largest
+    // in [2^7, 2^8): q = q1 + q2 exactly, but for numbers below 2^-9 of the
+    // largest, which are off by at most 2^-17 of it
+    uint32_t qa[C::kQ][4];
     float scale[2] = {a.scale, a.scale};
     {
       const uint16_t* qp = a.q + cur.b * a.q_stride + static_cast<int64_t>(hq0) * D;
@@ -334,37 +389,40 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             const uint32_t* p = reinterpret_cast<const uint32_t*>(qp + r * D + k * 16 + 2 * col);
-            qa[k][half] = in ? p[0] : 0u;                      // columns 2 col, 2 col + 1
-            qa[k][half + (kR16 ? 2 : 1)] = in ? p[4] : 0u;     // and 8 further
+            qa[k][half] = in ? p[0] : 0u;      // columns 2 col, 2 col + 1
+            qa[k][half + 2] = in ? p[4] : 0u;  // and 8 further
+            if constexpr (!kR16) qa[k][1] = qa[k][3] = 0u;
           }
         } else {
-          // columns 4 col .. 4 col + 3 of each 16: the order in which a row of
-          // codes comes out of ldmatrix
+          // 4 columns at 4 col of every 16
+          uint2 w[kK];
           uint32_t top = 0;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
-            const uint2 w = in ? *reinterpret_cast<const uint2*>(qp + r * D + k * 16 + 4 * col) : make_uint2(0u, 0u);
-            qa[k][half] = w.x;
-            qa[k][half + (kR16 ? 2 : 1)] = w.y;
-            const uint32_t m1 = __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu);
-            top = __vmaxu2(top, m1);
+            w[k] = in ? *reinterpret_cast<const uint2*>(qp + r * D + k * 16 + 4 * col) : make_uint2(0u, 0u);
+            top = __vmaxu2(top, __vmaxu2(w[k].x & 0x7FFF7FFFu, w[k].y & 0x7FFF7FFFu));
           }
           top = (top >> 16) > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu;
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          const bool wrong = top >= 0x7F80u;     // an infinite or NaN query: NaN
           int e = static_cast<int>(top >> 7) - 127;  // the largest is in [2^e, 2^(e + 1))
-          if (top == 0 || top >= 0x7F80u) e = 13;
-          e = 13 - e < -100 ? 113 : (13 - e > 100 ? -87 : e);
-          const float up = __int_as_float((13 - e + 127) << 23), down = __int_as_float((e - 13 + 127) << 23);
+          e = top == 0 || wrong ? 7 : (e < -93 ? -93 : (e > 107 ? 107 : e));
+          const float up = __int_as_float((7 - e + 127) << 23), down = __int_as_float((e - 7 + 127) << 23);
           scale[half] = a.scale * a.kv.k_scale[h] * down;
 #pragma unroll
-          for (int k = 0; k < kK; ++k)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t w = qa[k][half + j * (kR16 ? 2 : 1)];
-              const __half2 f = __floats2half2_rn(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
-              qa[k][half + j * (kR16 ? 2 : 1)] = *reinterpret_cast<const uint32_t*>(&f);
+          for (int k = 0; k < kK; ++k) {
+            uint32_t hi, lo;
+            split_e4m3(w[k], up, hi, lo);
+            if (wrong) hi = 0x7F7F7F7Fu;
+            if constexpr (kR16) {  // q1 and q2 in operands of their own
+              qa[k >> 1][half + 2 * (k & 1)] = hi;
+              qa[kK / 2 + (k >> 1)][half + 2 * (k & 1)] = lo;
+            } else {  // q2 in the rows 8 below
+              qa[k >> 1][2 * (k & 1)] = hi;
+              qa[k >> 1][2 * (k & 1) + 1] = lo;
             }
+          }
         }
       }
     }
@@ -380,40 +438,43 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
       cp_async_wait<C::kStages - 2>();
       __syncwarp();
       // the stage read in the step before is free again
-      if (to_load > 0) load(stage == 0 ? C::kStages - 1 : stage - 1);
+      if (ld.at < stop) load(stage == 0 ? C::kStages - 1 : stage - 1);
       cp_async_commit();
       const uint32_t mask = vmask[warp * C::kStages + stage];
       const uint32_t kbase = ring + stage * C::kStage, vbase = kbase + C::kSide;
       if (mask != 0) {
         // scores of 16 tokens: s[j] has tokens 8 j + 2 col, + 1 of rows `row` and row + 8
-        float s[2][4] = {};
+        float s[2][4] = {}, s2[2][4] = {};  // two chains
         if constexpr (!kE4m3) {
           const uint32_t addr = kbase + ((lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             uint32_t b[4];
             ldsm4(addr + k * 32, b);
-            if constexpr (kR16) {
-              mma<false>(s[0], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b[0], b[1]);
-              mma<false>(s[1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b[2], b[3]);
-            } else {
-              mma<false>(s[0], qa[k][0], 0u, qa[k][1], 0u, b[0], b[1]);
-              mma<false>(s[1], qa[k][0], 0u, qa[k][1], 0u, b[2], b[3]);
-            }
+            mma<false>((k & 1) ? s2[0] : s[0], qa[k], b[0], b[1]);
+            mma<false>((k & 1) ? s2[1] : s[1], qa[k], b[2], b[3]);
           }
         } else {
           const uint32_t addr = kbase + (lane & 15) * C::kPitch + (lane >> 4) * 16;
 #pragma unroll
-          for (int k2 = 0; k2 < kK / 2; ++k2) {
-            uint32_t b[4];  // 16 columns of tokens 0-7, 8-15, then the next 16 columns
-            ldsm4(addr + k2 * 32, b);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int k = 2 * k2 + (j >> 1);
-              const uint32_t b0 = widen(b[j], false), b1 = widen(b[j], true);
-              if constexpr (kR16) mma<true>(s[j & 1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
-              else mma<true>(s[j & 1], qa[k][0], 0u, qa[k][1], 0u, b0, b1);
+          for (int k = 0; k < kK / 2; ++k) {
+            uint32_t b[4];  // 16 codes of tokens 0-7, 8-15, then the next 16
+            ldsm4(addr + k * 32, b);
+            mma_e4m3((k & 1) ? s2[0] : s[0], qa[k], b[0], b[2]);
+            mma_e4m3((k & 1) ? s2[1] : s[1], qa[k], b[1], b[3]);
+            if constexpr (kR16) {
+              mma_e4m3((k & 1) ? s[0] : s2[0], qa[kK / 2 + k], b[0], b[2]);
+              mma_e4m3((k & 1) ? s[1] : s2[1], qa[kK / 2 + k], b[1], b[3]);
             }
+          }
+          if constexpr (!kR16) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                s[j][i] += s[j][i + 2];
+                s2[j][i] += s2[j][i + 2];
+              }
           }
         }
         float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
@@ -421,8 +482,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < (kR16 ? 4 : 2); ++i) {
-            s[j][i] *= scale[i >> 1];
-            if (((mask >> (8 * j + 2 * col + (i & 1))) & 1u) == 0) s[j][i] = -CUDART_INF_F;
+            s[j][i] = (s[j][i] + s2[j][i]) * scale[i >> 1];
+            if (mask != 0xFFFFu && ((mask >> (8 * j + 2 * col + (i & 1))) & 1u) == 0) s[j][i] = -CUDART_INF_F;
             top[i >> 1] = fmaxf(top[i >> 1], s[j][i]);
           }
         bool raised = false;
@@ -461,10 +522,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
         const uint32_t addr = vbase + (lane & 15) * C::kPitch + (lane >> 4) * 16;
         auto accumulate = [&](int n, uint32_t b0, uint32_t b1) {
           if constexpr (kR16) {
-            mma<kE4m3>(acc[n], hi[0][0], hi[0][1], hi[1][0], hi[1][1], b0, b1);
-            mma<kE4m3>(acc[n], lo[0][0], lo[0][1], lo[1][0], lo[1][1], b0, b1);
+            mma<kE4m3>(acc[n], {hi[0][0], hi[0][1], hi[1][0], hi[1][1]}, b0, b1);
+            mma<kE4m3>(acc[n], {lo[0][0], lo[0][1], lo[1][0], lo[1][1]}, b0, b1);
           } else {
-            mma<kE4m3>(acc[n], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b0, b1);
+            mma<kE4m3>(acc[n], {hi[0][0], lo[0][0], hi[1][0], lo[1][0]}, b0, b1);
           }
         };
         if constexpr (!kE4m3) {
@@ -493,11 +554,14 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
         }
       }
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
-      cur.unit++;
     }
-    done += units;
+    // to the piece's last unit; next() below leaves the item or ends the share
+    cur.unit += units - 1;
+    cur.at += units - 1;
 
-    // ---- the four warps' parts, in their order
+    // ---- the warps' parts, in their order: each puts its sums where the stage
+    // of the step just done lies (the next load into it comes after the
+    // barriers), then every thread adds up some columns of all warps
     if constexpr (!kR16) {
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
@@ -514,139 +578,121 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Args a) {
         ml[(warp * 16 + row + 8 * i) * 2 + 1] = l[i];
       }
     }
-    __syncthreads();
-    float mm[2], ll[2];
-#pragma unroll
-    for (int i = 0; i < (kR16 ? 2 : 1); ++i) {
-      const float* p = ml + (row + 8 * i) * 2;
-      mm[i] = p[0];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) mm[i] = fmaxf(mm[i], p[w * 32]);
-      const float base = mm[i] == -CUDART_INF_F ? 0.0f : mm[i];
-      ll[i] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) ll[i] += p[w * 32 + 1] * exp2_fast(p[w * 32] - base);
-      const float f = exp2_fast(m[i] - base);
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        acc[n][2 * i] *= f;
-        acc[n][2 * i + 1] *= f;
-      }
-    }
-    auto exchange = [&](int buf, bool store) {
-#pragma unroll
-      for (int i = 0; i < (kR16 ? 2 : 1); ++i)
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          float2* p = reinterpret_cast<float2*>(obuf + buf * (C::kOBuf / 4) + (row + 8 * i) * C::kOPitch + 8 * n + 2 * col);
-          if (store) {
-            *p = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
-          } else {
-            const float2 v = *p;
-            acc[n][2 * i] += v.x;
-            acc[n][2 * i + 1] += v.y;
-          }
-        }
-    };
-    if (warp >= 2) exchange(warp - 2, true);
-    __syncthreads();
-    if (warp < 2) exchange(warp, false);
-    if (warp == 1) exchange(1, true);
-    __syncthreads();
     const bool whole = item0 >= start && item1 <= stop;
-    // column of acc[n][2 i + e]: e4m3 tiles hold the even or the odd columns
-    auto column = [&](int n, int e) { return kE4m3 ? (n >> 1) * 16 + 2 * (2 * col + e) + (n & 1) : 8 * n + 2 * col + e; };
     const float vs = kE4m3 ? a.kv.v_scale[h] : 1.0f;
-    if (warp == 0) {
-      exchange(1, false);
-      if (whole) {
+    uint8_t* outs = smem + (stage == 0 ? C::kStages - 1 : stage - 1) * C::kStage;
+    // a part of several: rows of D sums, then (m, l) of each row; slot 1 for
+    // the item's first part, 0 for a continued one
+    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (item0 >= start)) * C::kRows * (D + 2);
+    __syncwarp();  // all lanes have read the stage
 #pragma unroll
-        for (int i = 0; i < (kR16 ? 2 : 1); ++i) {
-          const int r = row + 8 * i;
-          if (r >= rows) continue;
-          const float f = ll[i] == 0.0f ? 0.0f : vs / ll[i];
-          uint16_t* o = a.out + (cur.b * a.Hq + hq0 + r) * D;
-          if constexpr (!kE4m3) {
+    for (int r0 = 0; r0 < C::kRows; r0 += C::kOut) {
+      float* mine = reinterpret_cast<float*>(outs + warp * C::kStages * C::kStage);
+      if (r0 > 0) __syncthreads();
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(acc[n][2 * i] * f, acc[n][2 * i + 1] * f);
-              *reinterpret_cast<__nv_bfloat162*>(o + 8 * n + 2 * col) = v;
-            }
-          } else {
-#pragma unroll
-            for (int n = 0; n < kN; n += 2) {
-              const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[n][2 * i] * f, acc[n + 1][2 * i] * f);
-              const __nv_bfloat162 v1 = __floats2bfloat162_rn(acc[n][2 * i + 1] * f, acc[n + 1][2 * i + 1] * f);
-              *reinterpret_cast<uint2*>(o + column(n, 0)) = make_uint2(*reinterpret_cast<const uint32_t*>(&v0),
-                                                                      *reinterpret_cast<const uint32_t*>(&v1));
-            }
-          }
-          if (a.lse != nullptr && col == 0)
-            a.lse[cur.b * a.Hq + hq0 + r] = ll[i] == 0.0f ? -CUDART_INF_F : (mm[i] + log2f(ll[i])) * 0.6931471805599453f;
-        }
-      } else {
-        // one part of several: rows of D + 2 floats (o, m, l); slot 1 for the
-        // item's first part, 0 for a continued one
-        float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (item0 >= start)) * C::kRows * (D + 2);
-#pragma unroll
-        for (int i = 0; i < (kR16 ? 2 : 1); ++i) {
-          const int r = row + 8 * i;
-          if (r >= rows) continue;
+      for (int i = r0 / 8; i < (r0 + C::kOut) / 8; ++i) {
+        float* p = mine + (row + 8 * i - r0) * C::kOPitch;
+        if constexpr (!kE4m3) {
 #pragma unroll
           for (int n = 0; n < kN; ++n)
+            *reinterpret_cast<float2*>(p + 8 * n + 2 * col) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+        } else {  // tiles n and n + 1 hold the even and the odd columns
 #pragma unroll
-            for (int e = 0; e < 2; ++e) part[r * (D + 2) + column(n, e)] = acc[n][2 * i + e];
-          if (col == 0) {
-            part[r * (D + 2) + D] = mm[i];
-            part[r * (D + 2) + D + 1] = ll[i];
-          }
+          for (int n = 0; n < kN; n += 2)
+            *reinterpret_cast<float4*>(p + 8 * n + 4 * col) =
+                make_float4(acc[n][2 * i], acc[n + 1][2 * i], acc[n][2 * i + 1], acc[n + 1][2 * i + 1]);
         }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) {
-          const int64_t p0 = item0 / c, n_parts = (item1 - 1) / c - p0 + 1;
-          unsigned* count = a.arrived + cur.b * per_seq + cur.hc;
-          const bool is_last = atom_add_acq_rel_gpu(count, 1u) == static_cast<unsigned>(n_parts - 1);
-          if (is_last) *count = 0;  // nobody else will: all parts are here
-          *last = is_last;
+      }
+      __syncthreads();
+      const int here = rows - r0 < C::kOut ? rows - r0 : C::kOut;
+      for (int i = tid; i < here * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), d = 4 * (i - r * (D / 4));
+        const float* p = ml + (r0 + r) * 2;
+        float M = p[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, p[w * 32]);
+        const float base = M == -CUDART_INF_F ? 0.0f : M;
+        float L = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = exp2_fast(p[w * 32] - base);
+          const float4 v = *reinterpret_cast<const float4*>(outs + w * C::kStages * C::kStage + (r * C::kOPitch + d) * 4);
+          L += p[w * 32 + 1] * f;
+          o.x += v.x * f;
+          o.y += v.y * f;
+          o.z += v.z * f;
+          o.w += v.w * f;
+        }
+        if (whole) {
+          put<D>(a, cur.b, hq0 + r0 + r, d, o, M, L, vs);
+        } else {
+          *reinterpret_cast<float4*>(part + (r0 + r) * D + d) = o;
+          if (d == 0) *reinterpret_cast<float2*>(part + C::kRows * D + (r0 + r) * 2) = make_float2(M, L);
         }
       }
     }
+    __syncthreads();
     if (!whole) {
+      const int64_t p0 = item0 / c;
+      const int n_parts = static_cast<int>((item1 - 1) / c - p0) + 1;
+      if (tid == 0) {
+        unsigned* count = a.arrived + cur.b * per_seq + cur.hc;
+        __threadfence();
+        const bool is_last = atom_add_acq_rel_gpu(count, 1u) == static_cast<unsigned>(n_parts - 1);
+        if (is_last) *count = 0;  // nobody else will: all parts are here
+        *last = is_last;
+      }
       __syncthreads();
       if (*last) {
         __threadfence();
-        const int64_t p0 = item0 / c, p1 = (item1 - 1) / c;
-        for (int i = tid; i < rows * (D / 2); i += kThreads) {
-          const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
+        const auto at = [&](int p) { return a.parts + ((p0 + p) * 2 + (p == 0)) * C::kRows * (D + 2); };
+        // (m, l) of the whole: a warp per row, parts over the lanes
+        for (int r = warp; r < rows; r += kWarps) {
           float M = -CUDART_INF_F, L = 0.0f;
-          float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-          for (int64_t p = p0; p <= p1; ++p) {
-            const float* part = a.parts + (p * 2 + (p == p0)) * C::kRows * (D + 2) + r * (D + 2);
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(part + d));
-            const float2 s = __ldcg(reinterpret_cast<const float2*>(part + D));
-            const float M2 = fmaxf(M, s.x), base = M2 == -CUDART_INF_F ? 0.0f : M2;
-            const float f = exp2_fast(M - base), g = exp2_fast(s.x - base);
-            M = M2;
-            L = L * f + s.y * g;
-            o.x = o.x * f + v.x * g;
-            o.y = o.y * f + v.y * g;
+          for (int p = lane; p < n_parts; p += 32) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(at(p) + C::kRows * D + r * 2));
+            join(M, L, v.x, v.y);
           }
-          const float f = L == 0.0f ? 0.0f : vs / L;
-          *reinterpret_cast<__nv_bfloat162*>(a.out + (cur.b * a.Hq + hq0 + r) * D + d) =
-              __floats2bfloat162_rn(o.x * f, o.y * f);
-          if (a.lse != nullptr && d == 0)
-            a.lse[cur.b * a.Hq + hq0 + r] = L == 0.0f ? -CUDART_INF_F : (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float M2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), L2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
+            join(M, L, M2, L2);
+          }
+          if (lane == 0) {
+            whole_ml[2 * r] = M;
+            whole_ml[2 * r + 1] = L;
+          }
+        }
+        __syncthreads();
+        // 4 columns a thread; the parts over the warp's four groups of 8 lanes
+        for (int i0 = warp * 8; i0 < rows * (D / 4); i0 += kWarps * 8) {
+          const int i = i0 + (lane & 7), r = i / (D / 4), d = 4 * (i - r * (D / 4));  // rows * D / 4 is a multiple of 8
+          const float M = whole_ml[2 * r], base = M == -CUDART_INF_F ? 0.0f : M;
+          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+          for (int p = lane >> 3; p < n_parts; p += 4) {
+            const float* q = at(p);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
+            const float f = exp2_fast(__ldcg(q + C::kRows * D + r * 2) - base);
+            o.x += v.x * f;
+            o.y += v.y * f;
+            o.z += v.z * f;
+            o.w += v.w * f;
+          }
+#pragma unroll
+          for (int x = 8; x < 32; x <<= 1) {
+            o.x += __shfl_xor_sync(0xFFFFFFFFu, o.x, x);
+            o.y += __shfl_xor_sync(0xFFFFFFFFu, o.y, x);
+            o.z += __shfl_xor_sync(0xFFFFFFFFu, o.z, x);
+            o.w += __shfl_xor_sync(0xFFFFFFFFu, o.w, x);
+          }
+          if (lane < 8) put<D>(a, cur.b, hq0 + r, d, o, M, whole_ml[2 * r + 1], vs);
         }
       }
     }
-    // the next item
-    cur.unit--;
-    const int64_t b = cur.b;
-    const int64_t units_b = static_cast<int64_t>(cur.s.units) * per_seq;
     cur.next(a, per_seq);
-    if (cur.b != b) before += units_b;
   }
 }
 
@@ -657,11 +703,11 @@ cudaError_t launch(const Ctx& c, const Args& a) {
   cudaError_t e = raise_smem_limit(lim, attn_kernel<D, kE4m3, kR16>, c.device, C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t cap = a.kv.W * a.kv.S, most = a.window > 0 && a.window < cap ? a.window : cap;
-  const int64_t items = a.kv.B * a.kv.Hkv * a.chunks, units = (most + kUnit - 1) / kUnit;
+  const int64_t items = a.kv.B * a.kv.Hkv * a.chunks, units = (most + C::kUnit - 1) / C::kUnit;
   int64_t grid = static_cast<int64_t>(C::kBlocksPerSm) * c.sm_count;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
   if (items < grid && items * units < grid) grid = items * units;
-  attn_kernel<D, kE4m3, kR16><<<static_cast<unsigned>(grid), kThreads, C::kSmem, c.stream>>>(a);
+  attn_kernel<D, kE4m3, kR16><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, c.stream>>>(a);
   return cudaGetLastError();
 }
 
