@@ -293,12 +293,12 @@ size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
  *              count as W * S.
  *  window      0: all of them; otherwise the last `window` tokens.
  *  out         [B, Hq, D] bf16;  lse [B, Hq] float32 or NULL.
- *  workspace   at least kv_attn_workspace_bytes(); zero-filled before its
- *              first use and then left to this call alone (what it keeps there
- *              between calls is not zero). Not shared by calls that may run
- *              concurrently; zeroed again after a call that failed.
+ *  workspace   at least kv_attn_workspace_bytes(), contents undefined between
+ *              calls; not shared by calls that may run concurrently.
  * The result's bits do not depend on timing. B >= 0; Hq a multiple of Hkv.
- * NaN among the tokens used gives NaN, and so may infinite values of v.
+ * NaN among the numbers used gives NaN, and so may infinite ones of q or v.
+ * With an e4m3 cache a query's numbers are used to at least 2^-17 of the largest
+ * of their head.
  * bad_count: pages left out. Tokens on a page beyond the length are never
  * used, whatever they hold. */
 wq_status kv_attn_decode(const wq_bf16* q, int64_t q_stride, const void* kv, int kv_type,

@@ -467,7 +467,7 @@ def kv_attn_decode(q: torch.Tensor, kv: torch.Tensor, block_table: torch.Tensor,
         _need(bad_count, "bad_count", torch.int32)
     lib = load()
     if ws is None:
-        ws = _cached("kv_attn", lib.kv_attn_workspace_bytes(B, Hq, H, D))
+        ws = scratch(lib.kv_attn_workspace_bytes(B, Hq, H, D))
     _check(lib.kv_attn_decode(_ptr(q), qs, _ptr(kv), kind, _ptr(block_table), _ptr(lens), B, W, P, Hq, H, S, D,
                               _ptr(k_scale), _ptr(v_scale), D ** -0.5 if sm_scale is None else sm_scale, window,
                               _ptr(out), _ptr(lse), _ptr(bad_count), _ptr(ws),

@@ -1,29 +1,31 @@
 // Attention of one new token per sequence over a paged key-value cache.
 //
 // Mathematics: x_t = sm_scale <q, k_t>, out = sum_t e^(x_t) v_t / sum_t e^(x_t),
-// in one pass over the tokens with the running maximum m and sum l of the
-// softmax; two parts (m1, l1, o1), (m2, l2, o2) of one sequence join to
-// m = max, l = sum l_i e^(m_i - m), o = sum o_i e^(m_i - m).
+// in one pass over the tokens with a reference m (a maximum seen so far) and
+// the sum l of the softmax; two parts (m1, l1, o1), (m2, l2, o2) of one sequence
+// join to m = max, l = sum l_i e^(m_i - m), o = sum o_i e^(m_i - m).
 //
 // Each key and value is used by the G = Hq / Hkv query heads of its key head
 // only, G flop per byte of bf16 cache, so the bound is the cache's read from
 // HBM (or, for a few hundred tokens, the chain of latencies: lengths, page
 // ids, keys, weights, values). Everything follows from that:
-//  - the work of all sequences and key heads is one line of units of 64
-//    tokens, cut into equal shares, one per block, two blocks per SM (one where
-//    the stages need the shared memory); a share may begin and end inside a
-//    sequence. The pieces of a cut (sequence, head) are joined by the block
-//    that finishes last, in their order, so the bits do not depend on timing;
-//  - a warp takes 16 of a unit's 64 tokens through its own ring of stages
-//    filled with cp.async (rows found through the page table one step ahead,
-//    rows outside the sequence zero-filled and never read), so warps wait for
+//  - the work of all sequences and key heads is one line of units, cut into
+//    equal shares, one per block, as many blocks as fit the GPU at once; a share
+//    may begin and end inside a sequence. A second kernel joins the pieces of
+//    a cut (sequence, head) in their order, so the bits do not depend on timing;
+//  - a warp takes 16 of a unit's tokens through its own ring of stages filled
+//    with cp.async (rows found through the page table one step ahead, rows
+//    outside the sequence zero-filled and never read), so warps wait for
 //    nothing but their own loads until a (sequence, head) ends;
-//  - the products run on warp-level MMAs (m16n8k16): the 16 rows are the heads
-//    of the group, and with G <= 8 the second 8 rows carry the low part of the
-//    weights: p = hi + lo in two 16-bit numbers keeps the weights to 2^-17
-//    (2^-22 for e4m3, whose values are exact in fp16) at no further cost;
-//  - e4m3 caches are widened in registers; their scales are factors of the
-//    scores and of the output.
+//  - the products run on warp-level MMAs with the tokens (scores) and the
+//    columns (output) as the 16 rows and 8 query heads as the columns: no row
+//    is padding, and a thread keeps D / 4 sums for 8 heads. The weights go into
+//    the second product as hi + lo, two 16-bit numbers, which keeps them to
+//    2^-17 (2^-22 for e4m3, whose values are exact in fp16);
+//  - e4m3 keys are multiplied as they are, by queries split into two e4m3
+//    numbers; e4m3 values are widened to fp16 in registers. The caches' scales
+//    are factors of the scores and of the output.
+#include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
 
@@ -34,45 +36,56 @@
 namespace wq {
 namespace {
 
-constexpr int kStep = 16;        // tokens a warp takes at a time
-// A (sequence, head) of at most this many units is not cut: a join costs
-// about as much as a few units in a row.
-constexpr int kMinShare = 2;
+constexpr int kStep = 16;  // tokens a warp takes at a time
 // What beginning and ending an item costs, in units: every item takes so many
 // places more in the line, so that shares with many short items take no longer.
 constexpr int kItemCost = 1;
-constexpr int kMaxBlocks = 512;  // shares (the partial results' space)
+// Shares of kLeast units are not made smaller (a join costs about as much);
+// where no sequence can have more, every item is a share and nothing is joined.
+constexpr int kLeast = 4;
+// The weights are relative to a reference that is raised when a score passes it
+// by more than this (in powers of two), so that most steps need no maximum.
+constexpr float kSlack = 8.0f;
+
+// Blocks that share an SM: as many as the registers allow (a thread keeps D / 4
+// sums and D / 8 registers of queries for 8 heads, twice that for 16) and the
+// stages leave room for.
+constexpr int blocks_per_sm(int64_t d, bool e4m3, bool r16) {
+  if (r16) return d <= 64 ? 4 : (d <= 128 ? 3 : 2);
+  return d <= 96 || (e4m3 && d <= 128) ? 4 : (d == 128 || e4m3 ? 3 : 2);
+}
+// Shares that the space for partial results is for (a GB300 has 152 SMs).
+constexpr int max_shares(int64_t d, bool e4m3, bool r16) { return 160 * blocks_per_sm(d, e4m3, r16); }
 
 // A head chunk is at most 16 query heads of one key head (kR16), or 8.
 template <int D, bool kE4m3, bool kR16>
 struct Cfg {
   static constexpr int kRows = kR16 ? 16 : 8;
+  static constexpr int kTiles = kRows / 8;       // MMA columns of 8 heads
   static constexpr int kRowBytes = D * (kE4m3 ? 1 : 2);
   static constexpr int kPitch = kRowBytes + 16;  // an odd number of 16-byte words: ldmatrix without conflicts
   static constexpr int kSide = kStep * kPitch;   // a step's keys (or values)
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kMisc = 3072;
-  // Warps of a block and blocks of an SM: as many warps as the registers (a
-  // warp keeps D / 2 or more running sums a thread) and stages allow.
-  static constexpr int kBlocksPerSm = D == 64 ? 2 : 1;
-  static constexpr int kRoom = (kBlocksPerSm == 2 ? 113 : 227) * 1024 - kMisc;
-  static constexpr int kWarps = D <= 128 && D > 64 && kE4m3 ? 12 : (16 * kStage <= kRoom ? 8 : 4);
+  static constexpr int kMisc = 1024;
+  // Several blocks share an SM, so that one streams while another begins or
+  // ends a share.
+  static constexpr int kBlocksPerSm = blocks_per_sm(D, kE4m3, kR16);
+  static constexpr int kRoom = 226 * 1024 / kBlocksPerSm - kMisc;
+  static constexpr int kWarps = 8 * kStage <= kRoom ? 4 : 3;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kUnit = kStep * kWarps;  // tokens a block takes at a time
   static constexpr int kFit = kRoom / (kWarps * kStage);
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kSmem = kMisc + kWarps * kStages * kStage;
-  // A warp's sums on their way to the block's: kOut rows in the stage that was
-  // read last. The pitch keeps 8 rows of a store apart.
-  static constexpr int kOPitch = D + (kE4m3 ? 16 : 8);  // floats
+  // A warp's sums on their way to the block's: kOut heads in the stage that was
+  // read last. The pitch keeps the 32 words of a store apart.
+  static constexpr int kOPitch = D + 4;  // floats
   static constexpr int kOut = kE4m3 && kR16 ? 8 : kRows;
   static_assert(kOut * kOPitch * 4 <= kStage, "the sums fit a stage");
   // lanes that load one row (16 bytes each at a time)
   static constexpr int kLanes = kRowBytes % 128 == 0 ? 8 : (kRowBytes % 64 == 0 ? 4 : 2);
   static constexpr int kRowsPerLane = kStep * kLanes / 32;
   static constexpr int kChunks = kRowBytes / (16 * kLanes);
-  // registers of 4 for the queries: 16 columns each, or 32 of e4m3 codes (twice with kR16)
-  static constexpr int kQ = kE4m3 && !kR16 ? D / 32 : D / 16;
   static_assert(kStages >= 2, "at least two stages");
 };
 
@@ -87,9 +100,10 @@ struct Args {
   uint16_t* out;
   float* lse;
   int32_t* bad;
-  float* parts;       // partial results, two per block
-  unsigned* arrived;  // one per (sequence, head chunk), zero at rest
-  uint32_t div_mul;   // t / S = (t * div_mul) >> div_shift for t < 2^31
+  int64_t* plan;     // [0] places of a share, [1 + b] places before sequence b
+  float* parts;      // partial results, two per share
+  bool direct;       // a share per item, nothing cut
+  uint32_t div_mul;  // t / S = (t * div_mul) >> div_shift for t < 2^31
   int div_shift;
 };
 
@@ -113,23 +127,29 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
+// A matrix of 8 x 8 16-bit numbers, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 template <bool kF16>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   if constexpr (kF16)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
   else
-    mma_bf16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+    mma_bf16_16816(c, a[0], a[1], a[2], a[3], b[0], b[1]);
 }
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // Four bf16 numbers times `up` as hi + lo, four e4m3 codes each.
 __device__ __forceinline__ void split_e4m3(uint2 w, float up, uint32_t& hi, uint32_t& lo) {
@@ -236,13 +256,12 @@ template <int D, bool kE4m3, bool kR16>
 __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, kR16>::kBlocksPerSm)
     attn_kernel(const Args a) {
   using C = Cfg<D, kE4m3, kR16>;
-  constexpr int kK = D / 16, kN = D / 8, kWarps = C::kWarps, kThreads = C::kThreads, kUnit = C::kUnit;
+  constexpr int kK = kE4m3 ? D / 32 : D / 16, kT = D / 16, kWarps = C::kWarps, kThreads = C::kThreads;
+  constexpr int kUnit = C::kUnit, kTiles = C::kTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   float* ml = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStage);  // [kWarps][16][2]
-  uint32_t* vmask = reinterpret_cast<uint32_t*>(ml + kWarps * 16 * 2);           // [kWarps][kStages]
-  int64_t* share = reinterpret_cast<int64_t*>(vmask + 96);  // [0] places of a share, [1] b, [2] those before b, [3] all
-  float* whole_ml = reinterpret_cast<float*>(share + 4);                         // [16][2] of a join
-  unsigned* last = reinterpret_cast<unsigned*>(whole_ml + 32);
+  int64_t* share = reinterpret_cast<int64_t*>(ml + kWarps * 16 * 2);  // [0] places of a share, [1] b, [2] those before b, [3] all
+  uint32_t* vmask = reinterpret_cast<uint32_t*>(share + 4);           // [kWarps][kStages]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = lane >> 2, col = lane & 3;
@@ -257,8 +276,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         for (int i = lane; i < a.Hq; i += 32) a.lse[b * a.Hq + i] = -CUDART_INF_F;
     }
   }
-  // this block's share: warp 0 adds up the units, each lane some sequences
-  if (warp == 0) {
+  // this block's share: warp 0 adds up the places, each lane some sequences
+  if (warp == 0 && !a.direct) {
     const int64_t each = (a.kv.B + 31) / 32;
     const int64_t b0 = lane * each, b1 = b0 + each < a.kv.B ? b0 + each : a.kv.B;
     int64_t sum = 0;
@@ -277,8 +296,17 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31) * per_seq;
     int64_t c = (total + gridDim.x - 1) / gridDim.x;
-    const int least = most < kMinShare + kItemCost ? most : kMinShare + kItemCost;
-    if (c < least) c = least;
+    const int least = most < kLeast + kItemCost ? most : kLeast + kItemCost;
+    c = c > least ? c : least;
+    if (blockIdx.x == 0) {  // for the join
+      int64_t before = upto - sum;
+      for (int64_t b = b0; b < b1; ++b) {
+        a.plan[1 + b] = before;
+        before += places(span_of<kUnit>(a, b));
+      }
+      if (lane == 31) a.plan[1 + a.kv.B] = upto;
+      if (lane == 0) a.plan[0] = c;
+    }
     const int64_t start = c * blockIdx.x;
     if (lane == 0) {
       share[0] = c;
@@ -299,45 +327,56 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
       }
     }
   }
-  __syncthreads();
-  const int64_t c = share[0], total = share[3];
-  if (share[1] < 0) return;
-  const int64_t start = c * blockIdx.x, stop = start + c < total ? start + c : total;
+  int64_t start = 0, stop;
   Cursor<kUnit> cur;
-  cur.b = share[1];
-  cur.s = span_of<kUnit>(a, cur.b);
-  {
+  if (a.direct) {
+    cur.b = blockIdx.x / per_seq;
+    cur.hc = static_cast<int>(blockIdx.x - cur.b * per_seq);
+    cur.s = span_of<kUnit>(a, cur.b);
+    cur.unit = 0;
+    cur.at = 0;
+    stop = cur.s.units;
+  } else {
+    __syncthreads();
+    const int64_t c = share[0], total = share[3];
+    if (share[1] < 0) return;
+    start = c * blockIdx.x;
+    stop = start + c < total ? start + c : total;
+    cur.b = share[1];
+    cur.s = span_of<kUnit>(a, cur.b);
     const int64_t rel = start - share[2] * per_seq;
     cur.hc = static_cast<int>(rel / places(cur.s));
     const int in = static_cast<int>(rel - static_cast<int64_t>(cur.hc) * places(cur.s));
     cur.unit = in < kItemCost ? 0 : in - kItemCost;
     cur.at = start + (in < kItemCost ? kItemCost - in : 0);
   }
+  if (cur.at >= stop) return;
 
   // ---- the loads: a cursor of their own, the page ids one step ahead
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
   Cursor<kUnit> ld = cur;
   const unsigned S = static_cast<unsigned>(a.kv.S);
   const int64_t to_v = a.kv.Hkv * a.kv.S * C::kRowBytes;
-  int ld_slot = 0;
-  int32_t ld_page = -1;
-  bool ld_in = false;
-  auto look_up = [&]() {  // lanes 0..15 (and again 16..31): one token each
-    const unsigned t = ld.s.first + static_cast<unsigned>(ld.unit) * kUnit + warp * kStep + (lane & 15);
-    ld_in = t < ld.s.end;
-    const unsigned j = static_cast<unsigned>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
-    ld_slot = static_cast<int>(t - j * S);
-    ld_page = ld_in ? a.kv.table[ld.b * a.kv.W + j] : -1;
+  struct Rows {  // a step's, one token each in lanes 0..15 (and again in 16..31)
+    unsigned place;  // of the row within its page's keys; bit 0: count the page if it is out of range
+    int32_t page;    // -1 also where there is no token
+    bool in;
   };
-  auto load = [&](int stage) {
-    const bool ok = ld_in && ld_page >= 0 && ld_page < a.kv.P;
-    if (ld_in && !ok && a.bad != nullptr && ld.hc == 0 && lane < 16 &&
-        (ld_slot == 0 || (ld.unit == 0 && warp == 0 && lane == 0)))
-      atomicAdd(a.bad, 1);
+  auto look_up = [&](Rows& r) {
+    const unsigned t = ld.s.first + static_cast<unsigned>(ld.unit) * kUnit + warp * kStep + (lane & 15);
+    const unsigned j = static_cast<unsigned>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
+    const unsigned at = t - j * S, h = static_cast<unsigned>(ld.hc) / static_cast<unsigned>(a.chunks);
+    r.in = t < ld.s.end;
+    r.place = (h * S + at) * C::kRowBytes | (ld.hc == 0 && (at == 0 || t == ld.s.first));
+    r.page = r.in ? a.kv.table[ld.b * a.kv.W + j] : -1;
+    ld.next(a, per_seq);
+  };
+  auto load = [&](const Rows& x, int stage) {
+    const bool ok = x.page >= 0 && x.page < a.kv.P;
+    if (!ok && x.in && (x.place & 1u) && a.bad != nullptr && lane < kStep) atomicAdd(a.bad, 1);
     // a row that is left out reads nothing: its copies have no bytes
-    const int h = ld.hc / a.chunks;
     uint64_t from = reinterpret_cast<uint64_t>(a.kv.kv);
-    if (ok) from += ((static_cast<int64_t>(ld_page) * 2 * a.kv.Hkv + h) * a.kv.S + ld_slot) * C::kRowBytes;
+    if (ok) from += x.page * (2 * to_v) + (x.place & ~1u);
     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
     if (lane == 0) vmask[warp * C::kStages + stage] = mask;
     const uint32_t base = ring + stage * C::kStage + (lane / C::kLanes) * C::kPitch + (lane % C::kLanes) * 16;
@@ -354,14 +393,24 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
                    bytes);
       }
     }
-    ld.next(a, per_seq);
-    if (ld.at < stop) look_up();
   };
-  if (ld.at < stop) look_up();
+  Rows ahead{};  // the step to load next
+  bool have;     // whether there is one
+  {
+    Rows x[C::kStages - 1];  // the first steps' page ids all at once
+    bool got[C::kStages - 1];
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) {
-    if (ld.at < stop) load(i);
-    cp_async_commit();
+    for (int i = 0; i < C::kStages - 1; ++i) {
+      got[i] = ld.at < stop;
+      if (got[i]) look_up(x[i]);
+    }
+    have = ld.at < stop;
+    if (have) look_up(ahead);
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) {
+      if (got[i]) load(x[i], i);
+      cp_async_commit();
+    }
   }
 
   // ---- the pieces of (sequence, head chunk) items
@@ -373,211 +422,189 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     const int64_t item0 = cur.at - cur.unit, item1 = item0 + cur.s.units;
     const int units = static_cast<int>((item1 < stop ? item1 : stop) - cur.at);
 
-    // the queries as the MMA's row operand. For an e4m3 cache they are split
-    // into two e4m3 numbers behind a power of two that puts the row's largest
-    // in [2^7, 2^8): q = q1 + q2 exactly, but for numbers below 2^-9 of the
-    // largest, which are off by at most 2^-17 of it
-    uint32_t qa[C::kQ][4];
-    float scale[2] = {a.scale, a.scale};
-    {
-      const uint16_t* qp = a.q + cur.b * a.q_stride + static_cast<int64_t>(hq0) * D;
+    // the queries as the MMA's column operand, head 8 j + row in this lane.
+    // For an e4m3 cache they are split into two e4m3 numbers behind a power of
+    // two that puts the head's largest in [2^7, 2^8): q = q1 + q2 exactly, but
+    // for numbers below 2^-9 of the largest, which are off by at most 2^-17 of it
+    uint32_t q1[kTiles][kK][2], q2[kTiles][kE4m3 ? kK : 1][2];
+    float scale[kTiles][2];  // of heads 8 j + 2 col, + 1
 #pragma unroll
-      for (int half = 0; half < (kR16 ? 2 : 1); ++half) {
-        const int r = row + 8 * half;
-        const bool in = r < rows;
-        if constexpr (!kE4m3) {
+    for (int j = 0; j < kTiles; ++j) {
+      const int r = 8 * j + row;
+      const uint16_t* qp = a.q + cur.b * a.q_stride + static_cast<int64_t>(hq0 + r) * D;
+      if constexpr (!kE4m3) {
 #pragma unroll
-          for (int k = 0; k < kK; ++k) {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(qp + r * D + k * 16 + 2 * col);
-            qa[k][half] = in ? p[0] : 0u;      // columns 2 col, 2 col + 1
-            qa[k][half + 2] = in ? p[4] : 0u;  // and 8 further
-            if constexpr (!kR16) qa[k][1] = qa[k][3] = 0u;
-          }
-        } else {
-          // 4 columns at 4 col of every 16
-          uint2 w[kK];
-          uint32_t top = 0;
+        for (int k = 0; k < kK; ++k) {
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(qp + k * 16 + 2 * col);
+          q1[j][k][0] = r < rows ? p[0] : 0u;  // columns 2 col, 2 col + 1
+          q1[j][k][1] = r < rows ? p[4] : 0u;  // and 8 further
+        }
+        scale[j][0] = scale[j][1] = a.scale;
+      } else {
+        uint2 w[kT];  // 4 columns at 4 col of every 16
+        uint32_t top = 0;
 #pragma unroll
-          for (int k = 0; k < kK; ++k) {
-            w[k] = in ? *reinterpret_cast<const uint2*>(qp + r * D + k * 16 + 4 * col) : make_uint2(0u, 0u);
-            top = __vmaxu2(top, __vmaxu2(w[k].x & 0x7FFF7FFFu, w[k].y & 0x7FFF7FFFu));
-          }
-          top = (top >> 16) > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu;
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const bool wrong = top >= 0x7F80u;     // an infinite or NaN query: NaN
-          int e = static_cast<int>(top >> 7) - 127;  // the largest is in [2^e, 2^(e + 1))
-          e = top == 0 || wrong ? 7 : (e < -93 ? -93 : (e > 107 ? 107 : e));
-          const float up = __int_as_float((7 - e + 127) << 23), down = __int_as_float((e - 7 + 127) << 23);
-          scale[half] = a.scale * a.kv.k_scale[h] * down;
+        for (int k = 0; k < kT; ++k) {
+          w[k] = r < rows ? *reinterpret_cast<const uint2*>(qp + k * 16 + 4 * col) : make_uint2(0u, 0u);
+          top = __vmaxu2(top, __vmaxu2(w[k].x & 0x7FFF7FFFu, w[k].y & 0x7FFF7FFFu));
+        }
+        top = (top >> 16) > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu;
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const bool wrong = top >= 0x7F80u;         // an infinite or NaN query: NaN
+        int e = static_cast<int>(top >> 7) - 127;  // the largest is in [2^e, 2^(e + 1))
+        e = top == 0 || wrong ? 7 : (e < -93 ? -93 : (e > 107 ? 107 : e));
+        const float up = __int_as_float((7 - e + 127) << 23), down = __int_as_float((e - 7 + 127) << 23);
+        const float mine = a.scale * a.kv.k_scale[h] * down;
+        scale[j][0] = __shfl_sync(0xFFFFFFFFu, mine, 8 * col);
+        scale[j][1] = __shfl_sync(0xFFFFFFFFu, mine, 8 * col + 4);
 #pragma unroll
-          for (int k = 0; k < kK; ++k) {
-            uint32_t hi, lo;
-            split_e4m3(w[k], up, hi, lo);
-            if (wrong) hi = 0x7F7F7F7Fu;
-            if constexpr (kR16) {  // q1 and q2 in operands of their own
-              qa[k >> 1][half + 2 * (k & 1)] = hi;
-              qa[kK / 2 + (k >> 1)][half + 2 * (k & 1)] = lo;
-            } else {  // q2 in the rows 8 below
-              qa[k >> 1][2 * (k & 1)] = hi;
-              qa[k >> 1][2 * (k & 1) + 1] = lo;
-            }
-          }
+        for (int k = 0; k < kT; ++k) {
+          uint32_t hi, lo;
+          split_e4m3(w[k], up, hi, lo);
+          q1[j][k >> 1][k & 1] = wrong ? 0x7F7F7F7Fu : hi;
+          q2[j][k >> 1][k & 1] = lo;
         }
       }
     }
 
-    float acc[kN][4];
+    float acc[kTiles][kT][4];  // columns 16 t + row (and + 8) of heads 8 j + 2 col, + 1 (e4m3: see below)
+    float m[kTiles][2], l[kTiles][2];
 #pragma unroll
-    for (int n = 0; n < kN; ++n)
+    for (int j = 0; j < kTiles; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.0f, 0.0f};
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][t][i] = 0.0f;
+      m[j][0] = m[j][1] = -CUDART_INF_F;
+      l[j][0] = l[j][1] = 0.0f;
+    }
 
     for (int u = 0; u < units; ++u) {
       cp_async_wait<C::kStages - 2>();
       __syncwarp();
       // the stage read in the step before is free again
-      if (ld.at < stop) load(stage == 0 ? C::kStages - 1 : stage - 1);
+      if (have) load(ahead, stage == 0 ? C::kStages - 1 : stage - 1);
       cp_async_commit();
+      have = ld.at < stop;
+      if (have) look_up(ahead);
       const uint32_t mask = vmask[warp * C::kStages + stage];
       const uint32_t kbase = ring + stage * C::kStage, vbase = kbase + C::kSide;
       if (mask != 0) {
-        // scores of 16 tokens: s[j] has tokens 8 j + 2 col, + 1 of rows `row` and row + 8
-        float s[2][4] = {}, s2[2][4] = {};  // two chains
-        if constexpr (!kE4m3) {
-          const uint32_t addr = kbase + ((lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
+        // scores: s[j] has tokens row (and + 8) of heads 8 j + 2 col, + 1
+        float s[kTiles][4] = {}, s2[kTiles][4] = {};  // two chains
+        {
+          const uint32_t addr = kbase + (lane & 15) * C::kPitch + (lane >> 4) * 16;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             uint32_t b[4];
             ldsm4(addr + k * 32, b);
-            mma<false>((k & 1) ? s2[0] : s[0], qa[k], b[0], b[1]);
-            mma<false>((k & 1) ? s2[1] : s[1], qa[k], b[2], b[3]);
-          }
-        } else {
-          const uint32_t addr = kbase + (lane & 15) * C::kPitch + (lane >> 4) * 16;
 #pragma unroll
-          for (int k = 0; k < kK / 2; ++k) {
-            uint32_t b[4];  // 16 codes of tokens 0-7, 8-15, then the next 16
-            ldsm4(addr + k * 32, b);
-            mma_e4m3((k & 1) ? s2[0] : s[0], qa[k], b[0], b[2]);
-            mma_e4m3((k & 1) ? s2[1] : s[1], qa[k], b[1], b[3]);
-            if constexpr (kR16) {
-              mma_e4m3((k & 1) ? s[0] : s2[0], qa[kK / 2 + k], b[0], b[2]);
-              mma_e4m3((k & 1) ? s[1] : s2[1], qa[kK / 2 + k], b[1], b[3]);
+            for (int j = 0; j < kTiles; ++j) {
+              if constexpr (kE4m3) {
+                mma_e4m3(s[j], b, q1[j][k]);
+                mma_e4m3(s2[j], b, q2[j][k]);
+              } else {
+                mma<false>((k & 1) ? s2[j] : s[j], b, q1[j][k]);
+              }
             }
           }
-          if constexpr (!kR16) {
+        }
+        bool above = false;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                s[j][i] += s[j][i + 2];
-                s2[j][i] += s2[j][i + 2];
+          for (int i = 0; i < 4; ++i) {
+            s[j][i] = (s[j][i] + s2[j][i]) * scale[j][i & 1];
+            if (mask != 0xFFFFu && ((mask >> (row + (i >> 1) * 8)) & 1u) == 0) s[j][i] = -CUDART_INF_F;
+            above |= s[j][i] > m[j][i & 1] + kSlack;
+          }
+        if (__any_sync(0xFFFFFFFFu, above)) {
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float top = fmaxf(s[j][i], s[j][i + 2]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+              top = fmaxf(top, m[j][i]);
+              const float shrink = top == m[j][i] ? 1.0f : exp2_fast(m[j][i] - top);
+              m[j][i] = top;
+              l[j][i] *= shrink;
+#pragma unroll
+              for (int t = 0; t < kT; ++t) {
+                acc[j][t][i] *= shrink;
+                acc[j][t][i + 2] *= shrink;
               }
-          }
+            }
         }
-        float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+        uint32_t hi[kTiles][2], lo[kTiles][2];  // tokens 0-7 and 8-15 of head 8 j + row
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kTiles; ++j) {
+          const float b0 = m[j][0] == -CUDART_INF_F ? 0.0f : m[j][0], b1 = m[j][1] == -CUDART_INF_F ? 0.0f : m[j][1];
 #pragma unroll
-          for (int i = 0; i < (kR16 ? 4 : 2); ++i) {
-            s[j][i] = (s[j][i] + s2[j][i]) * scale[i >> 1];
-            if (mask != 0xFFFFu && ((mask >> (8 * j + 2 * col + (i & 1))) & 1u) == 0) s[j][i] = -CUDART_INF_F;
-            top[i >> 1] = fmaxf(top[i >> 1], s[j][i]);
-          }
-        bool raised = false;
-        float base[2], shrink[2];
-#pragma unroll
-        for (int i = 0; i < (kR16 ? 2 : 1); ++i) {
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-          const float m2 = fmaxf(m[i], top[i]);
-          raised |= m2 > m[i];
-          base[i] = m2 == -CUDART_INF_F ? 0.0f : m2;
-          shrink[i] = exp2_fast(m[i] - base[i]);
-          m[i] = m2;
-        }
-        if (__any_sync(0xFFFFFFFFu, raised)) {
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            acc[n][0] *= shrink[0];
-            acc[n][1] *= shrink[0];
-            acc[n][2] *= shrink[kR16 ? 1 : 0];
-            acc[n][3] *= shrink[kR16 ? 1 : 0];
-          }
-#pragma unroll
-          for (int i = 0; i < (kR16 ? 2 : 1); ++i) l[i] *= shrink[i];
-        }
-        uint32_t hi[2][2], lo[2][2];  // [tokens 8 j ..][rows, rows + 8]
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < (kR16 ? 2 : 1); ++i) {
-            const float p0 = exp2_fast(s[j][2 * i] - base[i]), p1 = exp2_fast(s[j][2 * i + 1] - base[i]);
-            l[i] += p0 + p1;
+          for (int i = 0; i < 2; ++i) {
+            const float p0 = exp2_fast(s[j][2 * i] - b0), p1 = exp2_fast(s[j][2 * i + 1] - b1);
+            l[j][0] += p0;
+            l[j][1] += p1;
             split_pair<kE4m3>(p0, p1, hi[j][i], lo[j][i]);
+            hi[j][i] = transpose8(hi[j][i]);
+            lo[j][i] = transpose8(lo[j][i]);
           }
-        // values: b[0], b[1] the tokens' halves of 8 columns, b[2], b[3] of the next 8
-        const uint32_t addr = vbase + (lane & 15) * C::kPitch + (lane >> 4) * 16;
-        auto accumulate = [&](int n, uint32_t b0, uint32_t b1) {
-          if constexpr (kR16) {
-            mma<kE4m3>(acc[n], {hi[0][0], hi[0][1], hi[1][0], hi[1][1]}, b0, b1);
-            mma<kE4m3>(acc[n], {lo[0][0], lo[0][1], lo[1][0], lo[1][1]}, b0, b1);
-          } else {
-            mma<kE4m3>(acc[n], {hi[0][0], lo[0][0], hi[1][0], lo[1][0]}, b0, b1);
+        }
+        // values, their columns as rows: b[0], b[1] 8 columns each of tokens
+        // 0-7, b[2], b[3] of tokens 8-15
+        const uint32_t addr = vbase + ((lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
+        auto accumulate = [&](int t, const uint32_t(&b)[4]) {
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j) {
+            mma<kE4m3>(acc[j][t], b, hi[j]);
+            mma<kE4m3>(acc[j][t], b, lo[j]);
           }
         };
         if constexpr (!kE4m3) {
 #pragma unroll
-          for (int n2 = 0; n2 < kN / 2; ++n2) {
+          for (int t = 0; t < kT; ++t) {
             uint32_t b[4];
-            ldsm4_trans(addr + n2 * 32, b);
-            accumulate(2 * n2, b[0], b[1]);
-            accumulate(2 * n2 + 1, b[2], b[3]);
+            ldsm4_trans(addr + t * 32, b);
+            accumulate(t, b);
           }
         } else {
-          // 16 columns of codes: a register holds columns 2 row, 2 row + 1 of
-          // two tokens; the even columns make one tile, the odd ones another
+          // 16 columns of codes a matrix: a register holds columns 2 row and
+          // 2 row + 1 of two tokens; the even columns of 32 make one tile, the
+          // odd ones the next
 #pragma unroll
-          for (int n4 = 0; n4 < kN / 4; ++n4) {
-            uint32_t b[4];
-            ldsm4_trans(addr + n4 * 32, b);
+          for (int t = 0; t < kT; t += 2) {
+            uint32_t b[4], even[4], odd[4];
+            ldsm4_trans(addr + t * 16, b);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = __byte_perm(b[j], 0u, 0x3120);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              accumulate(4 * n4 + 2 * j, widen(b[2 * j], false), widen(b[2 * j + 1], false));
-              accumulate(4 * n4 + 2 * j + 1, widen(b[2 * j], true), widen(b[2 * j + 1], true));
+            for (int i = 0; i < 4; ++i) {
+              b[i] = __byte_perm(b[i], 0u, 0x3120);
+              even[i] = widen(b[i], false);
+              odd[i] = widen(b[i], true);
             }
+            accumulate(t, even);
+            accumulate(t + 1, odd);
           }
         }
       }
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
-    // to the piece's last unit; next() below leaves the item or ends the share
-    cur.unit += units - 1;
-    cur.at += units - 1;
 
     // ---- the warps' parts, in their order: each puts its sums where the stage
     // of the step just done lies (the next load into it comes after the
     // barriers), then every thread adds up some columns of all warps
-    if constexpr (!kR16) {
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        acc[n][0] += acc[n][2];
-        acc[n][1] += acc[n][3];
-      }
-    }
+    for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-    for (int i = 0; i < (kR16 ? 2 : 1); ++i) {
-      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-      if (col == 0) {
-        ml[(warp * 16 + row + 8 * i) * 2] = m[i];
-        ml[(warp * 16 + row + 8 * i) * 2 + 1] = l[i];
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[j][i] += __shfl_xor_sync(0xFFFFFFFFu, l[j][i], o);
+        if (row == 0) {
+          ml[(warp * 16 + 8 * j + 2 * col + i) * 2] = m[j][i];
+          ml[(warp * 16 + 8 * j + 2 * col + i) * 2 + 1] = l[j][i];
+        }
       }
-    }
     const bool whole = item0 >= start && item1 <= stop;
     const float vs = kE4m3 ? a.kv.v_scale[h] : 1.0f;
     uint8_t* outs = smem + (stage == 0 ? C::kStages - 1 : stage - 1) * C::kStage;
@@ -590,19 +617,14 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
       float* mine = reinterpret_cast<float*>(outs + warp * C::kStages * C::kStage);
       if (r0 > 0) __syncthreads();
 #pragma unroll
-      for (int i = r0 / 8; i < (r0 + C::kOut) / 8; ++i) {
-        float* p = mine + (row + 8 * i - r0) * C::kOPitch;
-        if constexpr (!kE4m3) {
+      for (int j = r0 / 8; j < (r0 + C::kOut) / 8; ++j)
 #pragma unroll
-          for (int n = 0; n < kN; ++n)
-            *reinterpret_cast<float2*>(p + 8 * n + 2 * col) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
-        } else {  // tiles n and n + 1 hold the even and the odd columns
+        for (int t = 0; t < kT; ++t)
 #pragma unroll
-          for (int n = 0; n < kN; n += 2)
-            *reinterpret_cast<float4*>(p + 8 * n + 4 * col) =
-                make_float4(acc[n][2 * i], acc[n + 1][2 * i], acc[n][2 * i + 1], acc[n + 1][2 * i + 1]);
-        }
-      }
+          for (int i = 0; i < 4; ++i) {
+            const int d = kE4m3 ? (t & ~1) * 16 + (i >> 1) * 16 + 2 * row + (t & 1) : t * 16 + (i >> 1) * 8 + row;
+            mine[(8 * j - r0 + 2 * col + (i & 1)) * C::kOPitch + d] = acc[j][t][i];
+          }
       __syncthreads();
       const int here = rows - r0 < C::kOut ? rows - r0 : C::kOut;
       for (int i = tid; i < here * (D / 4); i += kThreads) {
@@ -632,83 +654,122 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         }
       }
     }
-    __syncthreads();
-    if (!whole) {
-      const int64_t p0 = item0 / c;
-      const int n_parts = static_cast<int>((item1 - 1) / c - p0) + 1;
-      if (tid == 0) {
-        unsigned* count = a.arrived + cur.b * per_seq + cur.hc;
-        __threadfence();
-        const bool is_last = atom_add_acq_rel_gpu(count, 1u) == static_cast<unsigned>(n_parts - 1);
-        if (is_last) *count = 0;  // nobody else will: all parts are here
-        *last = is_last;
+    // to the piece's last unit: next() leaves the item or ends the share
+    cur.unit += units - 1;
+    cur.at += units - 1;
+    cur.next(a, per_seq);
+    __syncthreads();  // the stage may be loaded again
+  }
+}
+
+// Joins the parts of an item that several shares hold, in their order: a block
+// per query head. Each thread has 4 columns of every kGroups-th part. Its
+// launch overlaps the end of the kernel above.
+constexpr int kJoinThreads = 128;
+
+template <int D, bool kE4m3, bool kR16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+  constexpr int kRows = kR16 ? 16 : 8, kCols = D / 4, kGroups = kJoinThreads / kCols, kBatch = 8;
+  __shared__ float2 some_ml[kJoinThreads / 32];
+  __shared__ float4 some[kGroups][kCols];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_seq = static_cast<int>(a.kv.Hkv) * a.chunks;
+  const int64_t b = blockIdx.x / a.Hq;
+  const int hq = static_cast<int>(blockIdx.x - b * a.Hq), h = hq / a.G, in = hq - h * a.G, r = in & 15;
+  const int hc = h * a.chunks + (in >> 4);
+  cl::griddep_wait();
+  const int64_t c = __ldcg(a.plan), before = __ldcg(a.plan + 1 + b), len = __ldcg(a.plan + 2 + b) - before;
+  if (len == 0) return;
+  const int64_t item0 = before * per_seq + hc * len + kItemCost, item1 = item0 + len - kItemCost;
+  const int64_t p0 = item0 / c;
+  const int n = static_cast<int>((item1 - 1) / c - p0) + 1;
+  if (n == 1) return;
+  const auto at = [&](int p) {
+    return a.parts + ((p0 + p) * 2 + (p == 0)) * kRows * (D + 2);
+  };
+  float M = -CUDART_INF_F, L = 0.0f;
+  for (int p = tid; p < n; p += kJoinThreads) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(at(p) + kRows * D + r * 2));
+    join(M, L, v.x, v.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float M2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), L2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
+    join(M, L, M2, L2);
+  }
+  if (lane == 0) some_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  M = some_ml[0].x;
+  L = some_ml[0].y;
+#pragma unroll
+  for (int w = 1; w < kJoinThreads / 32; ++w) join(M, L, some_ml[w].x, some_ml[w].y);
+  const float base = M == -CUDART_INF_F ? 0.0f : M;
+  const int g = tid / kCols, d = 4 * (tid - g * kCols);
+  if (g < kGroups) {
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p = g; p < n; p += kBatch * kGroups) {
+      float4 v[kBatch];
+      float m[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const bool there = p + i * kGroups < n;
+        const float* q = at(there ? p + i * kGroups : p);
+        v[i] = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
+        m[i] = there ? __ldcg(q + kRows * D + r * 2) : -CUDART_INF_F;
       }
-      __syncthreads();
-      if (*last) {
-        __threadfence();
-        const auto at = [&](int p) { return a.parts + ((p0 + p) * 2 + (p == 0)) * C::kRows * (D + 2); };
-        // (m, l) of the whole: a warp per row, parts over the lanes
-        for (int r = warp; r < rows; r += kWarps) {
-          float M = -CUDART_INF_F, L = 0.0f;
-#pragma unroll 4
-          for (int p = lane; p < n_parts; p += 32) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(at(p) + C::kRows * D + r * 2));
-            join(M, L, v.x, v.y);
-          }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            const float M2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), L2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
-            join(M, L, M2, L2);
-          }
-          if (lane == 0) {
-            whole_ml[2 * r] = M;
-            whole_ml[2 * r + 1] = L;
-          }
-        }
-        __syncthreads();
-        // 4 columns a thread; the parts over the warp's four groups of 8 lanes
-        for (int i0 = warp * 8; i0 < rows * (D / 4); i0 += kWarps * 8) {
-          const int i = i0 + (lane & 7), r = i / (D / 4), d = 4 * (i - r * (D / 4));  // rows * D / 4 is a multiple of 8
-          const float M = whole_ml[2 * r], base = M == -CUDART_INF_F ? 0.0f : M;
-          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-          for (int p = lane >> 3; p < n_parts; p += 4) {
-            const float* q = at(p);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
-            const float f = exp2_fast(__ldcg(q + C::kRows * D + r * 2) - base);
-            o.x += v.x * f;
-            o.y += v.y * f;
-            o.z += v.z * f;
-            o.w += v.w * f;
-          }
-#pragma unroll
-          for (int x = 8; x < 32; x <<= 1) {
-            o.x += __shfl_xor_sync(0xFFFFFFFFu, o.x, x);
-            o.y += __shfl_xor_sync(0xFFFFFFFFu, o.y, x);
-            o.z += __shfl_xor_sync(0xFFFFFFFFu, o.z, x);
-            o.w += __shfl_xor_sync(0xFFFFFFFFu, o.w, x);
-          }
-          if (lane < 8) put<D>(a, cur.b, hq0 + r, d, o, M, whole_ml[2 * r + 1], vs);
-        }
+      for (int i = 0; i < kBatch; ++i) {
+        if (p + i * kGroups >= n) continue;
+        const float f = exp2_fast(m[i] - base);
+        o.x += v[i].x * f;
+        o.y += v[i].y * f;
+        o.z += v[i].z * f;
+        o.w += v[i].w * f;
       }
     }
-    cur.next(a, per_seq);
+    some[g][d / 4] = o;
+  }
+  __syncthreads();
+  if (tid < kCols) {
+    float4 o = some[0][tid];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+      const float4 v = some[i][tid];
+      o.x += v.x;
+      o.y += v.y;
+      o.z += v.z;
+      o.w += v.w;
+    }
+    put<D>(a, b, hq, 4 * tid, o, M, L, kE4m3 ? a.kv.v_scale[h] : 1.0f);
   }
 }
 
 template <int D, bool kE4m3, bool kR16>
-cudaError_t launch(const Ctx& c, const Args& a) {
+cudaError_t launch(const Ctx& c, Args a) {
   using C = Cfg<D, kE4m3, kR16>;
   static SmemLimit lim;
   cudaError_t e = raise_smem_limit(lim, attn_kernel<D, kE4m3, kR16>, c.device, C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t cap = a.kv.W * a.kv.S, most = a.window > 0 && a.window < cap ? a.window : cap;
   const int64_t items = a.kv.B * a.kv.Hkv * a.chunks, units = (most + C::kUnit - 1) / C::kUnit;
-  int64_t grid = static_cast<int64_t>(C::kBlocksPerSm) * c.sm_count;
-  if (grid > kMaxBlocks) grid = kMaxBlocks;
-  if (items < grid && items * units < grid) grid = items * units;
+  int64_t grid = C::kBlocksPerSm * c.sm_count;
+  if (grid > max_shares(D, kE4m3, kR16)) grid = max_shares(D, kE4m3, kR16);
+  a.direct = units <= kLeast && items <= kMaxDim;
+  if (a.direct) grid = items;
+  else if (items < grid && items * units < grid) grid = items * units;
   attn_kernel<D, kE4m3, kR16><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, c.stream>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.direct) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.kv.B * a.Hq));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, kE4m3, kR16>, static_cast<const Args>(a));
 }
 
 template <int D>
@@ -718,17 +779,15 @@ cudaError_t launch_d(const Ctx& c, const Args& a) {
   return r16 ? launch<D, false, true>(c, a) : launch<D, false, false>(c, a);
 }
 
+// The plan, then partial results: two parts for each share.
+size_t plan_bytes(int64_t B) { return (static_cast<size_t>(B + 2) * 8 + 15) / 16 * 16; }
+
 }  // namespace
 
-// Partial results first, in a space that does not depend on the batch, then
-// the arrival counters: a call of another shape never writes partial results
-// where counters must be zero.
-constexpr size_t kPartsBytes = static_cast<size_t>(kMaxBlocks) * 2 * 16 * (256 + 2) * 4;
-
 size_t kv_attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
-  const int64_t G = Hq / Hkv;
-  (void)D;
-  return kPartsBytes + static_cast<size_t>(B) * Hkv * ((G + 15) / 16) * 4;
+  const bool r16 = Hq / Hkv > 8;
+  const int rows = r16 ? 16 : 8, x = max_shares(D, true, r16), y = max_shares(D, false, r16), shares = x > y ? x : y;
+  return plan_bytes(B) + static_cast<size_t>(shares) * 2 * rows * (D + 2) * 4;
 }
 
 cudaError_t launch_kv_attn(const Ctx& c, const KvCache& kv, const uint16_t* q, int64_t q_stride, const int32_t* lens,
@@ -747,8 +806,8 @@ cudaError_t launch_kv_attn(const Ctx& c, const KvCache& kv, const uint16_t* q, i
   a.out = out;
   a.lse = lse;
   a.bad = bad;
-  a.parts = static_cast<float*>(ws);
-  a.arrived = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kPartsBytes);
+  a.plan = static_cast<int64_t*>(ws);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan_bytes(kv.B));
   int l = 0;
   while ((int64_t{1} << l) < kv.S) ++l;
   a.div_shift = 31 + l;
