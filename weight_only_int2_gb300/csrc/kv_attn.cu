@@ -100,8 +100,8 @@ struct Args {
   uint16_t* out;
   float* lse;
   int32_t* bad;
-  int64_t* plan;     // [0] places of a share, [1 + b] places before sequence b
   float* parts;      // partial results, two per share
+  int shares;        // at most
   bool direct;       // a share per item, nothing cut
   uint32_t div_mul;  // t / S = (t * div_mul) >> div_shift for t < 2^31
   int div_shift;
@@ -193,6 +193,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// n / d of numbers that are rarely large (a 64-bit division takes a while).
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if ((n >> 32) == 0 && (d >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+  return n / d;
+}
+
 // The tokens of a sequence that count, in units.
 struct Span {
   unsigned first, end;  // below 2^31, but a unit may reach past that
@@ -214,31 +220,66 @@ __device__ __forceinline__ Span span_of(const Args& a, int64_t b) {
 // Places of an item in the line: its cost, then its units.
 __device__ __forceinline__ int places(const Span& s) { return s.units == 0 ? 0 : s.units + kItemCost; }
 
-// Unit `unit` of head chunk `hc` of sequence b, at place `at` of the line.
+// Unit `unit` of head chunk `hc` of sequence b, with `left` places of the share
+// from there on (a share of 2^31 places would take years).
 template <int kUnit>
 struct Cursor {
-  int64_t b, at;
-  int hc, unit;
+  int64_t b;
+  int hc, unit, left;
   Span s;
-  __device__ void next(const Args& a, int per_seq) {
-    ++at;
-    if (++unit < s.units) return;
-    at += kItemCost;
+  // To the next unit; true where that is another item's.
+  __device__ bool next(const Args& a, int per_seq) {
+    --left;
+    if (++unit < s.units) return false;
+    left -= kItemCost;
     unit = 0;
-    if (++hc < per_seq) return;
+    if (++hc < per_seq) return true;
     hc = 0;
     do {
-      if (++b >= a.kv.B) return;
+      if (++b >= a.kv.B) {
+        left = 0;
+        return true;
+      }
       s = span_of<kUnit>(a, b);
     } while (s.units == 0);
+    return true;
   }
 };
 
-// (m, l) of two parts of a softmax together, into the first.
-__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
-  const float top = fmaxf(m, m2), base = top == -CUDART_INF_F ? 0.0f : top;
-  l = l * exp2_fast(m - base) + l2 * exp2_fast(m2 - base);
-  m = top;
+// The line of all items, found by a warp: each lane adds up the places of
+// sequences b0 .. b1 - 1, which lie at before .. upto - 1 (times the items of a
+// sequence); `share` places make a share.
+struct Line {
+  int64_t total, share, before, upto, b0, b1;
+};
+template <int kUnit>
+__device__ __forceinline__ Line line_of(const Args& a, int per_seq, int shares) {
+  const int lane = threadIdx.x & 31;
+  const int64_t each = (a.kv.B + 31) / 32;
+  Line x;
+  x.b0 = lane * each;
+  x.b1 = x.b0 + each < a.kv.B ? x.b0 + each : a.kv.B;
+  int64_t sum = 0;
+  int most = 0;
+#pragma unroll 4
+  for (int64_t b = x.b0; b < x.b1; ++b) {
+    const int u = places(span_of<kUnit>(a, b));
+    sum += u;
+    most = u > most ? u : most;
+  }
+  x.upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x.upto, o);
+    if (lane >= o) x.upto += y;
+  }
+  x.before = x.upto - sum;
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  x.total = __shfl_sync(0xFFFFFFFFu, x.upto, 31) * per_seq;
+  x.share = quotient(x.total + shares - 1, shares);
+  const int least = most < kLeast + kItemCost ? most : kLeast + kItemCost;
+  x.share = x.share > least ? x.share : least;
+  return x;
 }
 
 // Four columns of a result.
@@ -267,6 +308,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
   const int row = lane >> 2, col = lane & 3;
   const int per_seq = static_cast<int>(a.kv.Hkv) * a.chunks;
 
+  cl::griddep_launch_dependents();  // the join may start; it waits for this kernel's end
   if (warp == 1) {  // sequences without tokens
     for (int64_t b = blockIdx.x; b < a.kv.B; b += gridDim.x) {
       if (span_of<kUnit>(a, b).units != 0) continue;
@@ -276,47 +318,18 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         for (int i = lane; i < a.Hq; i += 32) a.lse[b * a.Hq + i] = -CUDART_INF_F;
     }
   }
-  // this block's share: warp 0 adds up the places, each lane some sequences
   if (warp == 0 && !a.direct) {
-    const int64_t each = (a.kv.B + 31) / 32;
-    const int64_t b0 = lane * each, b1 = b0 + each < a.kv.B ? b0 + each : a.kv.B;
-    int64_t sum = 0;
-    int most = 0;
-    for (int64_t b = b0; b < b1; ++b) {
-      const int u = places(span_of<kUnit>(a, b));
-      sum += u;
-      most = u > most ? u : most;
-    }
-    int64_t upto = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
-    const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31) * per_seq;
-    int64_t c = (total + gridDim.x - 1) / gridDim.x;
-    const int least = most < kLeast + kItemCost ? most : kLeast + kItemCost;
-    c = c > least ? c : least;
-    if (blockIdx.x == 0) {  // for the join
-      int64_t before = upto - sum;
-      for (int64_t b = b0; b < b1; ++b) {
-        a.plan[1 + b] = before;
-        before += places(span_of<kUnit>(a, b));
-      }
-      if (lane == 31) a.plan[1 + a.kv.B] = upto;
-      if (lane == 0) a.plan[0] = c;
-    }
-    const int64_t start = c * blockIdx.x;
+    const Line line = line_of<kUnit>(a, per_seq, gridDim.x);
+    const int64_t start = line.share * blockIdx.x;
     if (lane == 0) {
-      share[0] = c;
+      share[0] = line.share;
       share[1] = -1;
-      share[3] = total;
+      share[3] = line.total;
     }
     __syncwarp();
-    if (start < total && start >= (upto - sum) * per_seq && start < upto * per_seq) {
-      int64_t before = upto - sum;
-      for (int64_t b = b0; b < b1; ++b) {
+    if (start < line.total && start >= line.before * per_seq && start < line.upto * per_seq) {
+      int64_t before = line.before;
+      for (int64_t b = line.b0; b < line.b1; ++b) {
         const int u = places(span_of<kUnit>(a, b));
         if (start < (before + u) * per_seq) {
           share[1] = b;
@@ -327,15 +340,14 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
       }
     }
   }
-  int64_t start = 0, stop;
+  int64_t start = 0, stop = 0;
   Cursor<kUnit> cur;
   if (a.direct) {
     cur.b = blockIdx.x / per_seq;
     cur.hc = static_cast<int>(blockIdx.x - cur.b * per_seq);
     cur.s = span_of<kUnit>(a, cur.b);
     cur.unit = 0;
-    cur.at = 0;
-    stop = cur.s.units;
+    cur.left = cur.s.units;
   } else {
     __syncthreads();
     const int64_t c = share[0], total = share[3];
@@ -345,54 +357,67 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     cur.b = share[1];
     cur.s = span_of<kUnit>(a, cur.b);
     const int64_t rel = start - share[2] * per_seq;
-    cur.hc = static_cast<int>(rel / places(cur.s));
+    cur.hc = static_cast<int>(quotient(rel, places(cur.s)));
     const int in = static_cast<int>(rel - static_cast<int64_t>(cur.hc) * places(cur.s));
     cur.unit = in < kItemCost ? 0 : in - kItemCost;
-    cur.at = start + (in < kItemCost ? kItemCost - in : 0);
+    cur.left = static_cast<int>(stop - start) - (in < kItemCost ? kItemCost - in : 0);
   }
-  if (cur.at >= stop) return;
+  if (cur.left <= 0) return;
 
   // ---- the loads: a cursor of their own, the page ids one step ahead
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
   Cursor<kUnit> ld = cur;
   const unsigned S = static_cast<unsigned>(a.kv.S);
-  const int64_t to_v = a.kv.Hkv * a.kv.S * C::kRowBytes;
+  const uint32_t to_v = static_cast<uint32_t>(a.kv.Hkv) * S * C::kRowBytes;  // a page has fewer than 2^32 bytes
+  const int32_t P = static_cast<int32_t>(a.kv.P);
   struct Rows {  // a step's, one token each in lanes 0..15 (and again in 16..31)
     unsigned place;  // of the row within its page's keys; bit 0: count the page if it is out of range
     int32_t page;    // -1 also where there is no token
     bool in;
   };
+  const int32_t* ld_table = nullptr;  // the item's
+  unsigned ld_head = 0;
+  auto new_item = [&]() {
+    ld_table = a.kv.table + ld.b * a.kv.W;
+    ld_head = static_cast<unsigned>(ld.hc) / static_cast<unsigned>(a.chunks) * S * C::kRowBytes;
+  };
+  new_item();
   auto look_up = [&](Rows& r) {
     const unsigned t = ld.s.first + static_cast<unsigned>(ld.unit) * kUnit + warp * kStep + (lane & 15);
     const unsigned j = static_cast<unsigned>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
-    const unsigned at = t - j * S, h = static_cast<unsigned>(ld.hc) / static_cast<unsigned>(a.chunks);
+    const unsigned at = t - j * S;
     r.in = t < ld.s.end;
-    r.place = (h * S + at) * C::kRowBytes | (ld.hc == 0 && (at == 0 || t == ld.s.first));
-    r.page = r.in ? a.kv.table[ld.b * a.kv.W + j] : -1;
-    ld.next(a, per_seq);
+    r.place = ld_head + at * C::kRowBytes;
+    if (ld.hc == 0 && (at == 0 || t == ld.s.first)) r.place |= 1u;
+    r.page = r.in ? ld_table[j] : -1;
+    if (ld.next(a, per_seq) && ld.left > 0) new_item();
   };
   auto load = [&](const Rows& x, int stage) {
-    const bool ok = x.page >= 0 && x.page < a.kv.P;
+    const bool ok = static_cast<uint32_t>(x.page) < static_cast<uint32_t>(P);
     if (!ok && x.in && (x.place & 1u) && a.bad != nullptr && lane < kStep) atomicAdd(a.bad, 1);
     // a row that is left out reads nothing: its copies have no bytes
     uint64_t from = reinterpret_cast<uint64_t>(a.kv.kv);
-    if (ok) from += x.page * (2 * to_v) + (x.place & ~1u);
+    if (ok) from += static_cast<uint64_t>(static_cast<uint32_t>(x.page)) * (2 * to_v) + (x.place & ~1u);
     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
     if (lane == 0) vmask[warp * C::kStages + stage] = mask;
     const uint32_t base = ring + stage * C::kStage + (lane / C::kLanes) * C::kPitch + (lane % C::kLanes) * 16;
+    const auto rows_from = [&](auto whole) {
 #pragma unroll
-    for (int i = 0; i < C::kRowsPerLane; ++i) {
-      const int r = lane / C::kLanes + i * (32 / C::kLanes);
-      const uint64_t src = __shfl_sync(0xFFFFFFFFu, from, r) + (lane % C::kLanes) * 16;
-      const uint32_t bytes = (mask >> r & 1u) * 16u;
-      const uint32_t dst = base + i * (32 / C::kLanes) * C::kPitch;
+      for (int i = 0; i < C::kRowsPerLane; ++i) {
+        const int r = lane / C::kLanes + i * (32 / C::kLanes);
+        const uint64_t src = __shfl_sync(0xFFFFFFFFu, from, r) + (lane % C::kLanes) * 16;
+        const uint32_t bytes = whole() ? 16u : (mask >> r & 1u) * 16u;
+        const uint32_t dst = base + i * (32 / C::kLanes) * C::kPitch;
 #pragma unroll
-      for (int j = 0; j < C::kChunks; ++j) {
-        cp_async16(dst + j * C::kLanes * 16, reinterpret_cast<const void*>(src + j * C::kLanes * 16), bytes);
-        cp_async16(dst + C::kSide + j * C::kLanes * 16, reinterpret_cast<const void*>(src + to_v + j * C::kLanes * 16),
-                   bytes);
+        for (int j = 0; j < C::kChunks; ++j) {
+          cp_async16(dst + j * C::kLanes * 16, reinterpret_cast<const void*>(src + j * C::kLanes * 16), bytes);
+          cp_async16(dst + C::kSide + j * C::kLanes * 16,
+                     reinterpret_cast<const void*>(src + to_v + j * C::kLanes * 16), bytes);
+        }
       }
-    }
+    };
+    if (mask == 0xFFFFu) rows_from([] { return true; });
+    else rows_from([] { return false; });
   };
   Rows ahead{};  // the step to load next
   bool have;     // whether there is one
@@ -401,10 +426,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     bool got[C::kStages - 1];
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
-      got[i] = ld.at < stop;
+      got[i] = ld.left > 0;
       if (got[i]) look_up(x[i]);
     }
-    have = ld.at < stop;
+    have = ld.left > 0;
     if (have) look_up(ahead);
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
@@ -415,12 +440,12 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
 
   // ---- the pieces of (sequence, head chunk) items
   int stage = 0;
-  while (cur.at < stop) {
+  while (cur.left > 0) {
     const int h = cur.hc / a.chunks, chunk = cur.hc - h * a.chunks;
     const int hq0 = h * a.G + chunk * 16;
     const int rows = a.G - chunk * 16 < 16 ? a.G - chunk * 16 : 16;
-    const int64_t item0 = cur.at - cur.unit, item1 = item0 + cur.s.units;
-    const int units = static_cast<int>((item1 < stop ? item1 : stop) - cur.at);
+    const int to_end = cur.s.units - cur.unit, units = to_end < cur.left ? to_end : cur.left;
+    const bool begins = cur.unit == 0, whole = begins && units == to_end;  // the item's first part, all of it
 
     // the queries as the MMA's column operand, head 8 j + row in this lane.
     // For an e4m3 cache they are split into two e4m3 numbers behind a power of
@@ -469,14 +494,16 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     }
 
     float acc[kTiles][kT][4];  // columns 16 t + row (and + 8) of heads 8 j + 2 col, + 1 (e4m3: see below)
-    float m[kTiles][2], l[kTiles][2];
+    float m[kTiles][2], l[kTiles][2];  // the reference (0 before the first score) and the sum
+    float limit[kTiles][2];           // the reference is raised for scores above
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
 #pragma unroll
       for (int t = 0; t < kT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][t][i] = 0.0f;
-      m[j][0] = m[j][1] = -CUDART_INF_F;
+      m[j][0] = m[j][1] = 0.0f;
+      limit[j][0] = limit[j][1] = -CUDART_INF_F;
       l[j][0] = l[j][1] = 0.0f;
     }
 
@@ -486,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
       // the stage read in the step before is free again
       if (have) load(ahead, stage == 0 ? C::kStages - 1 : stage - 1);
       cp_async_commit();
-      have = ld.at < stop;
+      have = ld.left > 0;
       if (have) look_up(ahead);
       const uint32_t mask = vmask[warp * C::kStages + stage];
       const uint32_t kbase = ring + stage * C::kStage, vbase = kbase + C::kSide;
@@ -517,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
           for (int i = 0; i < 4; ++i) {
             s[j][i] = (s[j][i] + s2[j][i]) * scale[j][i & 1];
             if (mask != 0xFFFFu && ((mask >> (row + (i >> 1) * 8)) & 1u) == 0) s[j][i] = -CUDART_INF_F;
-            above |= s[j][i] > m[j][i & 1] + kSlack;
+            above |= s[j][i] > limit[j][i & 1];
           }
         if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
@@ -527,9 +554,11 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
               float top = fmaxf(s[j][i], s[j][i + 2]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-              top = fmaxf(top, m[j][i]);
-              const float shrink = top == m[j][i] ? 1.0f : exp2_fast(m[j][i] - top);
-              m[j][i] = top;
+              const bool raise = top > limit[j][i];
+              float shrink = exp2_fast(limit[j][i] == -CUDART_INF_F ? -CUDART_INF_F : m[j][i] - top);
+              shrink = raise ? shrink : 1.0f;
+              m[j][i] = raise ? top : m[j][i];
+              limit[j][i] = raise ? top + kSlack : limit[j][i];
               l[j][i] *= shrink;
 #pragma unroll
               for (int t = 0; t < kT; ++t) {
@@ -541,10 +570,9 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         uint32_t hi[kTiles][2], lo[kTiles][2];  // tokens 0-7 and 8-15 of head 8 j + row
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
-          const float b0 = m[j][0] == -CUDART_INF_F ? 0.0f : m[j][0], b1 = m[j][1] == -CUDART_INF_F ? 0.0f : m[j][1];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = exp2_fast(s[j][2 * i] - b0), p1 = exp2_fast(s[j][2 * i + 1] - b1);
+            const float p0 = exp2_fast(s[j][2 * i] - m[j][0]), p1 = exp2_fast(s[j][2 * i + 1] - m[j][1]);
             l[j][0] += p0;
             l[j][1] += p1;
             split_pair<kE4m3>(p0, p1, hi[j][i], lo[j][i]);
@@ -601,16 +629,16 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[j][i] += __shfl_xor_sync(0xFFFFFFFFu, l[j][i], o);
         if (row == 0) {
-          ml[(warp * 16 + 8 * j + 2 * col + i) * 2] = m[j][i];
+          // no score yet: nothing, from -inf (but NaN stays)
+          ml[(warp * 16 + 8 * j + 2 * col + i) * 2] = limit[j][i] == -CUDART_INF_F ? -CUDART_INF_F : m[j][i];
           ml[(warp * 16 + 8 * j + 2 * col + i) * 2 + 1] = l[j][i];
         }
       }
-    const bool whole = item0 >= start && item1 <= stop;
     const float vs = kE4m3 ? a.kv.v_scale[h] : 1.0f;
     uint8_t* outs = smem + (stage == 0 ? C::kStages - 1 : stage - 1) * C::kStage;
     // a part of several: rows of D sums, then (m, l) of each row; slot 1 for
     // the item's first part, 0 for a continued one
-    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (item0 >= start)) * C::kRows * (D + 2);
+    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + begins) * C::kRows * (D + 2);
     __syncwarp();  // all lanes have read the stage
 #pragma unroll
     for (int r0 = 0; r0 < C::kRows; r0 += C::kOut) {
@@ -656,71 +684,77 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     }
     // to the piece's last unit: next() leaves the item or ends the share
     cur.unit += units - 1;
-    cur.at += units - 1;
+    cur.left -= units - 1;
     cur.next(a, per_seq);
     __syncthreads();  // the stage may be loaded again
   }
 }
 
 // Joins the parts of an item that several shares hold, in their order: a block
-// per query head. Each thread has 4 columns of every kGroups-th part. Its
-// launch overlaps the end of the kernel above.
+// per query head, each thread with 4 columns of every kGroups-th part. It is
+// launched with the kernel above and finds its parts before that one has ended;
+// what is left after its end is one round of loads.
 constexpr int kJoinThreads = 128;
 
 template <int D, bool kE4m3, bool kR16>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   constexpr int kRows = kR16 ? 16 : 8, kCols = D / 4, kGroups = kJoinThreads / kCols, kBatch = 8;
-  __shared__ float2 some_ml[kJoinThreads / 32];
+  constexpr int kUnit = Cfg<D, kE4m3, kR16>::kUnit;
+  __shared__ int64_t found[3];  // share, places before the sequence, its places
   __shared__ float4 some[kGroups][kCols];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ float2 some_ml[kGroups];
+  const int tid = threadIdx.x;
   const int per_seq = static_cast<int>(a.kv.Hkv) * a.chunks;
   const int64_t b = blockIdx.x / a.Hq;
   const int hq = static_cast<int>(blockIdx.x - b * a.Hq), h = hq / a.G, in = hq - h * a.G, r = in & 15;
   const int hc = h * a.chunks + (in >> 4);
-  cl::griddep_wait();
-  const int64_t c = __ldcg(a.plan), before = __ldcg(a.plan + 1 + b), len = __ldcg(a.plan + 2 + b) - before;
-  if (len == 0) return;
-  const int64_t item0 = before * per_seq + hc * len + kItemCost, item1 = item0 + len - kItemCost;
-  const int64_t p0 = item0 / c;
-  const int n = static_cast<int>((item1 - 1) / c - p0) + 1;
-  if (n == 1) return;
-  const auto at = [&](int p) {
-    return a.parts + ((p0 + p) * 2 + (p == 0)) * kRows * (D + 2);
-  };
-  float M = -CUDART_INF_F, L = 0.0f;
-  for (int p = tid; p < n; p += kJoinThreads) {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(at(p) + kRows * D + r * 2));
-    join(M, L, v.x, v.y);
+  if (tid < 32) {
+    const Line line = line_of<kUnit>(a, per_seq, a.shares);
+    if (b >= line.b0 && b < line.b1) {
+      int64_t before = line.before;
+      for (int64_t i = line.b0; i < b; ++i) before += places(span_of<kUnit>(a, i));
+      found[0] = line.share;
+      found[1] = before;
+      found[2] = places(span_of<kUnit>(a, b));
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float M2 = __shfl_xor_sync(0xFFFFFFFFu, M, o), L2 = __shfl_xor_sync(0xFFFFFFFFu, L, o);
-    join(M, L, M2, L2);
-  }
-  if (lane == 0) some_ml[warp] = make_float2(M, L);
   __syncthreads();
-  M = some_ml[0].x;
-  L = some_ml[0].y;
-#pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) join(M, L, some_ml[w].x, some_ml[w].y);
-  const float base = M == -CUDART_INF_F ? 0.0f : M;
+  const int64_t c = found[0], before = found[1], len = found[2];
+  const int64_t item0 = before * per_seq + hc * len + kItemCost, item1 = item0 + len - kItemCost;
+  const int64_t p0 = len == 0 ? 0 : quotient(item0, c);
+  const int n = len == 0 ? 0 : static_cast<int>(quotient(item1 - 1, c) - p0) + 1;
   const int g = tid / kCols, d = 4 * (tid - g * kCols);
+  cl::griddep_wait();
+  if (n <= 1) return;
+  float M = -CUDART_INF_F, L = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (g < kGroups) {
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int p = g; p < n; p += kBatch * kGroups) {
       float4 v[kBatch];
-      float m[kBatch];
+      float2 ml[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const bool there = p + i * kGroups < n;
-        const float* q = at(there ? p + i * kGroups : p);
+        const int part = p + i * kGroups < n ? p + i * kGroups : p;
+        const float* q = a.parts + ((p0 + part) * 2 + (part == 0)) * kRows * (D + 2);
         v[i] = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
-        m[i] = there ? __ldcg(q + kRows * D + r * 2) : -CUDART_INF_F;
+        ml[i] = __ldcg(reinterpret_cast<const float2*>(q + kRows * D + r * 2));
       }
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (p + i * kGroups < n) top = fmaxf(top, ml[i].x);
+      const float base = top == -CUDART_INF_F ? 0.0f : top, shrink = exp2_fast(M - base);
+      M = top;
+      L *= shrink;
+      o.x *= shrink;
+      o.y *= shrink;
+      o.z *= shrink;
+      o.w *= shrink;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (p + i * kGroups >= n) continue;
-        const float f = exp2_fast(m[i] - base);
+        const float f = exp2_fast(ml[i].x - base);
+        L += ml[i].y * f;
         o.x += v[i].x * f;
         o.y += v[i].y * f;
         o.z += v[i].z * f;
@@ -728,17 +762,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
       }
     }
     some[g][d / 4] = o;
+    if (d == 0) some_ml[g] = make_float2(M, L);
   }
   __syncthreads();
   if (tid < kCols) {
-    float4 o = some[0][tid];
+    M = some_ml[0].x;
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) {
+    for (int i = 1; i < kGroups; ++i) M = fmaxf(M, some_ml[i].x);
+    const float base = M == -CUDART_INF_F ? 0.0f : M;
+    L = 0.0f;
+    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const float f = exp2_fast(some_ml[i].x - base);
       const float4 v = some[i][tid];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
+      L += some_ml[i].y * f;
+      o.x += v.x * f;
+      o.y += v.y * f;
+      o.z += v.z * f;
+      o.w += v.w * f;
     }
     put<D>(a, b, hq, 4 * tid, o, M, L, kE4m3 ? a.kv.v_scale[h] : 1.0f);
   }
@@ -757,6 +799,7 @@ cudaError_t launch(const Ctx& c, Args a) {
   a.direct = units <= kLeast && items <= kMaxDim;
   if (a.direct) grid = items;
   else if (items < grid && items * units < grid) grid = items * units;
+  a.shares = static_cast<int>(grid);
   attn_kernel<D, kE4m3, kR16><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, c.stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.direct) return e;
@@ -779,15 +822,13 @@ cudaError_t launch_d(const Ctx& c, const Args& a) {
   return r16 ? launch<D, false, true>(c, a) : launch<D, false, false>(c, a);
 }
 
-// The plan, then partial results: two parts for each share.
-size_t plan_bytes(int64_t B) { return (static_cast<size_t>(B + 2) * 8 + 15) / 16 * 16; }
-
 }  // namespace
 
 size_t kv_attn_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   const bool r16 = Hq / Hkv > 8;
   const int rows = r16 ? 16 : 8, x = max_shares(D, true, r16), y = max_shares(D, false, r16), shares = x > y ? x : y;
-  return plan_bytes(B) + static_cast<size_t>(shares) * 2 * rows * (D + 2) * 4;
+  (void)B;
+  return static_cast<size_t>(shares) * 2 * rows * (D + 2) * 4;  // two parts for each share
 }
 
 cudaError_t launch_kv_attn(const Ctx& c, const KvCache& kv, const uint16_t* q, int64_t q_stride, const int32_t* lens,
@@ -806,8 +847,7 @@ cudaError_t launch_kv_attn(const Ctx& c, const KvCache& kv, const uint16_t* q, i
   a.out = out;
   a.lse = lse;
   a.bad = bad;
-  a.plan = static_cast<int64_t*>(ws);
-  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan_bytes(kv.B));
+  a.parts = static_cast<float*>(ws);
   int l = 0;
   while ((int64_t{1} << l) < kv.S) ++l;
   a.div_shift = 31 + l;
