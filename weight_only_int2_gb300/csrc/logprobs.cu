@@ -1,5 +1,30 @@
 // Log probabilities of given tokens, entropy and the best alternatives, from
 // logits.
+//
+// Mathematics, with c = log2(e) / temperature and any reference m (a maximum
+// seen so far): u_i = (x_i - m) c (the difference of near logits is exact),
+// l = sum 2^u_i, t = sum 2^u_i u_i. Raising m by d / c turns (l, t) into
+// 2^-d (l, t - d l), so all comes from one pass, and with the final sums
+//   logprob = ln 2 (u_id - log2 l),  entropy = ln 2 (log2 l - t / l).
+// The t of a row that is nearly certain is small beside no other number, so the
+// entropy does not lose digits.
+//
+// Bound: the read of the logits, and right behind it the issue of about eight
+// instructions per logit (at the copy rate an SM gets 12 bf16 logits a clock and
+// issues 128 lanes). So: everything in one pass, in registers; the rank by
+// packed compares; no running maximum but a test per 8 logits (4 for float32)
+// against the reference and against the top_k'th best so far.
+//  - All rows are one line of units of 4 KB (a 16-byte vector per thread), cut
+//    into equal shares, one per block, three blocks per SM; a second kernel joins
+//    rows that were cut, in the order of their parts: bits do not depend on
+//    timing, and one row keeps many SMs busy.
+//  - A block takes four units a round, the next round's loads in flight. The
+//    best top_k are kept as 64-bit keys (logit, then id) in shared memory: the
+//    first round's bound is the top_k'th largest of 32 groups' maxima; later
+//    logits are noted only above the current bound, a few per row in the usual
+//    order. Where more than the buffer holds are noted (ascending rows), the
+//    round is repeated with a bound found by bisection over the keys.
+#include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
 
@@ -8,101 +33,540 @@
 namespace wq {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlocksPerSm = 3;
+constexpr int kRound = 4;      // units (vectors of a thread) in flight
+constexpr int kRowCost = 4;    // what beginning and ending a row costs, in units
+constexpr int kLeast = 2;      // units of a share at least
+constexpr int kNotes = 1024;   // keys noted at a time
+constexpr int kMaxShares = 160 * kBlocksPerSm;
+constexpr float kSlack = 4.0f;  // the reference is raised when a logit passes it by more (in powers of two)
 
-template <bool kBf16>
-__device__ __forceinline__ float logit(const void* row, int64_t i) {
-  if constexpr (kBf16) return bf16_bits_to_float(static_cast<const uint16_t*>(row)[i]);
-  else return static_cast<const float*>(row)[i];
+// A row's sums, or those of a part of it.
+struct Sums {
+  float m, l, t;  // m = -inf: nothing yet
+  int before;     // tokens that come before the given one
+};
+struct Part {
+  Sums s;
+  uint64_t keys[kMaxTopK];  // best first; 0: none
+};
+
+struct Args {
+  LogprobArgs a;
+  float c;         // log2(e) / temperature
+  int units;       // of a row
+  int64_t share;   // places of a share
+  int64_t shares;
+  Part* parts;     // two per share
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
 }
 
-// The order of the tokens as one number: a larger logit is larger (NaN above
-// all, -0.0 as 0.0), then a smaller id.
-__device__ __forceinline__ uint64_t order_key(float x, uint32_t id) {
-  uint32_t u = __float_as_uint(x + 0.0f);
-  u = x != x ? 0xFFFFFFFFu : ((u >> 31) != 0 ? ~u : u | 0x80000000u);
-  return static_cast<uint64_t>(u) << 32 | (0xFFFFFFFFu - id);
+// A logit's place in the order as an unsigned number: NaN above all, -0.0 as 0.0.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return x != x ? 0xFFFFFFFFu : ((u >> 31) != 0 ? ~u : u | 0x80000000u);
 }
-
-template <typename X, typename Op>
-__device__ X block_reduce(X v, Op op) {
-  __shared__ X part[kThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
-  for (int i = 1; i < kThreads / 32; ++i) v = op(v, part[i]);
-  return v;
+__device__ __forceinline__ float value_of(uint32_t order) {
+  if (order == 0xFFFFFFFFu) return CUDART_NAN_F;
+  return __uint_as_float((order >> 31) != 0 ? order & 0x7FFFFFFFu : ~order);
 }
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t id) {
+  return static_cast<uint64_t>(order_of(x)) << 32 | (0xFFFFFFFFu - id);
+}
+__device__ __forceinline__ uint32_t id_of(uint64_t key) { return 0xFFFFFFFFu - static_cast<uint32_t>(key); }
 
-// One block per row: the largest logit, then the sums, then the best top_k by
-// as many passes.
-template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
-  const int64_t t = blockIdx.x;
-  const void* row = static_cast<const uint8_t*>(a.logits) + t * a.ld * (kBf16 ? 2 : 4);
-  auto max_op = [](uint64_t x, uint64_t y) { return x > y ? x : y; };
-  auto add = [](float x, float y) { return x + y; };
-  uint64_t best = 0;
-  for (int64_t i = threadIdx.x; i < a.V; i += kThreads) best = max_op(best, order_key(logit<kBf16>(row, i), i));
-  best = block_reduce(best, max_op);
-  const float m = logit<kBf16>(row, 0xFFFFFFFFu - static_cast<uint32_t>(best));
-  const bool none = m == -CUDART_INF_F;
-
-  const int64_t id = a.ids != nullptr ? a.ids[t] : -1;
-  const bool given = id >= 0 && id < a.V;
-  const float xt = given ? logit<kBf16>(row, id) : 0.0f;
-  const uint64_t key_t = given ? order_key(xt, id) : 0;
-  const float inv = 1.0f / a.temperature;
-  float l = 0.0f, s = 0.0f;
-  int before = 0;
-  for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
-    const float x = logit<kBf16>(row, i);
-    before += order_key(x, i) > key_t;
-    const float d = none ? 0.0f : (x - m) * inv, e = expf(d);
-    l += e;
-    if (!(d == -CUDART_INF_F)) s += e * d;
+__device__ __forceinline__ void raise(Sums& s, float m, float c) {
+  const float d = s.m == -CUDART_INF_F || s.m == m ? 0.0f : (m - s.m) * c;
+  const float f = s.m == -CUDART_INF_F ? 0.0f : exp2_fast(-d);
+  s.t = f * (s.t - d * s.l);
+  s.l = f * s.l;
+  s.m = m;
+}
+// The sums of both.
+__device__ __forceinline__ void join(Sums& s, Sums o, float c) {
+  const float m = fmaxf(s.m, o.m);
+  if (m != -CUDART_INF_F) {
+    raise(s, m, c);
+    raise(o, m, c);
   }
-  l = block_reduce(l, add);
-  s = block_reduce(s, add);
-  before = block_reduce(before, [](int x, int y) { return x + y; });
-  const float log_l = logf(l);
-  if (threadIdx.x == 0) {
+  s.l += o.l;
+  s.t += o.t;
+  s.before += o.before;
+}
+
+// The given token's logit.
+__device__ __forceinline__ float given_logit(const LogprobArgs& a, int64_t row, int32_t id) {
+  if (id < 0 || id >= a.V) return 0.0f;
+  return a.type == WQ_LOGITS_BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.logits)[row * a.ld + id])
+                                  : static_cast<const float*>(a.logits)[row * a.ld + id];
+}
+
+// A row's results from its sums and keys (threads 0 .. top_k - 1 and 0).
+__device__ __forceinline__ void put(const Args& g, int64_t row, const Sums& s, uint64_t key, bool given, float xt) {
+  const LogprobArgs& a = g.a;
+  const bool none = s.m == -CUDART_INF_F && s.l == 0.0f;
+  const float log_l = log2f(s.l), ref = s.m == -CUDART_INF_F ? 0.0f : s.m;
+  const auto lp = [&](float x) {
+    return none ? -CUDART_INF_F : 0.6931471805599453f * ((x - ref) * g.c - log_l);
+  };
+  const int i = threadIdx.x;
+  if (i < a.top_k) {
+    a.top_ids[row * a.top_k + i] = static_cast<int32_t>(id_of(key));
+    a.top_logprobs[row * a.top_k + i] = lp(value_of(static_cast<uint32_t>(key >> 32)));
+  }
+  if (i == 0) {
     if (a.ids != nullptr) {
-      a.logprob[t] = given && !none ? (xt - m) * inv - log_l : -CUDART_INF_F;
-      a.rank[t] = given ? 1 + before : 0;
+      a.logprob[row] = given ? lp(xt) : -CUDART_INF_F;
+      a.rank[row] = given ? 1 + s.before : 0;
       if (!given && a.bad != nullptr) atomicAdd(a.bad, 1);
     }
-    if (a.entropy != nullptr) a.entropy[t] = none ? 0.0f : log_l - s / l;
+    if (a.entropy != nullptr) a.entropy[row] = none ? 0.0f : 0.6931471805599453f * (log_l - s.t / s.l);
   }
-  for (int j = 0; j < a.top_k; ++j) {
-    const uint32_t tok = 0xFFFFFFFFu - static_cast<uint32_t>(best);
-    if (threadIdx.x == 0) {
-      a.top_ids[t * a.top_k + j] = static_cast<int32_t>(tok);
-      a.top_logprobs[t * a.top_k + j] = none ? -CUDART_INF_F : (logit<kBf16>(row, tok) - m) * inv - log_l;
+}
+
+// Four 32-bit words of logits: 8 bf16 or 4 float32.
+template <bool kBf16>
+struct Vec {
+  static constexpr int kN = kBf16 ? 8 : 4;
+  uint32_t w[4];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (kBf16) return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    else return __uint_as_float(w[i]);
+  }
+  // The largest, NaN if there is one.
+  __device__ __forceinline__ float top() const {
+    if constexpr (kBf16) {
+      uint32_t a, b;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[0]), "r"(w[1]));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2]), "r"(w[3]));
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    } else {
+      return max_nan(max_nan(at(0), at(1)), max_nan(at(2), at(3)));
     }
-    const uint64_t last = best;
-    best = 0;
-    for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
-      const uint64_t k = order_key(logit<kBf16>(row, i), i);
-      if (k < last) best = max_op(best, k);
+  }
+};
+
+// The vectors of a row: vector v has logits v kN - head .. v kN - head + kN - 1.
+template <bool kBf16>
+struct Row {
+  const uint8_t* base;  // 16-byte aligned
+  int nvec, head;
+  __device__ void set(const LogprobArgs& a, int64_t row) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.logits) + row * a.ld * (kBf16 ? 2 : 4);
+    base = reinterpret_cast<const uint8_t*>(p & ~uintptr_t{15});
+    head = static_cast<int>(p & 15) / (kBf16 ? 2 : 4);
+    nvec = static_cast<int>((a.V + head + Vec<kBf16>::kN - 1) / Vec<kBf16>::kN);
+  }
+  // Vector v; logits outside the row (of the first and last vector) are not
+  // read and become -inf.
+  __device__ __forceinline__ void load(Vec<kBf16>& x, int v, uint32_t V) const {
+    const uint8_t* p = base + static_cast<int64_t>(v) * 16;
+    if ((v > 0 || head == 0) && static_cast<uint32_t>(v + 1) * Vec<kBf16>::kN - head <= V) {
+      const uint4 y = __ldcs(reinterpret_cast<const uint4*>(p));
+      x.w[0] = y.x, x.w[1] = y.y, x.w[2] = y.z, x.w[3] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < Vec<kBf16>::kN; ++i) {
+        const uint32_t id = static_cast<uint32_t>(v) * Vec<kBf16>::kN + i - head;  // before the row: above V
+        if constexpr (kBf16) {
+          const uint32_t y = id < V ? reinterpret_cast<const uint16_t*>(p)[i] : 0xFF80u;
+          x.w[i >> 1] = (i & 1) ? x.w[i >> 1] | y << 16 : y;
+        } else {
+          x.w[i] = id < V ? reinterpret_cast<const uint32_t*>(p)[i] : 0xFF800000u;
+        }
+      }
     }
-    best = block_reduce(best, max_op);
+  }
+};
+
+struct Shared {
+  uint64_t notes[kNotes];
+  uint64_t best[kMaxTopK];
+  uint32_t groups[32];
+  Sums sums[kWarps];
+  int noted, count;
+};
+
+// Sorts the n <= kNotes noted keys' best top_k to the front (by counting, keys
+// are distinct). All threads; n is the same for all.
+__device__ void keep_best(Shared& sh, int n, int top_k) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t mine = sh.notes[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += sh.notes[j] > mine;
+    if (rank < top_k) sh.best[rank] = mine;
+  }
+  __syncthreads();
+  const int kept = n < top_k ? n : top_k;
+  if (threadIdx.x < kept) sh.notes[threadIdx.x] = sh.best[threadIdx.x];
+  if (threadIdx.x == 0) sh.noted = kept;
+  __syncthreads();
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const Args g) {
+  constexpr int kN = Vec<kBf16>::kN;
+  __shared__ Shared sh;
+  const LogprobArgs& a = g.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int places = g.units + kRowCost;
+  const uint32_t V = static_cast<uint32_t>(a.V);
+  const float slack = kSlack / g.c;
+  cl::griddep_launch_dependents();  // the join may start; it waits for this kernel's end
+
+  // a piece: units [unit, end) of row, `left` places of the share from there on
+  const int64_t total = a.T * places, first = g.share * blockIdx.x;
+  if (first >= total) return;
+  int64_t left = first + g.share < total ? g.share : total - first;
+  int64_t row = first / places;
+  int unit = static_cast<int>(first - row * places) - kRowCost;
+  if (unit < 0) {
+    left += unit;
+    unit = 0;
+  }
+  if (left <= 0) return;
+  Row<kBf16> r;
+  Vec<kBf16> next[kRound];
+  auto load_round = [&](int u, int end) {
+#pragma unroll
+    for (int j = 0; j < kRound; ++j) {
+      const int v = (u + j) * kThreads + tid;
+      if (u + j < end && v < r.nvec) {
+        r.load(next[j], v, V);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[j].w[i] = kBf16 ? 0xFF80FF80u : 0xFF800000u;
+      }
+    }
+  };
+  const auto end_of = [&]() { return g.units - unit < left ? g.units : unit + static_cast<int>(left); };
+  r.set(a, row);
+  load_round(unit, end_of());
+  // the given token and its logit, and the next row's token
+  const auto id_of_row = [&](int64_t t) { return a.ids != nullptr && t < a.T ? a.ids[t] : -1; };
+  int32_t id = id_of_row(row), id2 = id_of_row(row + 1);
+  float xt = given_logit(a, row, id);
+  while (true) {
+    const int end = end_of();
+    const bool begins = unit == 0, whole = begins && end == g.units;
+    const bool given = id >= 0 && id < a.V;
+    const uint64_t key_t = given ? key_of(xt, static_cast<uint32_t>(id)) : ~uint64_t{0};
+    const int v_id = given ? static_cast<int>((static_cast<uint32_t>(id) + r.head) / kN) : -1;
+    // vectors before v_id count logits that are not below xt: not at or below
+    // the number before it (NaN, unordered with all, where that is none)
+    float low = xt;
+    if (xt == -CUDART_INF_F) low = CUDART_NAN_F;
+    else if (kBf16) low = __uint_as_float(xt > 0.0f ? __float_as_uint(xt) - 0x10000u : (xt == 0.0f ? 0x80010000u : __float_as_uint(xt) + 0x10000u));
+    else low = __uint_as_float(xt > 0.0f ? __float_as_uint(xt) - 1u : (xt == 0.0f ? 0x80000001u : __float_as_uint(xt) + 1u));
+    const bool by_key = xt != xt;
+
+    Sums s{-CUDART_INF_F, 0.0f, 0.0f, 0};
+    float limit = -CUDART_INF_F, bound = -CUDART_INF_F;
+    uint64_t bound_key = 0;
+    bool closed = a.top_k == 0, opening = true;
+    int kept = 0;
+    if (tid == 0) sh.noted = 0;
+
+    for (int u = unit; u < end; u += kRound) {
+      Vec<kBf16> x[kRound];
+#pragma unroll
+      for (int j = 0; j < kRound; ++j) x[j] = next[j];
+      if (u + kRound < end) load_round(u + kRound, end);
+
+      float top[kRound];
+#pragma unroll
+      for (int j = 0; j < kRound; ++j) {
+        const int v = (u + j) * kThreads + tid;
+        top[j] = x[j].top();
+        if (top[j] > limit) {
+          raise(s, top[j], g.c);
+          limit = s.m + slack;
+        }
+        const float ref = s.m == -CUDART_INF_F ? 0.0f : s.m;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          // (far below the reference, -inf among them, the weight is 0)
+          const float d = max_nan((x[j].at(i) - ref) * g.c, -200.0f), e = exp2_fast(d);
+          s.l += e;
+          s.t = fmaf(e, d, s.t);
+        }
+        if (given) {
+          if (v == 0 || v >= r.nvec - 1 || v == v_id || by_key) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              const uint32_t n = static_cast<uint32_t>(v) * kN + i - r.head;
+              if (u + j < end && n < V) s.before += key_of(x[j].at(i), n) > key_t;
+            }
+          } else if (u + j < end) {
+            const float than = v < v_id ? low : xt;
+            if constexpr (kBf16) {
+              const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
+              uint32_t n = 0;  // two bf16 counts, at most 4 each
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t y;
+                asm("set.gtu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x[j].w[i]), "r"(than2));
+                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(n) : "r"(y));
+              }
+              s.before += static_cast<int>(__uint_as_float(n << 16) + __uint_as_float(n & 0xFFFF0000u));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s.before += !(x[j].at(i) <= than);
+            }
+          }
+        }
+      }
+      if (closed) continue;
+
+      // ---- the best top_k
+      if (opening) {
+        // the top_k'th largest of 32 groups' maxima: top_k logits are not below it
+        float mine = top[0];
+#pragma unroll
+        for (int j = 1; j < kRound; ++j) mine = max_nan(mine, top[j]);
+        uint32_t o = order_of(mine);
+#pragma unroll
+        for (int i = 1; i < 8; i <<= 1) o = max(o, __shfl_xor_sync(0xFFFFFFFFu, o, i));
+        if ((lane & 7) == 0) sh.groups[tid >> 3] = o;
+        __syncthreads();
+        o = sh.groups[lane];
+        int rank = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t y = __shfl_sync(0xFFFFFFFFu, o, i);
+          rank += y > o || (y == o && i < lane);
+        }
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, rank == a.top_k - 1)) - 1;
+        bound_key = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, o, from)) << 32;
+      }
+      bool over = false;  // more noted than a few times top_k
+      const auto note = [&](uint64_t least) {
+#pragma unroll
+        for (int j = 0; j < kRound; ++j) {
+          const int v = (u + j) * kThreads + tid;
+          if (u + j >= end || v >= r.nvec) continue;
+          if (!opening && top[j] <= bound) continue;
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const uint32_t n = static_cast<uint32_t>(v) * kN + i - r.head;
+            const uint64_t key = key_of(x[j].at(i), n);
+            if (n < V && key >= least) {
+              const int to = atomicAdd(&sh.noted, 1);
+              if (to < kNotes) sh.notes[to] = key;
+              over |= to >= 64 && to >= 2 * a.top_k;
+            }
+          }
+        }
+      };
+      note(bound_key);
+      if (__syncthreads_or(over) || opening) {
+        int n = sh.noted;
+        if (n > kNotes) {
+          // bisection for a bound that at least top_k and at most kNotes keys reach
+          uint64_t least = 0;
+          for (int bit = 63; bit >= 0; --bit) {
+            const uint64_t trial = least | uint64_t{1} << bit;
+            __syncthreads();
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            int c = tid < kept && sh.notes[tid] >= trial;
+#pragma unroll
+            for (int j = 0; j < kRound; ++j) {
+              const int v = (u + j) * kThreads + tid;
+#pragma unroll
+              for (int i = 0; i < kN; ++i) {
+                const uint32_t n2 = static_cast<uint32_t>(v) * kN + i - r.head;
+                c += u + j < end && v < r.nvec && n2 < V && key_of(x[j].at(i), n2) >= trial;
+              }
+            }
+            c = __reduce_add_sync(0xFFFFFFFFu, c);
+            if (lane == 0) atomicAdd(&sh.count, c);
+            __syncthreads();
+            if (sh.count >= a.top_k) least = trial;
+            if (sh.count >= a.top_k && sh.count <= kNotes - kMaxTopK) break;
+          }
+          __syncthreads();
+          if (tid == 0) sh.noted = kept;
+          __syncthreads();
+          opening = true;  // every vector is looked at
+          note(least > bound_key ? least : bound_key);
+          __syncthreads();
+          n = sh.noted;
+        }
+        __syncthreads();
+        keep_best(sh, n, a.top_k);
+        kept = sh.noted;
+        if (kept == a.top_k) {
+          bound_key = sh.notes[a.top_k - 1];
+          bound = value_of(static_cast<uint32_t>(bound_key >> 32));
+          closed = bound != bound;  // NaN: nothing that comes later is better
+        } else {
+          bound_key = 0;  // fewer than top_k logits so far
+        }
+        opening = kept < a.top_k;
+        __syncthreads();
+      }
+    }
+
+    // ---- the end of the piece
+    const int64_t done_row = row;
+    const float done_xt = xt;
+    left -= end - unit;
+    if (end == g.units) {
+      left -= kRowCost;
+      ++row;
+      unit = 0;
+    } else {
+      unit = end;
+    }
+    if (left > 0) {  // the next row
+      r.set(a, row);
+      load_round(unit, end_of());
+      id = id2;
+      xt = given_logit(a, row, id);
+      id2 = id_of_row(row + 1);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const Sums y{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
+                   __shfl_xor_sync(0xFFFFFFFFu, s.t, o), __shfl_xor_sync(0xFFFFFFFFu, s.before, o)};
+      join(s, y, g.c);
+    }
+    if (lane == 0) sh.sums[warp] = s;
+    __syncthreads();
+    if (a.top_k > 0) keep_best(sh, sh.noted, a.top_k);
+    s = sh.sums[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) join(s, sh.sums[w], g.c);
+    const uint64_t key = tid < a.top_k && tid < sh.noted ? sh.notes[tid] : 0;
+    if (whole) {
+      put(g, done_row, s, key, given, done_xt);
+    } else {
+      // slot 1 for the row's first part, 0 for a continued one
+      Part& p = g.parts[static_cast<int64_t>(blockIdx.x) * 2 + begins];
+      if (tid == 0) p.s = s;
+      if (tid < a.top_k) p.keys[tid] = key;
+    }
+    if (left <= 0) return;
+    __syncthreads();
+  }
+}
+
+// Joins the parts of rows that several shares hold, in their order: a block per
+// row. A warp merges the sorted keys of its parts (three a lane), then the first
+// warp those of the warps.
+__global__ void __launch_bounds__(kThreads) join_kernel(const Args g) {
+  constexpr int kLists = 3;
+  static_assert(kLists * kThreads >= kMaxShares + 1, "a list per part");
+  __shared__ uint64_t merged[kWarps][kMaxTopK];
+  __shared__ Sums sums[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t row = blockIdx.x, places = g.units + kRowCost;
+  const int64_t first = row * places + kRowCost, last = first + g.units - 1;
+  const int64_t p0 = first / g.share, n = last / g.share - p0 + 1;
+  const int32_t id = g.a.ids != nullptr && n > 1 ? g.a.ids[row] : -1;
+  cl::griddep_wait();
+  if (n <= 1) return;
+  const auto part = [&](int64_t p) -> const Part& { return g.parts[(p0 + p) * 2 + (p == 0)]; };
+  // the best top_k of the lanes' lists, each sorted
+  const auto merge = [&](const uint64_t* (&list)[kLists], uint64_t* to, int k) {
+    uint64_t head[kLists];
+    int used[kLists];
+#pragma unroll
+    for (int i = 0; i < kLists; ++i) {
+      used[i] = 0;
+      head[i] = list[i] != nullptr ? list[i][0] : 0;
+    }
+    for (int j = 0; j < k; ++j) {
+      uint64_t mine = head[0];
+#pragma unroll
+      for (int i = 1; i < kLists; ++i) mine = head[i] > mine ? head[i] : mine;
+      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32));
+      const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
+      const uint64_t best = static_cast<uint64_t>(hi) << 32 | lo;
+      if (lane == 0) to[j] = best;
+      if (best == 0) continue;
+#pragma unroll
+      for (int i = 0; i < kLists; ++i)
+        if (head[i] == best) head[i] = ++used[i] < k ? list[i][used[i]] : 0;
+    }
+  };
+  const uint64_t* list[kLists];
+  Sums s{-CUDART_INF_F, 0.0f, 0.0f, 0};
+#pragma unroll
+  for (int i = 0; i < kLists; ++i) {
+    const int64_t p = tid + i * kThreads;
+    list[i] = p < n ? part(p).keys : nullptr;
+    if (p < n) join(s, part(p).s, g.c);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Sums y{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
+                 __shfl_xor_sync(0xFFFFFFFFu, s.t, o), __shfl_xor_sync(0xFFFFFFFFu, s.before, o)};
+    join(s, y, g.c);
+  }
+  if (lane == 0) sums[warp] = s;
+  merge(list, merged[warp], g.a.top_k);
+  __syncthreads();
+  s = sums[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) join(s, sums[w], g.c);
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 0; i < kLists; ++i) list[i] = i == 0 && lane < kWarps ? merged[lane] : nullptr;
+    __shared__ uint64_t out[kMaxTopK];
+    merge(list, out, g.a.top_k);
+    __syncwarp();
+    put(g, row, s, lane < g.a.top_k ? out[lane] : 0, id >= 0 && id < g.a.V, given_logit(g.a, row, id));
   }
 }
 
 }  // namespace
 
-size_t logprobs_ws_bytes(int64_t, int64_t, int) { return 0; }
+size_t logprobs_ws_bytes(int64_t, int64_t, int) { return sizeof(Part) * 2 * kMaxShares; }
 
 cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
-  if (a.type == WQ_LOGITS_BF16)
-    logprobs_kernel<true><<<static_cast<unsigned>(a.T), kThreads, 0, c.stream>>>(a);
-  else
-    logprobs_kernel<false><<<static_cast<unsigned>(a.T), kThreads, 0, c.stream>>>(a);
-  return cudaGetLastError();
+  Args g{};
+  g.a = a;
+  g.c = 1.4426950408889634f / a.temperature;
+  const int64_t per = a.type == WQ_LOGITS_BF16 ? 8 : 4;
+  // a row may begin anywhere within its first vector
+  g.units = static_cast<int>(((a.V + 2 * (per - 1)) / per + kThreads - 1) / kThreads);
+  const int64_t total = a.T * (g.units + kRowCost);
+  int64_t blocks = static_cast<int64_t>(kBlocksPerSm) * c.sm_count;
+  if (blocks > kMaxShares) blocks = kMaxShares;
+  g.share = (total + blocks - 1) / blocks;
+  if (g.share < kLeast) g.share = kLeast;
+  g.shares = (total + g.share - 1) / g.share;
+  g.parts = static_cast<Part*>(a.ws);
+  const unsigned grid = static_cast<unsigned>(g.shares);
+  if (a.type == WQ_LOGITS_BF16) logprobs_kernel<true><<<grid, kThreads, 0, c.stream>>>(g);
+  else logprobs_kernel<false><<<grid, kThreads, 0, c.stream>>>(g);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.T));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const Args>(g));
 }
 
 }  // namespace wq
