@@ -9,21 +9,24 @@
 // The t of a row that is nearly certain is small beside no other number, so the
 // entropy does not lose digits.
 //
-// Bound: the read of the logits, and right behind it the issue of about eight
+// Bound: the read of the logits, and right behind it the issue of about seven
 // instructions per logit (at the copy rate an SM gets 12 bf16 logits a clock and
-// issues 128 lanes). So: everything in one pass, in registers; the rank by
-// packed compares; no running maximum but a test per 8 logits (4 for float32)
-// against the reference and against the top_k'th best so far.
+// issues 128 lanes). So: everything in one pass; pairs of float32 operations
+// where there are such; the rank by packed compares; no running maximum but a
+// test per 8 logits (4 for float32) against the reference and against the
+// top_k'th best so far.
 //  - All rows are one line of units of 4 KB (a 16-byte vector per thread), cut
-//    into equal shares, one per block, three blocks per SM; a second kernel joins
-//    rows that were cut, in the order of their parts: bits do not depend on
+//    into equal shares, one per block, several blocks per SM; a second kernel
+//    joins rows that were cut, in the order of their parts: bits do not depend on
 //    timing, and one row keeps many SMs busy.
-//  - A block takes four units a round, the next round's loads in flight. The
-//    best top_k are kept as 64-bit keys (logit, then id) in shared memory: the
+//  - A thread copies its own vectors to shared memory, two rounds of four units
+//    ahead (cp.async), and reads them back itself: no barrier.
+//  - The best top_k are kept as 64-bit keys (logit, then id) in shared memory: the
 //    first round's bound is the top_k'th largest of 32 groups' maxima; later
-//    logits are noted only above the current bound, a few per row in the usual
-//    order. Where more than the buffer holds are noted (ascending rows), the
-//    round is repeated with a bound found by bisection over the keys.
+//    logits are noted only above the bound, which is raised after 1, 2, 4, 8 ..
+//    rounds: a few notes per row in the usual order. Where they do not fit
+//    (ascending rows), the piece's best are found again with a bound for every
+//    round, by bisection over the keys.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
@@ -35,11 +38,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 3;
-constexpr int kRound = 4;      // units (vectors of a thread) in flight
+constexpr int kBlocksPerSm = 4;
+constexpr int kRound = 4;      // units a block takes at a time
+constexpr int kStages = 3;     // rounds in shared memory
 constexpr int kRowCost = 4;    // what beginning and ending a row costs, in units
 constexpr int kLeast = 2;      // units of a share at least
-constexpr int kNotes = 1024;   // keys noted at a time
+constexpr int kNotes = 512;    // keys noted at a time
 constexpr int kMaxShares = 160 * kBlocksPerSm;
 constexpr float kSlack = 4.0f;  // the reference is raised when a logit passes it by more (in powers of two)
 
@@ -136,10 +140,28 @@ __device__ __forceinline__ void put(const Args& g, int64_t row, const Sums& s, u
   }
 }
 
-// Four 32-bit words of logits: 8 bf16 or 4 float32.
+// Pairs of float32 operations.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  return static_cast<uint64_t>(__float_as_uint(y)) << 32 | __float_as_uint(x);
+}
+__device__ __forceinline__ float low_of(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float high_of(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// A 16-byte vector of logits: 8 bf16 or 4 float32.
 template <bool kBf16>
 struct Vec {
   static constexpr int kN = kBf16 ? 8 : 4;
+  static constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
   uint32_t w[4];
   __device__ __forceinline__ float at(int i) const {
     if constexpr (kBf16) return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
@@ -170,29 +192,14 @@ struct Row {
     head = static_cast<int>(p & 15) / (kBf16 ? 2 : 4);
     nvec = static_cast<int>((a.V + head + Vec<kBf16>::kN - 1) / Vec<kBf16>::kN);
   }
-  // Vector v; logits outside the row (of the first and last vector) are not
-  // read and become -inf.
-  __device__ __forceinline__ void load(Vec<kBf16>& x, int v, uint32_t V) const {
-    const uint8_t* p = base + static_cast<int64_t>(v) * 16;
-    if ((v > 0 || head == 0) && static_cast<uint32_t>(v + 1) * Vec<kBf16>::kN - head <= V) {
-      const uint4 y = __ldcs(reinterpret_cast<const uint4*>(p));
-      x.w[0] = y.x, x.w[1] = y.y, x.w[2] = y.z, x.w[3] = y.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < Vec<kBf16>::kN; ++i) {
-        const uint32_t id = static_cast<uint32_t>(v) * Vec<kBf16>::kN + i - head;  // before the row: above V
-        if constexpr (kBf16) {
-          const uint32_t y = id < V ? reinterpret_cast<const uint16_t*>(p)[i] : 0xFF80u;
-          x.w[i >> 1] = (i & 1) ? x.w[i >> 1] | y << 16 : y;
-        } else {
-          x.w[i] = id < V ? reinterpret_cast<const uint32_t*>(p)[i] : 0xFF800000u;
-        }
-      }
-    }
+  // The id of logit i of vector v (before the row: above any V).
+  __device__ __forceinline__ uint32_t id(int v, int i) const {
+    return static_cast<uint32_t>(v) * Vec<kBf16>::kN + i - head;
   }
 };
 
 struct Shared {
+  uint8_t ring[kStages][kRound][kThreads * 16];
   uint64_t notes[kNotes];
   uint64_t best[kMaxTopK];
   uint32_t groups[32];
@@ -203,6 +210,7 @@ struct Shared {
 // Sorts the n <= kNotes noted keys' best top_k to the front (by counting, keys
 // are distinct). All threads; n is the same for all.
 __device__ void keep_best(Shared& sh, int n, int top_k) {
+  n = n < kNotes ? n : kNotes;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t mine = sh.notes[i];
     int rank = 0;
@@ -216,10 +224,97 @@ __device__ void keep_best(Shared& sh, int n, int top_k) {
   __syncthreads();
 }
 
+// Notes every logit of the vector in shared memory whose key is at least
+// `least`.
+template <bool kBf16>
+__device__ __noinline__ void note(Shared& sh, const uint8_t* x, uint32_t id, uint32_t V, uint64_t least) {
+  for (int i = 0; i < Vec<kBf16>::kN; ++i) {
+    float y;
+    if constexpr (kBf16) y = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i]);
+    else y = reinterpret_cast<const float*>(x)[i];
+    const uint64_t key = key_of(y, id + i);
+    if (id + i < V && key >= least) {
+      const int to = atomicAdd(&sh.noted, 1);
+      if (to < kNotes) sh.notes[to] = key;
+    }
+  }
+}
+
+// The best top_k of units [unit, end) of a row, in whatever order they come:
+// sorted in sh.notes, sh.noted of them. Reads the logits again.
+template <bool kBf16>
+__device__ __noinline__ void best_of(Shared& sh, const LogprobArgs& a, int64_t row, int unit, int end) {
+  constexpr int kN = Vec<kBf16>::kN;
+  const int tid = threadIdx.x;
+  const void* x = static_cast<const uint8_t*>(a.logits) + row * a.ld * (kBf16 ? 2 : 4);
+  Row<kBf16> r;
+  r.set(a, row);
+  // logits unit .. end - 1 hold, in steps of what a block reads at once
+  const int64_t first = static_cast<int64_t>(unit) * kThreads * kN - r.head, last = static_cast<int64_t>(end) * kThreads * kN - r.head;
+  const int64_t from = first < 0 ? 0 : first, to = last < a.V ? last : a.V;
+  constexpr int kPer = 8;
+  __syncthreads();
+  if (tid == 0) sh.noted = 0;
+  __syncthreads();
+  for (int64_t i0 = from; i0 < to; i0 += kThreads * kPer) {
+    const int kept = sh.noted;
+    uint64_t key[kPer];
+    const uint64_t bound = kept == a.top_k ? sh.notes[kept - 1] : 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t i = i0 + j * kThreads + tid;
+      float y = 0.0f;
+      if (i < to) {
+        if constexpr (kBf16) y = bf16_bits_to_float(static_cast<const uint16_t*>(x)[i]);
+        else y = static_cast<const float*>(x)[i];
+      }
+      key[j] = i < to ? key_of(y, static_cast<uint32_t>(i)) : 0;
+      if (key[j] <= bound) key[j] = 0;  // none, or not among the best
+    }
+    // all of them if they fit; else a bound that at least top_k of them reach:
+    // the top_k'th largest found bit by bit, or an earlier one that few enough reach
+    uint64_t least = 1;
+    for (int bit = 64; bit >= 0; --bit) {
+      const uint64_t trial = bit == 64 ? 1 : ((bit == 63 ? 0 : least) | uint64_t{1} << bit);
+      __syncthreads();
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) c += key[j] >= trial;
+      c = __reduce_add_sync(0xFFFFFFFFu, c);
+      if ((tid & 31) == 0) atomicAdd(&sh.count, c);
+      __syncthreads();
+      const int n = sh.count;
+      if (bit == 64) {
+        if (n <= kNotes - kMaxTopK) break;
+        continue;
+      }
+      if (bit == 63) least = 0;
+      if (n < a.top_k) continue;
+      least = trial;
+      if (n <= kNotes - kMaxTopK) break;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (key[j] != 0 && key[j] >= least) {
+        const int n = atomicAdd(&sh.noted, 1);
+        if (n < kNotes) sh.notes[n] = key[j];
+      }
+    __syncthreads();
+    const int n = sh.noted;
+    __syncthreads();
+    if (n > kept) keep_best(sh, n, a.top_k);
+  }
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const Args g) {
-  constexpr int kN = Vec<kBf16>::kN;
-  __shared__ Shared sh;
+  constexpr int kN = Vec<kBf16>::kN, kElem = kBf16 ? 2 : 4;
+  extern __shared__ __align__(128) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
   const LogprobArgs& a = g.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int places = g.units + kRowCost;
@@ -239,191 +334,216 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
   }
   if (left <= 0) return;
   Row<kBf16> r;
-  Vec<kBf16> next[kRound];
-  auto load_round = [&](int u, int end) {
+  r.set(a, row);
+
+  // ---- the copies: rounds of the share's pieces, kStages - 1 ahead
+  uint8_t* const mine = sh.ring[0][0] + tid * 16;
+  const uint32_t mine_s = smem_u32(mine);
+  constexpr int kUnitBytes = kThreads * 16, kStageBytes = kRound * kUnitBytes;
+  Row<kBf16> lr = r;
+  int64_t l_row = row, l_left = left;
+  int l_unit = unit;
+  auto copy_round = [&](int stage) {
+    if (l_left > 0) {
+      const int end = g.units - l_unit < l_left ? g.units : l_unit + static_cast<int>(l_left);
+      const int row_end = (lr.head + static_cast<int>(V & 7)) * kElem & 15;  // bytes of the last vector, 0: all
+      const uint8_t* src = lr.base + (static_cast<int64_t>(l_unit) * kThreads + tid) * 16;
 #pragma unroll
-    for (int j = 0; j < kRound; ++j) {
-      const int v = (u + j) * kThreads + tid;
-      if (u + j < end && v < r.nvec) {
-        r.load(next[j], v, V);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) next[j].w[i] = kBf16 ? 0xFF80FF80u : 0xFF800000u;
+      for (int j = 0; j < kRound; ++j) {
+        const int v = (l_unit + j) * kThreads + tid;
+        if (l_unit + j < end && v < lr.nvec) {
+          const int bytes = v == lr.nvec - 1 && row_end != 0 ? row_end : 16;  // not past the row
+          asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(mine_s + stage * kStageBytes +
+                                                                                      j * kUnitBytes),
+                       "l"(src + static_cast<int64_t>(j) * kUnitBytes), "r"(bytes)
+                       : "memory");
+        }
+      }
+      const int n = end - l_unit < kRound ? end - l_unit : kRound;
+      l_left -= n;
+      l_unit += n;
+      if (l_unit == g.units) {
+        l_left -= kRowCost;
+        l_unit = 0;
+        if (l_left > 0) lr.set(a, ++l_row);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const auto end_of = [&]() { return g.units - unit < left ? g.units : unit + static_cast<int>(left); };
-  r.set(a, row);
-  load_round(unit, end_of());
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) copy_round(i);
+  int stage = 0;
+
   // the given token and its logit, and the next row's token
   const auto id_of_row = [&](int64_t t) { return a.ids != nullptr && t < a.T ? a.ids[t] : -1; };
   int32_t id = id_of_row(row), id2 = id_of_row(row + 1);
   float xt = given_logit(a, row, id);
   while (true) {
-    const int end = end_of();
+    const int end = g.units - unit < left ? g.units : unit + static_cast<int>(left);
     const bool begins = unit == 0, whole = begins && end == g.units;
     const bool given = id >= 0 && id < a.V;
     const uint64_t key_t = given ? key_of(xt, static_cast<uint32_t>(id)) : ~uint64_t{0};
     const int v_id = given ? static_cast<int>((static_cast<uint32_t>(id) + r.head) / kN) : -1;
     // vectors before v_id count logits that are not below xt: not at or below
     // the number before it (NaN, unordered with all, where that is none)
-    float low = xt;
+    float low;
     if (xt == -CUDART_INF_F) low = CUDART_NAN_F;
     else if (kBf16) low = __uint_as_float(xt > 0.0f ? __float_as_uint(xt) - 0x10000u : (xt == 0.0f ? 0x80010000u : __float_as_uint(xt) + 0x10000u));
     else low = __uint_as_float(xt > 0.0f ? __float_as_uint(xt) - 1u : (xt == 0.0f ? 0x80000001u : __float_as_uint(xt) + 1u));
-    const bool by_key = xt != xt;
 
     Sums s{-CUDART_INF_F, 0.0f, 0.0f, 0};
     float limit = -CUDART_INF_F, bound = -CUDART_INF_F;
+    // The terms are added up in pairs, relative to ref = m c rounded (one fma for
+    // an exponent); flush() brings them to m. Where that rounding is no small
+    // number (`far`), each exponent is a difference's.
+    uint64_t l2 = 0, t2 = 0;
+    float ref = 0.0f;
+    bool far = false;
+    const auto flush = [&]() {
+      if (far) return;
+      const float l = low_of(l2) + high_of(l2), t = low_of(t2) + high_of(t2);
+      const float off = s.m == -CUDART_INF_F ? 0.0f : fmaf(s.m, g.c, -ref), f = exp2_fast(-off);
+      s.l += f * l;
+      s.t += f * (t - off * l);
+      l2 = t2 = 0;
+    };
     uint64_t bound_key = 0;
-    bool closed = a.top_k == 0, opening = true;
-    int kept = 0;
+    bool closed = a.top_k == 0, lost = false;
     if (tid == 0) sh.noted = 0;
 
-    for (int u = unit; u < end; u += kRound) {
-      Vec<kBf16> x[kRound];
-#pragma unroll
-      for (int j = 0; j < kRound; ++j) x[j] = next[j];
-      if (u + kRound < end) load_round(u + kRound, end);
-
-      float top[kRound];
+    for (int u = unit, rounds = 1; u < end; u += kRound, ++rounds) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      copy_round(stage == 0 ? kStages - 1 : stage - 1);  // read in the round before
+      const uint8_t* in = mine + stage * kStageBytes;
+      // does the block's round have a row's first or last vector, the given
+      // token's, or fewer units? (then logits are looked at one by one)
+      const int v0 = u * kThreads, v1 = v0 + kRound * kThreads;
+      const bool plain = v0 > 0 && v1 < r.nvec && u + kRound <= end && (v_id < v0 || v_id >= v1) && xt == xt;
+      const bool opening = rounds == 1;
+      float most = -CUDART_INF_F;  // of the round, for the opening
+      uint32_t above = 0;          // two bf16 counts, at most 16 each
+      const float than = v_id >= v1 ? low : xt;
+      const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
 #pragma unroll
       for (int j = 0; j < kRound; ++j) {
-        const int v = (u + j) * kThreads + tid;
-        top[j] = x[j].top();
-        if (top[j] > limit) {
-          raise(s, top[j], g.c);
-          limit = s.m + slack;
+        Vec<kBf16> x;
+        const int v = v0 + j * kThreads + tid;
+        {
+          const uint4 y = *reinterpret_cast<const uint4*>(in + j * kUnitBytes);
+          x.w[0] = y.x, x.w[1] = y.y, x.w[2] = y.z, x.w[3] = y.w;
         }
-        const float ref = s.m == -CUDART_INF_F ? 0.0f : s.m;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          // (far below the reference, -inf among them, the weight is 0)
-          const float d = max_nan((x[j].at(i) - ref) * g.c, -200.0f), e = exp2_fast(d);
-          s.l += e;
-          s.t = fmaf(e, d, s.t);
-        }
-        if (given) {
-          if (v == 0 || v >= r.nvec - 1 || v == v_id || by_key) {
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-              const uint32_t n = static_cast<uint32_t>(v) * kN + i - r.head;
-              if (u + j < end && n < V) s.before += key_of(x[j].at(i), n) > key_t;
-            }
-          } else if (u + j < end) {
-            const float than = v < v_id ? low : xt;
-            if constexpr (kBf16) {
-              const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
-              uint32_t n = 0;  // two bf16 counts, at most 4 each
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t y;
-                asm("set.gtu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x[j].w[i]), "r"(than2));
-                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(n) : "r"(y));
-              }
-              s.before += static_cast<int>(__uint_as_float(n << 16) + __uint_as_float(n & 0xFFFF0000u));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s.before += !(x[j].at(i) <= than);
-            }
-          }
-        }
-      }
-      if (closed) continue;
-
-      // ---- the best top_k
-      if (opening) {
-        // the top_k'th largest of 32 groups' maxima: top_k logits are not below it
-        float mine = top[0];
-#pragma unroll
-        for (int j = 1; j < kRound; ++j) mine = max_nan(mine, top[j]);
-        uint32_t o = order_of(mine);
-#pragma unroll
-        for (int i = 1; i < 8; i <<= 1) o = max(o, __shfl_xor_sync(0xFFFFFFFFu, o, i));
-        if ((lane & 7) == 0) sh.groups[tid >> 3] = o;
-        __syncthreads();
-        o = sh.groups[lane];
-        int rank = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t y = __shfl_sync(0xFFFFFFFFu, o, i);
-          rank += y > o || (y == o && i < lane);
-        }
-        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, rank == a.top_k - 1)) - 1;
-        bound_key = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, o, from)) << 32;
-      }
-      bool over = false;  // more noted than a few times top_k
-      const auto note = [&](uint64_t least) {
-#pragma unroll
-        for (int j = 0; j < kRound; ++j) {
-          const int v = (u + j) * kThreads + tid;
-          if (u + j >= end || v >= r.nvec) continue;
-          if (!opening && top[j] <= bound) continue;
+        if (!plain) {
+          const bool none = u + j >= end || v >= r.nvec;
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
-            const uint32_t n = static_cast<uint32_t>(v) * kN + i - r.head;
-            const uint64_t key = key_of(x[j].at(i), n);
-            if (n < V && key >= least) {
-              const int to = atomicAdd(&sh.noted, 1);
-              if (to < kNotes) sh.notes[to] = key;
-              over |= to >= 64 && to >= 2 * a.top_k;
-            }
+            if (!none && r.id(v, i) < V) continue;
+            if constexpr (kBf16) x.w[i >> 1] = __byte_perm(x.w[i >> 1], Vec<kBf16>::kNone, (i & 1) ? 0x5410 : 0x3254);
+            else x.w[i] = Vec<kBf16>::kNone;
           }
         }
-      };
-      note(bound_key);
-      if (__syncthreads_or(over) || opening) {
-        int n = sh.noted;
-        if (n > kNotes) {
-          // bisection for a bound that at least top_k and at most kNotes keys reach
-          uint64_t least = 0;
-          for (int bit = 63; bit >= 0; --bit) {
-            const uint64_t trial = least | uint64_t{1} << bit;
-            __syncthreads();
-            if (tid == 0) sh.count = 0;
-            __syncthreads();
-            int c = tid < kept && sh.notes[tid] >= trial;
+        const float top = x.top();
+        if (top > limit) {
+          flush();
+          raise(s, top, g.c);
+          limit = top + slack;
+          ref = top * g.c;
+          far = fabsf(ref) >= 16777216.0f;
+        }
+        if (!far) {
+          const uint64_t c2 = pair(g.c, g.c), m2 = pair(-ref, -ref);
 #pragma unroll
-            for (int j = 0; j < kRound; ++j) {
-              const int v = (u + j) * kThreads + tid;
+          for (int i = 0; i < kN; i += 2) {
+            const uint64_t d = fma2(pair(x.at(i), x.at(i + 1)), c2, m2);
+            // (far below the reference, -inf among them, the weight is 0)
+            const float d0 = max_nan(low_of(d), -200.0f), d1 = max_nan(high_of(d), -200.0f);
+            const uint64_t e = pair(exp2_fast(d0), exp2_fast(d1));
+            l2 = add2(l2, e);
+            t2 = fma2(e, pair(d0, d1), t2);
+          }
+        } else {
 #pragma unroll
-              for (int i = 0; i < kN; ++i) {
-                const uint32_t n2 = static_cast<uint32_t>(v) * kN + i - r.head;
-                c += u + j < end && v < r.nvec && n2 < V && key_of(x[j].at(i), n2) >= trial;
+          for (int i = 0; i < kN; ++i) {
+            const float d = max_nan((x.at(i) - s.m) * g.c, -200.0f), e = exp2_fast(d);
+            s.l += e;
+            s.t = fmaf(e, d, s.t);
+          }
+        }
+        if (given) {
+          if (plain) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kBf16) {
+                uint32_t y;
+                asm("set.gtu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x.w[i]), "r"(than2));
+                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(above) : "r"(y));
+              } else {
+                s.before += !(x.at(i) <= than);
               }
             }
-            c = __reduce_add_sync(0xFFFFFFFFu, c);
-            if (lane == 0) atomicAdd(&sh.count, c);
-            __syncthreads();
-            if (sh.count >= a.top_k) least = trial;
-            if (sh.count >= a.top_k && sh.count <= kNotes - kMaxTopK) break;
+          } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (u + j < end && v < r.nvec && r.id(v, i) < V) s.before += key_of(x.at(i), r.id(v, i)) > key_t;
+          }
+        }
+        most = max_nan(most, top);
+        if (!closed && !opening && !(top <= bound) && u + j < end && v < r.nvec)
+          note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
+      }
+      if constexpr (kBf16)
+        s.before += static_cast<int>(__uint_as_float(above << 16) + __uint_as_float(above & 0xFFFF0000u));
+
+      // ---- the best top_k
+      if (!closed && (rounds & (rounds - 1)) == 0) {
+        if (opening) {
+          // the top_k'th largest of 32 groups' maxima: top_k logits are not below it
+          uint32_t o = order_of(most);
+#pragma unroll
+          for (int i = 1; i < 8; i <<= 1) o = max(o, __shfl_xor_sync(0xFFFFFFFFu, o, i));
+          if ((lane & 7) == 0) sh.groups[tid >> 3] = o;
+          __syncthreads();
+          o = sh.groups[lane];
+          int rank = 0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t y = __shfl_sync(0xFFFFFFFFu, o, i);
+            rank += y > o || (y == o && i < lane);
+          }
+          const int from = __ffs(__ballot_sync(0xFFFFFFFFu, rank == a.top_k - 1)) - 1;
+          const uint32_t least = __shfl_sync(0xFFFFFFFFu, o, from);
+          bound_key = static_cast<uint64_t>(least) << 32;
+          if (order_of(most) >= least) {
+            for (int j = 0; j < kRound; ++j) {
+              const int v = v0 + j * kThreads + tid;
+              if (u + j < end && v < r.nvec) note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
+            }
+          }
+        }
+        __syncthreads();
+        const int n = sh.noted;
+        __syncthreads();
+        if (n > kNotes) {
+          closed = lost = true;
+        } else {
+          keep_best(sh, n, a.top_k);
+          if (sh.noted == a.top_k) {
+            bound_key = sh.notes[a.top_k - 1];
+            bound = value_of(static_cast<uint32_t>(bound_key >> 32));
+            closed = bound != bound;  // NaN: nothing that comes later is better
+          } else {
+            closed = lost = u + kRound < end;  // fewer logits than top_k in the round
           }
           __syncthreads();
-          if (tid == 0) sh.noted = kept;
-          __syncthreads();
-          opening = true;  // every vector is looked at
-          note(least > bound_key ? least : bound_key);
-          __syncthreads();
-          n = sh.noted;
         }
-        __syncthreads();
-        keep_best(sh, n, a.top_k);
-        kept = sh.noted;
-        if (kept == a.top_k) {
-          bound_key = sh.notes[a.top_k - 1];
-          bound = value_of(static_cast<uint32_t>(bound_key >> 32));
-          closed = bound != bound;  // NaN: nothing that comes later is better
-        } else {
-          bound_key = 0;  // fewer than top_k logits so far
-        }
-        opening = kept < a.top_k;
-        __syncthreads();
       }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
     // ---- the end of the piece
+    flush();
     const int64_t done_row = row;
     const float done_xt = xt;
+    const int done_unit = unit;
     left -= end - unit;
     if (end == g.units) {
       left -= kRowCost;
@@ -432,9 +552,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
     } else {
       unit = end;
     }
-    if (left > 0) {  // the next row
-      r.set(a, row);
-      load_round(unit, end_of());
+    if (left > 0) {  // the next row's token and its logit
       id = id2;
       xt = given_logit(a, row, id);
       id2 = id_of_row(row + 1);
@@ -447,10 +565,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
     }
     if (lane == 0) sh.sums[warp] = s;
     __syncthreads();
-    if (a.top_k > 0) keep_best(sh, sh.noted, a.top_k);
     s = sh.sums[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) join(s, sh.sums[w], g.c);
+    if (a.top_k > 0) {
+      const int n = sh.noted;
+      __syncthreads();
+      if (lost || n > kNotes) best_of<kBf16>(sh, a, done_row, done_unit, end);
+      else keep_best(sh, n, a.top_k);
+    }
     const uint64_t key = tid < a.top_k && tid < sh.noted ? sh.notes[tid] : 0;
     if (whole) {
       put(g, done_row, s, key, given, done_xt);
@@ -461,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       if (tid < a.top_k) p.keys[tid] = key;
     }
     if (left <= 0) return;
+    r.set(a, row);
     __syncthreads();
   }
 }
@@ -553,9 +677,13 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
   g.shares = (total + g.share - 1) / g.share;
   g.parts = static_cast<Part*>(a.ws);
   const unsigned grid = static_cast<unsigned>(g.shares);
-  if (a.type == WQ_LOGITS_BF16) logprobs_kernel<true><<<grid, kThreads, 0, c.stream>>>(g);
-  else logprobs_kernel<false><<<grid, kThreads, 0, c.stream>>>(g);
-  const cudaError_t e = cudaGetLastError();
+  static SmemLimit lim[2];
+  cudaError_t e = a.type == WQ_LOGITS_BF16 ? raise_smem_limit(lim[0], logprobs_kernel<true>, c.device, sizeof(Shared))
+                                           : raise_smem_limit(lim[1], logprobs_kernel<false>, c.device, sizeof(Shared));
+  if (e != cudaSuccess) return e;
+  if (a.type == WQ_LOGITS_BF16) logprobs_kernel<true><<<grid, kThreads, sizeof(Shared), c.stream>>>(g);
+  else logprobs_kernel<false><<<grid, kThreads, sizeof(Shared), c.stream>>>(g);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
