@@ -23,7 +23,7 @@
 //    ahead (cp.async), and reads them back itself: no barrier.
 //  - The best top_k are kept as 64-bit keys (logit, then id) in shared memory: the
 //    first round's bound is the top_k'th largest of 32 groups' maxima; later
-//    logits are noted only above the bound, which is raised after 1, 2, 4, 8 ..
+//    logits are noted only above the bound, which is raised after 1, 4, 16 ..
 //    rounds: a few notes per row in the usual order. Where they do not fit
 //    (ascending rows), the piece's best are found again with a bound for every
 //    round, by bisection over the keys.
@@ -161,11 +161,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 template <bool kBf16>
 struct Vec {
   static constexpr int kN = kBf16 ? 8 : 4;
-  static constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
   uint32_t w[4];
   __device__ __forceinline__ float at(int i) const {
     if constexpr (kBf16) return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
     else return __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ static Vec from(const uint8_t* p) {
+    const uint4 y = *reinterpret_cast<const uint4*>(p);
+    return Vec{{y.x, y.y, y.z, y.w}};
   }
   // The largest, NaN if there is one.
   __device__ __forceinline__ float top() const {
@@ -222,6 +225,41 @@ __device__ void keep_best(Shared& sh, int n, int top_k) {
   if (threadIdx.x < kept) sh.notes[threadIdx.x] = sh.best[threadIdx.x];
   if (threadIdx.x == 0) sh.noted = kept;
   __syncthreads();
+}
+
+// A vector in shared memory with logits id, id + 1 .., which may be its row's
+// first or last or none of it: what lies outside becomes -inf. Returns how many
+// of its logits come before the given token.
+template <bool kBf16>
+__device__ __noinline__ int look_closer(uint8_t* x, uint32_t id, uint32_t V, uint64_t key_t) {
+  int before = 0;
+  for (int i = 0; i < Vec<kBf16>::kN; ++i) {
+    if constexpr (kBf16) {
+      uint16_t& y = reinterpret_cast<uint16_t*>(x)[i];
+      if (id + i < V) before += key_of(bf16_bits_to_float(y), id + i) > key_t;
+      else y = 0xFF80u;
+    } else {
+      float& y = reinterpret_cast<float*>(x)[i];
+      if (id + i < V) before += key_of(y, id + i) > key_t;
+      else y = -CUDART_INF_F;
+    }
+  }
+  return before;
+}
+
+// A vector's terms with a difference for each exponent: l and t.
+template <bool kBf16>
+__device__ __noinline__ float2 far_sums(const uint8_t* x, float m, float c) {
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int i = 0; i < Vec<kBf16>::kN; ++i) {
+    float y;
+    if constexpr (kBf16) y = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i]);
+    else y = reinterpret_cast<const float*>(x)[i];
+    const float d = max_nan((y - m) * c, -200.0f), e = exp2_fast(d);
+    s.x += e;
+    s.y = fmaf(e, d, s.y);
+  }
+  return s;
 }
 
 // Notes every logit of the vector in shared memory whose key is at least
@@ -348,15 +386,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       const int end = g.units - l_unit < l_left ? g.units : l_unit + static_cast<int>(l_left);
       const int row_end = (lr.head + static_cast<int>(V & 7)) * kElem & 15;  // bytes of the last vector, 0: all
       const uint8_t* src = lr.base + (static_cast<int64_t>(l_unit) * kThreads + tid) * 16;
+      const auto copy = [&](int j, int bytes) {
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(mine_s + stage * kStageBytes +
+                                                                                    j * kUnitBytes),
+                     "l"(src + j * kUnitBytes), "r"(bytes)
+                     : "memory");
+      };
+      if (l_unit + kRound <= end && (l_unit + kRound) * kThreads < lr.nvec) {
 #pragma unroll
-      for (int j = 0; j < kRound; ++j) {
-        const int v = (l_unit + j) * kThreads + tid;
-        if (l_unit + j < end && v < lr.nvec) {
-          const int bytes = v == lr.nvec - 1 && row_end != 0 ? row_end : 16;  // not past the row
-          asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(mine_s + stage * kStageBytes +
-                                                                                      j * kUnitBytes),
-                       "l"(src + static_cast<int64_t>(j) * kUnitBytes), "r"(bytes)
-                       : "memory");
+        for (int j = 0; j < kRound; ++j) copy(j, 16);
+      } else {
+        for (int j = 0; j < kRound; ++j) {
+          const int v = (l_unit + j) * kThreads + tid;
+          if (l_unit + j < end && v < lr.nvec) copy(j, v == lr.nvec - 1 && row_end != 0 ? row_end : 16);  // not past the row
         }
       }
       const int n = end - l_unit < kRound ? end - l_unit : kRound;
@@ -414,40 +456,74 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
     for (int u = unit, rounds = 1; u < end; u += kRound, ++rounds) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       copy_round(stage == 0 ? kStages - 1 : stage - 1);  // read in the round before
-      const uint8_t* in = mine + stage * kStageBytes;
-      // does the block's round have a row's first or last vector, the given
-      // token's, or fewer units? (then logits are looked at one by one)
-      const int v0 = u * kThreads, v1 = v0 + kRound * kThreads;
-      const bool plain = v0 > 0 && v1 < r.nvec && u + kRound <= end && (v_id < v0 || v_id >= v1) && xt == xt;
-      const bool opening = rounds == 1;
-      float most = -CUDART_INF_F;  // of the round, for the opening
-      uint32_t above = 0;          // two bf16 counts, at most 16 each
-      const float than = v_id >= v1 ? low : xt;
-      const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
-#pragma unroll
-      for (int j = 0; j < kRound; ++j) {
-        Vec<kBf16> x;
-        const int v = v0 + j * kThreads + tid;
-        {
-          const uint4 y = *reinterpret_cast<const uint4*>(in + j * kUnitBytes);
-          x.w[0] = y.x, x.w[1] = y.y, x.w[2] = y.z, x.w[3] = y.w;
+      uint8_t* in = mine + stage * kStageBytes;
+      const int v0 = u * kThreads + warp * 32;
+      // the row's first and last vector, the given token's, and what lies
+      // outside the piece: logit by logit, by the warp that has it
+      unsigned special = 0;
+      if (!(v0 > 0 && v0 + (kRound - 1) * kThreads + 32 < r.nvec && u + kRound <= end &&
+            (v_id < v0 || v_id >= v0 + (kRound - 1) * kThreads + 32) && xt == xt)) {
+        for (int j = 0; j < kRound; ++j) {
+          const int w0 = v0 + j * kThreads, v = w0 + lane;
+          if (w0 > 0 && w0 + 32 < r.nvec && u + j < end && (v_id < w0 || v_id >= w0 + 32) && xt == xt) continue;
+          special |= 1u << j;
+          const uint32_t id0 = u + j < end && v < r.nvec ? r.id(v, 0) : 0xFFFFFF00u;  // none: above any V
+          s.before += look_closer<kBf16>(in + j * kUnitBytes, id0, V, key_t);
         }
-        if (!plain) {
-          const bool none = u + j >= end || v >= r.nvec;
+      }
+      if (rounds == 1) {
+        // The opening: the largest logit of the block's round is everyone's first
+        // reference, and the top_k'th largest of 32 groups' maxima the first bound
+        // (top_k logits are not below it).
+        float tops[kRound];
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            if (!none && r.id(v, i) < V) continue;
-            if constexpr (kBf16) x.w[i >> 1] = __byte_perm(x.w[i >> 1], Vec<kBf16>::kNone, (i & 1) ? 0x5410 : 0x3254);
-            else x.w[i] = Vec<kBf16>::kNone;
+        for (int j = 0; j < kRound; ++j) tops[j] = Vec<kBf16>::from(in + j * kUnitBytes).top();
+        uint32_t o = 0;
+#pragma unroll
+        for (int j = 0; j < kRound; ++j) o = max(o, order_of(tops[j]));
+#pragma unroll
+        for (int i = 1; i < 8; i <<= 1) o = max(o, __shfl_xor_sync(0xFFFFFFFFu, o, i));
+        if ((lane & 7) == 0) sh.groups[tid >> 3] = o;
+        __syncthreads();
+        o = sh.groups[lane];
+        const float top = value_of(__reduce_max_sync(0xFFFFFFFFu, o));
+        if (top > -CUDART_INF_F) {  // not NaN
+          s.m = top;
+          limit = top + slack;
+          ref = top * g.c;
+          far = !(fabsf(ref) < 16777216.0f);
+        }
+        if (!closed) {
+          int rank = 0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t y = __shfl_sync(0xFFFFFFFFu, o, i);
+            rank += y > o || (y == o && i < lane);
+          }
+          const int from = __ffs(__ballot_sync(0xFFFFFFFFu, rank == a.top_k - 1)) - 1;
+          const uint32_t least = __shfl_sync(0xFFFFFFFFu, o, from);
+          bound_key = static_cast<uint64_t>(least) << 32;
+#pragma unroll
+          for (int j = 0; j < kRound; ++j) {
+            const int v = v0 + j * kThreads + lane;
+            if (order_of(tops[j]) >= least && u + j < end && v < r.nvec)
+              note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
           }
         }
+      }
+      const bool opening = rounds == 1;
+      uint32_t above = 0;  // two bf16 counts, at most 16 each
+#pragma unroll 2
+      for (int j = 0; j < kRound; ++j) {
+        const int w0 = v0 + j * kThreads;
+        const Vec<kBf16> x = Vec<kBf16>::from(in + j * kUnitBytes);
         const float top = x.top();
         if (top > limit) {
           flush();
           raise(s, top, g.c);
           limit = top + slack;
           ref = top * g.c;
-          far = fabsf(ref) >= 16777216.0f;
+          far = !(fabsf(ref) < 16777216.0f);
         }
         if (!far) {
           const uint64_t c2 = pair(g.c, g.c), m2 = pair(-ref, -ref);
@@ -461,64 +537,35 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
             t2 = fma2(e, pair(d0, d1), t2);
           }
         } else {
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const float d = max_nan((x.at(i) - s.m) * g.c, -200.0f), e = exp2_fast(d);
-            s.l += e;
-            s.t = fmaf(e, d, s.t);
-          }
+          const float2 y = far_sums<kBf16>(in + j * kUnitBytes, s.m, g.c);
+          s.l += y.x;
+          s.t += y.y;
         }
-        if (given) {
-          if (plain) {
+        if (given && (special >> j & 1u) == 0) {
+          const float than = v_id >= w0 ? low : xt;
+          if constexpr (kBf16) {
+            const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if constexpr (kBf16) {
-                uint32_t y;
-                asm("set.gtu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x.w[i]), "r"(than2));
-                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(above) : "r"(y));
-              } else {
-                s.before += !(x.at(i) <= than);
-              }
+              uint32_t y;
+              asm("set.gtu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x.w[i]), "r"(than2));
+              asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(above) : "r"(y));
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (u + j < end && v < r.nvec && r.id(v, i) < V) s.before += key_of(x.at(i), r.id(v, i)) > key_t;
+            for (int i = 0; i < 4; ++i) s.before += !(x.at(i) <= than);
           }
         }
-        most = max_nan(most, top);
-        if (!closed && !opening && !(top <= bound) && u + j < end && v < r.nvec)
-          note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
+        if (!closed && !opening && !(top <= bound)) {
+          const int v = w0 + lane;
+          if (u + j < end && v < r.nvec) note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
+        }
       }
       if constexpr (kBf16)
         s.before += static_cast<int>(__uint_as_float(above << 16) + __uint_as_float(above & 0xFFFF0000u));
 
-      // ---- the best top_k
-      if (!closed && (rounds & (rounds - 1)) == 0) {
-        if (opening) {
-          // the top_k'th largest of 32 groups' maxima: top_k logits are not below it
-          uint32_t o = order_of(most);
-#pragma unroll
-          for (int i = 1; i < 8; i <<= 1) o = max(o, __shfl_xor_sync(0xFFFFFFFFu, o, i));
-          if ((lane & 7) == 0) sh.groups[tid >> 3] = o;
-          __syncthreads();
-          o = sh.groups[lane];
-          int rank = 0;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint32_t y = __shfl_sync(0xFFFFFFFFu, o, i);
-            rank += y > o || (y == o && i < lane);
-          }
-          const int from = __ffs(__ballot_sync(0xFFFFFFFFu, rank == a.top_k - 1)) - 1;
-          const uint32_t least = __shfl_sync(0xFFFFFFFFu, o, from);
-          bound_key = static_cast<uint64_t>(least) << 32;
-          if (order_of(most) >= least) {
-            for (int j = 0; j < kRound; ++j) {
-              const int v = v0 + j * kThreads + tid;
-              if (u + j < end && v < r.nvec) note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
-            }
-          }
-        }
+      // ---- the best top_k: the bound is raised after 1, 4, 16 .. rounds
+      if (!closed && (rounds & (rounds - 1)) == 0 && (rounds & 0x55555555) != 0) {
         __syncthreads();
         const int n = sh.noted;
         __syncthreads();
@@ -557,31 +604,45 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       xt = given_logit(a, row, id);
       id2 = id_of_row(row + 1);
     }
+    // mostly everyone's reference is still the opening's
+    const bool same = __all_sync(0xFFFFFFFFu, s.m == __shfl_sync(0xFFFFFFFFu, s.m, 0));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const Sums y{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
+      const Sums y{same ? s.m : __shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
                    __shfl_xor_sync(0xFFFFFFFFu, s.t, o), __shfl_xor_sync(0xFFFFFFFFu, s.before, o)};
-      join(s, y, g.c);
+      if (same) {
+        s.l += y.l;
+        s.t += y.t;
+        s.before += y.before;
+      } else {
+        join(s, y, g.c);
+      }
     }
     if (lane == 0) sh.sums[warp] = s;
     __syncthreads();
-    s = sh.sums[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) join(s, sh.sums[w], g.c);
     if (a.top_k > 0) {
       const int n = sh.noted;
       __syncthreads();
       if (lost || n > kNotes) best_of<kBf16>(sh, a, done_row, done_unit, end);
       else keep_best(sh, n, a.top_k);
     }
-    const uint64_t key = tid < a.top_k && tid < sh.noted ? sh.notes[tid] : 0;
-    if (whole) {
-      put(g, done_row, s, key, given, done_xt);
-    } else {
-      // slot 1 for the row's first part, 0 for a continued one
-      Part& p = g.parts[static_cast<int64_t>(blockIdx.x) * 2 + begins];
-      if (tid == 0) p.s = s;
-      if (tid < a.top_k) p.keys[tid] = key;
+    if (warp == 0) {
+      s = sh.sums[lane % kWarps];
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) {
+        const Sums y{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
+                     __shfl_xor_sync(0xFFFFFFFFu, s.t, o), __shfl_xor_sync(0xFFFFFFFFu, s.before, o)};
+        join(s, y, g.c);
+      }
+      const uint64_t key = lane < a.top_k && lane < sh.noted ? sh.notes[lane] : 0;
+      if (whole) {
+        put(g, done_row, s, key, given, done_xt);
+      } else {
+        // slot 1 for the row's first part, 0 for a continued one
+        Part& p = g.parts[static_cast<int64_t>(blockIdx.x) * 2 + begins];
+        if (lane == 0) p.s = s;
+        if (lane < a.top_k) p.keys[lane] = key;
+      }
     }
     if (left <= 0) return;
     r.set(a, row);
