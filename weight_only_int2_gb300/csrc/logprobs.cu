@@ -211,14 +211,17 @@ struct Shared {
 };
 
 // Sorts the n <= kNotes noted keys' best top_k to the front (by counting, keys
-// are distinct). All threads; n is the same for all.
-__device__ void keep_best(Shared& sh, int n, int top_k) {
+// are distinct): 8 to 1 threads a key. All threads; n is the same for all.
+__device__ __forceinline__ void keep_best(Shared& sh, int n, int top_k) {
   n = n < kNotes ? n : kNotes;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t mine = sh.notes[i];
+  const int shift = n <= 32 ? 3 : (n <= 64 ? 2 : (n <= 128 ? 1 : 0)), per = 1 << shift;
+  for (int i0 = 0; i0 < n; i0 += kThreads >> shift) {
+    const int i = i0 + (static_cast<int>(threadIdx.x) >> shift);
+    const uint64_t mine = i < n ? sh.notes[i] : 0;
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += sh.notes[j] > mine;
-    if (rank < top_k) sh.best[rank] = mine;
+    for (int j = threadIdx.x & (per - 1); j < n; j += per) rank += sh.notes[j] > mine;
+    for (int o = 1; o < per; o <<= 1) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, o);
+    if (i < n && rank < top_k) sh.best[rank] = mine;
   }
   __syncthreads();
   const int kept = n < top_k ? n : top_k;
@@ -263,13 +266,14 @@ __device__ __noinline__ float2 far_sums(const uint8_t* x, float m, float c) {
 }
 
 // Notes every logit of the vector in shared memory whose key is at least
-// `least`.
+// `least` (no smaller than that of the logit `bound`).
 template <bool kBf16>
-__device__ __noinline__ void note(Shared& sh, const uint8_t* x, uint32_t id, uint32_t V, uint64_t least) {
+__device__ __noinline__ void note(Shared& sh, const uint8_t* p, uint32_t id, uint32_t V, uint64_t least, float bound) {
+  const Vec<kBf16> x = Vec<kBf16>::from(p);
+#pragma unroll
   for (int i = 0; i < Vec<kBf16>::kN; ++i) {
-    float y;
-    if constexpr (kBf16) y = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i]);
-    else y = reinterpret_cast<const float*>(x)[i];
+    const float y = x.at(i);
+    if (y < bound) continue;
     const uint64_t key = key_of(y, id + i);
     if (id + i < V && key >= least) {
       const int to = atomicAdd(&sh.noted, 1);
@@ -348,7 +352,7 @@ __device__ __noinline__ void best_of(Shared& sh, const LogprobArgs& a, int64_t r
   }
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kIds>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const Args g) {
   constexpr int kN = Vec<kBf16>::kN, kElem = kBf16 ? 2 : 4;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -363,9 +367,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
   // a piece: units [unit, end) of row, `left` places of the share from there on
   const int64_t total = a.T * places, first = g.share * blockIdx.x;
   if (first >= total) return;
-  int64_t left = first + g.share < total ? g.share : total - first;
-  int64_t row = first / places;
-  int unit = static_cast<int>(first - row * places) - kRowCost;
+  int left = static_cast<int>(first + g.share < total ? g.share : total - first);
+  int row = static_cast<int>(first / places);
+  int unit = static_cast<int>(first - static_cast<int64_t>(row) * places) - kRowCost;
   if (unit < 0) {
     left += unit;
     unit = 0;
@@ -379,11 +383,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
   const uint32_t mine_s = smem_u32(mine);
   constexpr int kUnitBytes = kThreads * 16, kStageBytes = kRound * kUnitBytes;
   Row<kBf16> lr = r;
-  int64_t l_row = row, l_left = left;
-  int l_unit = unit;
+  int l_row = row, l_left = left, l_unit = unit;
   auto copy_round = [&](int stage) {
     if (l_left > 0) {
-      const int end = g.units - l_unit < l_left ? g.units : l_unit + static_cast<int>(l_left);
+      const int end = g.units - l_unit < l_left ? g.units : l_unit + l_left;
       const int row_end = (lr.head + static_cast<int>(V & 7)) * kElem & 15;  // bytes of the last vector, 0: all
       const uint8_t* src = lr.base + (static_cast<int64_t>(l_unit) * kThreads + tid) * 16;
       const auto copy = [&](int j, int bytes) {
@@ -417,13 +420,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
   int stage = 0;
 
   // the given token and its logit, and the next row's token
-  const auto id_of_row = [&](int64_t t) { return a.ids != nullptr && t < a.T ? a.ids[t] : -1; };
+  const auto id_of_row = [&](int t) { return kIds && t < a.T ? a.ids[t] : -1; };
   int32_t id = id_of_row(row), id2 = id_of_row(row + 1);
   float xt = given_logit(a, row, id);
   while (true) {
-    const int end = g.units - unit < left ? g.units : unit + static_cast<int>(left);
+    const int end = g.units - unit < left ? g.units : unit + left;
     const bool begins = unit == 0, whole = begins && end == g.units;
-    const bool given = id >= 0 && id < a.V;
+    const bool given = kIds && id >= 0 && id < a.V;
     const uint64_t key_t = given ? key_of(xt, static_cast<uint32_t>(id)) : ~uint64_t{0};
     const int v_id = given ? static_cast<int>((static_cast<uint32_t>(id) + r.head) / kN) : -1;
     // vectors before v_id count logits that are not below xt: not at or below
@@ -435,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
 
     Sums s{-CUDART_INF_F, 0.0f, 0.0f, 0};
     float limit = -CUDART_INF_F, bound = -CUDART_INF_F;
+    float gate = CUDART_NAN_F;  // a vector above it (always, for NaN) needs more than its terms
     // The terms are added up in pairs, relative to ref = m c rounded (one fma for
     // an exponent); flush() brings them to m. Where that rounding is no small
     // number (`far`), each exponent is a difference's.
@@ -442,7 +446,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
     float ref = 0.0f;
     bool far = false;
     const auto flush = [&]() {
-      if (far) return;
+      if (far) {
+        l2 = t2 = 0;
+        return;
+      }
       const float l = low_of(l2) + high_of(l2), t = low_of(t2) + high_of(t2);
       const float off = s.m == -CUDART_INF_F ? 0.0f : fmaf(s.m, g.c, -ref), f = exp2_fast(-off);
       s.l += f * l;
@@ -461,8 +468,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       // the row's first and last vector, the given token's, and what lies
       // outside the piece: logit by logit, by the warp that has it
       unsigned special = 0;
-      if (!(v0 > 0 && v0 + (kRound - 1) * kThreads + 32 < r.nvec && u + kRound <= end &&
-            (v_id < v0 || v_id >= v0 + (kRound - 1) * kThreads + 32) && xt == xt)) {
+      const bool plain = v0 > 0 && v0 + (kRound - 1) * kThreads + 32 < r.nvec && u + kRound <= end &&
+                         (v_id < v0 || v_id >= v0 + (kRound - 1) * kThreads + 32) && xt == xt;
+      if (!plain) {
         for (int j = 0; j < kRound; ++j) {
           const int w0 = v0 + j * kThreads, v = w0 + lane;
           if (w0 > 0 && w0 + 32 < r.nvec && u + j < end && (v_id < w0 || v_id >= w0 + 32) && xt == xt) continue;
@@ -507,42 +515,50 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           for (int j = 0; j < kRound; ++j) {
             const int v = v0 + j * kThreads + lane;
             if (order_of(tops[j]) >= least && u + j < end && v < r.nvec)
-              note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
+              note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key, value_of(least));
           }
         }
       }
       const bool opening = rounds == 1;
+      const auto set_gate = [&]() {
+        // far: always; before there is a reference, and for NaN: always
+        gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : (closed || opening || limit < bound ? limit : bound);
+      };
+      set_gate();
       uint32_t above = 0;  // two bf16 counts, at most 16 each
-#pragma unroll 2
-      for (int j = 0; j < kRound; ++j) {
-        const int w0 = v0 + j * kThreads;
+      const uint64_t c2 = pair(g.c, g.c);
+      const auto terms = [&](int j, bool count, float than) {
         const Vec<kBf16> x = Vec<kBf16>::from(in + j * kUnitBytes);
         const float top = x.top();
-        if (top > limit) {
-          flush();
-          raise(s, top, g.c);
-          limit = top + slack;
-          ref = top * g.c;
-          far = !(fabsf(ref) < 16777216.0f);
-        }
-        if (!far) {
-          const uint64_t c2 = pair(g.c, g.c), m2 = pair(-ref, -ref);
-#pragma unroll
-          for (int i = 0; i < kN; i += 2) {
-            const uint64_t d = fma2(pair(x.at(i), x.at(i + 1)), c2, m2);
-            // (far below the reference, -inf among them, the weight is 0)
-            const float d0 = max_nan(low_of(d), -200.0f), d1 = max_nan(high_of(d), -200.0f);
-            const uint64_t e = pair(exp2_fast(d0), exp2_fast(d1));
-            l2 = add2(l2, e);
-            t2 = fma2(e, pair(d0, d1), t2);
+        if (!(top <= gate)) {
+          if (top > limit) {
+            flush();
+            raise(s, top, g.c);
+            limit = top + slack;
+            ref = top * g.c;
+            far = !(fabsf(ref) < 16777216.0f);
           }
-        } else {
-          const float2 y = far_sums<kBf16>(in + j * kUnitBytes, s.m, g.c);
-          s.l += y.x;
-          s.t += y.y;
+          if (far) {
+            const float2 y = far_sums<kBf16>(in + j * kUnitBytes, s.m, g.c);
+            s.l += y.x;
+            s.t += y.y;
+          }
+          const int v = v0 + j * kThreads + lane;
+          if (!closed && !opening && !(top <= bound) && u + j < end && v < r.nvec)
+            note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key, bound);
+          set_gate();
         }
-        if (given && (special >> j & 1u) == 0) {
-          const float than = v_id >= w0 ? low : xt;
+        const uint64_t m2 = pair(-ref, -ref);  // (of no use where `far`: flush() drops these terms)
+#pragma unroll
+        for (int i = 0; i < kN; i += 2) {
+          const uint64_t d = fma2(pair(x.at(i), x.at(i + 1)), c2, m2);
+          // (far below the reference, -inf among them, the weight is 0)
+          const float d0 = max_nan(low_of(d), -200.0f), d1 = max_nan(high_of(d), -200.0f);
+          const uint64_t e = pair(exp2_fast(d0), exp2_fast(d1));
+          l2 = add2(l2, e);
+          t2 = fma2(e, pair(d0, d1), t2);
+        }
+        if (kIds && count) {
           if constexpr (kBf16) {
             const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
 #pragma unroll
@@ -556,16 +572,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
             for (int i = 0; i < 4; ++i) s.before += !(x.at(i) <= than);
           }
         }
-        if (!closed && !opening && !(top <= bound)) {
-          const int v = w0 + lane;
-          if (u + j < end && v < r.nvec) note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key);
-        }
+      };
+      if (plain) {
+        const float than = v_id >= v0 ? low : xt;
+#pragma unroll
+        for (int j = 0; j < kRound; ++j) terms(j, true, than);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < kRound; ++j) terms(j, (special >> j & 1u) == 0, v_id >= v0 + j * kThreads ? low : xt);
       }
       if constexpr (kBf16)
         s.before += static_cast<int>(__uint_as_float(above << 16) + __uint_as_float(above & 0xFFFF0000u));
 
-      // ---- the best top_k: the bound is raised after 1, 4, 16 .. rounds
-      if (!closed && (rounds & (rounds - 1)) == 0 && (rounds & 0x55555555) != 0) {
+      // ---- the best top_k: the bound is raised after 1, 4, 16 .. rounds (for many: 1, 2, 4 ..)
+      if (!closed && (rounds & (rounds - 1)) == 0 && (a.top_k >= 16 || (rounds & 0x55555555) != 0)) {
         __syncthreads();
         const int n = sh.noted;
         __syncthreads();
@@ -588,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
 
     // ---- the end of the piece
     flush();
-    const int64_t done_row = row;
+    const int done_row = row;
     const float done_xt = xt;
     const int done_unit = unit;
     left -= end - unit;
@@ -738,14 +758,14 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
   g.shares = (total + g.share - 1) / g.share;
   g.parts = static_cast<Part*>(a.ws);
   const unsigned grid = static_cast<unsigned>(g.shares);
-  static SmemLimit lim[2];
-  cudaError_t e = a.type == WQ_LOGITS_BF16 ? raise_smem_limit(lim[0], logprobs_kernel<true>, c.device, sizeof(Shared))
-                                           : raise_smem_limit(lim[1], logprobs_kernel<false>, c.device, sizeof(Shared));
+  static SmemLimit lim[4];
+  const bool bf16 = a.type == WQ_LOGITS_BF16, ids = a.ids != nullptr;
+  const auto kern = bf16 ? (ids ? logprobs_kernel<true, true> : logprobs_kernel<true, false>)
+                         : (ids ? logprobs_kernel<false, true> : logprobs_kernel<false, false>);
+  cudaError_t e = raise_smem_limit(lim[bf16 * 2 + ids], kern, c.device, sizeof(Shared));
   if (e != cudaSuccess) return e;
-  if (a.type == WQ_LOGITS_BF16) logprobs_kernel<true><<<grid, kThreads, sizeof(Shared), c.stream>>>(g);
-  else logprobs_kernel<false><<<grid, kThreads, sizeof(Shared), c.stream>>>(g);
+  kern<<<grid, kThreads, sizeof(Shared), c.stream>>>(g);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
