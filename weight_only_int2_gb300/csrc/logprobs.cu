@@ -23,7 +23,7 @@
 //    ahead (cp.async), and reads them back itself: no barrier.
 //  - The best top_k are kept as 64-bit keys (logit, then id) in shared memory: the
 //    first round's bound is the top_k'th largest of 32 groups' maxima; later
-//    logits are noted only above the bound, which is raised after 1, 4, 16 ..
+//    logits are noted only above the bound, which is raised after 1, 8 and 64
 //    rounds: a few notes per row in the usual order. Where they do not fit
 //    (ascending rows), the piece's best are found again with a bound for every
 //    round, by bisection over the keys.
@@ -212,7 +212,8 @@ struct Shared {
 
 // Sorts the n <= kNotes noted keys' best top_k to the front (by counting, keys
 // are distinct): 8 to 1 threads a key. All threads; n is the same for all.
-__device__ __forceinline__ void keep_best(Shared& sh, int n, int top_k) {
+// Returns how many are kept.
+__device__ __forceinline__ int keep_best(Shared& sh, int n, int top_k) {
   n = n < kNotes ? n : kNotes;
   const int shift = n <= 32 ? 3 : (n <= 64 ? 2 : (n <= 128 ? 1 : 0)), per = 1 << shift;
   for (int i0 = 0; i0 < n; i0 += kThreads >> shift) {
@@ -228,6 +229,7 @@ __device__ __forceinline__ void keep_best(Shared& sh, int n, int top_k) {
   if (threadIdx.x < kept) sh.notes[threadIdx.x] = sh.best[threadIdx.x];
   if (threadIdx.x == 0) sh.noted = kept;
   __syncthreads();
+  return kept;
 }
 
 // A vector in shared memory with logits id, id + 1 .., which may be its row's
@@ -584,23 +586,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       if constexpr (kBf16)
         s.before += static_cast<int>(__uint_as_float(above << 16) + __uint_as_float(above & 0xFFFF0000u));
 
-      // ---- the best top_k: the bound is raised after 1, 4, 16 .. rounds (for many: 1, 2, 4 ..)
-      if (!closed && (rounds & (rounds - 1)) == 0 && (a.top_k >= 16 || (rounds & 0x55555555) != 0)) {
+      // ---- the best top_k: the bound is raised after some rounds (each raise
+      // costs three barriers, each note above a low bound about 60 instructions)
+      if (!closed && (rounds == 1 || rounds == 8 || rounds == 64 || (a.top_k >= 16 && (rounds == 3 || rounds == 20)))) {
         __syncthreads();
         const int n = sh.noted;
-        __syncthreads();
         if (n > kNotes) {
           closed = lost = true;
+        } else if (keep_best(sh, n, a.top_k) == a.top_k) {
+          bound_key = sh.notes[a.top_k - 1];  // later notes come behind it
+          bound = value_of(static_cast<uint32_t>(bound_key >> 32));
+          closed = bound != bound;  // NaN: nothing that comes later is better
         } else {
-          keep_best(sh, n, a.top_k);
-          if (sh.noted == a.top_k) {
-            bound_key = sh.notes[a.top_k - 1];
-            bound = value_of(static_cast<uint32_t>(bound_key >> 32));
-            closed = bound != bound;  // NaN: nothing that comes later is better
-          } else {
-            closed = lost = u + kRound < end;  // fewer logits than top_k in the round
-          }
-          __syncthreads();
+          closed = lost = u + kRound < end;  // fewer logits than top_k in the round
         }
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -640,11 +638,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
     }
     if (lane == 0) sh.sums[warp] = s;
     __syncthreads();
+    int kept = 0;
     if (a.top_k > 0) {
-      const int n = sh.noted;
-      __syncthreads();
-      if (lost || n > kNotes) best_of<kBf16>(sh, a, done_row, done_unit, end);
-      else keep_best(sh, n, a.top_k);
+      kept = sh.noted;
+      if (lost || kept > kNotes) {
+        best_of<kBf16>(sh, a, done_row, done_unit, end);
+        kept = sh.noted;
+      } else {
+        kept = keep_best(sh, kept, a.top_k);
+      }
     }
     if (warp == 0) {
       s = sh.sums[lane % kWarps];
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
                      __shfl_xor_sync(0xFFFFFFFFu, s.t, o), __shfl_xor_sync(0xFFFFFFFFu, s.before, o)};
         join(s, y, g.c);
       }
-      const uint64_t key = lane < a.top_k && lane < sh.noted ? sh.notes[lane] : 0;
+      const uint64_t key = lane < kept ? sh.notes[lane] : 0;
       if (whole) {
         put(g, done_row, s, key, given, done_xt);
       } else {
@@ -665,8 +667,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       }
     }
     if (left <= 0) return;
-    r.set(a, row);
-    __syncthreads();
+    r.set(a, row);  // (what warp 0 still reads is written again only after the next opening's barrier)
   }
 }
 
