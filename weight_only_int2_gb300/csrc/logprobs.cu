@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 3;
 constexpr int kRound = 4;      // units a block takes at a time
 constexpr int kStages = 3;     // rounds in shared memory
 constexpr int kRowCost = 4;    // what beginning and ending a row costs, in units
@@ -170,16 +170,44 @@ struct Vec {
     const uint4 y = *reinterpret_cast<const uint4*>(p);
     return Vec{{y.x, y.y, y.z, y.w}};
   }
+  // The larger of each pair of words' logits, NaN before all.
+  __device__ __forceinline__ static uint32_t max_word(uint32_t x, uint32_t y) {
+    uint32_t z;
+    if constexpr (kBf16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    else z = __float_as_uint(max_nan(__uint_as_float(x), __uint_as_float(y)));
+    return z;
+  }
+  __device__ __forceinline__ uint32_t max_word() const {
+    return max_word(max_word(w[0], w[1]), max_word(w[2], w[3]));
+  }
+  __device__ __forceinline__ static float top_of(uint32_t x) {
+    if constexpr (kBf16) return max_nan(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+    else return __uint_as_float(x);
+  }
   // The largest, NaN if there is one.
-  __device__ __forceinline__ float top() const {
+  __device__ __forceinline__ float top() const { return top_of(max_word()); }
+  // How many logits of n vectors are above `than` (or NaN).
+  template <int n>
+  __device__ __forceinline__ static int above(const Vec (&x)[n], float than) {
     if constexpr (kBf16) {
-      uint32_t a, b;
-      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[0]), "r"(w[1]));
-      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2]), "r"(w[3]));
-      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
-      return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+      const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
+      uint32_t sum = 0;  // of masks, 0xFFFF for each half that is above
+#pragma unroll
+      for (int j = 0; j < n; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sum += __hgtu2_mask(*reinterpret_cast<const __nv_bfloat162*>(&x[j].w[i]),
+                              *reinterpret_cast<const __nv_bfloat162*>(&than2));
+      // L low and H high ones: sum = (L - H) 2^16 - L
+      const uint32_t low = -sum & 0xFFFFu;
+      return static_cast<int>(low + (low - ((sum + low) >> 16) & 0xFFFFu));
     } else {
-      return max_nan(max_nan(at(0), at(1)), max_nan(at(2), at(3)));
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < n; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c += !(x[j].at(i) <= than);
+      return c;
     }
   }
 };
@@ -267,20 +295,18 @@ __device__ __noinline__ float2 far_sums(const uint8_t* x, float m, float c) {
   return s;
 }
 
-// Notes every logit of the vector in shared memory whose key is at least
-// `least` (no smaller than that of the logit `bound`).
-template <bool kBf16>
-__device__ __noinline__ void note(Shared& sh, const uint8_t* p, uint32_t id, uint32_t V, uint64_t least, float bound) {
-  const Vec<kBf16> x = Vec<kBf16>::from(p);
-#pragma unroll
+// Notes the logits of the vector in shared memory that are above `bound` (or not
+// below it).
+template <bool kBf16, bool kEqual>
+__device__ __noinline__ void note(Shared& sh, const uint8_t* p, uint32_t id, uint32_t V, float bound) {
+#pragma unroll 1
   for (int i = 0; i < Vec<kBf16>::kN; ++i) {
-    const float y = x.at(i);
-    if (y < bound) continue;
-    const uint64_t key = key_of(y, id + i);
-    if (id + i < V && key >= least) {
-      const int to = atomicAdd(&sh.noted, 1);
-      if (to < kNotes) sh.notes[to] = key;
-    }
+    float y;
+    if constexpr (kBf16) y = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i]);
+    else y = reinterpret_cast<const float*>(p)[i];
+    if ((kEqual ? y < bound : y <= bound) || id + i >= V) continue;
+    const int to = atomicAdd(&sh.noted, 1);
+    if (to < kNotes) sh.notes[to] = key_of(y, id + i);
   }
 }
 
@@ -458,7 +484,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       s.t += f * (t - off * l);
       l2 = t2 = 0;
     };
-    uint64_t bound_key = 0;
     bool closed = a.top_k == 0, lost = false;
     if (tid == 0) sh.noted = 0;
 
@@ -512,12 +537,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           }
           const int from = __ffs(__ballot_sync(0xFFFFFFFFu, rank == a.top_k - 1)) - 1;
           const uint32_t least = __shfl_sync(0xFFFFFFFFu, o, from);
-          bound_key = static_cast<uint64_t>(least) << 32;
+          // (NaN: only NaN is as good; noting more does no harm)
+          const float from_here = least == 0xFFFFFFFFu ? CUDART_INF_F : value_of(least);
 #pragma unroll
           for (int j = 0; j < kRound; ++j) {
             const int v = v0 + j * kThreads + lane;
             if (order_of(tops[j]) >= least && u + j < end && v < r.nvec)
-              note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key, value_of(least));
+              note<kBf16, true>(sh, in + j * kUnitBytes, r.id(v, 0), V, from_here);
           }
         }
       }
@@ -527,64 +553,65 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : (closed || opening || limit < bound ? limit : bound);
       };
       set_gate();
-      uint32_t above = 0;  // two bf16 counts, at most 16 each
-      const uint64_t c2 = pair(g.c, g.c);
-      const auto terms = [&](int j, bool count, float than) {
-        const Vec<kBf16> x = Vec<kBf16>::from(in + j * kUnitBytes);
-        const float top = x.top();
-        if (!(top <= gate)) {
-          if (top > limit) {
-            flush();
-            raise(s, top, g.c);
-            limit = top + slack;
-            ref = top * g.c;
-            far = !(fabsf(ref) < 16777216.0f);
-          }
-          if (far) {
+      Vec<kBf16> x[kRound];
+#pragma unroll
+      for (int j = 0; j < kRound; ++j) x[j] = Vec<kBf16>::from(in + j * kUnitBytes);
+      uint32_t word = x[0].max_word();
+#pragma unroll
+      for (int j = 1; j < kRound; ++j) word = Vec<kBf16>::max_word(word, x[j].max_word());
+      const float top = Vec<kBf16>::top_of(word);
+      if (!(top <= gate)) {
+        if (top > limit) {
+          flush();
+          raise(s, top, g.c);
+          limit = top + slack;
+          ref = top * g.c;
+          far = !(fabsf(ref) < 16777216.0f);
+        }
+        if (far) {
+#pragma unroll 1
+          for (int j = 0; j < kRound; ++j) {
             const float2 y = far_sums<kBf16>(in + j * kUnitBytes, s.m, g.c);
             s.l += y.x;
             s.t += y.y;
           }
-          const int v = v0 + j * kThreads + lane;
-          if (!closed && !opening && !(top <= bound) && u + j < end && v < r.nvec)
-            note<kBf16>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound_key, bound);
-          set_gate();
         }
-        const uint64_t m2 = pair(-ref, -ref);  // (of no use where `far`: flush() drops these terms)
-#pragma unroll
-        for (int i = 0; i < kN; i += 2) {
-          const uint64_t d = fma2(pair(x.at(i), x.at(i + 1)), c2, m2);
-          // (far below the reference, -inf among them, the weight is 0)
-          const float d0 = max_nan(low_of(d), -200.0f), d1 = max_nan(high_of(d), -200.0f);
-          const uint64_t e = pair(exp2_fast(d0), exp2_fast(d1));
-          l2 = add2(l2, e);
-          t2 = fma2(e, pair(d0, d1), t2);
-        }
-        if (kIds && count) {
-          if constexpr (kBf16) {
-            const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t y;
-              asm("set.gtu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x.w[i]), "r"(than2));
-              asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(above) : "r"(y));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s.before += !(x.at(i) <= than);
+        if (!closed && !opening && !(top <= bound)) {
+#pragma unroll 1
+          for (int j = 0; j < kRound; ++j) {
+            const int v = v0 + j * kThreads + lane;
+            if (u + j < end && v < r.nvec && !(Vec<kBf16>::from(in + j * kUnitBytes).top() <= bound))
+              note<kBf16, false>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound);
           }
         }
-      };
-      if (plain) {
-        const float than = v_id >= v0 ? low : xt;
-#pragma unroll
-        for (int j = 0; j < kRound; ++j) terms(j, true, than);
-      } else {
-#pragma unroll 1
-        for (int j = 0; j < kRound; ++j) terms(j, (special >> j & 1u) == 0, v_id >= v0 + j * kThreads ? low : xt);
       }
-      if constexpr (kBf16)
-        s.before += static_cast<int>(__uint_as_float(above << 16) + __uint_as_float(above & 0xFFFF0000u));
+      {
+        const uint64_t c2 = pair(g.c, g.c), m2 = pair(-ref, -ref);  // (of no use where `far`: flush() drops these)
+#pragma unroll
+        for (int j = 0; j < kRound; ++j)
+#pragma unroll
+          for (int i = 0; i < kN; i += 2) {
+            const uint64_t d = fma2(pair(x[j].at(i), x[j].at(i + 1)), c2, m2);
+            // (far below the reference, -inf among them, the weight is 0)
+            const uint64_t near = pair(max_nan(low_of(d), -200.0f), max_nan(high_of(d), -200.0f));
+            const uint64_t e = pair(exp2_fast(low_of(near)), exp2_fast(high_of(near)));
+            l2 = add2(l2, e);
+            t2 = fma2(e, near, t2);
+          }
+      }
+      if constexpr (kIds) {
+        if (plain) {
+          s.before += Vec<kBf16>::template above<kRound>(x, v_id >= v0 ? low : xt);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kRound; ++j) {
+            if ((special >> j & 1u) != 0) continue;
+            const Vec<kBf16> y[1] = {Vec<kBf16>::from(in + j * kUnitBytes)};
+            s.before += Vec<kBf16>::template above<1>(y, v_id >= v0 + j * kThreads ? low : xt);
+          }
+        }
+      }
+
 
       // ---- the best top_k: the bound is raised after some rounds (each raise
       // costs three barriers, each note above a low bound about 60 instructions)
@@ -594,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         if (n > kNotes) {
           closed = lost = true;
         } else if (keep_best(sh, n, a.top_k) == a.top_k) {
-          bound_key = sh.notes[a.top_k - 1];  // later notes come behind it
-          bound = value_of(static_cast<uint32_t>(bound_key >> 32));
+          // (equal ones that come later are behind it)
+          bound = value_of(static_cast<uint32_t>(sh.notes[a.top_k - 1] >> 32));
           closed = bound != bound;  // NaN: nothing that comes later is better
         } else {
           closed = lost = u + kRound < end;  // fewer logits than top_k in the round
