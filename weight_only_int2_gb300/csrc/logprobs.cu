@@ -186,28 +186,26 @@ struct Vec {
   }
   // The largest, NaN if there is one.
   __device__ __forceinline__ float top() const { return top_of(max_word()); }
-  // How many logits of n vectors are above `than` (or NaN).
-  template <int n>
-  __device__ __forceinline__ static int above(const Vec (&x)[n], float than) {
+  // Adds how many logits are above `than` (or NaN): for bf16 a sum of masks,
+  // 0xFFFF for each half that is above, that count_of() takes apart.
+  __device__ __forceinline__ void add_above(float than, uint32_t& sum) const {
     if constexpr (kBf16) {
       const uint32_t than2 = __byte_perm(__float_as_uint(than), 0u, 0x3232);
-      uint32_t sum = 0;  // of masks, 0xFFFF for each half that is above
 #pragma unroll
-      for (int j = 0; j < n; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sum += __hgtu2_mask(*reinterpret_cast<const __nv_bfloat162*>(&x[j].w[i]),
-                              *reinterpret_cast<const __nv_bfloat162*>(&than2));
-      // L low and H high ones: sum = (L - H) 2^16 - L
-      const uint32_t low = -sum & 0xFFFFu;
-      return static_cast<int>(low + (low - ((sum + low) >> 16) & 0xFFFFu));
+      for (int i = 0; i < 4; ++i)
+        sum += __hgtu2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                            *reinterpret_cast<const __nv_bfloat162*>(&than2));
     } else {
-      int c = 0;
 #pragma unroll
-      for (int j = 0; j < n; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c += !(x[j].at(i) <= than);
-      return c;
+      for (int i = 0; i < 4; ++i) sum += !(at(i) <= than);
+    }
+  }
+  __device__ __forceinline__ static int count_of(uint32_t sum) {
+    if constexpr (kBf16) {  // L low and H high ones, below 2^16: sum = (L - H) 2^16 - L
+      const uint32_t low = -sum & 0xFFFFu, high = (low - ((sum + low) >> 16)) & 0xFFFFu;
+      return static_cast<int>(low + high);
+    } else {
+      return static_cast<int>(sum);
     }
   }
 };
@@ -412,24 +410,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
   constexpr int kUnitBytes = kThreads * 16, kStageBytes = kRound * kUnitBytes;
   Row<kBf16> lr = r;
   int l_row = row, l_left = left, l_unit = unit;
+  const uint8_t* l_src = nullptr;  // of the next round, where it is known to be a whole one
+  const auto copy = [&](const uint8_t* src, int stage, int j, int bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(mine_s + stage * kStageBytes +
+                                                                                j * kUnitBytes),
+                 "l"(src + j * kUnitBytes), "r"(bytes)
+                 : "memory");
+  };
   auto copy_round = [&](int stage) {
     if (l_left > 0) {
       const int end = g.units - l_unit < l_left ? g.units : l_unit + l_left;
       const int row_end = (lr.head + static_cast<int>(V & 7)) * kElem & 15;  // bytes of the last vector, 0: all
       const uint8_t* src = lr.base + (static_cast<int64_t>(l_unit) * kThreads + tid) * 16;
-      const auto copy = [&](int j, int bytes) {
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(mine_s + stage * kStageBytes +
-                                                                                    j * kUnitBytes),
-                     "l"(src + j * kUnitBytes), "r"(bytes)
-                     : "memory");
-      };
       if (l_unit + kRound <= end && (l_unit + kRound) * kThreads < lr.nvec) {
 #pragma unroll
-        for (int j = 0; j < kRound; ++j) copy(j, 16);
+        for (int j = 0; j < kRound; ++j) copy(src, stage, j, 16);
       } else {
         for (int j = 0; j < kRound; ++j) {
           const int v = (l_unit + j) * kThreads + tid;
-          if (l_unit + j < end && v < lr.nvec) copy(j, v == lr.nvec - 1 && row_end != 0 ? row_end : 16);  // not past the row
+          if (l_unit + j < end && v < lr.nvec) copy(src, stage, j, v == lr.nvec - 1 && row_end != 0 ? row_end : 16);  // not past the row
         }
       }
       const int n = end - l_unit < kRound ? end - l_unit : kRound;
@@ -486,25 +485,73 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
     };
     bool closed = a.top_k == 0, lost = false;
     if (tid == 0) sh.noted = 0;
+    // logits this far below the reference (-inf among them) have weight 0; they
+    // count as this one, so that every term is finite
+    uint32_t floor_word = 0;
+    const auto set_floor = [&]() {
+      const float f = (s.m == -CUDART_INF_F ? 0.0f : s.m) - 160.0f / g.c;
+      floor_word = __float_as_uint(f);
+      if constexpr (kBf16) {  // rounded down
+        floor_word += (floor_word >> 31) != 0 ? 0xFFFFu : 0u;
+        floor_word = __byte_perm(floor_word, 0u, 0x3232);
+      }
+    };
+    set_floor();
+    // whole rounds without a special vector that follow, for which also the copy
+    // is a whole round's; the logit to compare theirs with
+    int fast = 0;
+    float than_fast = xt;
+    uint32_t above = 0;
 
     for (int u = unit, rounds = 1; u < end; u += kRound, ++rounds) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      copy_round(stage == 0 ? kStages - 1 : stage - 1);  // read in the round before
       uint8_t* in = mine + stage * kStageBytes;
-      const int v0 = u * kThreads + warp * 32;
-      // the row's first and last vector, the given token's, and what lies
-      // outside the piece: logit by logit, by the warp that has it
+      const int v0 = u * kThreads + warp * 32, freed = stage == 0 ? kStages - 1 : stage - 1;  // read in the round before
       unsigned special = 0;
-      const bool plain = v0 > 0 && v0 + (kRound - 1) * kThreads + 32 < r.nvec && u + kRound <= end &&
-                         (v_id < v0 || v_id >= v0 + (kRound - 1) * kThreads + 32) && xt == xt;
-      if (!plain) {
-        for (int j = 0; j < kRound; ++j) {
-          const int w0 = v0 + j * kThreads, v = w0 + lane;
-          if (w0 > 0 && w0 + 32 < r.nvec && u + j < end && (v_id < w0 || v_id >= w0 + 32) && xt == xt) continue;
-          special |= 1u << j;
-          const uint32_t id0 = u + j < end && v < r.nvec ? r.id(v, 0) : 0xFFFFFF00u;  // none: above any V
-          s.before += look_closer<kBf16>(in + j * kUnitBytes, id0, V, key_t);
+      bool plain = true;
+      float than = than_fast;
+      if (fast > 0) {
+        --fast;
+#pragma unroll
+        for (int j = 0; j < kRound; ++j) copy(l_src, freed, j, 16);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        l_src += kStageBytes;
+        l_unit += kRound;
+        l_left -= kRound;
+      } else {
+        copy_round(freed);
+        // the row's first and last vector, the given token's, and what lies
+        // outside the piece: logit by logit, by the warp that has it
+        plain = v0 > 0 && v0 + (kRound - 1) * kThreads + 32 < r.nvec && u + kRound <= end &&
+                (v_id < v0 || v_id >= v0 + (kRound - 1) * kThreads + 32) && xt == xt;
+        than = v_id >= v0 ? low : xt;
+        if (!plain) {
+          for (int j = 0; j < kRound; ++j) {
+            const int w0 = v0 + j * kThreads, v = w0 + lane;
+            if (w0 > 0 && w0 + 32 < r.nvec && u + j < end && (v_id < w0 || v_id >= w0 + 32) && xt == xt) continue;
+            special |= 1u << j;
+            const uint32_t id0 = u + j < end && v < r.nvec ? r.id(v, 0) : 0xFFFFFF00u;  // none: above any V
+            s.before += look_closer<kBf16>(in + j * kUnitBytes, id0, V, key_t);
+          }
+          if constexpr (kIds) {
+            for (int j = 0; j < kRound; ++j)
+              if ((special >> j & 1u) == 0)
+                Vec<kBf16>::from(in + j * kUnitBytes).add_above(v_id >= v0 + j * kThreads ? low : xt, above);
+          }
         }
+        const int u2 = u + kRound, l_end = g.units - l_unit < l_left ? g.units : l_unit + l_left;
+        const int whole = (r.nvec - 1) / kThreads, l_whole = (lr.nvec - 1) / kThreads;
+        fast = ((end < whole ? end : whole) - u2) / kRound;
+        const int l_fast = l_left > 0 ? ((l_end < l_whole ? l_end : l_whole) - l_unit) / kRound : 0;
+        fast = fast < l_fast ? fast : l_fast;
+        than_fast = xt;
+        if (v_id >= u2 * kThreads) {
+          than_fast = low;
+          const int to_id = (v_id / kThreads - u2) / kRound;
+          fast = fast < to_id ? fast : to_id;
+        }
+        if (xt != xt) fast = 0;
+        l_src = lr.base + (static_cast<int64_t>(l_unit) * kThreads + tid) * 16;
       }
       if (rounds == 1) {
         // The opening: the largest logit of the block's round is everyone's first
@@ -527,7 +574,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           limit = top + slack;
           ref = top * g.c;
           far = !(fabsf(ref) < 16777216.0f);
+          set_floor();
         }
+        // far: always; before there is a reference, and for NaN: always; in the
+        // opening the notes are taken already
+        gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : limit;
         if (!closed) {
           int rank = 0;
 #pragma unroll
@@ -547,12 +598,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           }
         }
       }
-      const bool opening = rounds == 1;
       const auto set_gate = [&]() {
-        // far: always; before there is a reference, and for NaN: always
-        gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : (closed || opening || limit < bound ? limit : bound);
+        gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : (closed || limit < bound ? limit : bound);
       };
-      set_gate();
       Vec<kBf16> x[kRound];
 #pragma unroll
       for (int j = 0; j < kRound; ++j) x[j] = Vec<kBf16>::from(in + j * kUnitBytes);
@@ -567,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           limit = top + slack;
           ref = top * g.c;
           far = !(fabsf(ref) < 16777216.0f);
+          set_floor();
         }
         if (far) {
 #pragma unroll 1
@@ -576,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
             s.t += y.y;
           }
         }
-        if (!closed && !opening && !(top <= bound)) {
+        if (!closed && rounds > 1 && !(top <= bound)) {
 #pragma unroll 1
           for (int j = 0; j < kRound; ++j) {
             const int v = v0 + j * kThreads + lane;
@@ -584,34 +633,31 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
               note<kBf16, false>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound);
           }
         }
+        set_gate();
+      }
+      if (kIds && plain) {
+#pragma unroll
+        for (int j = 0; j < kRound; ++j) x[j].add_above(than, above);
       }
       {
         const uint64_t c2 = pair(g.c, g.c), m2 = pair(-ref, -ref);  // (of no use where `far`: flush() drops these)
 #pragma unroll
-        for (int j = 0; j < kRound; ++j)
+        for (int j = 0; j < kRound; ++j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[j].w[i] = Vec<kBf16>::max_word(x[j].w[i], floor_word);
 #pragma unroll
           for (int i = 0; i < kN; i += 2) {
             const uint64_t d = fma2(pair(x[j].at(i), x[j].at(i + 1)), c2, m2);
-            // (far below the reference, -inf among them, the weight is 0)
-            const uint64_t near = pair(max_nan(low_of(d), -200.0f), max_nan(high_of(d), -200.0f));
-            const uint64_t e = pair(exp2_fast(low_of(near)), exp2_fast(high_of(near)));
+            const uint64_t e = pair(exp2_fast(low_of(d)), exp2_fast(high_of(d)));
             l2 = add2(l2, e);
-            t2 = fma2(e, near, t2);
-          }
-      }
-      if constexpr (kIds) {
-        if (plain) {
-          s.before += Vec<kBf16>::template above<kRound>(x, v_id >= v0 ? low : xt);
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < kRound; ++j) {
-            if ((special >> j & 1u) != 0) continue;
-            const Vec<kBf16> y[1] = {Vec<kBf16>::from(in + j * kUnitBytes)};
-            s.before += Vec<kBf16>::template above<1>(y, v_id >= v0 + j * kThreads ? low : xt);
+            t2 = fma2(e, d, t2);
           }
         }
       }
-
+      if ((rounds & 1023) == 0) {  // before the counts of 16 a round pass 16 bits
+        s.before += Vec<kBf16>::count_of(above);
+        above = 0;
+      }
 
       // ---- the best top_k: the bound is raised after some rounds (each raise
       // costs three barriers, each note above a low bound about 60 instructions)
@@ -627,12 +673,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         } else {
           closed = lost = u + kRound < end;  // fewer logits than top_k in the round
         }
+        set_gate();
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
     // ---- the end of the piece
     flush();
+    s.before += Vec<kBf16>::count_of(above);
     const int done_row = row;
     const float done_xt = xt;
     const int done_unit = unit;

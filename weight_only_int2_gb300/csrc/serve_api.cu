@@ -271,9 +271,8 @@ wq_status token_logprobs(const void* logits, int logits_type, int64_t ld, int64_
   if (ld < V || ld > kMaxDim) return fail(WQ_EINVAL, "ld must be in V..2^31-1 (got %lld)", (long long)ld);
   if (top_k < 0 || top_k > kMaxTopK || top_k > V)
     return fail(WQ_EINVAL, "top_k must be in 0..min(%d, V) (got %d)", kMaxTopK, top_k);
-  if (!(temperature > 0.0f) || !std::isfinite(temperature))
-    return fail(WQ_EINVAL, "temperature must be positive and finite");
-  if (!std::isfinite(1.0f / temperature)) return fail(WQ_EINVAL, "1 / temperature must be finite");
+  if (!(temperature >= 1e-30f && temperature <= 1e30f))
+    return fail(WQ_EINVAL, "temperature must be in 1e-30..1e30 (got %g)", static_cast<double>(temperature));
   if (T == 0) return WQ_OK;
   WQ_PTR(logits);
   if (ids != nullptr) {
