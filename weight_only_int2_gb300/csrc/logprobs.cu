@@ -23,7 +23,7 @@
 //    ahead (cp.async), and reads them back itself: no barrier.
 //  - The best top_k are kept as 64-bit keys (logit, then id) in shared memory: the
 //    first round's bound is the top_k'th largest of 32 groups' maxima; later
-//    logits are noted only above the bound, which is raised after 1, 8 and 64
+//    logits are noted only above the bound, which is raised after 1, 2, 4 ..
 //    rounds: a few notes per row in the usual order. Where they do not fit
 //    (ascending rows), the piece's best are found again with a bound for every
 //    round, by bisection over the keys.
@@ -293,19 +293,11 @@ __device__ __noinline__ float2 far_sums(const uint8_t* x, float m, float c) {
   return s;
 }
 
-// Notes the logits of the vector in shared memory that are above `bound` (or not
-// below it).
-template <bool kBf16, bool kEqual>
-__device__ __noinline__ void note(Shared& sh, const uint8_t* p, uint32_t id, uint32_t V, float bound) {
-#pragma unroll 1
-  for (int i = 0; i < Vec<kBf16>::kN; ++i) {
-    float y;
-    if constexpr (kBf16) y = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i]);
-    else y = reinterpret_cast<const float*>(p)[i];
-    if ((kEqual ? y < bound : y <= bound) || id + i >= V) continue;
-    const int to = atomicAdd(&sh.noted, 1);
-    if (to < kNotes) sh.notes[to] = key_of(y, id + i);
-  }
+// Notes a logit of the row.
+__device__ __noinline__ void note(Shared& sh, float x, uint32_t id, uint32_t V) {
+  if (id >= V) return;
+  const int to = atomicAdd(&sh.noted, 1);
+  if (to < kNotes) sh.notes[to] = key_of(x, id);
 }
 
 // The best top_k of units [unit, end) of a row, in whatever order they come:
@@ -590,11 +582,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           const uint32_t least = __shfl_sync(0xFFFFFFFFu, o, from);
           // (NaN: only NaN is as good; noting more does no harm)
           const float from_here = least == 0xFFFFFFFFu ? CUDART_INF_F : value_of(least);
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < kRound; ++j) {
             const int v = v0 + j * kThreads + lane;
-            if (order_of(tops[j]) >= least && u + j < end && v < r.nvec)
-              note<kBf16, true>(sh, in + j * kUnitBytes, r.id(v, 0), V, from_here);
+            const Vec<kBf16> x = Vec<kBf16>::from(in + j * kUnitBytes);
+            if (x.top() < from_here || u + j >= end || v >= r.nvec) continue;
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (!(x.at(i) < from_here)) note(sh, x.at(i), r.id(v, i), V);
           }
         }
       }
@@ -626,11 +621,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           }
         }
         if (!closed && rounds > 1 && !(top <= bound)) {
-#pragma unroll 1
+          // (what lies outside the piece is -inf: not above any bound)
+#pragma unroll
           for (int j = 0; j < kRound; ++j) {
-            const int v = v0 + j * kThreads + lane;
-            if (u + j < end && v < r.nvec && !(Vec<kBf16>::from(in + j * kUnitBytes).top() <= bound))
-              note<kBf16, false>(sh, in + j * kUnitBytes, r.id(v, 0), V, bound);
+            if (x[j].top() <= bound) continue;
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (!(x[j].at(i) <= bound)) note(sh, x[j].at(i), r.id(v0 + j * kThreads + lane, i), V);
           }
         }
         set_gate();
@@ -659,9 +656,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         above = 0;
       }
 
-      // ---- the best top_k: the bound is raised after some rounds (each raise
-      // costs three barriers, each note above a low bound about 60 instructions)
-      if (!closed && (rounds == 1 || rounds == 8 || rounds == 64 || (a.top_k >= 16 && (rounds == 3 || rounds == 20)))) {
+      // ---- the best top_k: the bound is raised after 1, 2, 4 .. rounds (a raise
+      // costs a block about ten notes, and twice the logits bring top_k notes)
+      if (!closed && (rounds & (rounds - 1)) == 0) {
         __syncthreads();
         const int n = sh.noted;
         if (n > kNotes) {
