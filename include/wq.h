@@ -397,7 +397,7 @@ size_t token_logprobs_workspace_bytes(int64_t T, int64_t V, int top_k);
  *              float32, top_ids [T, top_k] int32 (not NULL when top_k > 0);
  *              entropy may be NULL.
  *  top_k       0 .. min(32, V);  temperature 1e-30 .. 1e30.
- *  workspace   as kv_attn_decode's, its own.
+ *  workspace   as kv_attn_decode's.
  * -inf logits have no probability and add nothing; a row of nothing but -inf
  * has log probabilities -inf and entropy 0. A row with NaN or +inf has NaN for
  * its numbers; NaN comes first in the order, all NaN being equal, as are 0.0

@@ -84,6 +84,8 @@ _lib_lock = threading.Lock()
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Loads libwq.so (once) and attaches the C signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -95,7 +97,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
-            _lib = lib
+            _lib = lib  # complete before another thread can see it
         return _lib
 
 
@@ -120,11 +122,21 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+# The current device and stream as numbers: what torch.cuda.current_stream()
+# wraps, at a fraction of its cost (a small call takes as long on the host as on
+# the GPU).
+def _device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None) -> None:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -146,11 +158,15 @@ _ws_lock = threading.Lock()
 def _cached(kind: str, nbytes: int, device=None) -> torch.Tensor | None:
     if nbytes == 0:
         return None
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    key = (kind, dev.index, _stream())
+    index = _device() if device is None else torch.device(device).index
+    key = (kind, index, _stream())
+    buf = _ws_cache.get(key)
+    if buf is not None and buf.numel() >= nbytes:
+        return buf
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
+            dev = "cuda" if index is None else torch.device("cuda", index)
             buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
             _ws_cache[key] = buf
         return buf
@@ -618,7 +634,7 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
     top_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     lib = load()
     if ws is None:
-        ws = _cached("logprobs", lib.token_logprobs_workspace_bytes(T, V, k))
+        ws = scratch(lib.token_logprobs_workspace_bytes(T, V, k))
     _check(lib.token_logprobs(_ptr(logits), _LOGIT_TYPES[logits.dtype], V if T <= 1 else logits.stride(0), T, V,
                               _ptr(ids), temperature, top_k, _ptr(lp), _ptr(rank), _ptr(entropy), _ptr(top),
                               _ptr(top_ids), _ptr(bad_count), _ptr(ws),
