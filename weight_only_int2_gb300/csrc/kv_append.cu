@@ -1,5 +1,17 @@
 // Writes new keys and values into the pages of a paged cache (bf16 as they
 // are, or rounded to e4m3 with a scale per key head).
+//
+// Bound: a token's place takes three loads one after the other (its sequence and
+// position, then the page id), so a few tokens cost that latency, and many the
+// read and the write of their values, if enough of them are on their way: a
+// thread loads its values before it knows where they go, and with many tokens it
+// has four of them at once (one each, 75 MB took 34.5 us: the chain, ten waves of
+// blocks long).
+//
+// The e4m3 code is that of the IEEE quotient x / w. With y = RN(1 / w),
+// q = RN(x y) and r = x - q w (exact in one fma), RN(q + r y) is the correctly
+// rounded quotient (Markstein, IBM J. Res. Dev. 34(1), 1990); x is clamped to
+// +-500 w first, beyond the largest code, so that nothing overflows on the way.
 #include "wq_device.cuh"
 #include "wq_internal.h"
 
@@ -10,55 +22,82 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ float clamp_nan(float x, float lim) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(lim));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(-lim));
+  return y;
 }
 
-// One thread per 8 values: chunk i of token t, keys first.
-template <bool kE4m3>
+// Two bf16 numbers (the halves of p) over w as two e4m3 codes; y = RN(1 / w).
+__device__ __forceinline__ uint32_t codes_of(uint32_t p, float w, float y, float lim) {
+  float q[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float x = clamp_nan(__uint_as_float(i ? p & 0xFFFF0000u : p << 16), lim), z = __fmul_rn(x, y);
+    q[i] = copysignf(__fmaf_rn(__fmaf_rn(-z, w, x), y, z), z);  // (-0.0 stays)
+  }
+  return __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+}
+
+// One thread per 16 bytes of the cache (8 bf16 values or 16 codes) of kTokens
+// tokens in a row: chunk i of a token, keys first.
+template <bool kE4m3, int kTokens>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCache a, const uint16_t* __restrict__ k,
                                                             const uint16_t* __restrict__ v, int64_t k_stride,
                                                             int64_t v_stride, int64_t T,
                                                             const int32_t* __restrict__ seq,
                                                             const int32_t* __restrict__ pos,
                                                             int32_t* __restrict__ bad) {
-  const int row = static_cast<int>(a.Hkv * a.D / 8);  // chunks of a token's keys
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t t = u / (2 * row);
-  if (t >= T) return;
-  const int i = static_cast<int>(u - t * 2 * row);
-  const int side = i >= row, at = i - side * row;
+  constexpr int kValues = kE4m3 ? 16 : 8, kLoads = kValues / 8;
+  const uint32_t per_head = static_cast<uint32_t>(a.D) / kValues, row = static_cast<uint32_t>(a.Hkv) * per_head;
+  // (a block's first thread divides in 64 bits, the others add)
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads, g0 = u0 / (2 * row);
+  const uint32_t in = static_cast<uint32_t>(u0 - g0 * 2 * row) + threadIdx.x;
+  const int64_t t0 = (g0 + in / (2 * row)) * kTokens;
+  if (t0 >= T) return;
+  const uint32_t i = in % (2 * row), side = i >= row, at = i - side * row, h = at / per_head, d = (at - h * per_head) * kValues;
 
-  const int64_t s = seq != nullptr ? seq[t] : t;
-  const int64_t p = pos[t];
-  int64_t page = -1;
-  if (s >= 0 && s < a.B && p >= 0 && p < a.W * a.S) page = a.table[s * a.W + p / a.S];
-  if (page < 0 || page >= a.P) {
-    if (i == 0 && bad != nullptr) atomicAdd(bad, 1);
-    return;
+  uint4 x[kTokens][kLoads];
+  int64_t s[kTokens], p[kTokens];
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    s[j] = p[j] = -1;
+    if (t0 + j >= T) continue;
+    s[j] = seq != nullptr ? seq[t0 + j] : t0 + j;
+    p[j] = pos[t0 + j];
+    const uint16_t* src = side ? v + (t0 + j) * v_stride : k + (t0 + j) * k_stride;
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) x[j][l] = __ldcs(reinterpret_cast<const uint4*>(src + h * a.D + d) + l);
   }
-  const int per_head = static_cast<int>(a.D / 8);
-  const int h = at / per_head, d = (at - h * per_head) * 8;
-  const uint16_t* src = side ? v + t * v_stride : k + t * k_stride;
-  const uint4 x = *reinterpret_cast<const uint4*>(src + h * a.D + d);
-  const int64_t dst = (((page * 2 + side) * a.Hkv + h) * a.S + p % a.S) * a.D + d;
-  if constexpr (!kE4m3) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.kv) + dst) = x;
-  } else {
-    const float w = side ? a.v_scale[h] : a.k_scale[h];
-    const uint32_t r[4] = {x.x, x.y, x.z, x.w};
-    uint32_t o[2];
+  int64_t page[kTokens];
+  const uint32_t S = static_cast<uint32_t>(a.S);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t b[2];
+  for (int j = 0; j < kTokens; ++j) {
+    page[j] = -1;
+    if (s[j] >= 0 && s[j] < a.B && p[j] >= 0 && p[j] < a.W * a.S) page[j] = a.table[s[j] * a.W + static_cast<uint32_t>(p[j]) / S];
+  }
+  float w = 1.0f;
+  if constexpr (kE4m3) w = side ? a.v_scale[h] : a.k_scale[h];
+  const float y = __frcp_rn(w), lim = fminf(500.0f * w, 3.0e38f);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t y = r[2 * j + e];
-        b[e] = e4m3x2(__fdiv_rn(__uint_as_float(y << 16), w), __fdiv_rn(__uint_as_float(y & 0xFFFF0000u), w));
-      }
-      o[j] = b[0] | (b[1] << 16);
+  for (int j = 0; j < kTokens; ++j) {
+    if (page[j] < 0 || page[j] >= a.P) {
+      if (i == 0 && bad != nullptr && t0 + j < T) atomicAdd(bad, 1);
+      continue;
     }
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.kv) + dst) = make_uint2(o[0], o[1]);
+    const int64_t dst = (((page[j] * 2 + side) * a.Hkv + h) * a.S + static_cast<uint32_t>(p[j]) % S) * a.D + d;
+    if constexpr (!kE4m3) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.kv) + dst) = x[j][0];
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        o[2 * l] = codes_of(x[j][l].x, w, y, lim) | codes_of(x[j][l].y, w, y, lim) << 16;
+        o[2 * l + 1] = codes_of(x[j][l].z, w, y, lim) | codes_of(x[j][l].w, w, y, lim) << 16;
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.kv) + dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
@@ -66,15 +105,15 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCache a, co
 
 cudaError_t launch_kv_append(const Ctx& c, const KvCache& a, const uint16_t* k, const uint16_t* v, int64_t k_stride,
                              int64_t v_stride, int64_t T, const int32_t* seq, const int32_t* pos, int32_t* bad) {
-  const int64_t chunks = T * 2 * (a.Hkv * a.D / 8);
-  const int64_t grid = (chunks + kThreads - 1) / kThreads;
+  const bool e4m3 = a.type == WQ_KV_E4M3;
+  const int64_t chunks = 2 * a.Hkv * a.D / (e4m3 ? 16 : 8);
+  // four tokens a thread once every SM has its eight blocks
+  const bool many = T * chunks > int64_t{8} * kThreads * c.sm_count;
+  const int64_t grid = ((many ? (T + 3) / 4 : T) * chunks + kThreads - 1) / kThreads;
   if (grid > kMaxDim) return cudaErrorInvalidConfiguration;
-  if (a.type == WQ_KV_E4M3)
-    kv_append_kernel<true><<<static_cast<unsigned>(grid), kThreads, 0, c.stream>>>(a, k, v, k_stride, v_stride, T,
-                                                                                  seq, pos, bad);
-  else
-    kv_append_kernel<false><<<static_cast<unsigned>(grid), kThreads, 0, c.stream>>>(a, k, v, k_stride, v_stride, T,
-                                                                                   seq, pos, bad);
+  const auto kern = e4m3 ? (many ? kv_append_kernel<true, 4> : kv_append_kernel<true, 1>)
+                         : (many ? kv_append_kernel<false, 4> : kv_append_kernel<false, 1>);
+  kern<<<static_cast<unsigned>(grid), kThreads, 0, c.stream>>>(a, k, v, k_stride, v_stride, T, seq, pos, bad);
   return cudaGetLastError();
 }
 

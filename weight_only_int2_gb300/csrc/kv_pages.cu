@@ -162,10 +162,11 @@ __device__ __forceinline__ int rank_of(uint32_t bits, int i, int& seen) {
   return r;
 }
 
-// The first `want` free pages in ascending order, into ids; returns how many
-// there are (at most want). Ends with a barrier of the cluster.
-__device__ int64_t find_free(Team& team, const int32_t* ref, int64_t P, int64_t want, int32_t* ids) {
-  int64_t got = 0;
+// The free pages in ascending order, into ids: as many as *asked, which block 0
+// writes before the call. Returns how many there are (at most *asked). Ends with
+// a barrier of the cluster; whatever was written before it is seen after it.
+__device__ int64_t find_free(Team& team, const int32_t* ref, int64_t P, const int64_t* asked, int32_t* ids) {
+  int64_t got = 0, want = 1;  // (known after the first pass's barrier)
   for (int64_t p0 = 0; p0 < P && got < want; p0 += static_cast<int64_t>(kAll) * kPer) {
     int64_t first;
     uint32_t there;
@@ -173,6 +174,7 @@ __device__ int64_t find_free(Team& team, const int32_t* ref, int64_t P, int64_t 
     const int mine = __reduce_add_sync(0xFFFFFFFFu, __popc(free));
     uint64_t all;
     const int64_t r0 = got + static_cast<int64_t>(team.before(mine, &all));
+    want = __ldcg(asked);
     int seen = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -189,6 +191,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
     fork_kernel(SeqTables t, const int32_t* parent, const int32_t* child, int n, int32_t* table_out,
                 int32_t* lens_out, int32_t* ref_out, int32_t* granted, Scratch w) {
   WQ_TEAM(team);
+  cl::cluster_arrive();
   cl::griddep_launch_dependents();  // the copy may start; it waits for this kernel's end
   const int64_t cap = t.W * t.S;
   auto good = [&](int i) {
@@ -219,9 +222,9 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
   }
   copy_array(team, t.ref, ref_out, t.P);
   copy_array(team, t.table, table_out, t.B * t.W);
-  team.sync();
   copy_array(team, t.lens, lens_out, t.B);
-  const int64_t have = find_free(team, t.ref, t.P, __ldcg(w.asked), w.ids);
+  cl::cluster_wait();  // every block runs, before the first store into another's shared memory
+  const int64_t have = find_free(team, t.ref, t.P, w.asked, w.ids);
   const int lane = threadIdx.x & 31;
   for (int i = team.rank * kMetaWarps + (threadIdx.x >> 5); i < n; i += kBlocks * kMetaWarps) {  // a warp per pair
     const bool ok0 = good(i);
@@ -257,6 +260,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
     reserve_kernel(SeqTables t, const int32_t* new_lens, int32_t* table_out, int32_t* ref_out, int32_t* granted,
                    Scratch w) {
   WQ_TEAM(team);
+  cl::cluster_arrive();
   const int64_t cap = t.W * t.S;
   auto needs = [&](int64_t b) -> int64_t {
     if (new_lens[b] > cap) return 0;
@@ -277,8 +281,8 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
   }
   copy_array(team, t.ref, ref_out, t.P);
   copy_array(team, t.table, table_out, t.B * t.W);
-  team.sync();
-  const int64_t have = find_free(team, t.ref, t.P, __ldcg(w.asked), w.ids);
+  cl::cluster_wait();  // every block runs, before the first store into another's shared memory
+  const int64_t have = find_free(team, t.ref, t.P, w.asked, w.ids);
   const int lane = threadIdx.x & 31;
   for (int64_t b = team.rank * kMetaWarps + (threadIdx.x >> 5); b < t.B; b += kBlocks * kMetaWarps) {
     const int64_t need = needs(b), o = __ldcg(w.off + b);
@@ -298,25 +302,35 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
     free_kernel(SeqTables t, const int32_t* seqs, int64_t n, int32_t* lens_out, int32_t* ref_out, int32_t* bad) {
   WQ_TEAM(team);
+  const int lane = threadIdx.x & 31;
   copy_array(team, t.ref, ref_out, t.P);
   copy_array(team, t.lens, lens_out, t.B);
+  // a warp per sequence; the first one's pages are on their way before the barrier
+  int64_t i = team.rank * kMetaWarps + (threadIdx.x >> 5), b = -1;
+  int have = 0;
+  int32_t page[kPer];
+  const auto pages_from = [&](int j0) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = j0 + 32 * k + lane;
+      page[k] = j < have ? t.table[b * t.W + j] : -1;
+    }
+  };
+  const auto begin = [&]() {
+    if (i >= n) return;
+    b = seqs[i];
+    have = b >= 0 && b < t.B ? pages_of(t.lens[b], t.S, t.W) : 0;
+    pages_from(0);
+  };
+  begin();
   team.sync();
-  // (the lengths are read before the update in place below)
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = team.rank * kMetaWarps + (threadIdx.x >> 5); i < n; i += kBlocks * kMetaWarps) {
-    const int64_t b = seqs[i];
+  for (; i < n; i += kBlocks * kMetaWarps, begin()) {
     if (b < 0 || b >= t.B) {
       if (lane == 0 && bad != nullptr) atomicAdd(bad, 1);
       continue;
     }
-    const int have = pages_of(t.lens[b], t.S, t.W);
     for (int j0 = 0; j0 < have; j0 += 32 * kPer) {
-      int32_t page[kPer];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int j = j0 + 32 * k + lane;
-        page[k] = j < have ? t.table[b * t.W + j] : -1;
-      }
+      if (j0 > 0) pages_from(j0);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (j0 + 32 * k + lane >= have) continue;
@@ -328,11 +342,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
         if (wrong && bad != nullptr) atomicAdd(bad, 1);
       }
     }
-  }
-  team.sync();
-  for (int64_t i = team.rank * kMeta + threadIdx.x; i < n; i += kAll) {
-    const int64_t b = seqs[i];
-    if (b >= 0 && b < t.B) lens_out[b] = 0;
+    if (lane == 0) lens_out[b] = 0;  // (in place: nobody else reads it)
   }
 }
 
@@ -400,18 +410,21 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
   }
 }
 
-// Moves pages src[i] -> dst[i] in every layer, i < n or *count. A unit is kUnit
-// bytes of one page of one layer, 64 bytes a thread, all of a unit's loads in
-// flight before its first store; 8 blocks of an SM have 128 KB on their way.
-constexpr int kCopyThreads = 256;
+// Moves pages src[i] -> dst[i] in every layer, i < n or *count. A unit is 64
+// bytes a thread of one page of one layer, all of them on their way before the
+// first store: 16 KB with blocks of 256, 4 KB with blocks of 64 for small pages.
+// Several times as many blocks as fit the GPU at once: 1.07 GB moved in 160 us
+// (6.7 TB/s); with just as many, in a loop, 180 us: nothing hid the index
+// arithmetic and the ids' loads.
+constexpr int kCopyThreads = 256, kSmallCopyThreads = 64;
 constexpr int kVecs = 4;
-constexpr int64_t kUnit = kCopyThreads * kVecs * 16;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PagePool p, const int32_t* src, const int32_t* dst,
                                                            int64_t n, const int32_t* count, int32_t* bad) {
   cl::griddep_wait();
   if (count != nullptr) n = __ldcg(count);
-  const int64_t per_page = (p.page_bytes + kUnit - 1) / kUnit, per_pair = p.L * per_page, units = n * per_pair;
+  const int threads = blockDim.x;
+  const int64_t unit = threads * kVecs * 16, per_page = (p.page_bytes + unit - 1) / unit, per_pair = p.L * per_page, units = n * per_pair;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     int64_t i, layer, r;
     if (units <= 0x7FFFFFFF) {  // (32-bit divisions take a fraction of the others' time)
@@ -428,18 +441,18 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PagePool p, const in
       if (bad != nullptr && r == 0 && threadIdx.x == 0) atomicAdd(bad, 1);
       continue;
     }
-    const int64_t at = (r - layer * per_page) * kUnit + threadIdx.x * 16;
+    const int64_t at = (r - layer * per_page) * unit + threadIdx.x * 16;
     const uint8_t* from = static_cast<const uint8_t*>(p.kv) + (layer * p.P + s) * p.page_bytes;
     uint8_t* to = static_cast<uint8_t*>(p.kv) + (layer * p.P + d) * p.page_bytes;
     uint4 x[kVecs];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const int64_t o = at + j * kCopyThreads * 16;
+      const int64_t o = at + j * threads * 16;
       if (o < p.page_bytes) x[j] = __ldcs(reinterpret_cast<const uint4*>(from + o));
     }
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const int64_t o = at + j * kCopyThreads * 16;
+      const int64_t o = at + j * threads * 16;
       if (o < p.page_bytes) __stcs(reinterpret_cast<uint4*>(to + o), x[j]);
     }
   }
@@ -449,15 +462,16 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PagePool p, const in
 cudaError_t copy_pages(const Ctx& c, const PagePool& p, const int32_t* src, const int32_t* dst, int64_t most,
                        const int32_t* count, int32_t* bad, bool after) {
   if (most == 0) return cudaSuccess;
-  const int64_t per_page = (p.page_bytes + kUnit - 1) / kUnit;
-  int64_t grid = 8 * static_cast<int64_t>(c.sm_count);
+  const int threads = p.page_bytes > kCopyThreads * kVecs * 8 ? kCopyThreads : kSmallCopyThreads;
+  const int64_t unit = threads * kVecs * 16, per_page = (p.page_bytes + unit - 1) / unit;
+  int64_t grid = (threads == kCopyThreads ? 64 : 256) * static_cast<int64_t>(c.sm_count);
   if (most < grid && most * p.L < grid && most * p.L * per_page < grid) grid = most * p.L * per_page;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kCopyThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = after ? 1 : 0;
