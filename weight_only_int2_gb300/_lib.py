@@ -8,6 +8,7 @@ There is no fallback: if libwq.so is missing the import of a call fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -422,14 +423,17 @@ def _need_pool(kv: torch.Tensor):
     return L, P, S, two * H * S * D * kv.element_size()
 
 
+@functools.lru_cache(maxsize=4096)
 def kv_attn_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
     return int(load().kv_attn_workspace_bytes(B, Hq, Hkv, D))
 
 
+@functools.lru_cache(maxsize=4096)
 def kv_pages_scratch_bytes(n: int, B: int, W: int, P: int) -> int:
     return int(load().kv_pages_scratch_bytes(n, B, W, P))
 
 
+@functools.lru_cache(maxsize=4096)
 def token_logprobs_workspace_bytes(T: int, V: int, top_k: int) -> int:
     return int(load().token_logprobs_workspace_bytes(T, V, top_k))
 
@@ -450,8 +454,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, block_table: 
         _need(seq, "seq", torch.int32, (T,))
     if bad_count is not None:
         _need(bad_count, "bad_count", torch.int32)
-    _check(load().kv_append(_ptr(k), _ptr(v), ks, vs, T, _ptr(seq), _ptr(pos), _ptr(block_table), B, W, _ptr(kv),
-                            kind, P, H, S, D, _ptr(k_scale), _ptr(v_scale), _ptr(bad_count), _stream()), "kv_append")
+    _check(load().kv_append(k.data_ptr(), v.data_ptr(), ks, vs, T, _ptr(seq), pos.data_ptr(),
+                            block_table.data_ptr(), B, W, kv.data_ptr(), kind, P, H, S, D, _ptr(k_scale),
+                            _ptr(v_scale), _ptr(bad_count), _stream()), "kv_append")
     return kv
 
 
@@ -483,11 +488,11 @@ def kv_attn_decode(q: torch.Tensor, kv: torch.Tensor, block_table: torch.Tensor,
         _need(bad_count, "bad_count", torch.int32)
     lib = load()
     if ws is None:
-        ws = scratch(lib.kv_attn_workspace_bytes(B, Hq, H, D))
-    _check(lib.kv_attn_decode(_ptr(q), qs, _ptr(kv), kind, _ptr(block_table), _ptr(lens), B, W, P, Hq, H, S, D,
-                              _ptr(k_scale), _ptr(v_scale), D ** -0.5 if sm_scale is None else sm_scale, window,
-                              _ptr(out), _ptr(lse), _ptr(bad_count), _ptr(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(), _stream()), "kv_attn_decode")
+        ws = scratch(kv_attn_workspace_bytes(B, Hq, H, D))
+    _check(lib.kv_attn_decode(q.data_ptr(), qs, kv.data_ptr(), kind, block_table.data_ptr(), lens.data_ptr(), B, W,
+                              P, Hq, H, S, D, _ptr(k_scale), _ptr(v_scale), D ** -0.5 if sm_scale is None else
+                              sm_scale, window, out.data_ptr(), _ptr(lse), _ptr(bad_count), _ptr(ws), 0 if ws is
+                              None else ws.numel() * ws.element_size(), _stream()), "kv_attn_decode")
     return (out, lse) if return_lse else out
 
 
@@ -500,8 +505,8 @@ def kv_pages_copy(kv: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
     _need(dst, "dst", torch.int32, (n,))
     if bad_count is not None:
         _need(bad_count, "bad_count", torch.int32)
-    _check(load().kv_pages_copy(_ptr(kv), L, P, size, _ptr(src), _ptr(dst), n, _ptr(bad_count), _stream()),
-           "kv_pages_copy")
+    _check(load().kv_pages_copy(kv.data_ptr(), L, P, size, src.data_ptr(), dst.data_ptr(), n, _ptr(bad_count),
+                                _stream()), "kv_pages_copy")
     return kv
 
 
@@ -546,10 +551,11 @@ def kv_pages_fork(kv: torch.Tensor, block_table: torch.Tensor, lens: torch.Tenso
     lens_out, ref_out = _or_in_place(lens_out, lens, "lens_out"), _or_in_place(ref_out, ref, "ref_out")
     granted = _out_32(granted, (n,), "granted", kv.device)
     lib = load()
-    scr = scratch(lib.kv_pages_scratch_bytes(n, B, W, P))
-    _check(lib.kv_pages_fork(_ptr(kv), L, P, size, _ptr(block_table), _ptr(lens), _ptr(ref), B, W, S, _ptr(parent),
-                             _ptr(child), n, _ptr(table_out), _ptr(lens_out), _ptr(ref_out), _ptr(granted),
-                             _ptr(scr), scr.numel(), _stream()), "kv_pages_fork")
+    scr = scratch(kv_pages_scratch_bytes(n, B, W, P))
+    _check(lib.kv_pages_fork(kv.data_ptr(), L, P, size, block_table.data_ptr(), lens.data_ptr(), ref.data_ptr(), B,
+                             W, S, parent.data_ptr(), child.data_ptr(), n, table_out.data_ptr(),
+                             lens_out.data_ptr(), ref_out.data_ptr(), granted.data_ptr(), _ptr(scr), scr.numel(),
+                             _stream()), "kv_pages_fork")
     return table_out, lens_out, ref_out, granted
 
 
@@ -564,10 +570,10 @@ def kv_pages_reserve(block_table: torch.Tensor, lens: torch.Tensor, new_lens: to
     table_out, ref_out = _or_in_place(table_out, block_table, "table_out"), _or_in_place(ref_out, ref, "ref_out")
     granted = _out_32(granted, (B,), "granted", ref.device)
     lib = load()
-    scr = scratch(lib.kv_pages_scratch_bytes(B, B, W, P))
-    _check(lib.kv_pages_reserve(_ptr(block_table), _ptr(lens), _ptr(new_lens), _ptr(ref), B, W, page_size, P,
-                                _ptr(table_out), _ptr(ref_out), _ptr(granted), _ptr(scr),
-                                0 if scr is None else scr.numel(), _stream()), "kv_pages_reserve")
+    scr = scratch(kv_pages_scratch_bytes(B, B, W, P))
+    _check(lib.kv_pages_reserve(block_table.data_ptr(), lens.data_ptr(), new_lens.data_ptr(), ref.data_ptr(), B, W,
+                                page_size, P, table_out.data_ptr(), ref_out.data_ptr(), granted.data_ptr(),
+                                _ptr(scr), 0 if scr is None else scr.numel(), _stream()), "kv_pages_reserve")
     return table_out, ref_out, granted
 
 
@@ -582,8 +588,9 @@ def kv_pages_free(block_table: torch.Tensor, lens: torch.Tensor, ref: torch.Tens
     lens_out, ref_out = _or_in_place(lens_out, lens, "lens_out"), _or_in_place(ref_out, ref, "ref_out")
     if bad_count is not None:
         _need(bad_count, "bad_count", torch.int32)
-    _check(load().kv_pages_free(_ptr(block_table), _ptr(lens), _ptr(ref), B, W, page_size, P, _ptr(seqs), n,
-                                _ptr(lens_out), _ptr(ref_out), _ptr(bad_count), _stream()), "kv_pages_free")
+    _check(load().kv_pages_free(block_table.data_ptr(), lens.data_ptr(), ref.data_ptr(), B, W, page_size, P,
+                                seqs.data_ptr(), n, lens_out.data_ptr(), ref_out.data_ptr(), _ptr(bad_count),
+                                _stream()), "kv_pages_free")
     return lens_out, ref_out
 
 
@@ -599,10 +606,10 @@ def kv_pages_compact(kv: torch.Tensor, block_table: torch.Tensor, lens: torch.Te
     table_out, ref_out = _or_in_place(table_out, block_table, "table_out"), _or_in_place(ref_out, ref, "ref_out")
     remap, n_live = _out_32(remap, (P,), "remap", kv.device), _out_32(n_live, (1,), "n_live", kv.device)
     lib = load()
-    scr = scratch(lib.kv_pages_scratch_bytes(0, B, W, P))
-    _check(lib.kv_pages_compact(_ptr(kv), L, P, size, _ptr(block_table), _ptr(lens), _ptr(ref), B, W, S,
-                                _ptr(table_out), _ptr(ref_out), _ptr(remap), _ptr(n_live), _ptr(scr), scr.numel(),
-                                _stream()), "kv_pages_compact")
+    scr = scratch(kv_pages_scratch_bytes(0, B, W, P))
+    _check(lib.kv_pages_compact(kv.data_ptr(), L, P, size, block_table.data_ptr(), lens.data_ptr(), ref.data_ptr(),
+                                B, W, S, table_out.data_ptr(), ref_out.data_ptr(), remap.data_ptr(),
+                                n_live.data_ptr(), _ptr(scr), scr.numel(), _stream()), "kv_pages_compact")
     return table_out, ref_out, remap, n_live
 
 
@@ -634,11 +641,11 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
     top_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     lib = load()
     if ws is None:
-        ws = scratch(lib.token_logprobs_workspace_bytes(T, V, k))
-    _check(lib.token_logprobs(_ptr(logits), _LOGIT_TYPES[logits.dtype], V if T <= 1 else logits.stride(0), T, V,
-                              _ptr(ids), temperature, top_k, _ptr(lp), _ptr(rank), _ptr(entropy), _ptr(top),
-                              _ptr(top_ids), _ptr(bad_count), _ptr(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(), _stream()), "token_logprobs")
+        ws = scratch(token_logprobs_workspace_bytes(T, V, k))
+    _check(lib.token_logprobs(logits.data_ptr(), _LOGIT_TYPES[logits.dtype], V if T <= 1 else logits.stride(0), T,
+                              V, _ptr(ids), temperature, top_k, _ptr(lp), _ptr(rank), entropy.data_ptr(),
+                              top.data_ptr(), top_ids.data_ptr(), _ptr(bad_count), _ptr(ws), 0 if ws is None else
+                              ws.numel() * ws.element_size(), _stream()), "token_logprobs")
     return lp, rank, entropy, top, top_ids
 
 
