@@ -744,71 +744,76 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
 }
 
 // Joins the parts of rows that several shares hold, in their order: a block per
-// row. A warp merges the sorted keys of its parts (three a lane), then the first
-// warp those of the warps.
+// row. Of n sorted lists, the r'th largest of their j'th keys bounds the best
+// top_k from below where r j >= top_k; what reaches it (at most top_k lists of
+// top_k keys) is ranked by counting.
+constexpr int kMaxParts = kMaxShares + 1;
+
 __global__ void __launch_bounds__(kThreads) join_kernel(const Args g) {
-  constexpr int kLists = 3;
-  static_assert(kLists * kThreads >= kMaxShares + 1, "a list per part");
-  __shared__ uint64_t merged[kWarps][kMaxTopK];
+  __shared__ uint64_t lead[kMaxParts], some[kMaxTopK * kMaxTopK], best[kMaxTopK];
   __shared__ Sums sums[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint64_t bound;
+  __shared__ int count;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = g.a.top_k;
   const int64_t row = blockIdx.x, places = g.units + kRowCost;
   const int64_t first = row * places + kRowCost, last = first + g.units - 1;
-  const int64_t p0 = first / g.share, n = last / g.share - p0 + 1;
+  const int64_t p0 = first / g.share;
+  const int n = static_cast<int>(last / g.share - p0) + 1;
   const int32_t id = g.a.ids != nullptr && n > 1 ? g.a.ids[row] : -1;
+  const float xt = n > 1 ? given_logit(g.a, row, id) : 0.0f;
+  if (tid == 0) {
+    count = 0;
+    bound = 0;
+  }
+  if (tid < kMaxTopK) best[tid] = 0;
   cl::griddep_wait();
   if (n <= 1) return;
-  const auto part = [&](int64_t p) -> const Part& { return g.parts[(p0 + p) * 2 + (p == 0)]; };
-  // the best top_k of the lanes' lists, each sorted
-  const auto merge = [&](const uint64_t* (&list)[kLists], uint64_t* to, int k) {
-    uint64_t head[kLists];
-    int used[kLists];
-#pragma unroll
-    for (int i = 0; i < kLists; ++i) {
-      used[i] = 0;
-      head[i] = list[i] != nullptr ? list[i][0] : 0;
-    }
-    for (int j = 0; j < k; ++j) {
-      uint64_t mine = head[0];
-#pragma unroll
-      for (int i = 1; i < kLists; ++i) mine = head[i] > mine ? head[i] : mine;
-      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32));
-      const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
-      const uint64_t best = static_cast<uint64_t>(hi) << 32 | lo;
-      if (lane == 0) to[j] = best;
-      if (best == 0) continue;
-#pragma unroll
-      for (int i = 0; i < kLists; ++i)
-        if (head[i] == best) head[i] = ++used[i] < k ? list[i][used[i]] : 0;
-    }
-  };
-  const uint64_t* list[kLists];
+  const auto part = [&](int p) -> const Part& { return g.parts[(p0 + p) * 2 + (p == 0)]; };
+  const int j = (k + n - 1) / n, r = j > 0 ? (k + j - 1) / j : 0;
   Sums s{-CUDART_INF_F, 0.0f, 0.0f, 0};
-#pragma unroll
-  for (int i = 0; i < kLists; ++i) {
-    const int64_t p = tid + i * kThreads;
-    list[i] = p < n ? part(p).keys : nullptr;
-    if (p < n) join(s, part(p).s, g.c);
+  for (int p = tid; p < n; p += kThreads) {
+    const Part& x = part(p);
+    if (k > 0) lead[p] = x.keys[j - 1];
+    join(s, x.s, g.c);
   }
+  if (warp * 32 < n) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Sums y{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
-                 __shfl_xor_sync(0xFFFFFFFFu, s.t, o), __shfl_xor_sync(0xFFFFFFFFu, s.before, o)};
-    join(s, y, g.c);
+    for (int o = 16; o > 0; o >>= 1) {
+      const Sums y{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.l, o),
+                   __shfl_xor_sync(0xFFFFFFFFu, s.t, o), __shfl_xor_sync(0xFFFFFFFFu, s.before, o)};
+      join(s, y, g.c);
+    }
   }
   if (lane == 0) sums[warp] = s;
-  merge(list, merged[warp], g.a.top_k);
   __syncthreads();
-  s = sums[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) join(s, sums[w], g.c);
+  if (k > 0) {
+    for (int p = tid; p < n; p += kThreads) {
+      const uint64_t mine = lead[p];
+      int rank = 0;
+      for (int i = 0; i < n; ++i) rank += lead[i] > mine;
+      if (rank == r - 1) bound = mine;  // (no keys at all: 0, from whichever)
+    }
+    __syncthreads();
+    const uint64_t least = bound > 0 ? bound : 1;
+    for (int i = tid; i < n * k; i += kThreads) {
+      const int p = i / k;
+      const uint64_t key = part(p).keys[i - p * k];
+      if (key >= least) some[atomicAdd(&count, 1)] = key;
+    }
+    __syncthreads();
+    const int c = count;
+    for (int i = tid; i < c; i += kThreads) {
+      const uint64_t mine = some[i];
+      int rank = 0;
+      for (int q = 0; q < c; ++q) rank += some[q] > mine;
+      if (rank < k) best[rank] = mine;
+    }
+    __syncthreads();
+  }
   if (warp == 0) {
-#pragma unroll
-    for (int i = 0; i < kLists; ++i) list[i] = i == 0 && lane < kWarps ? merged[lane] : nullptr;
-    __shared__ uint64_t out[kMaxTopK];
-    merge(list, out, g.a.top_k);
-    __syncwarp();
-    put(g, row, s, lane < g.a.top_k ? out[lane] : 0, id >= 0 && id < g.a.V, given_logit(g.a, row, id));
+    s = sums[0];
+    for (int w = 1; w < kWarps && w * 32 < n; ++w) join(s, sums[w], g.c);
+    put(g, row, s, best[lane], id >= 0 && id < g.a.V, xt);
   }
 }
 
