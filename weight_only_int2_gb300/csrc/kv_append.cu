@@ -2,11 +2,14 @@
 // are, or rounded to e4m3 with a scale per key head).
 //
 // Bound: a token's place takes three loads one after the other (its sequence and
-// position, then the page id), so a few tokens cost that latency, and many the
-// read and the write of their values, if enough of them are on their way: a
-// thread loads its values before it knows where they go, and with many tokens it
-// has four of them at once (one each, 75 MB took 34.5 us: the chain, ten waves of
-// blocks long).
+// position, then the page id), so a few tokens cost that latency (64 tokens of 8
+// key heads by 128: 2.2 us, nearly all of it the launch), and many the read and
+// the write of their values, if enough of them are on their way: a thread loads
+// its values before it knows where they go, with many tokens for two in a row, in
+// no more than 32 registers, so that an SM holds its 2048 threads. 12289 tokens of 8 key
+// heads by 128 into e4m3, 75.7 MB: 18.5 us, 4.1 TB/s, of which the start and the
+// last blocks' chain are a third; one token a thread 19.2 us, four 20.3 us (72
+// registers), eight 23.6 us; blocks of 512 threads 19.3 us.
 //
 // The e4m3 code is that of the IEEE quotient x / w. With y = RN(1 / w),
 // q = RN(x y) and r = x - q w (exact in one fma), RN(q + r y) is the correctly
@@ -43,7 +46,7 @@ __device__ __forceinline__ uint32_t codes_of(uint32_t p, float w, float y, float
 // One thread per 16 bytes of the cache (8 bf16 values or 16 codes) of kTokens
 // tokens in a row: chunk i of a token, keys first.
 template <bool kE4m3, int kTokens>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCache a, const uint16_t* __restrict__ k,
+__global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCache a, const uint16_t* __restrict__ k,
                                                             const uint16_t* __restrict__ v, int64_t k_stride,
                                                             int64_t v_stride, int64_t T,
                                                             const int32_t* __restrict__ seq,
@@ -51,31 +54,33 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCache a, co
                                                             int32_t* __restrict__ bad) {
   constexpr int kValues = kE4m3 ? 16 : 8, kLoads = kValues / 8;
   const uint32_t per_head = static_cast<uint32_t>(a.D) / kValues, row = static_cast<uint32_t>(a.Hkv) * per_head;
-  // (a block's first thread divides in 64 bits, the others add)
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads, g0 = u0 / (2 * row);
+  // (64-bit places are divided only where they are past 32 bits)
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads;
+  const int64_t g0 = u0 <= 0xFFFFFFFFll ? static_cast<uint32_t>(u0) / (2 * row) : u0 / (2 * row);
   const uint32_t in = static_cast<uint32_t>(u0 - g0 * 2 * row) + threadIdx.x;
   const int64_t t0 = (g0 + in / (2 * row)) * kTokens;
   if (t0 >= T) return;
   const uint32_t i = in % (2 * row), side = i >= row, at = i - side * row, h = at / per_head, d = (at - h * per_head) * kValues;
 
   uint4 x[kTokens][kLoads];
-  int64_t s[kTokens], p[kTokens];
+  int32_t s[kTokens], p[kTokens];
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
     s[j] = p[j] = -1;
     if (t0 + j >= T) continue;
-    s[j] = seq != nullptr ? seq[t0 + j] : t0 + j;
+    s[j] = seq != nullptr ? seq[t0 + j] : static_cast<int32_t>(t0 + j);
     p[j] = pos[t0 + j];
     const uint16_t* src = side ? v + (t0 + j) * v_stride : k + (t0 + j) * k_stride;
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) x[j][l] = __ldcs(reinterpret_cast<const uint4*>(src + h * a.D + d) + l);
   }
-  int64_t page[kTokens];
+  int32_t page[kTokens];
   const uint32_t S = static_cast<uint32_t>(a.S);
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
     page[j] = -1;
-    if (s[j] >= 0 && s[j] < a.B && p[j] >= 0 && p[j] < a.W * a.S) page[j] = a.table[s[j] * a.W + static_cast<uint32_t>(p[j]) / S];
+    if (s[j] >= 0 && s[j] < a.B && p[j] >= 0 && p[j] < a.W * a.S)
+      page[j] = a.table[static_cast<int64_t>(s[j]) * a.W + static_cast<uint32_t>(p[j]) / S];
   }
   float w = 1.0f;
   if constexpr (kE4m3) w = side ? a.v_scale[h] : a.k_scale[h];
@@ -86,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCache a, co
       if (i == 0 && bad != nullptr && t0 + j < T) atomicAdd(bad, 1);
       continue;
     }
-    const int64_t dst = (((page[j] * 2 + side) * a.Hkv + h) * a.S + static_cast<uint32_t>(p[j]) % S) * a.D + d;
+    const int64_t dst = (((static_cast<int64_t>(page[j]) * 2 + side) * a.Hkv + h) * a.S + static_cast<uint32_t>(p[j]) % S) * a.D + d;
     if constexpr (!kE4m3) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.kv) + dst) = x[j][0];
     } else {
@@ -107,12 +112,13 @@ cudaError_t launch_kv_append(const Ctx& c, const KvCache& a, const uint16_t* k, 
                              int64_t v_stride, int64_t T, const int32_t* seq, const int32_t* pos, int32_t* bad) {
   const bool e4m3 = a.type == WQ_KV_E4M3;
   const int64_t chunks = 2 * a.Hkv * a.D / (e4m3 ? 16 : 8);
-  // four tokens a thread once every SM has its eight blocks
+  // one token a thread while the SMs hold them all at once (64 tokens: 2.2 us, two
+  // a thread 2.5 us)
   const bool many = T * chunks > int64_t{8} * kThreads * c.sm_count;
-  const int64_t grid = ((many ? (T + 3) / 4 : T) * chunks + kThreads - 1) / kThreads;
+  const int64_t grid = ((many ? (T + 1) / 2 : T) * chunks + kThreads - 1) / kThreads;
   if (grid > kMaxDim) return cudaErrorInvalidConfiguration;
-  const auto kern = e4m3 ? (many ? kv_append_kernel<true, 4> : kv_append_kernel<true, 1>)
-                         : (many ? kv_append_kernel<false, 4> : kv_append_kernel<false, 1>);
+  const auto kern = e4m3 ? (many ? kv_append_kernel<true, 2> : kv_append_kernel<true, 1>)
+                         : (many ? kv_append_kernel<false, 2> : kv_append_kernel<false, 1>);
   kern<<<static_cast<unsigned>(grid), kThreads, 0, c.stream>>>(a, k, v, k_stride, v_stride, T, seq, pos, bad);
   return cudaGetLastError();
 }
