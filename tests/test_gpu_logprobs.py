@@ -137,6 +137,37 @@ def test_padded_rows(pad, T, V, bf16):
     check(x, ids, 7, 1.0, wq.token_logprobs(dev[:, :V], ids.cuda(), top_k=7))
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("kind", ["normal", "masked", "ties", "ascending", "constant"])
+@pytest.mark.parametrize("T,V,k", [(9, 700, 32), (1100, 4001, 7), (1040, 2050, 32), (4100, 515, 0)])
+def test_many_rows(T, V, k, kind, bf16):
+    x = rows(T, V, bf16, 11, kind)
+    ids = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(V)).int()
+    check(x, ids, k, 1.3, run(x, ids, k, 1.3))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V", [(5, 70001), (5, 900), (900, 40003)])
+def test_few_logits_above_minus_infinity(T, V, bf16):
+    """Less than top_k of a row have weight, wherever they are: -inf follows by id."""
+    x = torch.full((T, V), -math.inf)
+    x[1, [0, V // 2, V - 1]] = torch.tensor([1.0, -2.0, 1.0])
+    x[2, :31] = torch.arange(31.0)
+    x[3, V - 40:] = torch.arange(40.0)
+    x[4, ::V // 33] = 0.5
+    x = x.bfloat16() if bf16 else x
+    ids = torch.zeros(T, dtype=torch.int32)
+    ids[:5] = torch.tensor([V - 1, 1, 31, V - 40, V // 33])
+    check(x, ids, 32, 1.0, run(x, ids, 32))
+
+
+@pytest.mark.parametrize("V", [62080, 65537, 8193, 16400])
+def test_rows_that_end_in_a_short_piece(V):
+    x = rows(3, V, True, V)
+    ids = torch.tensor([0, V - 1, V // 2], dtype=torch.int32)
+    check(x, ids, 32, 1.0, run(x, ids, 32))
+
+
 def test_repeats_and_streams():
     x, y = rows(3, 130001, True, 1).cuda(), rows(64, 3001, False, 2).cuda()
     ids = torch.tensor([3, 1, 2], dtype=torch.int32, device="cuda")
