@@ -14,7 +14,12 @@
 // issues 128 lanes). So: everything in one pass; pairs of float32 operations
 // where there are such; the rank by packed compares; no running maximum but a
 // test per 8 logits (4 for float32) against the reference and against the
-// top_k'th best so far.
+// top_k'th best so far. Measured: 64 rows of 8 M bf16 logits 6.8 TB/s without ids
+// and best, 6.6 with ids, 5.8 with the best 5; 2049 rows of 248320, 1.02 GB, 151
+// us (6.7 TB/s), 176, 222 and with the best 20 269: a row's ends, the barriers of
+// its notes and the notes themselves, about 10 us a row at three rows an SM, are
+// what the other two blocks do not hide. 1 row with the best 20: 13 us, of which
+// the join is 4; 96 float32 rows of 100003 with the best 8: 27 us.
 //  - All rows are one line of units of 4 KB (a 16-byte vector per thread), cut
 //    into equal shares, one per block, several blocks per SM; a second kernel
 //    joins rows that were cut, in the order of their parts: bits do not depend on
@@ -26,7 +31,9 @@
 //    logits are noted only above the bound, which is raised after 1, 2, 4 ..
 //    rounds: a few notes per row in the usual order. Where they do not fit
 //    (ascending rows), the piece's best are found again with a bound for every
-//    round, by bisection over the keys.
+//    round, by bisection over the keys. -inf is not noted: where too few logits
+//    are above it (a grammar's mask), the first of them follow at the end.
+//  - Short rows take a kernel of their own, a warp per row.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
@@ -162,6 +169,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 
@@ -537,15 +550,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         l_left -= kRound;
       } else {
         copy_round(freed);
-        // the row's first and last vector, the given token's, and what lies
-        // outside the piece: logit by logit, by the warp that has it
-        plain = v0 > 0 && v0 + (kRound - 1) * kThreads + 32 < r.nvec && u + kRound <= end &&
+        // the row's first and last vector where it is not all the row's, the given
+        // token's, and what lies outside the piece: logit by logit, by their warp
+        // the row's whole vectors: [head, full)
+        const int head = r.head > 0, full = static_cast<int>((V + r.head) / kN);
+        plain = v0 >= head && v0 + (kRound - 1) * kThreads + 32 <= full && u + kRound <= end &&
                 (v_id < v0 || v_id >= v0 + (kRound - 1) * kThreads + 32) && xt == xt;
         than = v_id >= v0 ? low : xt;
         if (!plain) {
           for (int j = 0; j < kRound; ++j) {
             const int w0 = v0 + j * kThreads, v = w0 + lane;
-            if (w0 > 0 && w0 + 32 < r.nvec && u + j < end && (v_id < w0 || v_id >= w0 + 32) && xt == xt) continue;
+            if (w0 >= head && w0 + 32 <= full && u + j < end && (v_id < w0 || v_id >= w0 + 32) && xt == xt) continue;
             special |= 1u << j;
             const uint32_t id0 = u + j < end && v < r.nvec ? r.id(v, 0) : 0xFFFFFF00u;  // none: above any V
             s.before += look_closer<kBf16>(in + j * kUnitBytes, id0, V, key_t);
@@ -557,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           }
         }
         const int u2 = u + kRound, l_end = g.units - l_unit < l_left ? g.units : l_unit + l_left;
-        const int whole = (r.nvec - 1) / kThreads, l_whole = (lr.nvec - 1) / kThreads;
+        const int whole = full / kThreads, l_whole = (lr.nvec - 1) / kThreads;
         fast = ((end < whole ? end : whole) - u2) / kRound;
         const int l_fast = l_left > 0 ? ((l_end < l_whole ? l_end : l_whole) - l_unit) / kRound : 0;
         fast = fast < l_fast ? fast : l_fast;
@@ -597,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : limit;
         if (!closed) {
           int rank = 0;
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < 32; ++i) {
             const uint32_t y = __shfl_sync(0xFFFFFFFFu, o, i);
             rank += y > o || (y == o && i < lane);
@@ -850,12 +865,14 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args g) {
 // row needs no barrier: a lane has every 32nd vector, four on their way, each
 // exponent is a difference, and the notes are taken by ballot, so that the list
 // never overflows: it is cut to the best as soon as it holds 16 more. 4096 rows
-// of 500 bf16 logits, best 5: 12.7 us (88 us in shares); 16384 rows of 8001
-// without the best: 89 us, 2.9 TB/s (174); the issue of about ten instructions
-// per logit bounds it.
+// of 500 bf16 logits, best 5: 10.7 us (88 us in shares); 16384 rows of 8001
+// without the best: 78 us, 3.4 TB/s (176), with the best 20 200 us (359). The
+// issue bounds it: about eight instructions per logit, and the notes. Two vectors
+// on their way or fewer registers (five blocks) cost 5 to 10 %.
 
 constexpr int kAhead = 4;  // vectors of a lane on their way
-constexpr int kWarpNotes = kMaxTopK + 32 * 8;
+constexpr int kSpare = 16;  // notes beyond top_k that are kept until the next cut
+constexpr int kWarpNotes = kMaxTopK + kSpare + 32 * 8;
 
 // Vector v of a row; what lies outside it is -inf and is not read.
 template <bool kBf16>
@@ -901,8 +918,27 @@ __device__ __noinline__ int keep_best_warp(uint64_t* notes, uint64_t* best, int 
   return n;
 }
 
+// Notes the logits id, id + 1 .. that are of the row and have keys above the
+// bound, whose logit is `least`; returns how many there are then. (Not inlined:
+// four copies of it, unrolled, are slower than the calls, by half at top_k 20.)
+template <bool kBf16>
+__device__ __noinline__ int note_warp(Vec<kBf16> x, uint32_t id, uint32_t V, uint64_t bound, float least,
+                                      uint64_t* notes, int noted) {
+  const uint32_t before = (1u << (threadIdx.x & 31)) - 1u;
+#pragma unroll
+  for (int i = 0; i < Vec<kBf16>::kN; ++i) {
+    if (!__any_sync(0xFFFFFFFFu, !(x.at(i) < least))) continue;
+    const uint64_t key = key_of(x.at(i), id + i);
+    const bool take = id + i < V && key > bound;
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, take);
+    if (take) notes[noted + __popc(who & before)] = key;
+    noted += __popc(who);
+  }
+  return noted;
+}
+
 template <bool kBf16, bool kIds>
-__global__ void __launch_bounds__(kThreads, 5) short_rows_kernel(const Args g) {
+__global__ void __launch_bounds__(kThreads, 4) short_rows_kernel(const Args g) {
   constexpr int kN = Vec<kBf16>::kN;
   __shared__ uint64_t all_notes[kWarps][kWarpNotes], all_best[kWarps][kMaxTopK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -921,8 +957,15 @@ __global__ void __launch_bounds__(kThreads, 5) short_rows_kernel(const Args g) {
   const float low = next_below<kBf16>(xt);
 
   Sums s{-CUDART_INF_F, 0.0f, 0.0f, 0};
+  uint64_t l2 = 0, t2 = 0;  // added up in pairs
+  const auto add_up = [&]() {
+    s.l += low_of(l2) + high_of(l2);
+    s.t += low_of(t2) + high_of(t2);
+    l2 = t2 = 0;
+  };
   uint32_t above = 0;
   uint64_t bound = 0;  // keys up to it are not among the best
+  float least = 0.0f;  // its logit
   int noted = 0;
   for (int v0 = 0; v0 < r.nvec; v0 += 32 * kAhead) {
     Vec<kBf16> x[kAhead];
@@ -935,16 +978,22 @@ __global__ void __launch_bounds__(kThreads, 5) short_rows_kernel(const Args g) {
     float top = tops[0];
 #pragma unroll
     for (int j = 1; j < kAhead; ++j) top = max_nan(top, tops[j]);
-    if (top > s.m) raise(s, top, g.c);
+    if (top > s.m) {
+      add_up();
+      raise(s, top, g.c);
+    }
     const float m = s.m == -CUDART_INF_F ? 0.0f : s.m;
+    const uint64_t c2 = pair(g.c, g.c), m2 = pair(-m, -m);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (v0 + j * 32 >= r.nvec) break;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const float d = max_nan((x[j].at(i) - m) * g.c, -200.0f), e = exp2_fast(d);
-        s.l += e;
-        s.t = fmaf(e, d, s.t);
+      for (int i = 0; i < kN; i += 2) {
+        uint64_t d = mul2(add2(pair(x[j].at(i), x[j].at(i + 1)), m2), c2);
+        d = pair(max_nan(low_of(d), -200.0f), max_nan(high_of(d), -200.0f));
+        const uint64_t e = pair(exp2_fast(low_of(d)), exp2_fast(high_of(d)));
+        l2 = add2(l2, e);
+        t2 = fma2(e, d, t2);
       }
     }
 
@@ -975,27 +1024,22 @@ __global__ void __launch_bounds__(kThreads, 5) short_rows_kernel(const Args g) {
         }
         const int from = __ffs(__ballot_sync(0xFFFFFFFFu, rank == a.top_k - 1)) - 1;
         bound = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, o, from)) << 32;
+        least = value_of(static_cast<uint32_t>(bound >> 32));
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        if (!__any_sync(0xFFFFFFFFu, order_of(tops[j]) >= static_cast<uint32_t>(bound >> 32))) continue;
-        const uint32_t id0 = r.id(v0 + j * 32 + lane, 0);
-        const bool mine = v0 + j * 32 + lane < r.nvec;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const uint64_t key = key_of(x[j].at(i), id0 + i);
-          const bool take = mine && id0 + i < V && key > bound;
-          const unsigned who = __ballot_sync(0xFFFFFFFFu, take);
-          if (take) notes[noted + __popc(who & ((1u << lane) - 1u))] = key;
-          noted += __popc(who);
-        }
-        if (noted > kMaxTopK || noted > a.top_k + 16) {
+        if (!__any_sync(0xFFFFFFFFu, !(tops[j] < least))) continue;
+        const int v = v0 + j * 32 + lane;
+        noted = note_warp(x[j], v < r.nvec ? r.id(v, 0) : 0xFFFFFF00u, V, bound, least, notes, noted);
+        if (noted > a.top_k + kSpare) {
           noted = keep_best_warp(notes, all_best[warp], noted, a.top_k);
           if (noted == a.top_k) bound = notes[noted - 1];
+          least = value_of(static_cast<uint32_t>(bound >> 32));
         }
       }
     }
   }
+  add_up();
   s.before += Vec<kBf16>::count_of(above);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -1018,9 +1062,9 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
   const bool bf16 = a.type == WQ_LOGITS_BF16, ids = a.ids != nullptr;
   const int64_t per = bf16 ? 8 : 4;
   // A warp per row for rows of 2 KB, and up to 32 KB where there are many: 1 row of
-  // 1000 bf16 logits with the best 20 takes 8.6 us this way, 9.3 in shares; of 4001,
-  // 22 and 9.7; but 16384 rows of 1000 55 and 370, 2048 of 4001 36 and 54, 4096 of
-  // 8001 97 and 94 (without the best 31 and 47), 256 of 2000 15 and 12.
+  // 1000 bf16 logits with the best 20 takes 7.6 us this way, 9.3 in shares; of 4001,
+  // 20 and 9.7; but 16384 rows of 1000 48 and 370, 4096 of 8001 61 and 94, 2048 of
+  // 8001 22 and 27 without the best, 256 of 2000 14 and 12.
   const int64_t vectors = (a.V + per - 1) / per;
   if (vectors <= 128 || (vectors <= 2048 && a.T >= 2 * vectors)) {
     const auto kern = bf16 ? (ids ? short_rows_kernel<true, true> : short_rows_kernel<true, false>)
