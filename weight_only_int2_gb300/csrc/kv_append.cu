@@ -6,18 +6,21 @@
 // key heads by 128: 2.2 us, nearly all of it the launch), and many the read and
 // the write of their values, if enough of them are on their way: a thread loads
 // its values before it knows where they go, with many tokens for two in a row, in
-// no more than 32 registers, so that an SM holds its 2048 threads. 12289 tokens of 8 key
-// heads by 128 into e4m3, 75.7 MB: 18.5 us, 4.1 TB/s, of which the start and the
-// last blocks' chain are a third; one token a thread 19.2 us, four 20.3 us (72
+// no more than 32 registers, so that an SM holds its 2048 threads. 12289 tokens of
+// 8 key heads by 128 into e4m3, 75.7 MB: 17.4 us, 4.3 TB/s; there the issue is
+// next (three quarters of its slots: the codes and the indexes; with float32
+// operations one by one 18.6 us). One token a thread 19.2 us, four 20.3 us (72
 // registers), eight 23.6 us; blocks of 512 threads 19.3 us.
 //
 // The e4m3 code is that of the IEEE quotient x / w. With y = RN(1 / w),
 // q = RN(x y) and r = x - q w (exact in one fma), RN(q + r y) is the correctly
 // rounded quotient (Markstein, IBM J. Res. Dev. 34(1), 1990); x is clamped to
-// +-500 w first, beyond the largest code, so that nothing overflows on the way.
+// +-500 w first (rounded to bf16, still beyond the largest code), so that nothing
+// overflows on the way.
 #include "wq_device.cuh"
 #include "wq_internal.h"
 
+#include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 namespace wq {
@@ -25,22 +28,43 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float clamp_nan(float x, float lim) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(lim));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(-lim));
-  return y;
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  return static_cast<uint64_t>(__float_as_uint(y)) << 32 | __float_as_uint(x);
+}
+__device__ __forceinline__ float low_of(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float high_of(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
-// Two bf16 numbers (the halves of p) over w as two e4m3 codes; y = RN(1 / w).
-__device__ __forceinline__ uint32_t codes_of(uint32_t p, float w, float y, float lim) {
-  float q[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float x = clamp_nan(__uint_as_float(i ? p & 0xFFFF0000u : p << 16), lim), z = __fmul_rn(x, y);
-    q[i] = copysignf(__fmaf_rn(__fmaf_rn(-z, w, x), y, z), z);  // (-0.0 stays)
+// A scale w for pairs of values: -w, RN(1 / w) and the two bf16 limits.
+struct Scale {
+  uint64_t minus_w, y;
+  uint32_t lim;
+  __device__ explicit Scale(float w) {
+    const float r = __frcp_rn(w);
+    minus_w = pair(-w, -w);
+    y = pair(r, r);
+    const __nv_bfloat162 l = __float2bfloat162_rn(fminf(500.0f * w, 3.0e38f));
+    lim = *reinterpret_cast<const uint32_t*>(&l);
   }
-  return __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+};
+
+// Two bf16 numbers (the halves of p) over w as two e4m3 codes.
+__device__ __forceinline__ uint32_t codes_of(uint32_t p, const Scale& s) {
+  asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(p) : "r"(s.lim));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(p) : "r"(s.lim | 0x80008000u));
+  const uint64_t x = pair(__uint_as_float(p << 16), __uint_as_float(p & 0xFFFF0000u)), z = mul2(x, s.y);
+  const uint64_t q = fma2(fma2(z, s.minus_w, x), s.y, z);
+  return __nv_cvt_float2_to_fp8x2(make_float2(copysignf(low_of(q), low_of(z)), copysignf(high_of(q), high_of(z))),
+                                  __NV_SATFINITE, __NV_E4M3);  // (-0.0 stays)
 }
 
 // One thread per 16 bytes of the cache (8 bf16 values or 16 codes) of kTokens
@@ -84,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCache a,
   }
   float w = 1.0f;
   if constexpr (kE4m3) w = side ? a.v_scale[h] : a.k_scale[h];
-  const float y = __frcp_rn(w), lim = fminf(500.0f * w, 3.0e38f);
+  const Scale scale(w);
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
     if (page[j] < 0 || page[j] >= a.P) {
@@ -98,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCache a,
       uint32_t o[4];
 #pragma unroll
       for (int l = 0; l < 2; ++l) {
-        o[2 * l] = codes_of(x[j][l].x, w, y, lim) | codes_of(x[j][l].y, w, y, lim) << 16;
-        o[2 * l + 1] = codes_of(x[j][l].z, w, y, lim) | codes_of(x[j][l].w, w, y, lim) << 16;
+        o[2 * l] = codes_of(x[j][l].x, scale) | codes_of(x[j][l].y, scale) << 16;
+        o[2 * l + 1] = codes_of(x[j][l].z, scale) | codes_of(x[j][l].w, scale) << 16;
       }
       *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.kv) + dst) = make_uint4(o[0], o[1], o[2], o[3]);
     }
