@@ -274,6 +274,31 @@ def test_append(D, S, Hkv, T, e4m3, sliced):
     kv.check("cache")
 
 
+@pytest.mark.parametrize("Hkv", [2, 40])
+def test_append_every_bf16_value(Hkv):
+    """All 65536 patterns by scales from 2^-126 to 2^100, with one or two tokens a thread and an odd number of them."""
+    T, D, S = 1025, 64, 16
+    W = -(-T // S)
+    r = np.random.default_rng(Hkv)
+    bits = np.resize(np.arange(65536, dtype=np.uint16), (T, D))
+    ks, vs = (np.exp2(r.uniform(-12, 4, Hkv)).astype(np.float32) for _ in range(2))
+    ks[0], vs[0], ks[1], vs[1] = 2.0 ** -126, 2.0 ** 100, 1e-30, 1.0
+    x = torch.from_numpy(np.broadcast_to(bits.view(np.int16)[:, None], (T, Hkv, D)).copy()).cuda().view(torch.bfloat16)
+    kv = torch.zeros((W, 2, Hkv, S, D), dtype=torch.uint8, device="cuda").view(E4M3)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    wq.kv_append(x, x, pos, torch.arange(W, dtype=torch.int32, device="cuda")[None], kv,
+                 seq=torch.zeros(T, dtype=torch.int32, device="cuda"),
+                 k_scale=torch.from_numpy(ks).cuda(), v_scale=torch.from_numpy(vs).cuda())
+    got = kv.view(torch.uint8).permute(0, 3, 1, 2, 4).reshape(W * S, 2, Hkv, D)[:T].cpu().numpy()
+    vals = bf16_values(bits).astype(np.float32)
+    for i, scales in ((0, ks), (1, vs)):
+        for h in range(Hkv):
+            with np.errstate(over="ignore", invalid="ignore"):
+                y = vals / scales[h]
+            want = np.where(np.isnan(y), 127, R.e4m3_codes(np.nan_to_num(y.astype(np.float64), nan=0.0, posinf=1e300, neginf=-1e300)))
+            assert np.array_equal(np.where((got[:, i, h] & 127) == 127, 127, got[:, i, h]), want), (i, h)
+
+
 def test_append_without_seq_and_empty():
     kv = torch.zeros((4, 2, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
     table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
@@ -286,3 +311,36 @@ def test_append_without_seq_and_empty():
     assert torch.equal(kv, before)
     out = wq.kv_attn_decode(x[:0], kv, table[:0], pos[:0])
     assert out.shape == (0, 2, 64)
+
+
+def test_a_captured_step_follows_its_inputs():
+    """Append, attention and log probabilities in one CUDA graph, replayed after the inputs changed."""
+    g = torch.Generator().manual_seed(3)
+    B, W, S, Hkv, D = 3, 40, 16, 2, 64
+    kv = torch.randn((B * W, 2, Hkv, S, D), generator=g).bfloat16().cuda()
+    table = torch.randperm(B * W, generator=g).int().reshape(B, W).cuda()
+    k, v, q = (torch.zeros((B, h, D), dtype=torch.bfloat16, device="cuda") for h in (Hkv, Hkv, 4 * Hkv))
+    pos, lens, ids = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
+    logits = torch.zeros((B, 5003), dtype=torch.bfloat16, device="cuda")
+
+    def step(kv):
+        wq.kv_append(k, v, pos, table, kv)
+        return wq.kv_attn_decode(q, kv, table, lens, return_lse=True) + wq.token_logprobs(logits, ids, top_k=3)
+
+    mine = kv.clone()
+    step(mine)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(mine)
+    mine.copy_(kv)
+    for n in (1, 17, 500, W * S):
+        for x in (k, v, q, logits):
+            x.copy_(torch.randn(x.shape, generator=g).bfloat16())
+        lens.copy_(torch.tensor([n, max(0, n - 5), 1]))
+        pos.copy_((lens - 1))
+        ids.copy_(torch.randint(0, 5003, (B,), generator=g))
+        graph.replay()
+        want = step(kv)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(mine, kv)

@@ -25,6 +25,17 @@
 //  - e4m3 keys are multiplied as they are, by queries split into two e4m3
 //    numbers; e4m3 values are widened to fp16 in registers. The caches' scales
 //    are factors of the scores and of the output.
+//
+// Measured (of a copy's 6.8 TB/s): 64 sequences of 1 to 8192 tokens, 8 key heads
+// of 4 query heads, D = 128, bf16, 1.07 GB: 174 us, 6.2 TB/s; one of 131071
+// tokens, 40 query heads, 537 MB: 92 us, 5.9 TB/s; 48 of up to 16384 tokens, 4
+// key heads of 6, D = 256, e4m3, 0.95 GB: 161 us, 5.9 TB/s, where the issue is half
+// taken (widening the values) and the tensor pipe a third. A call has about 12 us
+// that do not stream: the start, the last block's end and the join (8 us by
+// itself, half of it under the first kernel's end). 77 tokens: 4.5 us. From L2 the
+// same loops run at 10.7 TB/s, so they are not the bound. Several waves of shares
+// instead of one (the one long sequence: 145 us), shares taken by tickets (124 us)
+// and a join by the block that comes last (6 to 25 us more) were slower.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
