@@ -344,3 +344,29 @@ def test_a_captured_step_follows_its_inputs():
         want = step(kv)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.equal(mine, kv)
+
+
+def test_captured_calls_have_scratch_of_their_own():
+    """A replay leaves the buffers of uncaptured calls alone, whatever ran on its stream before."""
+    from weight_only_int2_gb300 import _lib
+
+    g = torch.Generator().manual_seed(4)
+    kv = torch.randn((64, 2, 2, 128, 64), generator=g).bfloat16().cuda()
+    table = torch.randperm(64, generator=g).int()[None].cuda()
+    lens = torch.tensor([64 * 128 - 3], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 8, 64), generator=g).bfloat16().cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = wq.kv_attn_decode(q, kv, table, lens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = wq.kv_attn_decode(q, kv, table, lens)
+    for b in _lib._ws_cache.values():
+        b.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all(not bool(b.any()) for b in _lib._ws_cache.values())

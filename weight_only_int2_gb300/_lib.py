@@ -153,6 +153,7 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None) -> None:
 # ---------------------------------------------------------------- workspaces
 
 _ws_cache: dict = {}
+_ws_replaced: list = []
 _ws_lock = threading.Lock()
 
 
@@ -167,6 +168,8 @@ def _cached(kind: str, nbytes: int, device=None) -> torch.Tensor | None:
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
+            if buf is not None:
+                _ws_replaced.append(buf)  # a captured graph may still use it
             dev = "cuda" if index is None else torch.device("cuda", index)
             buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
             _ws_cache[key] = buf
@@ -189,7 +192,12 @@ def workspace(nbytes: int, device=None) -> torch.Tensor | None:
 
 
 def scratch(nbytes: int, device=None) -> torch.Tensor | None:
-    """A scratch buffer (contents undefined between calls) for the current stream."""
+    """A scratch buffer (contents undefined between calls) for the current stream.
+    A call that is captured into a CUDA graph gets one of its own from the
+    graph's memory: a cached one could be replaced, or be in use by another
+    graph, when the graph runs."""
+    if nbytes and torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda" if device is None else device)
     return _cached("scratch", nbytes, device)
 
 
