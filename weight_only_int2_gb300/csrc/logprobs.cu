@@ -16,10 +16,10 @@
 // test per 8 logits (4 for float32) against the reference and against the
 // top_k'th best so far. Measured: 64 rows of 8 M bf16 logits 6.8 TB/s without ids
 // and best, 6.6 with ids, 5.8 with the best 5; 2049 rows of 248320, 1.02 GB, 151
-// us (6.7 TB/s), 176, 222 and with the best 20 269: a row's ends, the barriers of
+// us (6.7 TB/s), 176, 218 and with the best 20 267: a row's ends, the barriers of
 // its notes and the notes themselves, about 10 us a row at three rows an SM, are
 // what the other two blocks do not hide. 1 row with the best 20: 13 us, of which
-// the join is 4; 96 float32 rows of 100003 with the best 8: 27 us.
+// the join is 4; 96 float32 rows of 100003 with the best 8: 26 us.
 //  - All rows are one line of units of 4 KB (a 16-byte vector per thread), cut
 //    into equal shares, one per block, several blocks per SM; a second kernel
 //    joins rows that were cut, in the order of their parts: bits do not depend on
@@ -28,7 +28,7 @@
 //    ahead (cp.async), and reads them back itself: no barrier.
 //  - The best top_k are kept as 64-bit keys (logit, then id) in shared memory: the
 //    first round's bound is the top_k'th largest of 32 groups' maxima; later
-//    logits are noted only above the bound, which is raised after 1, 2, 4 ..
+//    logits are noted only above the bound, which is raised after 2, 4, 8 ..
 //    rounds: a few notes per row in the usual order. Where they do not fit
 //    (ascending rows), the piece's best are found again with a bound for every
 //    round, by bisection over the keys. -inf is not noted: where too few logits
@@ -514,6 +514,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
       l2 = t2 = 0;
     };
     bool closed = a.top_k == 0, lost = false;
+    // the opening's bound does for the second round, too, unless most of its groups
+    // have to be above it (top_k 32: 355 us with a raise after the first round, 1070
+    // without; 5: 222 and 218)
+    int raise_at = a.top_k > 24 ? 1 : 2;
     if (tid == 0) sh.noted = 0;
     // logits this far below the reference (-inf among them) have weight 0; they
     // count as this one, so that every term is finite
@@ -585,6 +589,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         if (xt != xt) fast = 0;
         l_src = lr.base + (static_cast<int64_t>(l_unit) * kThreads + tid) * 16;
       }
+      // far: always; before there is a reference, and for NaN: always
+      const auto set_gate = [&]() {
+        gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : (closed || limit < bound ? limit : bound);
+      };
       if (rounds == 1) {
         // The opening: the largest logit of the block's round is everyone's first
         // reference, and the top_k'th largest of 32 groups' maxima the first bound
@@ -607,9 +615,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
           far = !(fabsf(ref) < 16777216.0f);
           set_floor();
         }
-        // far: always; before there is a reference, and for NaN: always; in the
-        // opening the notes are taken already
-        gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : limit;
         if (!closed) {
           int rank = 0;
 #pragma unroll 4
@@ -631,11 +636,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
             for (int i = 0; i < kN; ++i)
               if (note_it(x.at(i))) note(sh, x.at(i), r.id(v, i), V);
           }
+          if (least != 0xFFFFFFFFu) bound = from_here;  // (equal ones that come later are behind)
         }
+        set_gate();
       }
-      const auto set_gate = [&]() {
-        gate = far || limit == -CUDART_INF_F ? CUDART_NAN_F : (closed || limit < bound ? limit : bound);
-      };
       Vec<kBf16> x[kRound];
 #pragma unroll
       for (int j = 0; j < kRound; ++j) x[j] = Vec<kBf16>::from(in + j * kUnitBytes);
@@ -696,9 +700,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
         above = 0;
       }
 
-      // ---- the best top_k: the bound is raised after 1, 2, 4 .. rounds (a raise
-      // costs a block about ten notes, and twice the logits bring top_k notes)
-      if (!closed && (rounds & (rounds - 1)) == 0) {
+      // ---- the best top_k: the bound is raised after 2, 4, 8 .. rounds (a raise
+      // costs a block about ten notes, and twice the logits bring top_k notes;
+      // fourfold steps, top_k 5: 215 us for 218, 20: 302 for 267)
+      if (!closed && rounds == raise_at) {
+        raise_at *= 2;
         __syncthreads();
         const int n = sh.noted;
         if (n > kNotes) {
