@@ -23,7 +23,7 @@
 //    the second product as hi + lo, two 16-bit numbers, which keeps them to
 //    2^-17 (2^-22 for e4m3, whose values are exact in fp16);
 //  - e4m3 keys are multiplied as they are, by queries split into two e4m3
-//    numbers; e4m3 values are widened to fp16 in registers. The caches' scales
+//    numbers; e4m3 values are transposed as codes and widened to fp16 in registers. The caches' scales
 //    are factors of the scores and of the output.
 //
 // Measured (of a copy's 6.8 TB/s): 64 sequences of 1 to 8192 tokens, 8 key heads
@@ -134,6 +134,14 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two matrices of 16 x 16 8-bit numbers: of columns lane / 4 and lane / 4 + 8 the
+// rows 4 (lane % 4) .. + 3, for either.
+__device__ __forceinline__ void ldsm2_codes(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
       }
     }
 
-    float acc[kTiles][kT][4];  // columns 16 t + row (and + 8) of heads 8 j + 2 col, + 1 (e4m3: see below)
+    float acc[kTiles][kT][4];  // columns 16 t + row (and + 8) of heads 8 j + 2 col, + 1
     float m[kTiles][2], l[kTiles][2];  // the reference (0 before the first score) and the sum
     float limit[kTiles][2];           // the reference is raised for scores above
 #pragma unroll
@@ -532,7 +540,9 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         // scores: s[j] has tokens row (and + 8) of heads 8 j + 2 col, + 1
         float s[kTiles][4] = {}, s2[kTiles][4] = {};  // two chains
         {
-          const uint32_t addr = kbase + (lane & 15) * C::kPitch + (lane >> 4) * 16;
+          // (e4m3: the second 8 rows are tokens 12-15 and 8-11, see the values)
+          const int token = kE4m3 ? (lane & 15) ^ ((lane & 8) >> 1) : lane & 15;
+          const uint32_t addr = kbase + token * C::kPitch + (lane >> 4) * 16;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             uint32_t b[4];
@@ -554,7 +564,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             s[j][i] = (s[j][i] + s2[j][i]) * scale[j][i & 1];
-            if (mask != 0xFFFFu && ((mask >> (row + (i >> 1) * 8)) & 1u) == 0) s[j][i] = -CUDART_INF_F;
+            if (mask != 0xFFFFu && ((mask >> ((i >> 1) == 0 ? row : 8 + (kE4m3 ? row ^ 4 : row))) & 1u) == 0) s[j][i] = -CUDART_INF_F;
             above |= s[j][i] > limit[j][i & 1];
           }
         if (__any_sync(0xFFFFFFFFu, above)) {
@@ -593,7 +603,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         }
         // values, their columns as rows: b[0], b[1] 8 columns each of tokens
         // 0-7, b[2], b[3] of tokens 8-15
-        const uint32_t addr = vbase + ((lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
         auto accumulate = [&](int t, const uint32_t(&b)[4]) {
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
@@ -602,6 +611,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
           }
         };
         if constexpr (!kE4m3) {
+          const uint32_t addr = vbase + ((lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
           for (int t = 0; t < kT; ++t) {
             uint32_t b[4];
@@ -609,21 +619,23 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
             accumulate(t, b);
           }
         } else {
-          // 16 columns of codes a matrix: a register holds columns 2 row and
-          // 2 row + 1 of two tokens; the even columns of 32 make one tile, the
-          // odd ones the next
+          // 16 x 16 codes a matrix: a register holds a column's codes of rows 4 col
+          // .. 4 col + 3, of which the first two go with weights 2 col, 2 col + 1 of
+          // tokens 0-7, the others of 8-15. The rows are the tokens that the
+          // weights have there; with 12-15 before 8-11 no 8 rows share a bank. (With
+          // 16-bit matrices and byte permutes D = 64 took 4 % longer, 128 2 %.)
+          const int at = (lane >> 2 & 3) * 2 + (lane & 1), token = (lane & 2) != 0 ? 8 + (at ^ 4) : at;
+          const uint32_t addr = vbase + token * C::kPitch + (lane >> 4) * 16;
 #pragma unroll
           for (int t = 0; t < kT; t += 2) {
-            uint32_t b[4], even[4], odd[4];
-            ldsm4_trans(addr + t * 16, b);
+            uint32_t b[4];
+            ldsm2_codes(addr + t * 16, b);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              b[i] = __byte_perm(b[i], 0u, 0x3120);
-              even[i] = widen(b[i], false);
-              odd[i] = widen(b[i], true);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t c[4] = {widen(b[2 * i], false), widen(b[2 * i + 1], false), widen(b[2 * i], true),
+                                     widen(b[2 * i + 1], true)};
+              accumulate(t + i, c);
             }
-            accumulate(t, even);
-            accumulate(t + 1, odd);
           }
         }
       }
@@ -661,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         for (int t = 0; t < kT; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int d = kE4m3 ? (t & ~1) * 16 + (i >> 1) * 16 + 2 * row + (t & 1) : t * 16 + (i >> 1) * 8 + row;
+            const int d = t * 16 + (i >> 1) * 8 + row;
             mine[(8 * j - r0 + 2 * col + (i & 1)) * C::kOPitch + d] = acc[j][t][i];
           }
       __syncthreads();
