@@ -23,8 +23,8 @@
 //    the second product as hi + lo, two 16-bit numbers, which keeps them to
 //    2^-17 (2^-22 for e4m3, whose values are exact in fp16);
 //  - e4m3 keys are multiplied as they are, by queries split into two e4m3
-//    numbers; e4m3 values are transposed as codes and widened to fp16 in registers. The caches' scales
-//    are factors of the scores and of the output.
+//    numbers; e4m3 values are transposed as codes and widened to fp16 in
+//    registers. The caches' scales are factors of the scores and of the output.
 //
 // Measured (of a copy's 6.8 TB/s): 64 sequences of 1 to 8192 tokens, 8 key heads
 // of 4 query heads, D = 128, bf16, 1.07 GB: 174 us, 6.2 TB/s; one of 131071
@@ -47,23 +47,24 @@
 namespace wq {
 namespace {
 
-constexpr int kStep = 16;  // tokens a warp takes at a time
 // What beginning and ending an item costs, in units: every item takes so many
 // places more in the line, so that shares with many short items take no longer.
 constexpr int kItemCost = 1;
-// Shares of kLeast units are not made smaller (a join costs about as much);
-// where no sequence can have more, every item is a share and nothing is joined.
-constexpr int kLeast = 4;
+// Shares of so many units are not made smaller (a join costs about as much); where
+// no sequence can have more, every item is a share and nothing is joined.
+constexpr int least_units(int unit) { return unit > 64 ? 2 : 4; }
 // The weights are relative to a reference that is raised when a score passes it
 // by more than this (in powers of two), so that most steps need no maximum.
 constexpr float kSlack = 8.0f;
 
 // Blocks that share an SM: as many as the registers allow (a thread keeps D / 4
-// sums and D / 8 registers of queries for 8 heads, twice that for 16) and the
-// stages leave room for.
+// sums and D / 8 registers of queries for 8 heads, twice that for 16, and with
+// e4m3 two parts of a step) and the stages leave room for.
 constexpr int blocks_per_sm(int64_t d, bool e4m3, bool r16) {
+  if (r16 && e4m3) return 2;
   if (r16) return d <= 64 ? 4 : (d <= 128 ? 3 : 2);
-  return d <= 96 || (e4m3 && d <= 128) ? 4 : (d == 128 || e4m3 ? 3 : 2);
+  if (e4m3) return d <= 128 ? 3 : 2;
+  return d <= 96 ? 4 : (d == 128 ? 3 : 2);
 }
 // Shares that the space for partial results is for (a GB300 has 152 SMs).
 constexpr int max_shares(int64_t d, bool e4m3, bool r16) { return 160 * blocks_per_sm(d, e4m3, r16); }
@@ -75,6 +76,11 @@ struct Cfg {
   static constexpr int kTiles = kRows / 8;       // MMA columns of 8 heads
   static constexpr int kRowBytes = D * (kE4m3 ? 1 : 2);
   static constexpr int kPitch = kRowBytes + 16;  // an odd number of 16-byte words: ldmatrix without conflicts
+  // Tokens a warp takes at a time: of e4m3 codes twice as many, the same bytes, so
+  // that the places are found once for 32 (D = 64: 98 us for 113; 16 heads of
+  // D = 128: 245 for 304); not where the sums of 16 heads leave no registers for
+  // it (D = 256: 215 us for 158).
+  static constexpr int kStep = kE4m3 && (!kR16 || D <= 192) ? 32 : 16;
   static constexpr int kSide = kStep * kPitch;   // a step's keys (or values)
   static constexpr int kStage = 2 * kSide;
   static constexpr int kMisc = 1024;
@@ -91,7 +97,7 @@ struct Cfg {
   // A warp's sums on their way to the block's: kOut heads in the stage that was
   // read last. The pitch keeps the 32 words of a store apart.
   static constexpr int kOPitch = D + 4;  // floats
-  static constexpr int kOut = kE4m3 && kR16 ? 8 : kRows;
+  static constexpr int kOut = kE4m3 && kR16 && kStep == 16 ? 8 : kRows;
   static_assert(kOut * kOPitch * 4 <= kStage, "the sums fit a stage");
   // lanes that load one row (16 bytes each at a time)
   static constexpr int kLanes = kRowBytes % 128 == 0 ? 8 : (kRowBytes % 64 == 0 ? 4 : 2);
@@ -184,11 +190,11 @@ __device__ __forceinline__ void split_e4m3(uint2 w, float up, uint32_t& hi, uint
     lo |= static_cast<uint32_t>(d) << (16 * j);
   }
 }
-// Two e4m3 codes (the low or high half of w) as two fp16 numbers, exactly.
-__device__ __forceinline__ uint32_t widen(uint32_t w, bool high) {
-  const __nv_fp8x2_storage_t v = static_cast<__nv_fp8x2_storage_t>(high ? w >> 16 : w & 0xFFFFu);
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+// Four e4m3 codes as fp16 numbers, exactly: the low two and the high two.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& low, uint32_t& high) {
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(low), "=r"(high)
+      : "r"(w));
 }
 // x, y rounded to 16 bits (hi), and what that leaves (lo), packed.
 template <bool kF16>
@@ -296,7 +302,7 @@ __device__ __forceinline__ Line line_of(const Args& a, int per_seq, int shares) 
   most = __reduce_max_sync(0xFFFFFFFFu, most);
   x.total = __shfl_sync(0xFFFFFFFFu, x.upto, 31) * per_seq;
   x.share = quotient(x.total + shares - 1, shares);
-  const int least = most < kLeast + kItemCost ? most : kLeast + kItemCost;
+  const int least = most < least_units(kUnit) + kItemCost ? most : least_units(kUnit) + kItemCost;
   x.share = x.share > least ? x.share : least;
   return x;
 }
@@ -317,7 +323,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     attn_kernel(const Args a) {
   using C = Cfg<D, kE4m3, kR16>;
   constexpr int kK = kE4m3 ? D / 32 : D / 16, kT = D / 16, kWarps = C::kWarps, kThreads = C::kThreads;
-  constexpr int kUnit = C::kUnit, kTiles = C::kTiles;
+  constexpr int kUnit = C::kUnit, kTiles = C::kTiles, kStep = C::kStep, kParts = kStep / 16;
+  constexpr uint32_t kFull = kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   extern __shared__ __align__(128) uint8_t smem[];
   float* ml = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStage);  // [kWarps][16][2]
   int64_t* share = reinterpret_cast<int64_t*>(ml + kWarps * 16 * 2);  // [0] places of a share, [1] b, [2] those before b, [3] all
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
   const unsigned S = static_cast<unsigned>(a.kv.S);
   const uint32_t to_v = static_cast<uint32_t>(a.kv.Hkv) * S * C::kRowBytes;  // a page has fewer than 2^32 bytes
   const int32_t P = static_cast<int32_t>(a.kv.P);
-  struct Rows {  // a step's, one token each in lanes 0..15 (and again in 16..31)
+  struct Rows {  // a step's, one token each in lanes 0 .. kStep - 1 (16: and again in 16..31)
     unsigned place;  // of the row within its page's keys; bit 0: count the page if it is out of range
     int32_t page;    // -1 also where there is no token
     bool in;
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
   };
   new_item();
   auto look_up = [&](Rows& r) {
-    const unsigned t = ld.s.first + static_cast<unsigned>(ld.unit) * kUnit + warp * kStep + (lane & 15);
+    const unsigned t = ld.s.first + static_cast<unsigned>(ld.unit) * kUnit + warp * kStep + (lane & (kStep - 1));
     const unsigned j = static_cast<unsigned>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
     const unsigned at = t - j * S;
     r.in = t < ld.s.end;
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     // a row that is left out reads nothing: its copies have no bytes
     uint64_t from = reinterpret_cast<uint64_t>(a.kv.kv);
     if (ok) from += static_cast<uint64_t>(static_cast<uint32_t>(x.page)) * (2 * to_v) + (x.place & ~1u);
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & kFull;
     if (lane == 0) vmask[warp * C::kStages + stage] = mask;
     const uint32_t base = ring + stage * C::kStage + (lane / C::kLanes) * C::kPitch + (lane % C::kLanes) * 16;
     const auto rows_from = [&](auto whole) {
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         }
       }
     };
-    if (mask == 0xFFFFu) rows_from([] { return true; });
+    if (mask == kFull) rows_from([] { return true; });
     else rows_from([] { return false; });
   };
   Rows ahead{};  // the step to load next
@@ -537,12 +544,13 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
       const uint32_t mask = vmask[warp * C::kStages + stage];
       const uint32_t kbase = ring + stage * C::kStage, vbase = kbase + C::kSide;
       if (mask != 0) {
-        // scores: s[j] has tokens row (and + 8) of heads 8 j + 2 col, + 1
-        float s[kTiles][4] = {}, s2[kTiles][4] = {};  // two chains
-        {
+        // scores: s[part][j] has tokens row (and + 8) of heads 8 j + 2 col, + 1
+        float s[kParts][kTiles][4] = {}, s2[kParts][kTiles][4] = {};  // two chains
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
           // (e4m3: the second 8 rows are tokens 12-15 and 8-11, see the values)
           const int token = kE4m3 ? (lane & 15) ^ ((lane & 8) >> 1) : lane & 15;
-          const uint32_t addr = kbase + token * C::kPitch + (lane >> 4) * 16;
+          const uint32_t addr = kbase + (part * 16 + token) * C::kPitch + (lane >> 4) * 16;
 #pragma unroll
           for (int k = 0; k < kK; ++k) {
             uint32_t b[4];
@@ -550,29 +558,34 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) {
               if constexpr (kE4m3) {
-                mma_e4m3(s[j], b, q1[j][k]);
-                mma_e4m3(s2[j], b, q2[j][k]);
+                mma_e4m3(s[part][j], b, q1[j][k]);
+                mma_e4m3(s2[part][j], b, q2[j][k]);
               } else {
-                mma<false>((k & 1) ? s2[j] : s[j], b, q1[j][k]);
+                mma<false>((k & 1) ? s2[part][j] : s[part][j], b, q1[j][k]);
               }
             }
           }
         }
         bool above = false;
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
+        for (int part = 0; part < kParts; ++part)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[j][i] = (s[j][i] + s2[j][i]) * scale[j][i & 1];
-            if (mask != 0xFFFFu && ((mask >> ((i >> 1) == 0 ? row : 8 + (kE4m3 ? row ^ 4 : row))) & 1u) == 0) s[j][i] = -CUDART_INF_F;
-            above |= s[j][i] > limit[j][i & 1];
-          }
+          for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float& x = s[part][j][i];
+              x = (x + s2[part][j][i]) * scale[j][i & 1];
+              const int token = part * 16 + ((i >> 1) == 0 ? row : 8 + (kE4m3 ? row ^ 4 : row));
+              if (mask != kFull && ((mask >> token) & 1u) == 0) x = -CUDART_INF_F;
+              above |= x > limit[j][i & 1];
+            }
         if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
           for (int j = 0; j < kTiles; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float top = fmaxf(s[j][i], s[j][i + 2]);
+              float top = fmaxf(s[0][j][i], s[0][j][i + 2]);
+              if constexpr (kParts == 2) top = fmaxf(top, fmaxf(s[1][j][i], s[1][j][i + 2]));
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
               const bool raise = top > limit[j][i];
@@ -588,53 +601,57 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
               }
             }
         }
-        uint32_t hi[kTiles][2], lo[kTiles][2];  // tokens 0-7 and 8-15 of head 8 j + row
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float p0 = exp2_fast(s[j][2 * i] - m[j][0]), p1 = exp2_fast(s[j][2 * i + 1] - m[j][1]);
-            l[j][0] += p0;
-            l[j][1] += p1;
-            split_pair<kE4m3>(p0, p1, hi[j][i], lo[j][i]);
-            hi[j][i] = transpose8(hi[j][i]);
-            lo[j][i] = transpose8(lo[j][i]);
-          }
-        }
-        // values, their columns as rows: b[0], b[1] 8 columns each of tokens
-        // 0-7, b[2], b[3] of tokens 8-15
-        auto accumulate = [&](int t, const uint32_t(&b)[4]) {
+        for (int part = 0; part < kParts; ++part) {
+            uint32_t hi[kTiles][2], lo[kTiles][2];  // tokens 0-7 and 8-15 of head 8 j + row
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
-            mma<kE4m3>(acc[j][t], b, hi[j]);
-            mma<kE4m3>(acc[j][t], b, lo[j]);
-          }
-        };
-        if constexpr (!kE4m3) {
-          const uint32_t addr = vbase + ((lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
-#pragma unroll
-          for (int t = 0; t < kT; ++t) {
-            uint32_t b[4];
-            ldsm4_trans(addr + t * 32, b);
-            accumulate(t, b);
-          }
-        } else {
-          // 16 x 16 codes a matrix: a register holds a column's codes of rows 4 col
-          // .. 4 col + 3, of which the first two go with weights 2 col, 2 col + 1 of
-          // tokens 0-7, the others of 8-15. The rows are the tokens that the
-          // weights have there; with 12-15 before 8-11 no 8 rows share a bank. (With
-          // 16-bit matrices and byte permutes D = 64 took 4 % longer, 128 2 %.)
-          const int at = (lane >> 2 & 3) * 2 + (lane & 1), token = (lane & 2) != 0 ? 8 + (at ^ 4) : at;
-          const uint32_t addr = vbase + token * C::kPitch + (lane >> 4) * 16;
-#pragma unroll
-          for (int t = 0; t < kT; t += 2) {
-            uint32_t b[4];
-            ldsm2_codes(addr + t * 16, b);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t c[4] = {widen(b[2 * i], false), widen(b[2 * i + 1], false), widen(b[2 * i], true),
-                                     widen(b[2 * i + 1], true)};
-              accumulate(t + i, c);
+              const float p0 = exp2_fast(s[part][j][2 * i] - m[j][0]), p1 = exp2_fast(s[part][j][2 * i + 1] - m[j][1]);
+              l[j][0] += p0;
+              l[j][1] += p1;
+              split_pair<kE4m3>(p0, p1, hi[j][i], lo[j][i]);
+              hi[j][i] = transpose8(hi[j][i]);
+              lo[j][i] = transpose8(lo[j][i]);
+            }
+          }
+          // values, their columns as rows: b[0], b[1] 8 columns each of tokens
+          // 0-7, b[2], b[3] of tokens 8-15
+          auto accumulate = [&](int t, const uint32_t(&b)[4]) {
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+              mma<kE4m3>(acc[j][t], b, hi[j]);
+              mma<kE4m3>(acc[j][t], b, lo[j]);
+            }
+          };
+          if constexpr (!kE4m3) {
+            const uint32_t addr = vbase + (part * 16 + (lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+              uint32_t b[4];
+              ldsm4_trans(addr + t * 32, b);
+              accumulate(t, b);
+            }
+          } else {
+            // 16 x 16 codes a matrix: a register holds a column's codes of rows 4 col
+            // .. 4 col + 3, of which the first two go with weights 2 col, 2 col + 1 of
+            // tokens 0-7, the others of 8-15. The rows are the tokens that the
+            // weights have there; with 12-15 before 8-11 no 8 rows share a bank. (With
+            // 16-bit matrices and byte permutes D = 64 took 4 % longer, 128 2 %.)
+            const int at = (lane >> 2 & 3) * 2 + (lane & 1), token = (lane & 2) != 0 ? 8 + (at ^ 4) : at;
+            const uint32_t addr = vbase + (part * 16 + token) * C::kPitch + (lane >> 4) * 16;
+#pragma unroll
+            for (int t = 0; t < kT; t += 2) {
+              uint32_t b[4];
+              ldsm2_codes(addr + t * 16, b);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t c[4];
+                widen(b[2 * i], c[0], c[2]);
+                widen(b[2 * i + 1], c[1], c[3]);
+                accumulate(t + i, c);
+              }
             }
           }
         }
@@ -819,7 +836,7 @@ cudaError_t launch(const Ctx& c, Args a) {
   const int64_t items = a.kv.B * a.kv.Hkv * a.chunks, units = (most + C::kUnit - 1) / C::kUnit;
   int64_t grid = C::kBlocksPerSm * c.sm_count;
   if (grid > max_shares(D, kE4m3, kR16)) grid = max_shares(D, kE4m3, kR16);
-  a.direct = units <= kLeast && items <= kMaxDim;
+  a.direct = units <= least_units(C::kUnit) && items <= kMaxDim;
   if (a.direct) grid = items;
   else if (items < grid && items * units < grid) grid = items * units;
   a.shares = static_cast<int>(grid);
