@@ -370,3 +370,51 @@ def test_captured_calls_have_scratch_of_their_own():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert all(not bool(b.any()) for b in _lib._ws_cache.values())
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_from_another_stream(captured):
+    """Lengths and tokens that another stream's kernels have just written, behind an event."""
+    g = torch.Generator().manual_seed(6)
+    B, W, S, Hkv, D = 4, 64, 16, 2, 64
+    kv = torch.randn((B * W, 2, Hkv, S, D), generator=g).bfloat16().cuda()
+    table = torch.randperm(B * W, generator=g).int().reshape(B, W).cuda()
+    q = torch.randn((B, 8, D), generator=g).bfloat16().cuda()
+    k = torch.randn((B, Hkv, D), generator=g).bfloat16().cuda()
+    lens, pos = (torch.ones(B, dtype=torch.int32, device="cuda") for _ in range(2))
+    slow = torch.ones((2048, 2048), device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(kv):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            y = slow @ slow  # 2048 in every place
+            pos.copy_((y[0, :B] / 4).int() + torch.arange(B, device="cuda", dtype=torch.int32))
+            lens.copy_(pos + 1)
+        torch.cuda.current_stream().wait_stream(side)
+        wq.kv_append(k, k, pos, table, kv)
+        return wq.kv_attn_decode(q, kv, table, lens)
+
+    mine = kv.clone()
+    n = 512 + torch.arange(B, dtype=torch.int32, device="cuda")
+    wq.kv_append(k, k, n, table, kv)
+    want = wq.kv_attn_decode(q, kv, table, n + 1)
+    torch.cuda.synchronize()
+    if captured:
+        step(mine.clone())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(mine)
+        for _ in range(5):
+            lens.fill_(1)
+            pos.fill_(0)
+            graph.replay()
+            assert torch.equal(got, want)
+        assert torch.equal(mine, kv)
+    else:
+        for _ in range(20):
+            lens.fill_(1)
+            pos.fill_(0)
+            assert torch.equal(step(mine), want)
+        assert torch.equal(mine, kv)

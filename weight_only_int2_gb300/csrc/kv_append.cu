@@ -17,6 +17,7 @@
 // rounded quotient (Markstein, IBM J. Res. Dev. 34(1), 1990); x is clamped to
 // +-500 w first (rounded to bf16, still beyond the largest code), so that nothing
 // overflows on the way.
+#include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
 
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCache a,
   if (t0 >= T) return;
   const uint32_t i = in % (2 * row), side = i >= row, at = i - side * row, h = at / per_head, d = (at - h * per_head) * kValues;
 
+  cl::griddep_wait();
   uint4 x[kTokens][kLoads];
   int32_t s[kTokens], p[kTokens];
 #pragma unroll
@@ -143,8 +145,7 @@ cudaError_t launch_kv_append(const Ctx& c, const KvCache& a, const uint16_t* k, 
   if (grid > kMaxDim) return cudaErrorInvalidConfiguration;
   const auto kern = e4m3 ? (many ? kv_append_kernel<true, 2> : kv_append_kernel<true, 1>)
                          : (many ? kv_append_kernel<false, 2> : kv_append_kernel<false, 1>);
-  kern<<<static_cast<unsigned>(grid), kThreads, 0, c.stream>>>(a, k, v, k_stride, v_stride, T, seq, pos, bad);
-  return cudaGetLastError();
+  return launch_early(c, grid, kThreads, 0, kern, a, k, v, k_stride, v_stride, T, seq, pos, bad);
 }
 
 }  // namespace wq

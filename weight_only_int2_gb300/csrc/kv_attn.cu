@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
   const int row = lane >> 2, col = lane & 3;
   const int per_seq = static_cast<int>(a.kv.Hkv) * a.chunks;
 
+  cl::griddep_wait();
   cl::griddep_launch_dependents();  // the join may start; it waits for this kernel's end
   if (warp == 1) {  // sequences without tokens
     for (int64_t b = blockIdx.x; b < a.kv.B; b += gridDim.x) {
@@ -840,19 +841,9 @@ cudaError_t launch(const Ctx& c, Args a) {
   if (a.direct) grid = items;
   else if (items < grid && items * units < grid) grid = items * units;
   a.shares = static_cast<int>(grid);
-  attn_kernel<D, kE4m3, kR16><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, c.stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_early(c, grid, C::kThreads, C::kSmem, attn_kernel<D, kE4m3, kR16>, a);
   if (e != cudaSuccess || a.direct) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.kv.B * a.Hq));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, kE4m3, kR16>, static_cast<const Args>(a));
+  return launch_early(c, a.kv.B * a.Hq, kJoinThreads, 0, join_kernel<D, kE4m3, kR16>, a);
 }
 
 template <int D>

@@ -195,6 +195,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
     fork_kernel(SeqTables t, const int32_t* parent, const int32_t* child, int n, int32_t* table_out,
                 int32_t* lens_out, int32_t* ref_out, int32_t* granted, Scratch w) {
   WQ_TEAM(team);
+  cl::griddep_wait();
   cl::cluster_arrive();
   cl::griddep_launch_dependents();  // the copy may start; it waits for this kernel's end
   const int64_t cap = t.W * t.S;
@@ -264,6 +265,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
     reserve_kernel(SeqTables t, const int32_t* new_lens, int32_t* table_out, int32_t* ref_out, int32_t* granted,
                    Scratch w) {
   WQ_TEAM(team);
+  cl::griddep_wait();
   cl::cluster_arrive();
   const int64_t cap = t.W * t.S;
   auto needs = [&](int64_t b) -> int64_t {
@@ -306,6 +308,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
     free_kernel(SeqTables t, const int32_t* seqs, int64_t n, int32_t* lens_out, int32_t* ref_out, int32_t* bad) {
   WQ_TEAM(team);
+  cl::griddep_wait();
   const int lane = threadIdx.x & 31;
   copy_array(team, t.ref, ref_out, t.P);
   copy_array(team, t.lens, lens_out, t.B);
@@ -353,6 +356,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kMeta)
     compact_kernel(SeqTables t, int32_t* table_out, int32_t* ref_out, int32_t* remap, int32_t* n_live, Scratch w) {
   WQ_TEAM(team);
+  cl::griddep_wait();
   cl::griddep_launch_dependents();  // the copy may start; it waits for this kernel's end
   const int lane = threadIdx.x & 31;
   team.sync();  // every block runs, before the first store into another's shared memory
@@ -462,24 +466,14 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PagePool p, const in
   }
 }
 
-// `after`: launched with the kernel before it in the stream, whose lists it reads.
 cudaError_t copy_pages(const Ctx& c, const PagePool& p, const int32_t* src, const int32_t* dst, int64_t most,
-                       const int32_t* count, int32_t* bad, bool after) {
+                       const int32_t* count, int32_t* bad) {
   if (most == 0) return cudaSuccess;
   const int threads = p.page_bytes > kCopyThreads * kVecs * 8 ? kCopyThreads : kSmallCopyThreads;
   const int64_t unit = threads * kVecs * 16, per_page = (p.page_bytes + unit - 1) / unit;
   int64_t grid = (threads == kCopyThreads ? 64 : 256) * static_cast<int64_t>(c.sm_count);
   if (most < grid && most * p.L < grid && most * p.L * per_page < grid) grid = most * p.L * per_page;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, copy_kernel, p, src, dst, most, count, bad);
+  return launch_early(c, grid, threads, 0, copy_kernel, p, src, dst, most, count, bad);
 }
 
 }  // namespace
@@ -491,39 +485,35 @@ size_t kv_pages_scratch(int64_t n, int64_t, int64_t, int64_t P) {
 
 cudaError_t launch_pages_copy(const Ctx& c, const PagePool& p, const int32_t* src, const int32_t* dst, int64_t n,
                               int32_t* bad) {
-  return copy_pages(c, p, src, dst, n, nullptr, bad, false);
+  return copy_pages(c, p, src, dst, n, nullptr, bad);
 }
 
 cudaError_t launch_pages_fork(const Ctx& c, const PagePool& p, const SeqTables& t, const int32_t* parent,
                               const int32_t* child, int64_t n, int32_t* table_out, int32_t* lens_out,
                               int32_t* ref_out, int32_t* granted, void* scratch) {
   const Scratch w = split_scratch(scratch, n, t.P);
-  fork_kernel<<<kBlocks, kMeta, 0, c.stream>>>(t, parent, child, static_cast<int>(n), table_out, lens_out, ref_out,
-                                               granted, w);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = copy_pages(c, p, w.src, w.dst, n, w.count, nullptr, true);
+  cudaError_t e = launch_early(c, kBlocks, kMeta, 0, fork_kernel, t, parent, child, static_cast<int>(n), table_out,
+                               lens_out, ref_out, granted, w);
+  if (e == cudaSuccess) e = copy_pages(c, p, w.src, w.dst, n, w.count, nullptr);
   return e;
 }
 
 cudaError_t launch_pages_reserve(const Ctx& c, const SeqTables& t, const int32_t* new_lens, int32_t* table_out,
                                  int32_t* ref_out, int32_t* granted, void* scratch) {
-  reserve_kernel<<<kBlocks, kMeta, 0, c.stream>>>(t, new_lens, table_out, ref_out, granted,
-                                                  split_scratch(scratch, t.B, t.P));
-  return cudaGetLastError();
+  return launch_early(c, kBlocks, kMeta, 0, reserve_kernel, t, new_lens, table_out, ref_out, granted,
+                      split_scratch(scratch, t.B, t.P));
 }
 
 cudaError_t launch_pages_free(const Ctx& c, const SeqTables& t, const int32_t* seqs, int64_t n, int32_t* lens_out,
                               int32_t* ref_out, int32_t* bad) {
-  free_kernel<<<kBlocks, kMeta, 0, c.stream>>>(t, seqs, n, lens_out, ref_out, bad);
-  return cudaGetLastError();
+  return launch_early(c, kBlocks, kMeta, 0, free_kernel, t, seqs, n, lens_out, ref_out, bad);
 }
 
 cudaError_t launch_pages_compact(const Ctx& c, const PagePool& p, const SeqTables& t, int32_t* table_out,
                                  int32_t* ref_out, int32_t* remap, int32_t* n_live, void* scratch) {
   const Scratch w = split_scratch(scratch, 0, t.P);
-  compact_kernel<<<kBlocks, kMeta, 0, c.stream>>>(t, table_out, ref_out, remap, n_live, w);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = copy_pages(c, p, w.src, w.dst, t.P / 2, w.count, nullptr, true);
+  cudaError_t e = launch_early(c, kBlocks, kMeta, 0, compact_kernel, t, table_out, ref_out, remap, n_live, w);
+  if (e == cudaSuccess) e = copy_pages(c, p, w.src, w.dst, t.P / 2, w.count, nullptr);
   return e;
 }
 

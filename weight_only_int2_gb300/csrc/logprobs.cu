@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
   const int places = g.units + kRowCost;
   const uint32_t V = static_cast<uint32_t>(a.V);
   const float slack = kSlack / g.c;
+  cl::griddep_wait();
   cl::griddep_launch_dependents();  // the join may start; it waits for this kernel's end
 
   // a piece: units [unit, end) of row, `left` places of the share from there on
@@ -947,6 +948,7 @@ template <bool kBf16, bool kIds>
 __global__ void __launch_bounds__(kThreads, 4) short_rows_kernel(const Args g) {
   constexpr int kN = Vec<kBf16>::kN;
   __shared__ uint64_t all_notes[kWarps][kWarpNotes], all_best[kWarps][kMaxTopK];
+  cl::griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const LogprobArgs& a = g.a;
@@ -1075,8 +1077,7 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
   if (vectors <= 128 || (vectors <= 2048 && a.T >= 2 * vectors)) {
     const auto kern = bf16 ? (ids ? short_rows_kernel<true, true> : short_rows_kernel<true, false>)
                            : (ids ? short_rows_kernel<false, true> : short_rows_kernel<false, false>);
-    kern<<<static_cast<unsigned>((a.T + kWarps - 1) / kWarps), kThreads, 0, c.stream>>>(g);
-    return cudaGetLastError();
+    return launch_early(c, (a.T + kWarps - 1) / kWarps, kThreads, 0, kern, g);
   }
   // a row may begin anywhere within its first vector
   g.units = static_cast<int>(((a.V + 2 * (per - 1)) / per + kThreads - 1) / kThreads);
@@ -1092,19 +1093,9 @@ cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a) {
                          : (ids ? logprobs_kernel<false, true> : logprobs_kernel<false, false>);
   cudaError_t e = raise_smem_limit(lim[bf16 * 2 + ids], kern, c.device, sizeof(Shared));
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(g.shares), kThreads, sizeof(Shared), c.stream>>>(g);
-  e = cudaGetLastError();
+  e = launch_early(c, g.shares, kThreads, sizeof(Shared), kern, g);
   if (e != cudaSuccess || g.shares < 2) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(g.shares - 1));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const Args>(g));
+  return launch_early(c, g.shares - 1, kThreads, 0, join_kernel, g);
 }
 
 }  // namespace wq

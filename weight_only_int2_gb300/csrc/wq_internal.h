@@ -69,6 +69,29 @@ cudaError_t raise_smem_limit(SmemLimit& lim, Kernel kern, int device, size_t byt
   return e;
 }
 
+// Launches a kernel that may begin while the one before it in the stream ends:
+// it reads and writes nothing before its griddepcontrol.wait, and lets the next
+// one begin only after that.
+template <typename T>
+struct Same {
+  using type = T;
+};
+template <typename... P>
+cudaError_t launch_early(const Ctx& c, int64_t grid, int threads, size_t smem, void (*kern)(P...),
+                         typename Same<P>::type... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Builds a 2-D tiled TMA descriptor over a row-major matrix of 32-bit words.
 // swizzle_bytes 0 (none), 32, 64 or 128: the shared-memory tile is written
 // with that TMA swizzle (16-byte chunk index XOR address bits 7 and up; the
