@@ -3,14 +3,14 @@
 //
 // Bound: a token's place takes three loads one after the other (its sequence and
 // position, then the page id), so a few tokens cost that latency (64 tokens of 8
-// key heads by 128: 2.2 us, nearly all of it the launch), and many the read and
+// key heads by 128: 1.8 us, nearly all of it the launch), and many the read and
 // the write of their values, if enough of them are on their way: a thread loads
 // its values before it knows where they go, with many tokens for two in a row, in
 // no more than 32 registers, so that an SM holds its 2048 threads. 12289 tokens of
-// 8 key heads by 128 into e4m3, 75.7 MB: 17.4 us, 4.3 TB/s; there the issue is
+// 8 key heads by 128 into e4m3, 75.7 MB: 16.9 us, 4.5 TB/s; there the issue is
 // next (three quarters of its slots: the codes and the indexes; with float32
-// operations one by one 18.6 us). One token a thread 19.2 us, four 20.3 us (72
-// registers), eight 23.6 us; blocks of 512 threads 19.3 us.
+// operations one by one 1.2 us more). Where two tokens a thread took 18.5
+// us, one took 19.2, four 20.3 (72 registers), eight 23.6; blocks of 512 threads 19.3.
 //
 // The e4m3 code is that of the IEEE quotient x / w. With y = RN(1 / w),
 // q = RN(x y) and r = x - q w (exact in one fma), RN(q + r y) is the correctly
@@ -138,8 +138,8 @@ cudaError_t launch_kv_append(const Ctx& c, const KvCache& a, const uint16_t* k, 
                              int64_t v_stride, int64_t T, const int32_t* seq, const int32_t* pos, int32_t* bad) {
   const bool e4m3 = a.type == WQ_KV_E4M3;
   const int64_t chunks = 2 * a.Hkv * a.D / (e4m3 ? 16 : 8);
-  // one token a thread while the SMs hold them all at once (64 tokens: 2.2 us, two
-  // a thread 2.5 us)
+  // one token a thread while the SMs hold them all at once (64 tokens: two a
+  // thread take 0.3 us more)
   const bool many = T * chunks > int64_t{8} * kThreads * c.sm_count;
   const int64_t grid = ((many ? (T + 1) / 2 : T) * chunks + kThreads - 1) / kThreads;
   if (grid > kMaxDim) return cudaErrorInvalidConfiguration;

@@ -32,7 +32,7 @@
 // key heads of 6, D = 256, e4m3, 0.95 GB: 161 us, 5.9 TB/s, where the issue is half
 // taken (widening the values) and the tensor pipe a third. A call has about 12 us
 // that do not stream: the start, the last block's end and the join (8 us by
-// itself, half of it under the first kernel's end). 77 tokens: 4.5 us. From L2 the
+// itself, half of it under the first kernel's end). 77 tokens: 3.8 us. From L2 the
 // same loops run at 10.7 TB/s, so they are not the bound. Several waves of shares
 // instead of one (the one long sequence: 145 us), shares taken by tickets (124 us)
 // and a join by the block that comes last (6 to 25 us more) were slower.

@@ -9,8 +9,8 @@
 // ascending ids, so nothing depends on timing. The pages themselves are moved by
 // a second kernel that reads the (source, destination) list from device memory;
 // it is bound by HBM and is launched before the first one has ended.
-// Measured: fork of 16 sequences in a pool of 1024 pages with its copies 9 us, free
-// and reserve for 256 sequences in a pool of 65536 pages 8.6 us each (one block:
+// Measured: fork of 16 sequences in a pool of 1024 pages with its copies 8.6 us,
+// free and reserve for 256 sequences in a pool of 65536 pages 8.2 us each (one block:
 // 32 and 31 us), compact's first kernel for 4096 pages 10 us, all latency:
 // barriers and dependent loads. Pages: 1.07 GB moved in 160 us, 6.7 TB/s.
 #include "wq_cluster.cuh"

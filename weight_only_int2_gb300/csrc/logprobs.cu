@@ -18,7 +18,7 @@
 // and best, 6.6 with ids, 5.8 with the best 5; 2049 rows of 248320, 1.02 GB, 151
 // us (6.7 TB/s), 176, 218 and with the best 20 267: a row's ends, the barriers of
 // its notes and the notes themselves, about 10 us a row at three rows an SM, are
-// what the other two blocks do not hide. 1 row with the best 20: 13 us, of which
+// what the other two blocks do not hide. 1 row with the best 20: 12 us, of which
 // the join is 4; 96 float32 rows of 100003 with the best 8: 26 us.
 //  - All rows are one line of units of 4 KB (a 16-byte vector per thread), cut
 //    into equal shares, one per block, several blocks per SM; a second kernel
