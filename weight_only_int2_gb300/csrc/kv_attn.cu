@@ -29,8 +29,8 @@
 // Measured (of a copy's 6.8 TB/s): 64 sequences of 1 to 8192 tokens, 8 key heads
 // of 4 query heads, D = 128, bf16, 1.07 GB: 174 us, 6.2 TB/s; one of 131071
 // tokens, 40 query heads, 537 MB: 92 us, 5.9 TB/s; 48 of up to 16384 tokens, 4
-// key heads of 6, D = 256, e4m3, 0.95 GB: 161 us, 5.9 TB/s, where the issue is half
-// taken (widening the values) and the tensor pipe a third. A call has about 12 us
+// key heads of 6, D = 256, e4m3, 0.95 GB: 160 to 165 us, 5.8 TB/s, where a third of
+// the issue and of the tensor pipe is taken. A call has about 12 us
 // that do not stream: the start, the last block's end and the join (8 us by
 // itself, half of it under the first kernel's end). 77 tokens: 3.8 us. From L2 the
 // same loops run at 10.7 TB/s, so they are not the bound. Several waves of shares
