@@ -120,6 +120,8 @@ struct Args {
   float* parts;      // partial results, two per share
   int shares;        // at most
   bool direct;       // a share per item, nothing cut
+  bool by_cut;       // the join has per_join blocks for every end of a share, else for every sequence
+  int per_join;
   uint32_t div_mul;  // t / S = (t * div_mul) >> div_shift for t < 2^31
   int div_shift;
 };
@@ -741,29 +743,56 @@ template <int D, bool kE4m3, bool kR16>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   constexpr int kRows = kR16 ? 16 : 8, kCols = D / 4, kGroups = kJoinThreads / kCols, kBatch = 8;
   constexpr int kUnit = Cfg<D, kE4m3, kR16>::kUnit;
-  __shared__ int64_t found[3];  // share, places before the sequence, its places
+  __shared__ int64_t found[4];  // share, sequence (-1: none), places before it, its places
   __shared__ float4 some[kGroups][kCols];
   __shared__ float2 some_ml[kGroups];
   const int tid = threadIdx.x;
   const int per_seq = static_cast<int>(a.kv.Hkv) * a.chunks;
-  const int64_t b = blockIdx.x / a.Hq;
-  const int hq = static_cast<int>(blockIdx.x - b * a.Hq), h = hq / a.G, in = hq - h * a.G, r = in & 15;
-  const int hc = h * a.chunks + (in >> 4);
+  // the head of this block, or the end of a share and a row of the item there
+  const int64_t at = blockIdx.x / a.per_join;
+  const int part = static_cast<int>(blockIdx.x - at * a.per_join);
   if (tid < 32) {
     const Line line = line_of<kUnit>(a, per_seq, a.shares);
-    if (b >= line.b0 && b < line.b1) {
+    const int64_t place = (at + 1) * line.share;
+    if (tid == 0) found[1] = -1;
+    __syncwarp();
+    if (a.by_cut ? place >= line.before * per_seq && place < line.upto * per_seq : at >= line.b0 && at < line.b1) {
       int64_t before = line.before;
-      for (int64_t i = line.b0; i < b; ++i) before += places(span_of<kUnit>(a, i));
-      found[0] = line.share;
-      found[1] = before;
-      found[2] = places(span_of<kUnit>(a, b));
+      for (int64_t b = line.b0; b < line.b1; ++b) {
+        const int u = places(span_of<kUnit>(a, b));
+        if (a.by_cut ? place < (before + u) * per_seq : b == at) {
+          found[0] = line.share;
+          found[1] = b;
+          found[2] = before;
+          found[3] = u;
+          break;
+        }
+        before += u;
+      }
     }
   }
   __syncthreads();
-  const int64_t c = found[0], before = found[1], len = found[2];
-  const int64_t item0 = before * per_seq + hc * len + kItemCost, item1 = item0 + len - kItemCost;
-  const int64_t p0 = len == 0 ? 0 : quotient(item0, c);
-  const int n = len == 0 ? 0 : static_cast<int>(quotient(item1 - 1, c) - p0) + 1;
+  const int64_t c = found[0], b = found[1], before = found[2], len = found[3];
+  int hc = 0, r = part, hq = part, n = 0;
+  int64_t p0 = 0;
+  if (b >= 0 && len > 0) {
+    if (a.by_cut) {
+      hc = static_cast<int>(quotient((at + 1) * c - before * per_seq, len));
+    } else {
+      const int in = hq % a.G;
+      hc = hq / a.G * a.chunks + (in >> 4);
+      r = in & 15;
+    }
+    const int64_t item0 = before * per_seq + hc * len + kItemCost, item1 = item0 + len - kItemCost;
+    p0 = quotient(item0, c);
+    n = static_cast<int>(quotient(item1 - 1, c) - p0) + 1;
+    if (a.by_cut) {
+      // an item is joined at the first end of a share inside it
+      const int chunk = hc % a.chunks;
+      if (p0 != at || r >= a.G - chunk * 16) n = 0;
+      hq = hc / a.chunks * a.G + chunk * 16 + r;
+    }
+  }
   const int g = tid / kCols, d = 4 * (tid - g * kCols);
   cl::griddep_wait();
   if (n <= 1) return;
@@ -823,7 +852,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
       o.z += v.z * f;
       o.w += v.w * f;
     }
-    put<D>(a, b, hq, 4 * tid, o, M, L, kE4m3 ? a.kv.v_scale[h] : 1.0f);
+    put<D>(a, b, hq, 4 * tid, o, M, L, kE4m3 ? a.kv.v_scale[hq / a.G] : 1.0f);
   }
 }
 
@@ -843,7 +872,11 @@ cudaError_t launch(const Ctx& c, Args a) {
   a.shares = static_cast<int>(grid);
   e = launch_early(c, grid, C::kThreads, C::kSmem, attn_kernel<D, kE4m3, kR16>, a);
   if (e != cudaSuccess || a.direct) return e;
-  return launch_early(c, a.kv.B * a.Hq, kJoinThreads, 0, join_kernel<D, kE4m3, kR16>, a);
+  const int64_t heads = a.kv.B * a.Hq, rows = a.G < 16 ? a.G : 16, cuts = (grid - 1) * rows;
+  a.by_cut = cuts < heads;
+  a.per_join = static_cast<int>(a.by_cut ? rows : a.Hq);
+  if (cuts == 0) return cudaSuccess;  // one share
+  return launch_early(c, a.by_cut ? cuts : heads, kJoinThreads, 0, join_kernel<D, kE4m3, kR16>, a);
 }
 
 template <int D>
