@@ -130,6 +130,16 @@ def test_attn_long_and_many(B, n, e4m3):
     c.check(*c.call())
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,G,Hkv,longest", [(200, 4, 4, 1100), (150, 23, 3, 1100), (200, 4, 4, 900), (450, 1, 2, 70)])
+def test_attn_more_items_than_blocks(B, G, Hkv, longest, e4m3):
+    """Uneven lengths, some zero, with more (sequence, head) items than blocks fit the GPU."""
+    lens = np.random.default_rng(B).integers(0, 120, B)
+    lens[[0, B // 2, B - 1]] = 0, longest, longest - 17
+    c = Case([int(n) for n in lens], Hkv=Hkv, G=G, e4m3=e4m3, seed=G + longest)
+    c.check(*c.call())
+
+
 def test_attn_large_scores():
     """Scores of some hundreds: weights that differ by more than float32 holds."""
     c = Case([200, 64, 333], q_scale=40.0, seed=9)
