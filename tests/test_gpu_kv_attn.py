@@ -123,6 +123,14 @@ def test_attn_window(window):
     c.check(*c.call(window=window, bad_count=bad), window=window, bad=bad)
 
 
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 12), (192, 5), (256, 16)])
+@pytest.mark.parametrize("window", [1, 15, 16, 31, 32, 33, 127, 129, 1000])
+def test_attn_window_of_an_e4m3_cache(window, D, G):
+    c = Case(LENS + [31, 32, 33, 1500], S=7, G=G, D=D, seed=window + D, e4m3=True)
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.check(*c.call(window=window, bad_count=bad), window=window, bad=bad)
+
+
 @pytest.mark.parametrize("B,n,e4m3", [(1, 1, False), (1, 5000, False), (1, 40000, False), (1, 40001, True),
                                      (3, 9001, False), (200, 37, False), (400, 3, True)])
 def test_attn_long_and_many(B, n, e4m3):
@@ -154,6 +162,17 @@ def test_attn_page_ids_and_lengths_out_of_range():
     c.table[2, :] = [2 ** 31 - 1, -2 ** 31, -5, -1, -1, -1, -1, -1, -1]  # nothing left
     c.lens[3] = -7
     c.lens[4] = 2 ** 31 - 1  # counts as W * S: the other pages are out of range
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.check(*c.call(bad_count=bad), bad=bad)
+
+
+@pytest.mark.parametrize("S", [3, 16, 40])
+def test_attn_pages_out_of_range_of_an_e4m3_cache(S):
+    c = Case([40, 64, 33, 100, 16], W=-(-160 // S), S=S, D=128, seed=S, e4m3=True)
+    c.table[0, 1] = -1
+    c.table[1, 0] = c.kv.shape[0]
+    c.table[2, :] = -5
+    c.lens[4] = 2 ** 31 - 1
     bad = torch.zeros(1, dtype=torch.int32, device="cuda")
     c.check(*c.call(bad_count=bad), bad=bad)
 
