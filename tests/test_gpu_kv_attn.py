@@ -168,11 +168,11 @@ def test_attn_page_ids_and_lengths_out_of_range():
 
 @pytest.mark.parametrize("S", [3, 16, 40])
 def test_attn_pages_out_of_range_of_an_e4m3_cache(S):
-    c = Case([40, 64, 33, 100, 16], W=-(-160 // S), S=S, D=128, seed=S, e4m3=True)
+    c = Case([40, 64, 33, 100, 4 * S], W=-(-160 // S), S=S, D=128, seed=S, e4m3=True)
     c.table[0, 1] = -1
     c.table[1, 0] = c.kv.shape[0]
     c.table[2, :] = -5
-    c.lens[4] = 2 ** 31 - 1
+    c.lens[4] = 2 ** 31 - 1  # counts as W * S (its last page is full: unused tokens are NaN)
     bad = torch.zeros(1, dtype=torch.int32, device="cuda")
     c.check(*c.call(bad_count=bad), bad=bad)
 
