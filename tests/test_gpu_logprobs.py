@@ -194,3 +194,40 @@ def test_offsets_beyond_32_bits():
     tail = x[-2:].cpu()
     check(tail, ids[-2:].cpu(), 4, 1.0, [v[-2:] for v in got])
     assert math.isclose(float(got[0][0]), -math.log(V), rel_tol=1e-6)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("S", [250, 1002])
+@pytest.mark.parametrize("shares", [1, 2])
+def test_rows_that_no_share_cuts(shares, S, captured):
+    """As many rows as shares (three blocks an SM), so that no row is joined from parts: the library's next
+    kernel, which writes over the logits, begins only after the last of them has been read."""
+    T, V = shares * 3 * torch.cuda.get_device_properties(0).multi_processor_count, 128 * S
+    g = torch.Generator(device="cuda").manual_seed(S)
+    x = torch.randn((2 * T, V), generator=g, device="cuda").bfloat16()
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda").int()
+    want = wq.token_logprobs(x[:T].clone(), ids, top_k=5)
+    torch.cuda.synchronize()
+    work = x.clone()
+    pages = work.view(2 * T, 2, 1, S, 64)  # a row is a page
+    here = torch.arange(T, dtype=torch.int32, device="cuda")
+
+    def step():
+        got = wq.token_logprobs(work[:T], ids, top_k=5)
+        wq.kv_pages_copy(pages, here + T, here)
+        return got
+
+    step()
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step()
+    for _ in range(10):
+        work.copy_(x)
+        if captured:
+            graph.replay()
+        else:
+            got = step()
+        assert torch.equal(work[:T], x[T:])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

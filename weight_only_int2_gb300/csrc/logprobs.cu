@@ -806,7 +806,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args g) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = g.a.top_k;
   const int64_t p0 = blockIdx.x, places = g.units + kRowCost, row = (p0 + 1) * g.share / places;
   const int64_t first = row * places + kRowCost, last = first + g.units - 1;
-  if (row >= g.a.T || first < p0 * g.share || first >= (p0 + 1) * g.share) return;
+  // A block with nothing to join waits all the same: where no row is cut that is
+  // every block, and whoever comes next in the stream waits for this grid alone.
+  if (row >= g.a.T || first < p0 * g.share || first >= (p0 + 1) * g.share) {
+    cl::griddep_wait();
+    return;
+  }
   const int n = static_cast<int>(last / g.share - p0) + 1;
   const int32_t id = g.a.ids != nullptr ? g.a.ids[row] : -1;
   const float xt = given_logit(g.a, row, id);

@@ -69,9 +69,12 @@ cudaError_t raise_smem_limit(SmemLimit& lim, Kernel kern, int device, size_t byt
   return e;
 }
 
-// Launches a kernel that may begin while the one before it in the stream ends:
-// it reads and writes nothing before its griddepcontrol.wait, and lets the next
-// one begin only after that.
+// Launches a kernel that may begin while the one before it in the stream ends.
+// Its rules: it writes nothing before its griddepcontrol.wait, and reads only
+// what that kernel has itself waited for (a join reads its main kernel's inputs);
+// at least one block reaches the wait before the grid can end, since a wait
+// covers the kernel just before and no other; and it lets the next one begin only
+// after its own wait.
 template <typename T>
 struct Same {
   using type = T;
