@@ -231,3 +231,46 @@ def test_rows_that_no_share_cuts(shares, S, captured):
             got = step()
         assert torch.equal(work[:T], x[T:])
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("temp", [0.7, 1.0, 1.3])
+@pytest.mark.parametrize("T,V", [(6, 300), (1, 70001), (6, 60000), (700, 4099)])
+def test_masks_of_the_lowest_value(T, V, temp, bf16):
+    """Logits forbidden by the type's lowest value weigh as little as by -inf, wherever the others lie.
+
+    With R the largest |x - m| / temperature of the others, the tolerances are those above. A forbidden logit's
+    log probability is within 2^-20 of (x - m) / temperature - ln l, and -inf where float32 cannot hold it."""
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    low = torch.finfo(dtype).min
+    x = rows(T, V, bf16, 17)
+    forbidden = torch.zeros((T, V), dtype=torch.bool)
+    for t in range(T):
+        kind = t % 6
+        if kind == 0:
+            forbidden[t, : V // 2] = True
+        elif kind == 1:
+            forbidden[t, :-1] = True
+        elif kind == 2:
+            forbidden[t, V // 3:] = True
+        elif kind == 3:
+            forbidden[t, ::2] = True
+        elif kind == 4:
+            forbidden[t] = True
+            forbidden[t, [V // 2, V - 3]] = False
+    x[forbidden] = low
+    ids = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(V)).int()
+    k = 8
+    lp, rank, ent, top, top_ids, _ = O.token_logprobs(x.double().numpy(), ids.numpy(), k, temp)
+    glp, grank, gent, gtop, gids = (v.cpu().numpy().astype(np.float64) for v in run(x, ids, k, temp))
+    assert np.array_equal(gids, top_ids) and np.array_equal(grank, rank)
+    a = np.where(forbidden.numpy(), np.nan, x.double().numpy())
+    R = np.nanmax(np.abs(a - np.nanmax(a, 1, keepdims=True)), 1) / temp
+    e = 4 * R * 2.0 ** -24 + 2.0 ** -17
+    assert np.all(np.abs(gent - ent) <= (1 + R) * e), np.abs(gent - ent).max()
+    for got, want, far in ((glp[:, None], lp[:, None], forbidden.gather(1, ids[:, None].long()).numpy()),
+                           (gtop, top, forbidden.gather(1, torch.from_numpy(top_ids).long()).numpy())):
+        tol = np.where(far, np.abs(want) * 2.0 ** -20, e[:, None] + np.abs(want) * 2.0 ** -22)
+        fits = np.abs(want) <= float(torch.finfo(torch.float32).max)
+        assert np.all(got[~fits] == -np.inf)
+        assert np.all(np.abs(got - want)[fits] <= tol[fits])

@@ -98,8 +98,10 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t id) {
 }
 __device__ __forceinline__ uint32_t id_of(uint64_t key) { return 0xFFFFFFFFu - static_cast<uint32_t>(key); }
 
+// (A difference beyond 200 leaves no weight, as 200 does; it may be infinite, as from
+// the type's lowest value, and t - d l would be so, too.)
 __device__ __forceinline__ void raise(Sums& s, float m, float c) {
-  const float d = s.m == -CUDART_INF_F || s.m == m ? 0.0f : (m - s.m) * c;
+  const float d = s.m == -CUDART_INF_F || s.m == m ? 0.0f : fminf((m - s.m) * c, 200.0f);
   const float f = s.m == -CUDART_INF_F ? 0.0f : exp2_fast(-d);
   s.t = f * (s.t - d * s.l);
   s.l = f * s.l;
@@ -139,7 +141,10 @@ __device__ __forceinline__ void put(const Args& g, int64_t row, int i, const Sum
   const bool none = s.m == -CUDART_INF_F && s.l == 0.0f;
   const float log_l = log2f(s.l), ref = s.m == -CUDART_INF_F ? 0.0f : s.m;
   const auto lp = [&](float x) {
-    return none ? -CUDART_INF_F : 0.6931471805599453f * ((x - ref) * g.c - log_l);
+    const float u = (x - ref) * g.c;
+    if (none) return -CUDART_INF_F;
+    // (in powers of two the type's lowest value overflows, in nats it need not)
+    return u == -CUDART_INF_F ? (x - ref) / a.temperature - 0.6931471805599453f * log_l : 0.6931471805599453f * (u - log_l);
   };
   if (i < a.top_k) {
     a.top_ids[row * a.top_k + i] = static_cast<int32_t>(id_of(key));
