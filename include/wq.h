@@ -283,7 +283,7 @@ size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
  *   x[t] = sm_scale * <q[b, h], k[t]>,  t in [max(0, len - window), len),
  *   out[b, h] = sum_t exp(x[t] - m) v[t] / l,  m = max_t x[t],
  *   l = sum_t exp(x[t] - m),  lse[b, h] = m + ln l,
- * all in float32, out rounded to bf16 once. A sequence without tokens (length
+ * summed in float32, out rounded to bf16 once. A sequence without tokens (length
  * 0 or less, or every page id out of range) gives zeros and lse = -inf, as do
  * scores that are all -inf.
  *  q           [B, Hq, D] bf16, rows q_stride elements apart (a multiple of 8,
@@ -297,8 +297,9 @@ size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
  *              calls; not shared by calls that may run concurrently.
  * The result's bits do not depend on timing. B >= 0; Hq a multiple of Hkv.
  * NaN among the numbers used gives NaN, and so may infinite ones of q or v.
- * With an e4m3 cache a query's numbers are used to at least 2^-17 of the largest
- * of their head.
+ * Each token's weight exp(x[t] - m) is used to 2^-17 of itself, however small it is
+ * beside the others. With an e4m3 cache a query's numbers are used to at least
+ * 2^-17 of the largest of their head.
  * bad_count: pages left out. Tokens on a page beyond the length are never
  * used, whatever they hold. */
 wq_status kv_attn_decode(const wq_bf16* q, int64_t q_stride, const void* kv, int kv_type,

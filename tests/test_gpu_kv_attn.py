@@ -447,3 +447,55 @@ def test_inputs_from_another_stream(captured):
             pos.fill_(0)
             assert torch.equal(step(mine), want)
         assert torch.equal(mine, kv)
+
+
+# ---------------------------------------------------------------- weights of very different sizes
+
+GAPS = [12.0, 13.0, 14.5, 16.0, 17.25, 17.375, 18.5, 20.0, 22.0, 30.0, 45.0, 60.0]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 8), (128, 12), (256, 4)])
+@pytest.mark.parametrize("n", [77, 1000, 32768])
+@pytest.mark.parametrize("where", [0.0, 0.5, 1.0])
+def test_attn_small_weights(where, n, D, G, e4m3):
+    """One token whose weight is all but 1 and whose value is 0: the output is the others' alone, each with a weight
+    of e^-gap. All values are positive, so the sum's relative error is at most a weight's: e as above (A the
+    gap) for itself and for l, 2^-17 for its two parts, 2^-24 n for n additions' worst case, 2^-8 for the result."""
+    S, B = 64, -(-len(GAPS) // G)
+    W = -(-n // S)
+    r = np.random.default_rng(n + D)
+    codes = r.integers(0x30, 0x48, (W, 2, 1, S, D)).astype(np.uint8)  # 0.5 .. 4
+    codes[:, 0] = 0
+    top = int(where * (n - 1))
+    codes[top // S, 0, 0, top % S, 0] = 0x38  # 1
+    codes[top // S, 1, 0, top % S] = 0
+    values = R.e4m3_values()[codes]
+    kv = torch.from_numpy(codes).cuda().view(E4M3)
+    kw = {"k_scale": torch.ones(1, device="cuda"), "v_scale": torch.ones(1, device="cuda")} if e4m3 else {}
+    kv = kv if e4m3 else torch.from_numpy(values).bfloat16().cuda()
+    gaps = np.resize(np.array(GAPS), (B, G))
+    q = np.zeros((B, G, D))
+    q[:, :, 0] = gaps
+    table = torch.arange(W, dtype=torch.int32, device="cuda").expand(B, W).contiguous()
+    out = wq.kv_attn_decode(torch.from_numpy(q).bfloat16().cuda(), kv, table,
+                            torch.full((B,), n, dtype=torch.int32, device="cuda"), sm_scale=1.0, **kw)
+    total = values[:, 1, 0].reshape(W * S, D)[:n].sum(0)
+    w = np.exp(-gaps)[..., None]
+    ref = w * total / (1 + (n - 1) * w)
+    e = (D * 2.0 ** -24 + 2.0 ** -21) * gaps[..., None] + 2.0 ** -18
+    off = np.abs(out.double().cpu().numpy() - ref) / ref
+    assert np.all(off <= 2.0 ** -8 + 2 * e + 2.0 ** -17 + n * 2.0 ** -24), (off.max((0, 2)), gaps[0])
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 5), (128, 16), (192, 3), (256, 12)])
+@pytest.mark.parametrize("spread", [3.0, 12.0, 40.0])
+def test_attn_steep_scores_of_an_e4m3_cache(spread, D, G):
+    """Scores from much less to much more than what came before, by the oracle: every weight in turn the largest."""
+    c = Case([64, 333, 2500], G=G, D=D, e4m3=True, q_scale=spread, seed=D + G)
+    c.check(*c.call())
+    c.kv_dev[c.table[1, 0], 1, 0, 3, 5] = math.nan  # a value of NaN, whichever way the values are widened
+    c.kv_dev[c.table[2, 9], 1, 1, 3, 7] = math.nan
+    out, _ = c.call()
+    assert torch.isnan(out[1, :G, 5]).all() and torch.isnan(out[2, G:, 7]).all()
+    assert int(torch.isnan(out).sum()) == 2 * G

@@ -20,11 +20,15 @@
 //  - the products run on warp-level MMAs with the tokens (scores) and the
 //    columns (output) as the 16 rows and 8 query heads as the columns: no row
 //    is padding, and a thread keeps D / 4 sums for 8 heads. The weights go into
-//    the second product as hi + lo, two 16-bit numbers, which keeps them to
-//    2^-17 (2^-22 for e4m3, whose values are exact in fp16);
+//    the second product as hi + lo, two 16-bit numbers, which keeps each to 2^-17
+//    of itself, however small it is beside the others;
 //  - e4m3 keys are multiplied as they are, by queries split into two e4m3
 //    numbers; e4m3 values are transposed as codes and widened to fp16 in
-//    registers. The caches' scales are factors of the scores and of the output.
+//    registers, or to bf16 (three more instructions for two values) with 16
+//    tokens among whose weights there are some that fp16 is too short for: where
+//    all are so, D = 64 takes 109 us for 100 (64 sequences of up to 16011), D = 128
+//    181 to 184 either way, 16 heads 118 for 107, D = 256 152 for 143. The caches' scales are factors of
+//    the scores and of the output.
 //
 // Measured (of a copy's 6.8 TB/s): 64 sequences of 1 to 8192 tokens, 8 key heads
 // of 4 query heads, D = 128, bf16, 1.07 GB: 174 us, 6.2 TB/s; one of 131071
@@ -44,6 +48,8 @@
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 namespace wq {
 namespace {
 
@@ -55,6 +61,11 @@ constexpr int least_units(int unit) { return unit > 64 ? 2 : 4; }
 // The weights are relative to a reference that is raised when a score passes it
 // by more than this (in powers of two), so that most steps need no maximum.
 constexpr float kSlack = 8.0f;
+// fp16 holds 2^-24 to 2^15: for e4m3 the reference lies so far below the first
+// largest score that weights come up to 2^15, and hi + lo, off by at most 2^-25,
+// is within 2^-17 of weights of kLeastF16 and more.
+constexpr float kDown = 7.0f;
+constexpr float kLeastF16 = 0.00390625f;
 
 // Blocks that share an SM: as many as the registers allow (a thread keeps D / 4
 // sums and D / 8 registers of queries for 8 heads, twice that for 16, and with
@@ -196,6 +207,15 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& low, uint32_t& high)
   asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
       : "=r"(low), "=r"(high)
       : "r"(w));
+}
+// The same as bf16 numbers, exactly, too.
+__device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t& low, uint32_t& high) {
+  uint32_t h[2];
+  widen(w, h[0], h[1]);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+  low = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+  high = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
 }
 // x, y rounded to 16 bits (hi), and what that leaves (lo), packed.
 template <bool kF16>
@@ -591,10 +611,12 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
               const bool raise = top > limit[j][i];
-              float shrink = exp2_fast(limit[j][i] == -CUDART_INF_F ? -CUDART_INF_F : m[j][i] - top);
+              // (rounded towards each other: no score is more than kSlack + kDown above)
+              const float ref = kE4m3 ? __fadd_ru(top, -kDown) : top;
+              float shrink = exp2_fast(limit[j][i] == -CUDART_INF_F ? -CUDART_INF_F : m[j][i] - ref);
               shrink = raise ? shrink : 1.0f;
-              m[j][i] = raise ? top : m[j][i];
-              limit[j][i] = raise ? top + kSlack : limit[j][i];
+              m[j][i] = raise ? ref : m[j][i];
+              limit[j][i] = raise ? __fadd_rd(top, kSlack) : limit[j][i];
               l[j][i] *= shrink;
 #pragma unroll
               for (int t = 0; t < kT; ++t) {
@@ -605,57 +627,75 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         }
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
-            uint32_t hi[kTiles][2], lo[kTiles][2];  // tokens 0-7 and 8-15 of head 8 j + row
+          bool tiny = false;
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float p0 = exp2_fast(s[part][j][2 * i] - m[j][0]), p1 = exp2_fast(s[part][j][2 * i + 1] - m[j][1]);
-              l[j][0] += p0;
-              l[j][1] += p1;
-              split_pair<kE4m3>(p0, p1, hi[j][i], lo[j][i]);
-              hi[j][i] = transpose8(hi[j][i]);
-              lo[j][i] = transpose8(lo[j][i]);
+            for (int i = 0; i < 4; ++i) {
+              float& p = s[part][j][i];
+              p = exp2_fast(p - m[j][i & 1]);
+              l[j][i & 1] += p;
+              tiny |= p < kLeastF16 && p != 0.0f;
             }
           }
-          // values, their columns as rows: b[0], b[1] 8 columns each of tokens
-          // 0-7, b[2], b[3] of tokens 8-15
-          auto accumulate = [&](int t, const uint32_t(&b)[4]) {
+          const auto products = [&](auto f16) {
+            constexpr bool kF16 = decltype(f16)::value;
+            uint32_t hi[kTiles][2], lo[kTiles][2];  // tokens 0-7 and 8-15 of head 8 j + row
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) {
-              mma<kE4m3>(acc[j][t], b, hi[j]);
-              mma<kE4m3>(acc[j][t], b, lo[j]);
-            }
-          };
-          if constexpr (!kE4m3) {
-            const uint32_t addr = vbase + (part * 16 + (lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
-#pragma unroll
-            for (int t = 0; t < kT; ++t) {
-              uint32_t b[4];
-              ldsm4_trans(addr + t * 32, b);
-              accumulate(t, b);
-            }
-          } else {
-            // 16 x 16 codes a matrix: a register holds a column's codes of rows 4 col
-            // .. 4 col + 3, of which the first two go with weights 2 col, 2 col + 1 of
-            // tokens 0-7, the others of 8-15. The rows are the tokens that the
-            // weights have there; with 12-15 before 8-11 no 8 rows share a bank. (With
-            // 16-bit matrices and byte permutes D = 64 took 4 % longer, 128 2 %.)
-            const int at = (lane >> 2 & 3) * 2 + (lane & 1), token = (lane & 2) != 0 ? 8 + (at ^ 4) : at;
-            const uint32_t addr = vbase + (part * 16 + token) * C::kPitch + (lane >> 4) * 16;
-#pragma unroll
-            for (int t = 0; t < kT; t += 2) {
-              uint32_t b[4];
-              ldsm2_codes(addr + t * 16, b);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                uint32_t c[4];
-                widen(b[2 * i], c[0], c[2]);
-                widen(b[2 * i + 1], c[1], c[3]);
-                accumulate(t + i, c);
+                split_pair<kF16>(s[part][j][2 * i], s[part][j][2 * i + 1], hi[j][i], lo[j][i]);
+                hi[j][i] = transpose8(hi[j][i]);
+                lo[j][i] = transpose8(lo[j][i]);
               }
             }
-          }
+            // values, their columns as rows: b[0], b[1] 8 columns each of tokens
+            // 0-7, b[2], b[3] of tokens 8-15
+            auto accumulate = [&](int t, const uint32_t(&b)[4]) {
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j) {
+                mma<kF16>(acc[j][t], b, hi[j]);
+                mma<kF16>(acc[j][t], b, lo[j]);
+              }
+            };
+            if constexpr (!kE4m3) {
+              const uint32_t addr = vbase + (part * 16 + (lane & 7) + (lane >> 4) * 8) * C::kPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+              for (int t = 0; t < kT; ++t) {
+                uint32_t b[4];
+                ldsm4_trans(addr + t * 32, b);
+                accumulate(t, b);
+              }
+            } else {
+              // 16 x 16 codes a matrix: a register holds a column's codes of rows 4 col
+              // .. 4 col + 3, of which the first two go with weights 2 col, 2 col + 1 of
+              // tokens 0-7, the others of 8-15. The rows are the tokens that the
+              // weights have there; with 12-15 before 8-11 no 8 rows share a bank. (With
+              // 16-bit matrices and byte permutes D = 64 took 4 % longer, 128 2 %.)
+              const int at = (lane >> 2 & 3) * 2 + (lane & 1), token = (lane & 2) != 0 ? 8 + (at ^ 4) : at;
+              const uint32_t addr = vbase + (part * 16 + token) * C::kPitch + (lane >> 4) * 16;
+#pragma unroll
+              for (int t = 0; t < kT; t += 2) {
+                uint32_t b[4];
+                ldsm2_codes(addr + t * 16, b);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t c[4];
+                  if constexpr (kF16) {
+                    widen(b[2 * i], c[0], c[2]);
+                    widen(b[2 * i + 1], c[1], c[3]);
+                  } else {
+                    widen_bf16(b[2 * i], c[0], c[2]);
+                    widen_bf16(b[2 * i + 1], c[1], c[3]);
+                  }
+                  accumulate(t + i, c);
+                }
+              }
+            }
+          };
+          if (kE4m3 && !__any_sync(0xFFFFFFFFu, tiny)) products(std::true_type{});
+          else products(std::false_type{});
         }
       }
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
