@@ -299,7 +299,7 @@ size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
  * NaN among the numbers used gives NaN, and so may infinite ones of q or v.
  * Each token's weight exp(x[t] - m) is used to 2^-17 of itself, however small it is
  * beside the others. With an e4m3 cache a query's numbers are used to at least
- * 2^-17 of the largest of their head.
+ * 2^-17 of the largest of their head (where that is at least 2^-119).
  * bad_count: pages left out. Tokens on a page beyond the length are never
  * used, whatever they hold. */
 wq_status kv_attn_decode(const wq_bf16* q, int64_t q_stride, const void* kv, int kv_type,

@@ -499,3 +499,18 @@ def test_attn_steep_scores_of_an_e4m3_cache(spread, D, G):
     out, _ = c.call()
     assert torch.isnan(out[1, :G, 5]).all() and torch.isnan(out[2, G:, 7]).all()
     assert int(torch.isnan(out).sum()) == 2 * G
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 16), (256, 3)])
+@pytest.mark.parametrize("power", [-118, -100, -94, 106, 108, 114])
+def test_attn_very_large_and_small_queries_of_an_e4m3_cache(power, D, G):
+    """Queries times a power of two and sm_scale divided by it: the same bits (2^114 times 8 is below 2^118, and
+    no scale leaves the normal numbers)."""
+    c = Case([64, 5, 333], G=G, D=D, e4m3=True, seed=D + G)
+    # at least 2^-1, so that no query leaves the normal numbers either
+    c.q = np.where(np.abs(c.q) < 0.5, np.copysign(0.5, c.q), c.q)
+    c.q_dev = torch.from_numpy(c.q).bfloat16().cuda()
+    out, lse = c.call()
+    c.check(out, lse)
+    out2, lse2 = c.call(q=c.q_dev * 2.0 ** power, sm_scale=c.sm * 2.0 ** -power)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)

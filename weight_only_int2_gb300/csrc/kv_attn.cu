@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
     // For an e4m3 cache they are split into two e4m3 numbers behind a power of
     // two that puts the head's largest in [2^7, 2^8): q = q1 + q2 exactly, but
     // for numbers below 2^-9 of the largest, which are off by at most 2^-17 of it
+    // (for any finite largest; below 2^-119 the power stays at 2^126)
     uint32_t q1[kTiles][kK][2], q2[kTiles][kE4m3 ? kK : 1][2];
     float scale[kTiles][2];  // of heads 8 j + 2 col, + 1
 #pragma unroll
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kR16>::kThreads, Cfg<D, kE4m3, k
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         const bool wrong = top >= 0x7F80u;         // an infinite or NaN query: NaN
         int e = static_cast<int>(top >> 7) - 127;  // the largest is in [2^e, 2^(e + 1))
-        e = top == 0 || wrong ? 7 : (e < -93 ? -93 : (e > 107 ? 107 : e));
+        e = top == 0 || wrong ? 7 : (e < -119 ? -119 : e);
         const float up = __int_as_float((7 - e + 127) << 23), down = __int_as_float((e - 7 + 127) << 23);
         const float mine = a.scale * a.kv.k_scale[h] * down;
         scale[j][0] = __shfl_sync(0xFFFFFFFFu, mine, 8 * col);
