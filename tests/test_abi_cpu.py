@@ -221,3 +221,61 @@ def test_device_failure_drops_cached_workspaces(lib):
         assert key in L._ws_cache
     finally:
         L._ws_cache.pop(key, None)
+
+
+class _Buffers:
+    """What the workspace cache uses of torch, on the CPU, with the live buffers counted."""
+
+    class Buffer:
+        def __init__(self, n):
+            self.n = n
+
+        def numel(self):
+            return self.n
+
+    def __init__(self):
+        import weakref
+
+        self.alive, self.capturing, self.uint8 = weakref.WeakSet(), False, None
+        self.cuda = self
+        self.Tensor = object
+
+    def zeros(self, n, dtype=None, device=None):
+        b = self.Buffer(n)
+        self.alive.add(b)
+        return b
+
+    def device(self, kind, index=0):
+        return kind
+
+    def is_current_stream_capturing(self):
+        return self.capturing
+
+    def total(self):
+        import gc
+
+        gc.collect()
+        return sum(b.n for b in self.alive)
+
+
+def test_replaced_workspaces_are_released(lib, monkeypatch):
+    """Of buffers that a larger one replaced, only those stay that a captured graph uses, until all are dropped."""
+    from weight_only_int2_gb300 import _lib as L
+
+    fake, MB = _Buffers(), 1 << 20
+    monkeypatch.setattr(L, "torch", fake)
+    monkeypatch.setattr(L, "_device", lambda: 0)
+    monkeypatch.setattr(L, "_stream", lambda: 0)
+    monkeypatch.setattr(L, "_ws_cache", {})
+    for n in range(1, 20):
+        assert L.scratch(n * MB).numel() == n * MB and L.workspace(n * MB).numel() == n * MB
+        assert fake.total() == 2 * n * MB
+    fake.capturing = True
+    for _ in range(3):
+        L.workspace(18 * MB)  # the 19 MB buffer, now a graph's, too
+    fake.capturing = False
+    for n in (25, 30):
+        L.workspace(n * MB)
+    assert fake.total() == (19 + 19 + 30) * MB
+    L.drop_workspaces()
+    assert fake.total() == 0

@@ -126,3 +126,25 @@ def test_host_threads_call_concurrently_with_identical_results():
             for ji, y in enumerate(ys):
                 _same(sets[i][ji], y, ref[i][ji], (i, rep, ji))
     wq.check_status()
+
+
+def test_workspaces_of_rising_sizes_are_not_kept():
+    """Calls whose scratch and workspaces grow hold the last ones only, and dropping them returns their memory."""
+    from weight_only_int2_gb300 import _lib
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    N, K, bits = 1024, 1024, 4
+    codes = torch.randint(0, 16, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    scales = (torch.rand((N, K // 128), generator=g, device="cuda") / 64).bfloat16()
+    packed, s_dev = wq.wna16_repack(codes, scales, bits)
+    wq.drop_workspaces()
+    torch.cuda.synchronize()
+    start = torch.cuda.memory_allocated()
+    for M in range(512, 8192, 512):
+        wq.w4a8_gemm(torch.randn((M, K), generator=g, device="cuda").bfloat16(), packed, s_dev, N, K)
+    torch.cuda.synchronize()
+    sizes = [b.numel() for b in _lib._ws_cache.values()]
+    assert max(sizes) > 4 << 20  # (it did grow)
+    assert torch.cuda.memory_allocated() - start <= sum(sizes) + (1 << 20)
+    wq.drop_workspaces()
+    assert torch.cuda.memory_allocated() <= start

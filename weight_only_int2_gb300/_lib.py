@@ -153,7 +153,7 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None) -> None:
 # ---------------------------------------------------------------- workspaces
 
 _ws_cache: dict = {}
-_ws_replaced: list = []
+_ws_captured: list = []  # buffers that captured graphs use: they outlive their place in the cache
 _ws_lock = threading.Lock()
 
 
@@ -168,8 +168,6 @@ def _cached(kind: str, nbytes: int, device=None) -> torch.Tensor | None:
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
-            if buf is not None:
-                _ws_replaced.append(buf)  # a captured graph may still use it
             dev = "cuda" if index is None else torch.device("cuda", index)
             buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
             _ws_cache[key] = buf
@@ -179,16 +177,24 @@ def _cached(kind: str, nbytes: int, device=None) -> torch.Tensor | None:
 def drop_workspaces() -> None:
     """Forgets every cached workspace and scratch buffer; later calls allocate
     fresh zero-filled ones. Called after a device-side failure. The memory
-    returns to PyTorch's allocator, which reuses it in stream order."""
+    returns to PyTorch's allocator, which reuses it in stream order: graphs
+    captured before are not to be replayed any more."""
     with _ws_lock:
         _ws_cache.clear()
+        _ws_captured.clear()
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor | None:
     """A zero-filled split-K workspace for the current stream, reused across
     calls. The library leaves it zero-filled after every successful call;
-    calls that share it are serialised by the stream."""
-    return _cached("zero-at-rest", nbytes, device)
+    calls that share it are serialised by the stream. One that a captured call
+    uses is kept for the graph when a larger one takes its place."""
+    buf = _cached("zero-at-rest", nbytes, device)
+    if buf is not None and torch.cuda.is_current_stream_capturing():
+        with _ws_lock:
+            if not any(b is buf for b in _ws_captured):
+                _ws_captured.append(buf)
+    return buf
 
 
 def scratch(nbytes: int, device=None) -> torch.Tensor | None:
