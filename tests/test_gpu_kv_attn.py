@@ -514,3 +514,31 @@ def test_attn_very_large_and_small_queries_of_an_e4m3_cache(power, D, G):
     c.check(out, lse)
     out2, lse2 = c.call(q=c.q_dev * 2.0 ** power, sm_scale=c.sm * 2.0 ** -power)
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("tokens", [1024, 2])
+def test_append_every_bf16_value_by_extreme_scales(tokens):
+    """All 65536 patterns by positive scales from the smallest number that float32 has to the largest."""
+    r = np.random.default_rng(tokens)
+    scales = [2.0 ** -149, 3 * 2.0 ** -149, 2.0 ** -141, 2.0 ** -133, 2.0 ** -128, 1e-38, 2.0 ** -126]
+    scales += list(np.exp2(r.uniform(-149, -60, 13))) + list(np.exp2(r.uniform(60, 127.9, 11))) + [3.4028234e38]
+    H, S, D = len(scales), 16, 64
+    ks, vs = np.array(scales, dtype=np.float32), np.array(scales[::-1], dtype=np.float32)
+    bits = np.arange(65536, dtype=np.uint16).reshape(1024, D)
+    want = []
+    for w in (ks, vs):
+        with np.errstate(over="ignore", invalid="ignore"):
+            y = bf16_values(bits).astype(np.float32)[:, None] / w[None, :, None]
+            want.append(np.where(np.isnan(y), 127, R.e4m3_codes(np.nan_to_num(y.astype(np.float64), nan=0.0, posinf=1e300, neginf=-1e300))))
+    table = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    for t0 in range(0, 1024, tokens) if tokens > 2 else (0, 254, 510, 768):
+        n = min(tokens, 1024 - t0)
+        x = torch.from_numpy(np.broadcast_to(bits[t0:t0 + n].view(np.int16)[:, None], (n, H, D)).copy()).cuda().view(torch.bfloat16)
+        kv = torch.zeros((64, 2, H, S, D), dtype=torch.uint8, device="cuda").view(E4M3)
+        wq.kv_append(x, x, torch.arange(n, dtype=torch.int32, device="cuda"), table, kv,
+                     seq=torch.zeros(n, dtype=torch.int32, device="cuda"), k_scale=torch.from_numpy(ks).cuda(),
+                     v_scale=torch.from_numpy(vs).cuda())
+        got = kv.view(torch.uint8).permute(1, 0, 3, 2, 4).reshape(2, 64 * S, H, D)[:, :n].cpu().numpy()
+        for i in range(2):
+            bad = np.where((got[i] & 127) == 127, 127, got[i]) != want[i][t0:t0 + n]
+            assert not bad.any(), (i, np.unique(np.nonzero(bad)[1]), [scales[::1 - 2 * i][h] for h in np.unique(np.nonzero(bad)[1])])

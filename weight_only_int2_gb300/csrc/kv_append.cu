@@ -14,9 +14,10 @@
 //
 // The e4m3 code is that of the IEEE quotient x / w. With y = RN(1 / w),
 // q = RN(x y) and r = x - q w (exact in one fma), RN(q + r y) is the correctly
-// rounded quotient (Markstein, IBM J. Res. Dev. 34(1), 1990); x is clamped to
-// +-500 w first (rounded to bf16, still beyond the largest code), so that nothing
-// overflows on the way.
+// rounded quotient (Markstein, IBM J. Res. Dev. 34(1), 1990). x is clamped to
+// +-500 w first (rounded up to bf16, beyond the largest code), and both are
+// multiplied by a power of two that is not 1 for w outside 2^-64 .. 2^64, so that on
+// the way nothing overflows and r loses no bits where the code is not 0 anyway.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
@@ -45,27 +46,56 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
-// A scale w for pairs of values: -w, RN(1 / w) and the two bf16 limits.
+// A scale for pairs of values: with f the power of two, -f, w = scale f,
+// -RN(1 / w) and the two bf16 limits.
 struct Scale {
-  uint64_t minus_w, y;
+  uint64_t minus_f, w, minus_y;
   uint32_t lim;
-  __device__ explicit Scale(float w) {
-    const float r = __frcp_rn(w);
-    minus_w = pair(-w, -w);
-    y = pair(r, r);
-    const __nv_bfloat162 l = __float2bfloat162_rn(fminf(500.0f * w, 3.0e38f));
+  __device__ explicit Scale(float s) {
+    const __nv_bfloat16 top = __float2bfloat16_ru(fminf(500.0f * s, 3.3895313892515355e38f));
+    const __nv_bfloat162 l = __nv_bfloat162(top, top);
     lim = *reinterpret_cast<const uint32_t*>(&l);
+    const float f = s < 5.421010862427522e-20f ? 3.8685626227668134e+25f : (s > 1.8446744073709552e19f ? 5.421010862427522e-20f : 1.0f);
+    const float r = -__frcp_rn(s * f);
+    minus_f = pair(-f, -f);
+    w = pair(s * f, s * f);
+    minus_y = pair(r, r);
   }
 };
 
-// Two bf16 numbers (the halves of p) over w as two e4m3 codes.
+// Two bf16 numbers (the halves of p) over w as two e4m3 codes. (With the signs as
+// they are here, -0.0 stays -0.0.)
 __device__ __forceinline__ uint32_t codes_of(uint32_t p, const Scale& s) {
   asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(p) : "r"(s.lim));
   asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(p) : "r"(s.lim | 0x80008000u));
-  const uint64_t x = pair(__uint_as_float(p << 16), __uint_as_float(p & 0xFFFF0000u)), z = mul2(x, s.y);
-  const uint64_t q = fma2(fma2(z, s.minus_w, x), s.y, z);
-  return __nv_cvt_float2_to_fp8x2(make_float2(copysignf(low_of(q), low_of(z)), copysignf(high_of(q), high_of(z))),
-                                  __NV_SATFINITE, __NV_E4M3);  // (-0.0 stays)
+  const uint64_t minus_x = mul2(pair(__uint_as_float(p << 16), __uint_as_float(p & 0xFFFF0000u)), s.minus_f);
+  const uint64_t z = mul2(minus_x, s.minus_y), q = fma2(fma2(z, s.w, minus_x), s.minus_y, z);
+  return __nv_cvt_float2_to_fp8x2(make_float2(low_of(q), high_of(q)), __NV_SATFINITE, __NV_E4M3);
+}
+
+// By scales beyond kHuge an infinite number clamped to bf16's largest does not
+// saturate: the thread writes the codes of those among its values once more. (A call
+// that finds everything again, so that the kernel keeps its registers.)
+constexpr float kHuge = 3.3e35f;
+__device__ __noinline__ void infinite_by_huge(uint8_t* kv, int side, const int32_t* table, int64_t B, int64_t W,
+                                              int64_t S, int64_t P, int Hkv, int D, const uint16_t* src, int64_t stride,
+                                              int tokens, int64_t T, const int32_t* seq, const int32_t* pos) {
+  const int row = Hkv * D / 16;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, t0 = u / (2 * row) * tokens;
+  const int at = static_cast<int>(u % (2 * row)) % row * 16, h = at / D;
+#pragma unroll 1
+  for (int64_t t = t0; t < t0 + tokens && t < T; ++t) {
+    const int64_t s = seq != nullptr ? seq[t] : t, p = pos[t];
+    if (s < 0 || s >= B || p < 0 || p >= W * S) continue;
+    const int64_t page = table[s * W + p / S];
+    if (page < 0 || page >= P) continue;
+    uint8_t* dst = kv + (((page * 2 + side) * Hkv + h) * S + p % S) * D + (at - h * D);
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x = src[t * stride + at + i];
+      if ((x & 0x7FFFu) == 0x7F80u) dst[i] = static_cast<uint8_t>(x >> 15 << 7 | 0x7Eu);
+    }
+  }
 }
 
 // One thread per 16 bytes of the cache (8 bf16 values or 16 codes) of kTokens
@@ -130,6 +160,9 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCache a,
       *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.kv) + dst) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+  if (kE4m3 && w > kHuge)
+    infinite_by_huge(static_cast<uint8_t*>(a.kv), side, a.table, a.B, a.W, a.S, a.P, static_cast<int>(a.Hkv),
+                     static_cast<int>(a.D), side ? v : k, side ? v_stride : k_stride, kTokens, T, seq, pos);
 }
 
 }  // namespace
