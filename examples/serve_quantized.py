@@ -8,7 +8,8 @@ answer. PyTorch does the norms and the activation, and holds the memory.
     python examples/serve_quantized.py
 
 A user of the library with a scheduler of their own needs `Decoder.step` and the
-four page calls in `main`.
+page calls in `advance` and `main`. A pool may run out: a reserve or a fork says
+for each sequence whether it was granted, and only granted tokens may be stored.
 """
 
 import os
@@ -82,53 +83,66 @@ class Decoder:
 
 
 def grow(table, lens, ref, page_size, tokens):
-    """Reserves the page that each sequence's next token needs."""
+    """Reserves the page that each sequence's next token needs. Returns 1 for the
+    sequences that have their page and 0 for those that the pool has none for:
+    their token must not be stored, since its place in the table is not theirs."""
     _, _, granted = wq.kv_pages_reserve(table, lens, torch.where(tokens >= 0, lens + 1, lens), ref, page_size)
     return granted
 
 
-def main(e4m3=False, steps=6, verbose=True):
+def advance(model, tokens, kv, table, lens, ref, logits):
+    """Stores each sequence's next token and computes what follows it. A sequence
+    without a page waits: its token becomes -1, its logits stay. Returns the tokens
+    that were stored and the logits; lens is updated."""
+    granted = grow(table, lens, ref, kv.shape[4], tokens)
+    tokens = torch.where(granted == 1, tokens, -1)
+    after = model.step(tokens, kv, table, lens)
+    lens += (tokens >= 0).int()
+    return tokens, torch.where((tokens >= 0)[:, None], after, logits)
+
+
+def main(e4m3=False, steps=6, verbose=True, pages=40):
     model = Decoder(e4m3=e4m3)
-    B, W, S, P = 6, 8, 16, 40
+    B, W, S, P = 6, 8, 16, pages
     kv = model.cache(P, S)
     table = torch.full((B, W), -1, dtype=torch.int32, device="cuda")
     lens = torch.zeros(B, dtype=torch.int32, device="cuda")
     ref = torch.zeros(P, dtype=torch.int32, device="cuda")
+    logits = torch.zeros((B, model.vocab), dtype=torch.bfloat16, device="cuda")
 
     # two prompts, token by token, in sequences 0 and 1
     g = torch.Generator(device="cuda").manual_seed(1)
     prompts = torch.randint(0, model.vocab, (2, 21), generator=g, device="cuda", dtype=torch.int32)
     tokens = torch.full((B,), -1, dtype=torch.int32, device="cuda")
-    for i in range(prompts.shape[1]):
+    n = prompts.shape[1]
+    for i in range(n):
         tokens[:2] = prompts[:, i]
-        grow(table, lens, ref, S, tokens)
-        logits = model.step(tokens, kv, table, lens)
-        lens += (tokens >= 0).int()
+        stored, logits = advance(model, tokens, kv, table, lens, ref, logits)
+    if lens[:2].min() < n:
+        raise RuntimeError("the pool has too few pages for the prompts")
 
-    # each prompt is continued twice: sequences 2 and 3 start as copies
+    # each prompt is continued twice: sequences 2 and 3 start as copies, if there is a page for them
     ids = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
-    wq.kv_pages_fork(kv, table, lens, ref, ids[0], ids[1])
+    _, _, _, granted = wq.kv_pages_fork(kv, table, lens, ref, ids[0], ids[1])
     logits[2:4] = logits[:2]
+    alive = torch.zeros(B, dtype=torch.bool, device="cuda")
+    alive[:2] = True
+    alive[2:4] = granted == 1
     total = torch.zeros(B, device="cuda")
     history = []
     for i in range(steps):
         # the best token continues 0 and 1, the second best the first step of 2 and 3
         _, _, entropy, best, best_ids = wq.token_logprobs(logits, top_k=2)
         pick = torch.zeros(B, dtype=torch.int64, device="cuda")
-        if i == 0:
-            pick[2:4] = 1
-        tokens = best_ids.gather(1, pick[:, None])[:, 0]
-        tokens[4:] = -1
-        if i > steps // 2:
-            tokens[0] = -1
+        pick[2:4] = lens[2:4] == n
+        tokens = torch.where(alive, best_ids.gather(1, pick[:, None])[:, 0], -1)
         lp, rank, _, _, _ = wq.token_logprobs(logits, tokens)
+        tokens, logits = advance(model, tokens, kv, table, lens, ref, logits)
         total += torch.where(tokens >= 0, lp, 0.0)
-        history.append((tokens.clone(), lp, rank, entropy))
-        grow(table, lens, ref, S, tokens)
-        logits = model.step(tokens, kv, table, lens)
-        lens += (tokens >= 0).int()
+        history.append((tokens, lp, rank, entropy))
         if i == steps // 2:
             # sequence 0 is finished: its pages go back, and the pool closes up
+            alive[0] = False
             wq.kv_pages_free(table, lens, ref, torch.zeros(1, dtype=torch.int32, device="cuda"), S)
             _, _, _, n_live = wq.kv_pages_compact(kv, table, lens, ref)
     wq.check_status()

@@ -97,3 +97,33 @@ def test_forked_and_moved_pages_give_the_same_step(ex):
     _, _, remap, n = wq.kv_pages_compact(kv, table, lens, ref)
     assert int(n) == 4 and sorted(set(table[:, :2].flatten().tolist())) == [0, 1, 2, 3]
     assert torch.equal(m.step(tokens, kv, table, lens), before)
+
+
+@pytest.mark.parametrize("pages", [4, 5, 6, 7, 40])
+def test_a_pool_that_runs_out(ex, pages):
+    """Sequences that get no page wait, and nobody's tokens end up in another's pages: what each stored is the
+    beginning of what it stores when there are pages for all, and the counts are right."""
+    steps = 18
+    r, full = (ex.main(steps=steps, verbose=False, pages=n) for n in (pages, 60))
+    stored, want = ([[int(h[0][b]) for h in x["history"] if int(h[0][b]) >= 0] for b in range(6)] for x in (r, full))
+    for b in range(6):
+        assert stored[b] == want[b][:len(stored[b])], b
+    lens, want_lens = r["lens"].tolist(), full["lens"].tolist()
+    assert all(n <= m for n, m in zip(lens, want_lens))
+    assert lens[1] == 21 + len(stored[1]) and lens[0] == 0
+    count = torch.zeros_like(r["ref"])
+    for b, n in enumerate(lens):
+        for j in range(-(-n // 16)):
+            count[r["table"][b, j]] += 1
+    assert torch.equal(count, r["ref"]) and int((count > 0).sum()) <= pages
+    if pages == 40:
+        assert lens == want_lens == [0, 39, 39, 39, 0, 0]
+    if pages == 4:
+        assert lens[2:4] == [0, 0] and len(stored[0]) == steps // 2 + 1
+    if pages == 5:
+        assert lens[2] > 0 and lens[3] == 0
+
+
+def test_prompts_that_do_not_fit(ex):
+    with pytest.raises(RuntimeError, match="too few pages"):
+        ex.main(verbose=False, pages=3)
