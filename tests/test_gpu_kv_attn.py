@@ -542,3 +542,64 @@ def test_append_every_bf16_value_by_extreme_scales(tokens):
         for i in range(2):
             bad = np.where((got[i] & 127) == 127, 127, got[i]) != want[i][t0:t0 + n]
             assert not bad.any(), (i, np.unique(np.nonzero(bad)[1]), [scales[::1 - 2 * i][h] for h in np.unique(np.nonzero(bad)[1])])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,Hkv,D,S", [(1221, 8, 128, 16), (2501, 8, 128, 17), (2500, 3, 192, 100), (7001, 2, 96, 8)])
+def test_append_of_prompts(T, Hkv, D, S, e4m3):
+    """So many tokens that a thread has two, odd numbers of them among these, some without a place; the fused
+    projection's rows."""
+    r = np.random.default_rng(T)
+    B = 4
+    W = -(-T // (B * S)) + 1
+    P = B * W + 1
+    table = r.permutation(P)[:B * W].reshape(B, W).astype(np.int32)
+    at = np.sort(r.permutation(B * W * S)[:T])
+    seq, pos = (at // (W * S)).astype(np.int32), (at % (W * S)).astype(np.int32)
+    seq[7], seq[8], pos[T - 1], pos[T - 4] = -1, B, W * S, -3
+    table[2, W // 2] = P
+    x = torch.from_numpy(r.standard_normal((T, (4 + 2) * Hkv * D)).astype(np.float32)).bfloat16().cuda()
+    k = x[:, 4 * Hkv * D:5 * Hkv * D].unflatten(1, (Hkv, D))
+    v = x[:, 5 * Hkv * D:].unflatten(1, (Hkv, D))
+    ks, vs = ((r.random(Hkv) + 0.5).astype(np.float32) / 60 for _ in range(2))
+    kv = Guarded((P, 2, Hkv, S, D), E4M3 if e4m3 else torch.bfloat16)
+    raw = torch.uint8 if e4m3 else torch.int16
+    want = kv.t.view(raw).cpu().numpy().copy()
+    places = R.token_places(table, P, S, seq, pos)
+    there = np.array([page >= 0 for page, _ in places])
+    page, slot = (np.array(c)[there] for c in zip(*places))
+    for i, (y, w) in enumerate(((k, ks), (v, vs))):
+        if e4m3:
+            q = y.float().cpu().numpy() / w[:, None]  # one IEEE division
+            want[page, i, :, slot] = R.e4m3_codes(q.astype(np.float64))[there]
+        else:
+            want[page, i, :, slot] = y.contiguous().view(torch.int16).cpu().numpy()[there]
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = {"k_scale": torch.from_numpy(ks).cuda(), "v_scale": torch.from_numpy(vs).cuda()} if e4m3 else {}
+    wq.kv_append(k, v, torch.from_numpy(pos).cuda(), torch.from_numpy(table).cuda(), kv.t,
+                 seq=torch.from_numpy(seq).cuda(), bad_count=count, **kw)
+    assert np.array_equal(kv.t.view(raw).cpu().numpy(), want)
+    assert int(count.item()) == int((~there).sum())
+    kv.check("cache")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_every_replay_follows_the_lengths(e4m3):
+    """A graph whose lengths change gives after each replay what a call gives that is not captured."""
+    c = Case([3000, 1, 777, 12000], Hkv=2, G=5, e4m3=e4m3, seed=6)
+    table, lens = torch.from_numpy(c.table).cuda(), torch.from_numpy(c.lens).cuda()
+    out, lse = torch.empty_like(c.q_dev), torch.empty((4, 10), device="cuda")
+    kw = {"sm_scale": c.sm, **c.scales()}
+    wq.kv_attn_decode(c.q_dev, c.kv_dev, table, lens, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wq.kv_attn_decode(c.q_dev, c.kv_dev, table, lens, out=out, lse=lse, **kw)
+    for n in ([3000, 1, 777, 12000], [5, 1, 1, 0], [0, 0, 0, 0], [0, 0, 0, 12000], [2999, 0, 64, 3], [3000, 1, 777, 12000]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        out.fill_(math.nan)
+        lse.fill_(math.nan)
+        graph.replay()
+        c.lens = np.array(n, dtype=np.int32)
+        c.check(out, lse)
+        want = wq.kv_attn_decode(c.q_dev, c.kv_dev, table, lens, return_lse=True, **kw)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

@@ -248,3 +248,33 @@ def test_a_pool_through_its_life():
             _, _, _, live = wq.kv_pages_compact(kv, table, lens, ref)
             assert not host(ref)[int(live.item()):].any() and host(ref)[:int(live.item())].all()
         verify()
+
+
+def test_guarded_outputs_have_the_oracles_values():
+    """The calls of test_outputs_stay_in_bounds, one after another into the same outputs, with their values."""
+    B, W, S, P = 33, 5, 4, 211
+    table, lens, ref = tables(B, W, S, P, 0.5, 1)
+    lens[3] = lens[4] = 0
+    t, l, f = Guarded((B, W), torch.int32), Guarded((B,), torch.int32), Guarded((P,), torch.int32)
+    m, n, g = Guarded((P,), torch.int32), Guarded((1,), torch.int32), Guarded((B,), torch.int32)
+    kv = Guarded((2, P, 2, 1, S, 64), torch.bfloat16)
+
+    def equal(*pairs):
+        for x, want in pairs:
+            x.check()
+            assert np.array_equal(host(x.t), want)
+
+    wq.kv_pages_compact(kv.t, dev(table), dev(lens), dev(ref), table_out=t.t, ref_out=f.t, remap=m.t, n_live=n.t)
+    want_t, want_r, want_m, live, _ = R.pages_compact(table, lens, ref, S)
+    equal((t, want_t), (f, want_r), (m, want_m), (n, [live]))
+    wq.kv_pages_reserve(dev(table), dev(lens), dev(lens + 9), dev(ref), S, table_out=t.t, ref_out=f.t, granted=g.t)
+    want_t, want_r, want_g = R.pages_reserve(table, lens, lens + 9, ref, S)
+    equal((t, want_t), (f, want_r), (g, want_g))
+    wq.kv_pages_free(dev(table), dev(lens), dev(ref), dev(np.arange(B)), S, lens_out=l.t, ref_out=f.t)
+    want_l, want_r, _ = R.pages_free(table, lens, ref, S, range(B))
+    equal((l, want_l), (f, want_r))
+    got = wq.kv_pages_fork(kv.t, dev(table), dev(lens), dev(ref), dev([1, 2]), dev([3, 4]), table_out=t.t, lens_out=l.t,
+                           ref_out=f.t)
+    want_t, want_l, want_r, want_g, _ = R.pages_fork(table, lens, ref, S, [1, 2], [3, 4])
+    equal((t, want_t), (l, want_l), (f, want_r))
+    assert np.array_equal(host(got[3]), want_g)
