@@ -294,7 +294,8 @@ size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
  *  window      0: all of them; otherwise the last `window` tokens.
  *  out         [B, Hq, D] bf16;  lse [B, Hq] float32 or NULL.
  *  workspace   at least kv_attn_workspace_bytes(), contents undefined between
- *              calls; not shared by calls that may run concurrently.
+ *              calls; not shared by calls that may run concurrently (calls of
+ *              several host threads on one stream do not).
  * The result's bits do not depend on timing. B >= 0; Hq a multiple of Hkv.
  * NaN among the numbers used gives NaN, and so may infinite ones of q or v.
  * Each token's weight exp(x[t] - m) is used to 2^-17 of itself, however small it is

@@ -148,3 +148,67 @@ def test_workspaces_of_rising_sizes_are_not_kept():
     assert torch.cuda.memory_allocated() - start <= sum(sizes) + (1 << 20)
     wq.drop_workspaces()
     assert torch.cuda.memory_allocated() <= start
+
+
+def test_host_threads_on_one_stream():
+    """Calls of several kernels that share the stream's scratch, from host threads that all use the default stream:
+    the results of the same calls one after another."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def bf16(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+    def attention(B, n, Hkv, G, D):
+        W = -(-n // 16)
+        kv, q = bf16(B * W, 2, Hkv, 16, D), bf16(B, Hkv * G, D)
+        table = torch.arange(B * W, dtype=torch.int32, device="cuda").view(B, W)
+        lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+        return lambda: wq.kv_attn_decode(q, kv, table, lens, return_lse=True)
+
+    def logprobs(T, V):
+        x, ids = bf16(T, V), torch.randint(0, V, (T,), generator=g, device="cuda").int()
+        return lambda: wq.token_logprobs(x, ids, top_k=7)
+
+    def compact(P):
+        kv = bf16(2, P, 2, 1, 16, 64)
+        live = torch.arange(1, P, 3, device="cuda")
+        ref = torch.zeros(P, dtype=torch.int32, device="cuda")
+        ref[live] = 1
+        table, lens = live.int()[None].contiguous(), torch.full((1,), live.numel() * 16, dtype=torch.int32, device="cuda")
+
+        def call():
+            x = kv.clone()
+            outs = [torch.empty_like(table), torch.empty_like(ref)]
+            return [x, *wq.kv_pages_compact(x, table, lens, ref, table_out=outs[0], ref_out=outs[1])]
+
+        return call
+
+    def w4a8(M):
+        codes = torch.randint(0, 16, (1024, 1024), generator=g, device="cuda", dtype=torch.uint8)
+        scales = (torch.rand((1024, 8), generator=g, device="cuda") / 64).bfloat16()
+        packed, s_dev = wq.wna16_repack(codes, scales, 4)
+        x = bf16(M, 1024)
+        return lambda: [wq.w4a8_gemm(x, packed, s_dev, 1024, 1024)]
+
+    jobs = [attention(1, 20000, 2, 4, 128), attention(3, 5000, 1, 12, 64), logprobs(1, 200000), logprobs(5, 90001),
+            compact(2000), compact(300), w4a8(192), w4a8(160)]
+    want = [[t.clone() for t in job()] for job in jobs]
+    torch.cuda.synchronize()
+    wrong, errors = [0] * len(jobs), []
+    start = threading.Barrier(len(jobs))
+
+    def work(i):
+        try:
+            start.wait()
+            got = [jobs[i]() for _ in range(40)]
+            wrong[i] = sum(not torch.equal(a, b) for r in got for a, b in zip(r, want[i]))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and wrong == [0] * len(jobs), (errors, wrong)

@@ -53,6 +53,11 @@ wq_status cuda_fail(cudaError_t e, const char* where) {
 
 void clear_error() { t_err[0] = 0; }
 
+std::mutex& launch_order() {
+  static std::mutex mu;
+  return mu;
+}
+
 wq_status get_ctx(void* stream, Ctx* c) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -477,12 +482,14 @@ static wq_status w4a8_body(const wq_bf16* x, int64_t M, const uint32_t* Wpacked4
     // many tokens: the codes as exact bf16 values into the tensor-core
     // kernel, which accumulates each group exactly and applies s and sx
     uint16_t* xqb = reinterpret_cast<uint16_t*>(sb);
+    const std::lock_guard<std::mutex> order(launch_order());
     cudaError_t e = launch_act_quant_bf16(c, x, M, K, xqb, sx);
     if (e != cudaSuccess) return cuda_fail(e, "act_quant launch");
     e = launch_w4a8_tc(c, xqb, sx, Wpacked4, scales, M, N, K, y, acc);
     if (e != cudaSuccess) return t_err[0] ? WQ_ECUDA : cuda_fail(e, "w4a8_gemm launch");
     return WQ_OK;
   }
+  const std::lock_guard<std::mutex> order(launch_order());
   cudaError_t e = launch_act_quant(c, x, M, K, xq, sx);
   if (e != cudaSuccess) return cuda_fail(e, "act_quant launch");
   a.xq = xq;

@@ -150,6 +150,7 @@ wq_status kv_attn_decode(const wq_bf16* q, int64_t q_stride, const void* kv, int
   WQ_TRY(check_space(workspace, ws_bytes, kv_attn_ws_bytes(B, Hq, Hkv, D), "workspace"));
   Ctx c{};
   WQ_TRY(get_ctx(stream, &c));
+  const std::lock_guard<std::mutex> order(launch_order());
   return launched(launch_kv_attn(c, a, q, q_stride, lens, Hq, sm_scale, window, out, lse, bad_count, workspace),
                   "kv_attn_decode launch");
 }
@@ -196,6 +197,7 @@ wq_status kv_pages_fork(void* kv, int64_t L, int64_t P, int64_t page_bytes, cons
   WQ_TRY(check_space(scratch, scratch_bytes, kv_pages_scratch(n, B, W, P), "scratch"));
   Ctx c{};
   WQ_TRY(get_ctx(stream, &c));
+  const std::lock_guard<std::mutex> order(launch_order());
   return launched(
       launch_pages_fork(c, p, t, parent, child, n, table_out, lens_out, ref_out, granted, scratch),
       "kv_pages_fork launch");
@@ -250,6 +252,7 @@ wq_status kv_pages_compact(void* kv, int64_t L, int64_t P, int64_t page_bytes, c
   WQ_TRY(check_space(scratch, scratch_bytes, kv_pages_scratch(0, B, W, P), "scratch"));
   Ctx c{};
   WQ_TRY(get_ctx(stream, &c));
+  const std::lock_guard<std::mutex> order(launch_order());
   return launched(launch_pages_compact(c, p, t, table_out, ref_out, remap, n_live, scratch),
                   "kv_pages_compact launch");
 }
@@ -291,6 +294,7 @@ wq_status token_logprobs(const void* logits, int logits_type, int64_t ld, int64_
   WQ_TRY(get_ctx(stream, &c));
   const LogprobArgs a{logits, logits_type, ld, T, V, ids, temperature, top_k, logprob, rank, entropy, top_logprobs,
                       top_ids, bad_count, workspace};
+  const std::lock_guard<std::mutex> order(launch_order());
   return launched(launch_logprobs(c, a), "token_logprobs launch");
 }
 

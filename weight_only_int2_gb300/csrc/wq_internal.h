@@ -30,6 +30,11 @@ wq_status fail(wq_status s, const char* fmt, ...);
 wq_status cuda_fail(cudaError_t e, const char* where);
 void clear_error();
 
+// Held while a call enqueues several kernels that hand one scratch buffer on to one
+// another: host threads that use one stream may share the buffer, and another
+// thread's kernels in between would write over it.
+std::mutex& launch_order();
+
 // Fills `c` for the current device; sets up the device's state on first use.
 wq_status get_ctx(void* stream, Ctx* c);
 
