@@ -298,8 +298,8 @@ size_t kv_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
  *              several host threads on one stream do not).
  * The result's bits do not depend on timing. B >= 0; Hq a multiple of Hkv.
  * NaN among the numbers used gives NaN, and so may infinite ones of q or v.
- * Each token's weight exp(x[t] - m) is used to 2^-17 of itself, however small it is
- * beside the others. With an e4m3 cache a query's numbers are used to at least
+ * Each token's weight exp(x[t] - m) is used to 2^-17 of itself down to e^-70, however
+ * small it is beside the others. With an e4m3 cache a query's numbers are used to at least
  * 2^-17 of the largest of their head (where that is at least 2^-119).
  * bad_count: pages left out. Tokens on a page beyond the length are never
  * used, whatever they hold. */

@@ -629,8 +629,8 @@ def kv_pages_compact(kv: torch.Tensor, block_table: torch.Tensor, lens: torch.Te
 
 def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k: int = 0, temperature: float = 1.0,
                    bad_count: torch.Tensor | None = None, ws: torch.Tensor | None = None):
-    """Per row of logits [T, V] (bf16 or float32, rows may be strided): the log
-    probability and rank of ids[t], the entropy, and the best top_k tokens.
+    """Per row of logits [T, V] (bf16 or float32, rows may be strided by any
+    number, the first logit 16-byte aligned): the log probability and rank of ids[t], the entropy, and the best top_k tokens.
     Returns (logprob [T], rank [T], entropy [T], top_logprobs [T, top_k],
     top_ids [T, top_k]); logprob and rank are None without ids."""
     if not isinstance(logits, torch.Tensor):

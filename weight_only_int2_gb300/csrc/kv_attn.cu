@@ -27,8 +27,8 @@
 //    registers, or to bf16 (three more instructions for two values) with 16
 //    tokens among whose weights there are some that fp16 is too short for: where
 //    all are so, D = 64 takes 109 us for 100 (64 sequences of up to 16011), D = 128
-//    181 to 184 either way, 16 heads 118 for 107, D = 256 152 for 143. The caches' scales are factors of
-//    the scores and of the output.
+//    181 to 184 either way, 16 heads 118 for 107, D = 256 152 for 143. The caches'
+//    scales are factors of the scores and of the output.
 //
 // Measured (of a copy's 6.8 TB/s): 64 sequences of 1 to 8192 tokens, 8 key heads
 // of 4 query heads, D = 128, bf16, 1.07 GB: 174 us, 6.2 TB/s; one of 131071
