@@ -409,6 +409,101 @@ wq_status token_logprobs(const void* logits, int logits_type, int64_t ld, int64_
                          float* top_logprobs, int32_t* top_ids, int32_t* bad_count, void* workspace, size_t ws_bytes,
                          void* stream);
 
+/* ---- operators that pick weights by token ------------------------------------
+ *
+ * What stands before and after wna16_moe_gemm (the choice of experts, the rows in
+ * their order and back), with the gradients of these, and low-rank adapters beside
+ * a linear layer. They have no counterpart on the source pages.
+ *
+ * T tokens have k choices each among E experts, 1 <= k <= min(32, E), E <= 1024,
+ * T * k < 2^31. ids [T, k] int32 name the experts; an id outside [0, E) (such as
+ * -1) is no choice, and slots [T, k] int32 name the choices' rows among R sorted
+ * ones, -1 (or any number outside [0, R)) for none. No device data can make these
+ * calls read or write out of range. Rows have D bf16 values, any D >= 1 (multiples
+ * of 8 go 16 bytes at a time). Outputs must not overlap inputs, unless it says so.
+ * The results' bits do not depend on timing. T >= 0 (T = 0 enqueues nothing, but
+ * that moe_sort's offsets are all 0). */
+#define WQ_SCORE_SOFTMAX 0
+#define WQ_SCORE_SIGMOID 1
+
+/* The router: per token the k experts with the largest logits, larger first, equal
+ * ones by ascending id (0.0 and -0.0 are equal, NaN comes first), and their weights,
+ *   weights[t, j] = scale * s[id_j]               (renormalize = 0), or
+ *   weights[t, j] = scale * s[id_j] / sum_i s[id_i],
+ * s being the softmax of the row's logits or the sigmoid of each, in float32. A
+ * logit of -inf is never chosen: where fewer than k are left, the rest have id -1
+ * and weight 0. NaN makes the weights that it enters NaN, as +inf does in a softmax.
+ *  logits      [T, E] bf16 or float32 (logits_type WQ_LOGITS_*), rows `ld` elements
+ *              apart (ld >= E).
+ *  score       WQ_SCORE_*;  scale finite.
+ *  ids [T, k] int32, weights [T, k] float32: outputs. */
+wq_status moe_route(const void* logits, int logits_type, int64_t ld, int64_t T, int64_t E, int k, int score,
+                    int renormalize, float scale, int32_t* ids, float* weights, void* stream);
+
+/* The gradient of moe_route's weights: dlogits [T, E], of the logits' type and
+ * contiguous, from ids [T, k] as moe_route gave them and dweights [T, k] float32.
+ * The choice itself has no gradient; choices without an expert, or of a logit that
+ * is -inf, add nothing. */
+wq_status moe_route_grad(const void* logits, int logits_type, int64_t ld, int64_t T, int64_t E, int k, int score,
+                         int renormalize, float scale, const int32_t* ids, const float* dweights, void* dlogits,
+                         void* stream);
+
+/* The tokens' rows in the order of their experts, as wna16_moe_gemm reads them.
+ * Choice i = t * k + j of expert e lies in row
+ *   slots[i] = #{ i' : (ids[i'], i') < (e, i) };  slots[i] = -1 without an expert,
+ * out[slots[i]] = x[t], and expert e owns rows offsets[e] .. offsets[e + 1] - 1.
+ * Rows of out [T * k, D] from offsets[E] on stay as they are.
+ *  x           [T, D] bf16, rows x_stride elements apart (x_stride >= D); x and out
+ *              both NULL: only slots and offsets.
+ *  offsets     [E + 1] int32, slots [T, k] int32: outputs.
+ *  bad_count   choices without an expert are added (NULL allowed).
+ * Its gradient is moe_combine of out's without weights. */
+wq_status moe_sort(const wq_bf16* x, int64_t x_stride, int64_t T, int64_t D, const int32_t* ids, int k, int64_t E,
+                   wq_bf16* out, int32_t* offsets, int32_t* slots, int32_t* bad_count, void* stream);
+
+/* The choices' rows back to their tokens:
+ *   out[t] = (residual[t] +) sum_j weights[t, j] * y[slots[t, j]],
+ * float32 in the order of j, rounded to bf16 once. A choice without a row adds
+ * nothing, whatever its weight.
+ *  y           [R, D] bf16.       weights  [T, k] float32, or NULL: all 1.
+ *  residual    [T, D] bf16, or NULL; out may be residual itself.
+ *  out         [T, D] bf16. */
+wq_status moe_combine(const wq_bf16* y, int64_t R, const int32_t* slots, const float* weights,
+                      const wq_bf16* residual, int64_t T, int64_t D, int k, wq_bf16* out, void* stream);
+
+/* The gradients of moe_combine (residual's is dout itself):
+ *   dy[slots[t, j]] = bf16(weights[t, j] * dout[t]),
+ *   dweights[t, j] = <dout[t], y[slots[t, j]]>  (float32; 0 without a row).
+ * Rows of dy [R, D] that no choice names stay as they are; no row may be named twice. */
+wq_status moe_combine_grad(const wq_bf16* dout, const wq_bf16* y, int64_t R, const int32_t* slots,
+                           const float* weights, int64_t T, int64_t D, int k, wq_bf16* dy, float* dweights,
+                           void* stream);
+
+/* Bytes of workspace lora_gemm needs (whatever the adapters of the rows). */
+size_t lora_workspace_bytes(int64_t M, int64_t n, int64_t r);
+
+/* Low-rank adapters of many requests beside a linear layer: with a = adapter[m],
+ *   y[m] = bf16(base[m] + scale[a] * (x[m] . A[a]^T) . B[a]^T),
+ * and y[m] = base[m] for a row whose adapter is outside [0, n) (such as -1). Sums are
+ * float32; x . A^T enters the second product to 2^-17 of itself.
+ *  x           [M, K] bf16, rows x_stride elements apart (a multiple of 8, at least
+ *              K); K a multiple of 8.
+ *  A [n, r, K], B [n, N, r] bf16: 1 <= n <= 1024, r a multiple of 8 up to 128
+ *              (adapters of lower rank are padded with zeros).
+ *  adapter     [M] int32, in any order.     scale [n] float32, or NULL: all 1.
+ *  base, y     [M, N] bf16, rows base_stride and y_stride elements apart (at least
+ *              N), 2-byte aligned: they may be columns of a fused projection (where
+ *              both are 16-byte aligned and N and the strides multiples of 8, 16
+ *              bytes are moved at a time). y may be base itself, with the same
+ *              stride, and must not overlap anything else.
+ *  workspace   as kv_attn_decode's.
+ * The result's bits do not depend on timing; a row's may depend on how many rows
+ * each adapter has in the call. M >= 0 (M = 0 enqueues nothing). */
+wq_status lora_gemm(const wq_bf16* x, int64_t x_stride, int64_t M, int64_t K, const wq_bf16* A, const wq_bf16* B,
+                    int64_t n, int64_t r, int64_t N, const int32_t* adapter, const float* scale, const wq_bf16* base,
+                    int64_t base_stride, wq_bf16* y, int64_t y_stride, void* workspace, size_t ws_bytes,
+                    void* stream);
+
 /* ---- test and debug entry points ---------------------------------------- */
 
 /* The launch plan of the CTA-pair decode kernel for a shape (host only, no

@@ -65,6 +65,18 @@ SIGNATURES = {
     "token_logprobs_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_int]),
     "token_logprobs": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, ctypes.c_float, _c_int, _c_ptr,
                                 _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "moe_route": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, ctypes.c_float, _c_ptr,
+                           _c_ptr, _c_ptr]),
+    "moe_route_grad": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, ctypes.c_float,
+                                _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "moe_sort": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_int, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                          _c_ptr]),
+    "moe_combine": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_int, _c_ptr, _c_ptr]),
+    "moe_combine_grad": (_c_int, [_c_ptr, _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_int, _c_ptr, _c_ptr,
+                                  _c_ptr]),
+    "lora_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "lora_gemm": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr,
+                           _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_size, _c_ptr]),
     "wq_debug_decode_plan": (_c_int, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_ptr]),
     "wq_debug_route": (_c_int, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_ptr]),
     "wq_debug_unpack": (_c_int, [_c_ptr, _c_i64, _c_i64, _c_int, _c_ptr, _c_ptr]),
@@ -661,6 +673,189 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
                               top.data_ptr(), top_ids.data_ptr(), _ptr(bad_count), _ptr(ws), 0 if ws is None else
                               ws.numel() * ws.element_size(), _stream()), "token_logprobs")
     return lp, rank, entropy, top, top_ids
+
+
+# ---------------------------------------------------------------- operators that pick weights by token
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _need_here(t: torch.Tensor, name: str) -> None:
+    """A tensor on the current device: the call's kernels run there, on its current stream."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_device()}")
+
+
+def _need_at(t: torch.Tensor, name: str, dtype, shape=None) -> None:
+    _need_here(t, name)
+    _need(t, name, dtype, shape)
+
+
+def _need_matrix(t: torch.Tensor, name: str, shape, dtypes=(torch.bfloat16,)) -> int:
+    """A matrix whose rows are contiguous and may lie any stride apart; returns that stride in elements."""
+    _need_here(t, name)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {'two dimensions' if shape is None else tuple(shape)} (got {tuple(t.shape)})")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1 and rows > 0:
+        raise ValueError(f"each row of {name} must be contiguous")
+    return cols if rows <= 1 else t.stride(0)
+
+
+def _score(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid' (got {score!r})")
+    return _SCORES[score]
+
+
+def _or_new(out, name, dtype, shape, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need_at(out, name, dtype, shape)
+    return out
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", renormalize: bool = False,
+              scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
+    """The top_k experts of each token by its logits [T, E] (bf16 or float32, rows may be strided) and their weights:
+    scale times the softmax or sigmoid score, divided by the chosen ones' sum with renormalize. Returns (ids [T, top_k]
+    int32, weights [T, top_k] float32); an expert whose logit is -inf is never chosen (id -1, weight 0)."""
+    ld = _need_matrix(logits, "logits", None, tuple(_LOGIT_TYPES))
+    (T, E), dev = logits.shape, logits.device
+    k = max(int(top_k), 0)
+    ids = _or_new(ids, "ids", torch.int32, (T, k), dev)
+    weights = _or_new(weights, "weights", torch.float32, (T, k), dev)
+    _check(load().moe_route(logits.data_ptr(), _LOGIT_TYPES[logits.dtype], ld, T, E, top_k, _score(score),
+                            1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _stream()), "moe_route")
+    return ids, weights
+
+
+def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
+                   renormalize: bool = False, scale: float = 1.0, dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of moe_route's weights: dlogits [T, E] of the logits' type, from the ids that it returned and
+    dweights [T, top_k] float32."""
+    ld = _need_matrix(logits, "logits", None, tuple(_LOGIT_TYPES))
+    T, E = logits.shape
+    _need_at(ids, "ids", torch.int32)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must have shape ({T}, top_k) (got {tuple(ids.shape)})")
+    k = ids.shape[1]
+    _need_at(dweights, "dweights", torch.float32, (T, k))
+    dlogits = _or_new(dlogits, "dlogits", logits.dtype, (T, E), logits.device)
+    _check(load().moe_route_grad(logits.data_ptr(), _LOGIT_TYPES[logits.dtype], ld, T, E, k, _score(score),
+                                 1 if renormalize else 0, scale, ids.data_ptr(), dweights.data_ptr(),
+                                 dlogits.data_ptr(), _stream()), "moe_route_grad")
+    return dlogits
+
+
+def moe_sort(x: torch.Tensor | None, ids: torch.Tensor, E: int, out: torch.Tensor | None = None,
+             offsets: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+             bad_count: torch.Tensor | None = None):
+    """x [T, D] bf16 (rows may be strided) in the order of the experts ids [T, k] int32, as wna16_moe_gemm reads it.
+    Returns (out [T * k, D], offsets [E + 1] int32, slots [T, k] int32, the row of each choice, -1 without an expert);
+    rows of out that no choice takes stay as they are. x None: out is None. The gradient of x is
+    moe_combine(dout, slots)."""
+    _need_at(ids, "ids", torch.int32)
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be [T, k] (got {tuple(ids.shape)})")
+    (T, k), dev = ids.shape, ids.device
+    D = xs = 0
+    if x is not None:
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a tensor [T, D]")
+        D = x.shape[1]
+        xs = _need_matrix(x, "x", (T, D))
+        out = _or_new(out, "out", torch.bfloat16, (T * k, D), dev)
+    elif out is not None:
+        raise ValueError("out is for a call with x")
+    offsets = _or_new(offsets, "offsets", torch.int32, (E + 1,), dev)
+    slots = _or_new(slots, "slots", torch.int32, (T, k), dev)
+    if bad_count is not None:
+        _need_at(bad_count, "bad_count", torch.int32)
+    _check(load().moe_sort(_ptr(x), xs, T, D, ids.data_ptr(), k, E, _ptr(out), offsets.data_ptr(), slots.data_ptr(),
+                           _ptr(bad_count), _stream()), "moe_sort")
+    return out, offsets, slots
+
+
+def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
+                residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = (residual[t] +) sum_j weights[t, j] * y[slots[t, j]], [T, D] bf16: the choices' rows y [R, D] bf16
+    back to their tokens (weights [T, k] float32; 1 without them). out may be residual itself."""
+    _need_at(y, "y", torch.bfloat16)
+    _need_at(slots, "slots", torch.int32)
+    if y.dim() != 2 or slots.dim() != 2:
+        raise ValueError(f"y must be [R, D] and slots [T, k] (got {tuple(y.shape)} and {tuple(slots.shape)})")
+    (R, D), (T, k) = y.shape, slots.shape
+    if weights is not None:
+        _need_at(weights, "weights", torch.float32, (T, k))
+    if residual is not None:
+        _need_at(residual, "residual", torch.bfloat16, (T, D))
+    out = _or_new(out, "out", torch.bfloat16, (T, D), y.device)
+    _check(load().moe_combine(y.data_ptr(), R, slots.data_ptr(), _ptr(weights), _ptr(residual), T, D, k,
+                              out.data_ptr(), _stream()), "moe_combine")
+    return out
+
+
+def moe_combine_grad(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
+                     dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None):
+    """The gradients of moe_combine from dout [T, D] bf16: dy [R, D] bf16 (rows that no choice names stay as they
+    are) and dweights [T, k] float32. The residual's is dout itself."""
+    _need_at(y, "y", torch.bfloat16)
+    _need_at(slots, "slots", torch.int32)
+    if y.dim() != 2 or slots.dim() != 2:
+        raise ValueError(f"y must be [R, D] and slots [T, k] (got {tuple(y.shape)} and {tuple(slots.shape)})")
+    (R, D), (T, k) = y.shape, slots.shape
+    _need_at(dout, "dout", torch.bfloat16, (T, D))
+    _need_at(weights, "weights", torch.float32, (T, k))
+    dy = _or_new(dy, "dy", torch.bfloat16, (R, D), y.device)
+    dweights = _or_new(dweights, "dweights", torch.float32, (T, k), y.device)
+    _check(load().moe_combine_grad(dout.data_ptr(), y.data_ptr(), R, slots.data_ptr(), weights.data_ptr(), T, D, k,
+                                   dy.data_ptr(), dweights.data_ptr(), _stream()), "moe_combine_grad")
+    return dy, dweights
+
+
+@functools.lru_cache(maxsize=4096)
+def lora_workspace_bytes(M: int, n: int, r: int) -> int:
+    return int(load().lora_workspace_bytes(M, n, r))
+
+
+def lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor, base: torch.Tensor,
+              scale: torch.Tensor | None = None, y: torch.Tensor | None = None,
+              ws: torch.Tensor | None = None) -> torch.Tensor:
+    """y[m] = base[m] + scale[a] * (x[m] . A[a]^T) . B[a]^T with a = adapter[m] (int32; -1: none, y[m] = base[m]).
+    x [M, K], base and y [M, N] bf16 (rows may be strided; y may be base), A [n, r, K], B [n, N, r] bf16, scale [n]
+    float32. base is the shared projection's output, such as wna16_gemm(x, ..)."""
+    _need_at(A, "A", torch.bfloat16)
+    _need_at(B, "B", torch.bfloat16)
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError(f"A must be [n, r, K] and B [n, N, r] (got {tuple(A.shape)} and {tuple(B.shape)})")
+    (n, r, K), N = A.shape, B.shape[1]
+    if tuple(B.shape) != (n, N, r):
+        raise ValueError(f"B must have shape {(n, N, r)} (got {tuple(B.shape)})")
+    _need_at(adapter, "adapter", torch.int32)
+    M = adapter.shape[0]
+    _need(adapter, "adapter", torch.int32, (M,))
+    xs, bs = _need_matrix(x, "x", (M, K)), _need_matrix(base, "base", (M, N))
+    if scale is not None:
+        _need_at(scale, "scale", torch.float32, (n,))
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=base.device)
+    ys = _need_matrix(y, "y", (M, N))
+    if M <= 1 and y.data_ptr() == base.data_ptr():
+        ys = bs
+    lib = load()
+    if ws is None:
+        ws = scratch(lora_workspace_bytes(M, n, r))
+    _check(lib.lora_gemm(x.data_ptr(), xs, M, K, A.data_ptr(), B.data_ptr(), n, r, N, adapter.data_ptr(), _ptr(scale),
+                         base.data_ptr(), bs, y.data_ptr(), ys, _ptr(ws), 0 if ws is None else
+                         ws.numel() * ws.element_size(), _stream()), "lora_gemm")
+    return y
 
 
 _PLAN_KEYS = ("ok", "C", "H", "nchunk", "T", "ksplit", "NS", "G", "Gh", "sbox", "sx0", "NT", "smem",

@@ -1,0 +1,193 @@
+// Groups entries by a small id, stably: entry i of id e gets the place
+// #{i' : (id', i') < (e, i)}, so that the entries of each id follow one another in
+// their own order. The experts' rows of a batch and the tiles of its adapters
+// begin with it.
+//
+// The ids are a few KB to a few hundred KB, so latency bounds it. A warp counts a
+// run of entries in its own row of counters (the lanes that share an id find each
+// other by a match, so nothing depends on the order of atomics), the rows and the
+// blocks are summed up, and the warp goes over its run once more and gives out
+// places. Few entries take one block; more take a cluster of 8 that exchange their
+// counts through distributed shared memory.
+#include "wq_cluster.cuh"
+#include "wq_device.cuh"
+#include "wq_internal.h"
+
+namespace wq {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRun = 8;  // ids a lane holds between the two passes
+constexpr int64_t kGroupOneBlock = 8192;
+
+// Exclusive prefix sum over the block of two counts a thread; *total receives the sum.
+__device__ int block_scan(int a, int b, int* warp_sum, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  int s = warp_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+    if (lane >= o) s += y;
+  }
+  *total = __shfl_sync(0xFFFFFFFFu, s, 31);
+  const int before = warp > 0 ? __shfl_sync(0xFFFFFFFFu, s, warp - 1) : 0;
+  __syncthreads();
+  return before + x - a - b;
+}
+
+template <int kBlocks>
+__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) group_kernel(const GroupArgs a) {
+  extern __shared__ int32_t smem[];
+  __shared__ int warp_sum[kWarps];
+  const int E1 = a.E + 1;               // ids outside [0, E) are the last group
+  int32_t* hist = smem;                 // [kWarps][E1] counts, then places given out before, of each warp
+  int32_t* count = hist + kWarps * E1;  // [E1] of this block
+  int32_t* first = count + E1;          // [E1] this block's first place of each id
+  int32_t* start = first + E1;          // [E1 + 1] the id's first place, and n
+  int32_t* tile0 = start + E1 + 1;      // [E1 + 1] tiles before the id's
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = kBlocks > 1 ? static_cast<int>(cl::cluster_rank()) : 0;
+  for (int i = threadIdx.x; i < kWarps * E1; i += kThreads) hist[i] = 0;
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+  const int64_t per = (a.n + kBlocks * kThreads - 1) / (kBlocks * kThreads) * 32;
+  const int64_t lo = (static_cast<int64_t>(rank) * kWarps + warp) * per, hi = lo + per < a.n ? lo + per : a.n;
+  int32_t* mine = hist + warp * E1;
+  int32_t id[kRun];
+  auto load = [&](int64_t i0) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const int64_t i = i0 + 32 * j + lane;
+      id[j] = i < hi ? a.ids[i] : -2;
+      if (i < hi && (id[j] < 0 || id[j] >= a.E)) id[j] = a.E;
+    }
+  };
+  __syncthreads();
+  for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRun) {
+    load(i0);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      if (i0 + 32 * j >= hi) break;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
+      if (id[j] >= 0 && lane == __ffs(same) - 1) mine[id[j]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E1; e += kThreads) {
+    int run = 0;
+#pragma unroll 8
+    for (int w = 0; w < kWarps; ++w) {
+      const int c = hist[w * E1 + e];
+      hist[w * E1 + e] = run;
+      run += c;
+    }
+    count[e] = run;
+  }
+  if (kBlocks > 1) {
+    cl::cluster_arrive();
+    cl::cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  // two ids a thread: E + 1 <= 1025
+  int lower[2] = {}, all[2] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * threadIdx.x + i;
+    if (e >= E1) continue;
+    if constexpr (kBlocks == 1) {
+      all[i] = count[e];
+    } else {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        int c;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(cl::map_peer(smem_u32(count + e), b)));
+        if (b < rank) lower[i] += c;
+        all[i] += c;
+      }
+    }
+  }
+  if (kBlocks > 1) cl::cluster_arrive();  // this block reads no other's counts any more
+  int total;
+  const int before = block_scan(all[0], all[1], warp_sum, &total);
+  int at = before;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * threadIdx.x + i;
+    if (e < E1) {
+      first[e] = at + lower[i];
+      start[e] = at;
+      if (rank == 0) {
+        if (a.offsets != nullptr) a.offsets[e] = at;
+        if (e == a.E && a.bad != nullptr && all[i] > 0) atomicAdd(a.bad, all[i]);
+      }
+    }
+    at += all[i];
+  }
+  if (a.tiles != nullptr && rank == 0) {
+    const int t0 = (all[0] + a.tile - 1) / a.tile, t1 = (all[1] + a.tile - 1) / a.tile;
+    int tiles;
+    const int tb = block_scan(t0, t1, warp_sum, &tiles);
+    if (2 * threadIdx.x < E1) tile0[2 * threadIdx.x] = tb;
+    if (2 * threadIdx.x + 1 < E1) tile0[2 * threadIdx.x + 1] = tb + t0;
+    if (threadIdx.x == 0) start[E1] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) a.tiles[0] = make_int4(tile0[a.E], tiles, start[a.E], 0);
+    for (int t = threadIdx.x; t < tiles; t += kThreads) {
+      int e = 0, end = E1;  // the last id whose tiles begin at t or before
+      while (end - e > 1) {
+        const int mid = (e + end) >> 1;
+        if (tile0[mid] <= t) e = mid; else end = mid;
+      }
+      const int r0 = start[e] + (t - tile0[e]) * a.tile, rows = start[e + 1] - r0;
+      a.tiles[1 + t] = make_int4(e < a.E ? e : -1, r0, rows < a.tile ? rows : a.tile, 0);
+    }
+  }
+  if (kBlocks > 1) cl::cluster_wait();
+  __syncthreads();
+  for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRun) {
+    if (per > 32 * kRun) load(i0);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      if (i0 + 32 * j >= hi) break;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
+      int place = 0;
+      if (id[j] >= 0) place = first[id[j]] + mine[id[j]] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (id[j] >= 0 && lane == __ffs(same) - 1) mine[id[j]] += __popc(same);
+      __syncwarp();
+      const int64_t i = i0 + 32 * j + lane;
+      if (i < hi) {
+        if (a.slots != nullptr) a.slots[i] = id[j] < a.E ? place : -1;
+        if (a.order != nullptr) a.order[place] = static_cast<int32_t>(i);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_group(const Ctx& c, const GroupArgs& a) {
+  const size_t smem = sizeof(int32_t) * ((kWarps + 2) * (static_cast<size_t>(a.E) + 1) + 2 * (a.E + 2));
+  // (a cluster's barriers cost about a microsecond: it pays from a few thousand ids on)
+  if (a.n <= kGroupOneBlock) {
+    static SmemLimit lim;
+    const cudaError_t e = raise_smem_limit(lim, group_kernel<1>, c.device, smem);
+    return e != cudaSuccess ? e : launch_early(c, 1, kThreads, smem, group_kernel<1>, a);
+  }
+  static SmemLimit lim;
+  const cudaError_t e = raise_smem_limit(lim, group_kernel<8>, c.device, smem);
+  return e != cudaSuccess ? e : launch_early(c, 8, kThreads, smem, group_kernel<8>, a);
+}
+
+}  // namespace wq

@@ -9,20 +9,6 @@
 namespace wq {
 namespace {
 
-wq_status check_opt32(const void* p, const char* name) {
-  if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return fail(WQ_EINVAL, "%s is not 4-byte aligned", name);
-  return WQ_OK;
-}
-
-// A device array of 32-bit values: non-NULL and 4-byte aligned (a caller's
-// slice of a larger array, so no more than that).
-wq_status check_32(const void* p, const char* name) {
-  if (p == nullptr) return fail(WQ_EINVAL, "%s is NULL", name);
-  return check_opt32(p, name);
-}
-#define WQ_PTR32(p) WQ_TRY(check_32((p), #p))
-#define WQ_OPT32(p) WQ_TRY(check_opt32((p), #p))
-
 wq_status check_cache(const KvCache& a) {
   if (a.type != WQ_KV_BF16 && a.type != WQ_KV_E4M3)
     return fail(WQ_EINVAL, "kv_type must be WQ_KV_BF16 or WQ_KV_E4M3 (got %d)", a.type);
@@ -54,14 +40,6 @@ wq_status check_row_stride(int64_t stride, int64_t least, const char* name) {
   return WQ_OK;
 }
 
-wq_status check_space(const void* p, size_t bytes, size_t need, const char* name) {
-  if (need == 0) return WQ_OK;
-  if (p == nullptr) return fail(WQ_EINVAL, "%s is NULL", name);
-  if (!aligned16(p)) return fail(WQ_EINVAL, "%s is not 16-byte aligned", name);
-  if (bytes < need) return fail(WQ_EINVAL, "%s too small: %zu < %zu bytes", name, bytes, need);
-  return WQ_OK;
-}
-
 wq_status check_pool(const PagePool& p) {
   WQ_TRY(check_size(p.L, "L"));
   WQ_TRY(check_size(p.P, "P"));
@@ -83,8 +61,6 @@ wq_status check_tables(const SeqTables& t) {
   WQ_PTR32(t.ref);
   return WQ_OK;
 }
-
-wq_status launched(cudaError_t e, const char* where) { return e == cudaSuccess ? WQ_OK : cuda_fail(e, where); }
 
 }  // namespace
 }  // namespace wq

@@ -56,6 +56,29 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
     if (!aligned16(p)) return fail(WQ_EINVAL, "%s is not 16-byte aligned", #p); \
   } while (0)
 
+inline wq_status check_opt32(const void* p, const char* name) {
+  if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return fail(WQ_EINVAL, "%s is not 4-byte aligned", name);
+  return WQ_OK;
+}
+// A device array of 32-bit values: non-NULL and 4-byte aligned (a caller's
+// slice of a larger array, so no more than that).
+inline wq_status check_32(const void* p, const char* name) {
+  if (p == nullptr) return fail(WQ_EINVAL, "%s is NULL", name);
+  return check_opt32(p, name);
+}
+#define WQ_PTR32(p) WQ_TRY(check_32((p), #p))
+#define WQ_OPT32(p) WQ_TRY(check_opt32((p), #p))
+
+inline wq_status check_space(const void* p, size_t bytes, size_t need, const char* name) {
+  if (need == 0) return WQ_OK;
+  if (p == nullptr) return fail(WQ_EINVAL, "%s is NULL", name);
+  if (!aligned16(p)) return fail(WQ_EINVAL, "%s is not 16-byte aligned", name);
+  if (bytes < need) return fail(WQ_EINVAL, "%s too small: %zu < %zu bytes", name, bytes, need);
+  return WQ_OK;
+}
+
+inline wq_status launched(cudaError_t e, const char* where) { return e == cudaSuccess ? WQ_OK : cuda_fail(e, where); }
+
 // A kernel's dynamic shared-memory limit per device, raised on demand and
 // never lowered, under a lock: host threads that launch concurrently never
 // see a limit below the one they raised (a lowered limit would fail their
@@ -380,5 +403,67 @@ struct LogprobArgs {
 constexpr int kMaxTopK = 32;
 size_t logprobs_ws_bytes(int64_t T, int64_t V, int top_k);
 cudaError_t launch_logprobs(const Ctx& c, const LogprobArgs& a);
+
+// ---- operators that pick weights by token (select_api.cu; kernels in group.cu,
+// moe.cu and lora.cu) ----------------------------------------------------------
+
+constexpr int kMaxGroups = 1024;  // experts, or adapters
+
+// Entries grouped by id (group.cu): entry i's place, the entry at each place, the
+// first place of each id; and tiles of at most `tile` entries of one id in a row.
+// Ids outside [0, E) come last.
+struct GroupArgs {
+  const int32_t* ids;  // [n]
+  int64_t n;
+  int E;
+  int32_t* slots;    // [n] or null; -1 for ids outside
+  int32_t* order;    // [n] or null
+  int32_t* offsets;  // [E + 1] or null
+  int32_t* bad;      // or null: the ids outside are added
+  int4* tiles;       // or null: {tiles of ids inside, all, entries of ids inside, 0},
+  int tile;          // then a tile's {id or -1, first place, entries, 0}
+};
+cudaError_t launch_group(const Ctx& c, const GroupArgs& a);
+
+struct RouteArgs {
+  const void* logits;
+  int type;  // WQ_LOGITS_*
+  int64_t ld, T, E;
+  int k, score, renormalize;
+  float scale;
+};
+cudaError_t launch_moe_route(const Ctx& c, const RouteArgs& a, int32_t* ids, float* weights);
+cudaError_t launch_moe_route_grad(const Ctx& c, const RouteArgs& a, const int32_t* ids, const float* dweights,
+                                  void* dlogits);
+
+// Rows of T tokens with k choices each; slots [T, k] in [0, R) or nothing.
+struct ChoiceRows {
+  const int32_t* slots;
+  const float* weights;  // [T, k] or null (1)
+  int64_t T, R, D;
+  int k;
+};
+cudaError_t launch_moe_spread(const Ctx& c, const ChoiceRows& a, const uint16_t* x, int64_t x_stride, uint16_t* out);
+cudaError_t launch_moe_combine(const Ctx& c, const ChoiceRows& a, const uint16_t* y, const uint16_t* residual,
+                               uint16_t* out);
+cudaError_t launch_moe_combine_grad(const Ctx& c, const ChoiceRows& a, const uint16_t* dout, const uint16_t* y,
+                                    uint16_t* dy, float* dweights);
+
+struct LoraArgs {
+  const uint16_t* x;  // [M, K]
+  int64_t x_stride, M, K, N, n, r;
+  const uint16_t* A;       // [n, r, K]
+  const uint16_t* B;       // [n, N, r]
+  const int32_t* adapter;  // [M]
+  const float* scale;      // [n] or null (1)
+  const uint16_t* base;    // [M, N]
+  int64_t base_stride;
+  uint16_t* y;  // [M, N], base itself or apart from it
+  int64_t y_stride;
+  void* ws;
+};
+constexpr int kMaxRank = 128;
+size_t lora_ws_bytes(int64_t M, int64_t n, int64_t r);
+cudaError_t launch_lora(const Ctx& c, const LoraArgs& a);
 
 }  // namespace wq
