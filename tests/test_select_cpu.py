@@ -191,7 +191,7 @@ def test_the_workspace_holds_every_share_of_the_first_product():
     import weight_only_int2_gb300 as wq
 
     for M in (1, 2, 15, 16, 17, 100, 511, 512, 513, 4000, 70000):
-        tile = 16 if M < 512 else 64
+        tile = 8 if M < 512 else 64
         for n in (1, 3, 1024):
             for r in (8, 128):
                 have = wq.lora_workspace_bytes(M, n, r)

@@ -19,7 +19,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRun = 8;  // ids a lane holds between the two passes
-constexpr int64_t kGroupOneBlock = 8192;
+constexpr int64_t kGroupOneBlock = 1024;
 
 // Exclusive prefix sum over the block of two counts a thread; *total receives the sum.
 __device__ int block_scan(int a, int b, int* warp_sum, int* total) {

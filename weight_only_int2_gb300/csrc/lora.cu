@@ -26,18 +26,19 @@
 namespace wq {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;    // of a block of the first product
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 4;
 constexpr int kMaxShares = 32;
 constexpr int kMaxGrid = 1024;   // blocks of the first product
-constexpr int kUnit = 128;       // columns of a unit of the second product's work
 
-// Rows of a tile. A decode batch has a few rows of each adapter: one MMA's 16 rows,
-// the four warps side by side along K or the columns. From kManyRows rows on a warp
-// has 16 rows of its own.
+// Rows of a tile. A decode batch has a few rows of each adapter: they are the 8
+// columns of an MMA, and A's or B's values its 16 rows. From kManyRows rows on tiles
+// are 64 rows, 16 a warp, and A's or B's values the columns.
 constexpr int64_t kManyRows = 512;
-constexpr int tile_of(int64_t M) { return M < kManyRows ? 16 : 64; }
+constexpr int kFewTile = 8;
+constexpr int tile_of(int64_t M) { return M < kManyRows ? kFewTile : 64; }
+// Up to so many rows every block groups them itself, one a thread.
+constexpr int64_t kFewRows = kThreads;
 
 struct Ws {
   int4* tiles;     // as launch_group writes them
@@ -55,6 +56,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
   const int size = real ? 16 : 0;  // 0: zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
+  const int size = real ? 8 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void cp_wait() {
@@ -67,137 +72,288 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&d)[4], uint32_t addr) {
                : "memory");
 }
 
-// How K is shared among blocks: `shares` of `per` stages each.
+// How K is shared among blocks: `shares` of `per` stages each. (Shares are added up
+// 16 at a time: beyond 16 they have four stages at least.)
 struct Shares {
   int shares, per;
 };
 __device__ __forceinline__ Shares shares_of(int stages, int tiles, int grid) {
   int s = tiles > 0 ? grid / tiles : 1;
-  s = max(1, min(min(s, kMaxShares), stages));
+  s = max(1, min(min(s, kMaxShares), min(stages, max(16, stages / 4))));
   const int per = (stages + s - 1) / s;
   return Shares{(stages + per - 1) / per, per};
 }
 
+// ---------------------------------------------------------------- rows by adapter
+
+// What both products know of the rows' order: as launch_group wrote it, or of few
+// rows in shared memory, found by the block itself (a launch less; 64 rows take ..).
+struct Few {
+  int key[kFewRows];      // (adapter, row) by row
+  int id[kFewRows + 1];   // adapters by place; id[0]: none
+  int32_t order[kFewRows];
+  int4 tiles[1 + kFewRows];
+};
+struct Rows {
+  const int4* tiles;
+  const int32_t* order;
+  // (past the first level cache, which may hold an earlier call's)
+  __device__ int4 tile(int i) const { return __ldcg(tiles + i); }
+  __device__ int row(int i) const { return __ldcg(order + i); }
+};
+struct FewRows {
+  const Few* f;
+  __device__ int4 tile(int i) const { return f->tiles[i]; }
+  __device__ int row(int i) const { return f->order[i]; }
+};
+// Every thread has a row, whose place is the number of rows before it by (adapter,
+// row); then it has the place with its number, and a tile begins at the places 0, 8,
+// 16 .. of a group.
+__device__ __forceinline__ void group_few(Few& f, const int32_t* ids, int M, int n) {
+  static_assert(kFewRows == kThreads && kMaxGroups < (1 << 24), "a row a thread");
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  int id = i < M ? __ldcg(ids + i) : 0x7FFFFF;
+  if (i < M && (id < 0 || id >= n)) id = n;
+  const int key = id << 7 | i;
+  f.key[i] = key;
+  if (i == 0) f.id[0] = -1;
+  __syncthreads();
+  int place = i;
+  if (32 * warp < M) {
+    place = 0;
+#pragma unroll 4
+    for (int j = 0; j < M; j += 4) {
+      const int4 k = *reinterpret_cast<const int4*>(f.key + j);
+      place += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+    }
+  }
+  f.id[1 + place] = id;
+  f.order[place] = i;
+  __syncthreads();
+  // the groups' first places as bits, then the tiles'
+  uint32_t first[kFewRows / 32], begin[kFewRows / 32];
+  int rows = 0, tiles = 0, inside = 0;
+#pragma unroll
+  for (int w = 0; w < kFewRows / 32; ++w) {
+    const int at = f.id[1 + 32 * w + lane], p = 32 * w + lane;
+    first[w] = __ballot_sync(0xFFFFFFFFu, p < M && at != f.id[p]);
+    const uint32_t have = __ballot_sync(0xFFFFFFFFu, p < M && at < n);
+    int start = 0;  // place p's group's
+#pragma unroll
+    for (int v = 0; v <= w; ++v) {
+      const uint32_t m = v < w ? first[v] : first[v] & (0xFFFFFFFFu >> (31 - lane));
+      if (m != 0) start = 32 * v + 31 - __clz(m);
+    }
+    begin[w] = __ballot_sync(0xFFFFFFFFu, p < M && (p - start) % kFewTile == 0);
+    rows += __popc(have);
+    inside += __popc(begin[w] & have);
+    if (w == warp && (begin[w] >> lane & 1) != 0) {
+      const int t = tiles + __popc(begin[w] & ((1u << lane) - 1));
+      int end = p + 1;
+      while (end < M && end < p + kFewTile && f.id[1 + end] == at) ++end;
+      f.tiles[1 + t] = make_int4(at < n ? at : -1, p, end - p, 0);
+    }
+    tiles += __popc(begin[w]);
+  }
+  if (i == 0) f.tiles[0] = make_int4(inside, tiles, rows, 0);
+  __syncthreads();
+}
+
 // ---------------------------------------------------------------- x A^T
 
-template <int kTile, int kR>
-struct Shrink {
-  static constexpr int kCols = kTile == 16 ? 128 : 64;  // of a stage
-  static constexpr int kRowBytes = 2 * kCols;
-  static constexpr int kChunks = kRowBytes / 16;
-  static constexpr int kRows = kTile + kR;
-  static constexpr int kStageBytes = kRows * kRowBytes;
-  static constexpr int kSmem = kStages * kStageBytes;
-  static constexpr int kStep = kThreads / kChunks;        // rows that the block copies at once
-  static constexpr int kXs = kTile / kStep;               // rows of x a thread copies
-  static constexpr int kAs = (kR + kStep - 1) / kStep;    // and of A
-  static_assert(kTile % kStep == 0, "");
-  static_assert(kTile == 64 || kWarps * 16 * kR * 4 <= kSmem, "the warps' sums lie in the ring");
+// Tiles of 8 rows. Few rows use A: a lane copies what it needs itself in the MMA's
+// layout (16 bytes are 8 values of K in a row, dealt out alike on x's side) into its
+// own places of a ring of stages of 32 of K, so that nothing waits for another lane.
+// The block's four warps take 128 of K in turn along its share and are added up at
+// its end.
+template <int kR>
+struct Shrink8 {
+  static constexpr int kCols = 512;  // of a stage of the shares: four warps' 128
+  static constexpr int kStages = kR == 128 ? 3 : 4;
+  static constexpr int kStageBytes = (kR / 8 + 1) * 512;
+  static constexpr int kSums = kWarps * 8 * kR * 4;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes;
+  static constexpr int kAll = kSmem + kSums + static_cast<int>(sizeof(Few)) + 1024;
+  static constexpr int kFit = 228 * 1024 / kAll < 4 ? 228 * 1024 / kAll : 4;
 };
 
-template <int kTile, int kR>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const LoraArgs a, const Ws ws) {
-  using C = Shrink<kTile, kR>;
+template <int kR, bool kFew>
+__global__ void __launch_bounds__(kThreads, Shrink8<kR>::kFit) shrink8_kernel(const LoraArgs a, const Ws ws) {
+  using C = Shrink8<kR>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float sums[kWarps][8 * kR];
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+  const auto rows = [&] {
+    if constexpr (kFew) {
+      __shared__ Few few;
+      group_few(few, a.adapter, static_cast<int>(a.M), static_cast<int>(a.n));
+      return FewRows{&few};
+    } else {
+      return Rows{ws.tiles, ws.order};
+    }
+  }();
+  const int4 head = rows.tile(0);
+  const int K = static_cast<int>(a.K), r = static_cast<int>(a.r), stages = (K - 1) / C::kCols + 1;
+  const Shares sh = shares_of(stages, head.x, gridDim.x);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const uint8_t* own = ring + warp * C::kStages * C::kStageBytes + lane * 16;
+  const uint32_t own_at = smem_u32(own);
+  const int units = head.x * sh.shares;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int t = u / sh.shares, share = u - t * sh.shares;
+    const int4 tile = rows.tile(1 + t);
+    const bool mine = g < tile.z;
+    const uint16_t* x = a.x + (mine ? rows.row(tile.y + g) : 0) * a.x_stride;
+    const uint16_t* A = a.A + (static_cast<int64_t>(tile.x) * r + g) * K;
+    const int k0 = share * sh.per * C::kCols + warp * 128 + q * 8;  // (stages end below 2^31 + 2^9)
+    const int blocks = 4 * (min(sh.per * (share + 1), stages) - share * sh.per);
+    auto fetch = [&](int b, uint32_t slot) {
+      const int k = k0 + (b >> 2) * C::kCols + (b & 3) * 32;
+      const bool in = k >= 0 && k < K;
+      const uint16_t* src = A + k;
+#pragma unroll
+      for (int n = 0; n < kR / 8; ++n) {
+        const bool real = in && 8 * n < r;
+        cp_async16(own_at + slot + n * 512, real ? src : a.A, real);
+        src += static_cast<int64_t>(8) * K;
+      }
+      cp_async16(own_at + slot + (kR / 8) * 512, in && mine ? x + k : a.x, in && mine);
+    };
+#pragma unroll
+    for (int b = 0; b < C::kStages - 1; ++b) {
+      if (b < blocks) fetch(b, b * C::kStageBytes);
+      cp_commit();
+    }
+    float acc[kR / 16][4] = {};
+    uint32_t slot = 0, ahead = (C::kStages - 1) * C::kStageBytes;
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+      if (b + C::kStages - 1 < blocks) fetch(b + C::kStages - 1, ahead);
+      cp_commit();
+      cp_wait<C::kStages - 1>();
+      const uint4 xv = *reinterpret_cast<const uint4*>(own + slot + (kR / 8) * 512);
+#pragma unroll
+      for (int n = 0; n < kR / 16; ++n) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(own + slot + (2 * n) * 512);
+        const uint4 hi = *reinterpret_cast<const uint4*>(own + slot + (2 * n + 1) * 512);
+        mma_bf16_16816(acc[n], lo.x, hi.x, lo.y, hi.y, xv.x, xv.y);
+        mma_bf16_16816(acc[n], lo.z, hi.z, lo.w, hi.w, xv.z, xv.w);
+      }
+      ahead = slot;
+      slot = slot + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : slot + C::kStageBytes;
+    }
+#pragma unroll
+    for (int n = 0; n < kR / 16; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums[warp][(2 * q + (i & 1)) * kR + 16 * n + g + 8 * (i >> 1)] = acc[n][i];
+    }
+    __syncthreads();
+    float* part = ws.part + (static_cast<int64_t>(share) * head.z + tile.y) * r;
+    for (int i = threadIdx.x; i < tile.z * kR; i += kThreads) {
+      const int row = i / kR, col = i % kR;
+      const float s = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+      if (col < r) part[row * r + col] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// Tiles of 64 rows: a ring of cp.async stages of x's rows and A's.
+template <int kR>
+struct Shrink64 {
+  static constexpr int kCols = 64;  // of a stage
+  static constexpr int kRowBytes = 2 * kCols;
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int kStages = 4;
+  static constexpr int kStageBytes = (64 + kR) * kRowBytes;
+  static constexpr int kSmem = kStages * kStageBytes;
+  static constexpr int kStep = kThreads / kChunks;  // rows that the block copies at once
+  static constexpr int kXs = 64 / kStep;            // rows of x a thread copies
+  static constexpr int kAs = kR / kStep;            // and of A
+};
+
+template <int kR>
+__global__ void __launch_bounds__(kThreads) shrink64_kernel(const LoraArgs a, const Ws ws) {
+  using C = Shrink64<kR>;
   extern __shared__ __align__(128) uint8_t ring[];
   cl::griddep_wait();
   cl::griddep_launch_dependents();
-  const int4 head = ws.tiles[0];
-  const int stages_all = static_cast<int>((a.K + C::kCols - 1) / C::kCols);
-  const Shares sh = shares_of(stages_all, head.x, gridDim.x);
+  const Rows rows{ws.tiles, ws.order};
+  const int4 head = rows.tile(0);
+  const int K = static_cast<int>(a.K), r = static_cast<int>(a.r), stages = (K - 1) / C::kCols + 1;
+  const Shares sh = shares_of(stages, head.x, gridDim.x);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = threadIdx.x % C::kChunks, row0 = threadIdx.x / C::kChunks;
   const uint32_t ring_at = smem_u32(ring);
   const int64_t units = static_cast<int64_t>(head.x) * sh.shares;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int t = static_cast<int>(u / sh.shares), share = static_cast<int>(u - static_cast<int64_t>(t) * sh.shares);
-    const int4 tile = ws.tiles[1 + t];
-    const int first = share * sh.per, last = min(first + sh.per, stages_all);
+    const int4 tile = rows.tile(1 + t);
+    const int first = share * sh.per, last = min(first + sh.per, stages);
     const uint16_t* src_x[C::kXs];
-    bool real_x[C::kXs];
 #pragma unroll
     for (int i = 0; i < C::kXs; ++i) {
       const int row = row0 + i * C::kStep;
-      real_x[i] = row < tile.z;
-      src_x[i] = a.x + (real_x[i] ? ws.order[tile.y + row] : 0) * a.x_stride;
+      src_x[i] = row < tile.z ? a.x + rows.row(tile.y + row) * a.x_stride : nullptr;
     }
-    const uint16_t* src_a = a.A + static_cast<int64_t>(tile.x) * a.r * a.K;
+    const uint16_t* src_a = a.A + static_cast<int64_t>(tile.x) * r * K;
     auto fetch = [&](int s, int slot) {
-      const int64_t col = static_cast<int64_t>(s) * C::kCols + chunk * 8;
-      const bool in = col < a.K;
+      const int col = s * C::kCols + chunk * 8;  // (stages end below 2^31 + 2^6)
+      const bool in = col >= 0 && col < K;
       const uint32_t at = ring_at + slot * C::kStageBytes;
 #pragma unroll
       for (int i = 0; i < C::kXs; ++i) {
         const int row = row0 + i * C::kStep;
-        cp_async16(at + row * C::kRowBytes + ((chunk ^ (row & 7)) << 4), in ? src_x[i] + col : a.x, in && real_x[i]);
+        const bool real = in && src_x[i] != nullptr;
+        cp_async16(at + row * C::kRowBytes + ((chunk ^ (row & 7)) << 4), real ? src_x[i] + col : a.x, real);
       }
 #pragma unroll
       for (int i = 0; i < C::kAs; ++i) {
         const int row = row0 + i * C::kStep;
-        if (C::kAs * C::kStep > kR && row >= kR) break;
-        const bool real = in && row < a.r;
-        cp_async16(at + (kTile + row) * C::kRowBytes + ((chunk ^ (row & 7)) << 4),
-                   real ? src_a + row * a.K + col : a.A, real);
+        const bool real = in && row < r;
+        cp_async16(at + (64 + row) * C::kRowBytes + ((chunk ^ (row & 7)) << 4),
+                   real ? src_a + static_cast<int64_t>(row) * K + col : a.A, real);
       }
     };
     float acc[kR / 8][4] = {};
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
+    for (int s = 0; s < C::kStages - 1; ++s) {
       if (first + s < last) fetch(first + s, s);
       cp_commit();
     }
     int slot = 0;
     for (int s = first; s < last; ++s) {
-      cp_wait<kStages - 2>();
+      cp_wait<C::kStages - 2>();
       __syncthreads();
-      if (s + kStages - 1 < last) fetch(s + kStages - 1, (slot + kStages - 1) % kStages);
+      if (s + C::kStages - 1 < last) fetch(s + C::kStages - 1, (slot + C::kStages - 1) % C::kStages);
       cp_commit();
       const uint32_t at = ring_at + slot * C::kStageBytes;
-      slot = (slot + 1) % kStages;
+      slot = (slot + 1) % C::kStages;
 #pragma unroll
       for (int kk = 0; kk < C::kCols / 16; ++kk) {
-        if (kTile == 16 && (kk & (kWarps - 1)) != warp) continue;
-        const int xr = (kTile == 16 ? 0 : warp * 16) + (lane & 15);
+        const int xr = warp * 16 + (lane & 15);
         uint32_t x[4];
         ldmatrix4(x, at + xr * C::kRowBytes + (((2 * kk + (lane >> 4)) ^ (xr & 7)) << 4));
 #pragma unroll
         for (int n = 0; n < kR / 16; ++n) {
           const int ar = n * 16 + (lane & 7) + ((lane >> 4) << 3);
           uint32_t b[4];
-          ldmatrix4(b, at + (kTile + ar) * C::kRowBytes + (((2 * kk + ((lane >> 3) & 1)) ^ (ar & 7)) << 4));
+          ldmatrix4(b, at + (64 + ar) * C::kRowBytes + (((2 * kk + ((lane >> 3) & 1)) ^ (ar & 7)) << 4));
           mma_bf16_16816(acc[2 * n], x[0], x[1], x[2], x[3], b[0], b[1]);
           mma_bf16_16816(acc[2 * n + 1], x[0], x[1], x[2], x[3], b[2], b[3]);
         }
       }
     }
     __syncthreads();
-    float* part = ws.part + (static_cast<int64_t>(share) * head.z + tile.y) * a.r;
+    float* part = ws.part + (static_cast<int64_t>(share) * head.z + tile.y) * r;
     const int g = lane >> 2, q = 2 * (lane & 3);
-    if constexpr (kTile == 16) {
-      float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
-      for (int n = 0; n < kR / 8; ++n) {
-        float* p = sums + (warp * 16 + g) * kR + n * 8 + q;
-        p[0] = acc[n][0], p[1] = acc[n][1];
-        p[8 * kR] = acc[n][2], p[8 * kR + 1] = acc[n][3];
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < 16 * kR; i += kThreads) {
-        const int row = i / kR, col = i % kR;
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += sums[w * 16 * kR + i];
-        if (row < tile.z && col < a.r) part[row * a.r + col] = s;
-      }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int n = 0; n < kR / 8; ++n) {
-        const int col = n * 8 + q, row = warp * 16 + g;
-        if (col >= a.r) break;
-        if (row < tile.z) *reinterpret_cast<float2*>(part + row * a.r + col) = make_float2(acc[n][0], acc[n][1]);
-        if (row + 8 < tile.z)
-          *reinterpret_cast<float2*>(part + (row + 8) * a.r + col) = make_float2(acc[n][2], acc[n][3]);
-      }
+    for (int n = 0; n < kR / 8; ++n) {
+      const int col = n * 8 + q, row = warp * 16 + g;
+      if (col >= r) break;
+      if (row < tile.z) *reinterpret_cast<float2*>(part + row * r + col) = make_float2(acc[n][0], acc[n][1]);
+      if (row + 8 < tile.z) *reinterpret_cast<float2*>(part + (row + 8) * r + col) = make_float2(acc[n][2], acc[n][3]);
     }
   }
 }
@@ -216,158 +372,576 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack2(fabsf(xh) < INFINITY ? x - xh : 0.0f, fabsf(yh) < INFINITY ? y - yh : 0.0f);
 }
 
-template <int kTile, int kR, bool kVec>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a, const Ws ws, int shrink_grid,
-                                                          int shrink_cols) {
-  constexpr int kSteps = kR / 16;
-  constexpr int kPiece = kR == 16 ? 4 : 8;  // values of B's row that a thread holds in a row: the MMA's order of r
-                                            // is dealt out alike on both sides
-  __shared__ float h[kTile * kR];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  cl::griddep_wait();
-  cl::griddep_launch_dependents();
-  const int4 head = ws.tiles[0];
-  const bool in_place = a.y == a.base;
-  const int tiles = in_place ? head.x : head.y;
-  const int per_tile = static_cast<int>((a.N + kUnit - 1) / kUnit);
-  const int64_t units = static_cast<int64_t>(tiles) * per_tile;
-  int64_t u = units * blockIdx.x / gridDim.x;
-  const int64_t u_end = units * (blockIdx.x + 1) / gridDim.x;
-  const Shares sh = shares_of(static_cast<int>((a.K + shrink_cols - 1) / shrink_cols), head.x, shrink_grid);
-  while (u < u_end) {
-    const int t = static_cast<int>(u / per_tile);
-    const int c0 = static_cast<int>(u - static_cast<int64_t>(t) * per_tile);
-    const int c1 = static_cast<int>(min(static_cast<int64_t>(per_tile), c0 + (u_end - u)));
-    u += c1 - c0;
-    const int4 tile = ws.tiles[1 + t];
-    const bool adapted = tile.x >= 0;
-    uint32_t hi[kSteps][4], lo[kSteps][4];
-    const int rowA = (kTile == 16 ? 0 : warp * 16) + g;
-    if (adapted) {
-      __syncthreads();
-      const float scale = a.scale != nullptr ? a.scale[tile.x] : 1.0f;
-      const int64_t stride = static_cast<int64_t>(head.z) * a.r;
-      for (int i = threadIdx.x; i < kTile * kR / 4; i += kThreads) {
-        const int row = i / (kR / 4), col = i % (kR / 4) * 4;
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row < tile.z && col < a.r) {
-          const float* p = ws.part + static_cast<int64_t>(tile.y + row) * a.r + col;
-#pragma unroll 8
-          for (int j = 0; j < sh.shares; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(p + j * stride);
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-          }
-          s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
-        }
-        *reinterpret_cast<float4*>(h + row * kR + col) = s;
-      }
-      __syncthreads();
+// Where B's row of column c lies: the columns of MMA j of 32, which are 8 i + 2 j and
+// the next, one after another; and a piece of it, swizzled so that the 8 rows of an
+// ldmatrix are in different banks.
+template <int kR>
+__device__ __forceinline__ uint32_t b_place(int row, int chunk) {
+  const int sw = kR == 16 ? row >> 2 & 1 : (kR == 32 ? row >> 1 & 3 : row & 7);
+  return row * (2 * kR) + ((chunk ^ sw) << 4);
+}
+__device__ __forceinline__ int b_row(int c) { return (c & ~31) + (c >> 1 & 3) * 8 + (c >> 3 & 3) * 2 + (c & 1); }
+
+// x A^T of 16 rows as the MMA's left operand, each value as two bf16 numbers.
+template <int kR>
+struct Low {
+  uint32_t hi[kR / 16][4], lo[kR / 16][4];
+  // h: float32 [rows][kR]; row: this thread's first
+  __device__ __forceinline__ void load(const float* h, int row, int q) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int col = kR == 16 ? q * 4 : (s / 2) * 32 + q * 8 + (s % 2) * 4;
-        const float4 top = *reinterpret_cast<const float4*>(h + rowA * kR + col);
-        const float4 low = *reinterpret_cast<const float4*>(h + (rowA + 8) * kR + col);
-        split2(top.x, top.y, hi[s][0], lo[s][0]);
-        split2(low.x, low.y, hi[s][1], lo[s][1]);
-        split2(top.z, top.w, hi[s][2], lo[s][2]);
-        split2(low.z, low.w, hi[s][3], lo[s][3]);
-      }
-    }
-    const bool real0 = rowA < tile.z, real1 = rowA + 8 < tile.z;
-    const int64_t m0 = real0 ? ws.order[tile.y + rowA] : 0, m1 = real1 ? ws.order[tile.y + rowA + 8] : 0;
-    const uint16_t* base0 = a.base + m0 * a.base_stride;
-    const uint16_t* base1 = a.base + m1 * a.base_stride;
-    uint16_t* y0 = a.y + m0 * a.y_stride;
-    uint16_t* y1 = a.y + m1 * a.y_stride;
-    const uint16_t* Bt = a.B + static_cast<int64_t>(adapted ? tile.x : 0) * a.N * a.r;
-    const int64_t col_end = min(a.N, static_cast<int64_t>(c1) * kUnit);
-    for (int64_t col = static_cast<int64_t>(c0) * kUnit + (kTile == 16 ? warp * 32 : 0); col < col_end;
-         col += kTile == 16 ? kUnit : 32) {
-      const int64_t mine = col + 8 * q;  // this thread's 8 columns
-      uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-      if constexpr (kVec) {
-        if (real0 && mine < a.N) b0 = *reinterpret_cast<const uint4*>(base0 + mine);
-        if (real1 && mine < a.N) b1 = *reinterpret_cast<const uint4*>(base1 + mine);
-      }
-      float acc[4][4] = {};
-      if (adapted) {
+    for (int s = 0; s < kR / 16; ++s) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // MMA j's column g is column 8 (g / 2) + 2 j + g % 2 of the 32
-          const int64_t n = min(col + 8 * (g >> 1) + 2 * j + (g & 1), a.N - 1);
-          const uint16_t* row = Bt + n * a.r + q * kPiece;
-          if constexpr (kR == 16) {
-            uint2 b = make_uint2(0, 0);
-            if (q * 4 < a.r) b = *reinterpret_cast<const uint2*>(row);
-            mma_bf16_16816(acc[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], b.x, b.y);
-            mma_bf16_16816(acc[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], b.x, b.y);
-          } else {
-#pragma unroll
-            for (int s = 0; s < kR / 32; ++s) {
-              uint4 b = make_uint4(0, 0, 0, 0);
-              if (s * 32 + q * 8 < a.r) b = *reinterpret_cast<const uint4*>(row + s * 32);
-              mma_bf16_16816(acc[j], lo[2 * s][0], lo[2 * s][1], lo[2 * s][2], lo[2 * s][3], b.x, b.y);
-              mma_bf16_16816(acc[j], lo[2 * s + 1][0], lo[2 * s + 1][1], lo[2 * s + 1][2], lo[2 * s + 1][3], b.z, b.w);
-              mma_bf16_16816(acc[j], hi[2 * s][0], hi[2 * s][1], hi[2 * s][2], hi[2 * s][3], b.x, b.y);
-              mma_bf16_16816(acc[j], hi[2 * s + 1][0], hi[2 * s + 1][1], hi[2 * s + 1][2], hi[2 * s + 1][3], b.z, b.w);
-            }
-          }
-        }
-      }
-      if constexpr (kVec) {
-        auto add = [](uint32_t b, float x, float y) {
-          return pack2(__uint_as_float(b << 16) + x, __uint_as_float(b & 0xFFFF0000u) + y);
-        };
-        if (adapted) {
-          b0 = make_uint4(add(b0.x, acc[0][0], acc[0][1]), add(b0.y, acc[1][0], acc[1][1]),
-                          add(b0.z, acc[2][0], acc[2][1]), add(b0.w, acc[3][0], acc[3][1]));
-          b1 = make_uint4(add(b1.x, acc[0][2], acc[0][3]), add(b1.y, acc[1][2], acc[1][3]),
-                          add(b1.z, acc[2][2], acc[2][3]), add(b1.w, acc[3][2], acc[3][3]));
-        }
-        if (real0 && mine < a.N) *reinterpret_cast<uint4*>(y0 + mine) = b0;
-        if (real1 && mine < a.N) *reinterpret_cast<uint4*>(y1 + mine) = b1;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (mine + i >= a.N) break;
-          if (real0) {
-            const uint16_t b = base0[mine + i];
-            y0[mine + i] = adapted ? float_to_bf16_bits_rn(bf16_bits_to_float(b) + acc[i / 2][i % 2]) : b;
-          }
-          if (real1) {
-            const uint16_t b = base1[mine + i];
-            y1[mine + i] = adapted ? float_to_bf16_bits_rn(bf16_bits_to_float(b) + acc[i / 2][2 + i % 2]) : b;
-          }
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = *reinterpret_cast<const float2*>(h + (row + 8 * (i & 1)) * kR + 16 * s + 8 * (i >> 1) + 2 * q);
+        split2(v.x, v.y, hi[s][i], lo[s][i]);
       }
     }
   }
+  // acc += x A^T B^T for 32 columns whose rows of B begin at `at`
+  __device__ __forceinline__ void times(uint32_t at, float (&acc)[4][4], int lane) const {
+#pragma unroll
+    for (int s = 0; s < kR / 16; ++s) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t b[4];  // both halves of 16 values of r, for two MMAs
+        ldmatrix4(b, at + b_place<kR>(j * 8 + (lane & 7) + (lane >> 4) * 8, 2 * s + (lane >> 3 & 1)));
+        mma_bf16_16816(acc[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], b[0], b[1]);
+        mma_bf16_16816(acc[j + 1], lo[s][0], lo[s][1], lo[s][2], lo[s][3], b[2], b[3]);
+        mma_bf16_16816(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], b[0], b[1]);
+        mma_bf16_16816(acc[j + 1], hi[s][0], hi[s][1], hi[s][2], hi[s][3], b[2], b[3]);
+      }
+    }
+  }
+};
+
+// The shares of x A^T of a tile's rows added up in their order and scaled, into h
+// [kTile][kR] float32; rows and columns that are not there are zeros. By `threads`
+// threads, `kSums` shares on their way at once.
+template <int kTile, int kR, int kSums>
+__device__ __forceinline__ void add_shares(float* h, const LoraArgs& a, const float* part, int4 tile, int64_t rows,
+                                           int shares, int thread, int threads) {
+  const float scale = a.scale != nullptr ? a.scale[tile.x] : 1.0f;
+  const int r = static_cast<int>(a.r);
+  const int64_t stride = rows * r;
+#pragma unroll 1
+  for (int i = thread; i < kTile * kR / 4; i += threads) {
+    const int row = i / (kR / 4), col = i % (kR / 4) * 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (row < tile.z && col < r) {
+      const float* p = part + (static_cast<int64_t>(tile.y) + row) * r + col;
+#pragma unroll 1
+      for (int j0 = 0; j0 < shares; j0 += kSums) {
+        float4 v[kSums];
+#pragma unroll
+        for (int j = 0; j < kSums; ++j) {
+          if (j0 + j < shares) v[j] = __ldcg(reinterpret_cast<const float4*>(p));
+          p += stride;
+        }
+#pragma unroll
+        for (int j = 0; j < kSums; ++j)
+          if (j0 + j < shares) s.x += v[j].x, s.y += v[j].y, s.z += v[j].z, s.w += v[j].w;
+      }
+      s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
+    }
+    *reinterpret_cast<float4*>(h + row * kR + col) = s;
+  }
 }
 
-template <int kTile, int kR>
-cudaError_t launch_products(const Ctx& c, const LoraArgs& a, const Ws& ws) {
-  using C = Shrink<kTile, kR>;
+// The MMAs' sums begin with base: 8 columns of this thread's row g + 8 i.
+__device__ __forceinline__ void begin_with(float (&acc)[4][4], int i, const uint4& b) {
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    acc[j][2 * i] = __uint_as_float(w[j] << 16);
+    acc[j][2 * i + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 rounded(const float (&acc)[4][4], int i) {
+  return make_uint4(pack2(acc[0][2 * i], acc[0][2 * i + 1]), pack2(acc[1][2 * i], acc[1][2 * i + 1]),
+                    pack2(acc[2][2 * i], acc[2][2 * i + 1]), pack2(acc[3][2 * i], acc[3][2 * i + 1]));
+}
+
+// 16 rows by 32 columns of base and y that lie at any 2-byte address: lanes side by
+// side along a row, through a warp's own shared memory (kOddRow values a row).
+constexpr int kOddRow = 34;
+struct OddRows {
+  uint16_t* stage;
+  int64_t m;  // lane l < 16: the row, or -1
+  __device__ __forceinline__ void read(const LoraArgs& a, int64_t col, int lane, float (&acc)[4][4]) const {
+    const bool in = col + lane < a.N;
+    __syncwarp();
+#pragma unroll 8
+    for (int i = 0; i < 16; ++i) {
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, m, i);
+      stage[i * kOddRow + lane] = in && row >= 0 ? a.base[row * a.base_stride + col + lane] : 0;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(stage + ((lane >> 2) + 8 * i) * kOddRow + 8 * (lane & 3));
+      begin_with(acc, i, make_uint4(p[0], p[1], p[2], p[3]));
+    }
+  }
+  __device__ __forceinline__ void write(const LoraArgs& a, int64_t col, int lane, const float (&acc)[4][4]) const {
+    const bool in = col + lane < a.N;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(stage + ((lane >> 2) + 8 * i) * kOddRow + 8 * (lane & 3));
+      const uint4 v = rounded(acc, i);
+      p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+    }
+    __syncwarp();
+#pragma unroll 8
+    for (int i = 0; i < 16; ++i) {
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, m, i);
+      if (in && row >= 0) a.y[row * a.y_stride + col + lane] = stage[i * kOddRow + lane];
+    }
+  }
+};
+
+// Where a run of units (a tile's columns, some at a time) stands.
+struct Walk {
+  int t, c;  // tile, place in its columns
+  __device__ __forceinline__ void to(int64_t u, int per_tile) {
+    t = static_cast<int>(u / per_tile);
+    c = static_cast<int>(u - static_cast<int64_t>(t) * per_tile);
+  }
+  // true: a new tile
+  __device__ __forceinline__ bool next(int per_tile) {
+    if (++c < per_tile) return false;
+    c = 0;
+    ++t;
+    return true;
+  }
+};
+
+// Tiles of 8 rows: a warp for itself, 64 columns at a time, without barriers. B, which
+// few rows use, is the left operand of four MMAs of 16 columns, dealt out so that a
+// lane's are 8 in a row of two rows of y; x A^T is the right one. A lane copies its
+// values of B and base itself into its own places of a ring of stages.
+template <int kR>
+struct Expand8 {
+  static constexpr int kPieces = kR == 16 ? 1 : kR / 32;   // a lane's of a row of B
+  static constexpr int kPieceBytes = kR == 16 ? 8 : 16;
+  static constexpr int kBBytes = 8 * kPieces * kPieceBytes * 32;
+  static constexpr int kStageBytes = kBBytes + 2 * 16 * 32;
+  static constexpr int kStages = kR == 16 ? 4 : (kR == 128 ? 2 : 3);
+  static constexpr int kWarpBytes = kStages * kStageBytes + 8 * kR * 4;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kAll = kSmem + static_cast<int>(sizeof(Few)) + 1024;
+  static constexpr int kFit = 228 * 1024 / kAll < 4 ? 228 * 1024 / kAll : 4;
+};
+constexpr int kFewCols = 64;
+
+template <int kR, bool kVec, bool kFew>
+__global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
+    expand8_kernel(const LoraArgs a, const Ws ws, int shrink_grid, int shrink_cols) {
+  using C = Expand8<kR>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  float* h = reinterpret_cast<float*>(ring + warp * C::kWarpBytes + C::kStages * C::kStageBytes);
+  const uint8_t* own_b = ring + warp * C::kWarpBytes + lane * C::kPieceBytes;
+  const uint8_t* own_base = ring + warp * C::kWarpBytes + C::kBBytes + lane * 16;
+  const uint32_t own_b_at = smem_u32(own_b), own_base_at = smem_u32(own_base);
+  // What comes before the wait reads the order of the rows, base and B, all complete
+  // when the first product's kernel began its own work.
+  const auto rows = [&] {
+    if constexpr (kFew) {
+      __shared__ Few few;
+      group_few(few, a.adapter, static_cast<int>(a.M), static_cast<int>(a.n));
+      return FewRows{&few};
+    } else {
+      return Rows{ws.tiles, ws.order};
+    }
+  }();
+  const int4 head = rows.tile(0);
+  const int r = static_cast<int>(a.r), N = static_cast<int>(a.N), per_tile = (N - 1) / kFewCols + 1;
+  const int64_t units = static_cast<int64_t>(a.y == a.base ? head.x : head.y) * per_tile;
+  // (neighbours in the line of units go to different blocks)
+  const uint32_t w = warp * gridDim.x + blockIdx.x, all = gridDim.x * kWarps;
+  Walk f;
+  int todo;
+  if (units <= 0x7FFFFFFF) {  // (divisions of 64 bits take as long as a few units)
+    const uint32_t each = static_cast<uint32_t>(units) / all, more = static_cast<uint32_t>(units) - each * all;
+    const uint32_t u0 = w * each + min(w, more);
+    todo = static_cast<int>(each + (w < more ? 1 : 0));
+    f.t = static_cast<int>(u0 / static_cast<uint32_t>(per_tile));
+    f.c = static_cast<int>(u0 - static_cast<uint32_t>(f.t) * per_tile);
+  } else {
+    f.to(units / all * w, per_tile);
+    todo = static_cast<int>(units / all + (w == all - 1 ? units % all : 0));
+  }
+  const Shares sh = shares_of((static_cast<int>(a.K) - 1) / shrink_cols + 1, head.x, shrink_grid);
+  Walk now = f;
+  int left = todo;  // units not fetched yet
+  int4 ftile;
+  const uint16_t *fB, *fbase[2];
+  // this lane's rows of y are 2 q and 2 q + 1, its columns 8 g .. 8 g + 7, its values of r 4 or 8 from here on
+  const int piece = (kR == 16 ? 4 : 8) * q;
+  auto fetch_tile = [&] {
+    ftile = rows.tile(1 + f.t);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      fbase[i] = 2 * q + i < ftile.z ? a.base + rows.row(ftile.y + 2 * q + i) * a.base_stride + 8 * g : nullptr;
+    fB = a.B + (static_cast<int64_t>(ftile.x) * N + 8 * g) * r + piece;
+  };
+  if (left > 0) fetch_tile();
+  auto fetch = [&](uint32_t slot) {
+    if (left <= 0) return;
+    --left;
+    const int col = f.c * kFewCols;
+    if (ftile.x >= 0) {
+      const uint16_t* src = fB + static_cast<int64_t>(col) * r;
+      auto copy = [&](int j, int i, const uint16_t* from, bool real) {
+        const uint32_t at = own_b_at + slot + (j * C::kPieces + i) * (32 * C::kPieceBytes);
+        if constexpr (kR == 16)
+          cp_async8(at, from, real);
+        else
+          cp_async16(at, from, real);
+      };
+      if (r == kR && col + kFewCols <= N) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int i = 0; i < C::kPieces; ++i) copy(j, i, src + j * kR + 32 * i, true);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int i = 0; i < C::kPieces; ++i) {
+            const bool real = col + 8 * g + j < N && piece + 32 * i < r;
+            copy(j, i, real ? src + j * r + 32 * i : a.B, real);
+          }
+        }
+      }
+    }
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (fbase[i] != nullptr && col + 8 * g < N) cp_async16(own_base_at + slot + i * 512, fbase[i] + col, true);
+    }
+    if (f.next(per_tile) && left > 0) fetch_tile();
+  };
+#pragma unroll 1
+  for (int s = 0; s < C::kStages - 1; ++s) {
+    fetch(s * C::kStageBytes);
+    cp_commit();
+  }
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+
+  int4 tile;
+  const uint16_t* base[2];
+  uint16_t* y[2];
+  uint32_t hi[kR / 16][2], lo[kR / 16][2];
+  bool fresh = true;
+  uint32_t slot = 0, ahead = (C::kStages - 1) * C::kStageBytes;
+#pragma unroll 1
+  for (int u = 0; u < todo; ++u) {
+    fetch(ahead);
+    cp_commit();
+    if (fresh) {
+      tile = rows.tile(1 + now.t);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        base[i] = nullptr, y[i] = nullptr;
+        if (2 * q + i < tile.z) {
+          const int64_t m = rows.row(tile.y + 2 * q + i);
+          base[i] = a.base + m * a.base_stride + 8 * g;
+          y[i] = a.y + m * a.y_stride + 8 * g;
+        }
+      }
+      if (tile.x >= 0) {
+        __syncwarp();
+        add_shares<8, kR, 8>(h, a, ws.part, tile, head.z, sh.shares, lane, 32);
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < kR / 16; ++s) {
+          const int col = kR == 16 ? 4 * q : 32 * (s >> 1) + 8 * q + 4 * (s & 1);
+          const float4 v = *reinterpret_cast<const float4*>(h + g * kR + col);
+          split2(v.x, v.y, hi[s][0], lo[s][0]);
+          split2(v.z, v.w, hi[s][1], lo[s][1]);
+        }
+      }
+    }
+    cp_wait<C::kStages - 1>();
+    const int col = now.c * kFewCols;
+    // MMA j: its rows g and g + 8 are columns 8 g + 2 j and the next of y, its columns rows of y
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if constexpr (kVec) {
+        v = *reinterpret_cast<const uint4*>(own_base + slot + i * 512);
+      } else if (base[i] != nullptr) {
+        uint32_t e[8];
+#pragma unroll
+        for (int l = 0; l < 8; ++l) e[l] = col + 8 * g + l < N ? base[i][col + l] : 0;
+        v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+      }
+      const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[j][i] = __uint_as_float(w4[j] << 16);
+        acc[j][2 + i] = __uint_as_float(w4[j] & 0xFFFF0000u);
+      }
+    }
+    if (tile.x >= 0) {
+#pragma unroll
+      for (int i = 0; i < C::kPieces; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint8_t* at = own_b + slot + (2 * j * C::kPieces + i) * (32 * C::kPieceBytes);
+          if constexpr (kR == 16) {
+            const uint2 e = *reinterpret_cast<const uint2*>(at);
+            const uint2 o = *reinterpret_cast<const uint2*>(at + 32 * C::kPieceBytes);
+            mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, lo[0][0], lo[0][1]);
+            mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, hi[0][0], hi[0][1]);
+          } else {
+            const uint4 e = *reinterpret_cast<const uint4*>(at);
+            const uint4 o = *reinterpret_cast<const uint4*>(at + C::kPieces * 32 * C::kPieceBytes);
+            mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, lo[2 * i][0], lo[2 * i][1]);
+            mma_bf16_16816(acc[j], e.z, o.z, e.w, o.w, lo[2 * i + 1][0], lo[2 * i + 1][1]);
+            mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, hi[2 * i][0], hi[2 * i][1]);
+            mma_bf16_16816(acc[j], e.z, o.z, e.w, o.w, hi[2 * i + 1][0], hi[2 * i + 1][1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (y[i] == nullptr) continue;
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = pack2(acc[j][i], acc[j][2 + i]);
+      if constexpr (kVec) {
+        if (col + 8 * g < N) *reinterpret_cast<uint4*>(y[i] + col) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+#pragma unroll
+        for (int l = 0; l < 8; ++l)
+          if (col + 8 * g + l < N) y[i][col + l] = static_cast<uint16_t>(o[l / 2] >> (16 * (l % 2)));
+      }
+    }
+    fresh = now.next(per_tile);
+    ahead = slot;
+    slot = slot + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : slot + C::kStageBytes;
+  }
+}
+
+// Tiles of 64 rows: 8 warps, 16 rows and half of the columns each, share a ring of
+// stages of B's rows and base's.
+template <int kR>
+struct Expand64 {
+  static constexpr int kWarps = 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kUnit = kR == 128 ? 64 : 128;  // columns of a stage
+  static constexpr int kStages = 3;
+  static constexpr int kBaseBytes = 64 * kUnit * 2;
+  static constexpr int kStageBytes = kBaseBytes + kUnit * kR * 2;
+  static constexpr int kOddBytes = kWarps * 16 * kOddRow * 2;
+  static constexpr int kLow = 64 * kR * 4 > kOddBytes ? 64 * kR * 4 : kOddBytes;
+  static constexpr int kSmem = kStages * kStageBytes + kLow;
+  static constexpr int kBaseChunks = kUnit / 8;             // 16-byte pieces of a row
+  static constexpr int kBaseStep = kThreads / kBaseChunks;  // rows that the block copies at once
+  static constexpr int kBases = 64 / kBaseStep;             // rows a thread copies
+  static constexpr int kBs = kUnit * (kR / 8) / kThreads;   // pieces of B a thread copies
+  static constexpr int kFit = kR <= 16 ? 3 : (kR <= 64 ? 2 : 1);
+  static_assert(kFit * (kSmem + 1024) <= 228 * 1024, "");
+};
+
+template <int kR, bool kVec>
+__global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
+    expand64_kernel(const LoraArgs a, const Ws ws, int shrink_grid, int shrink_cols) {
+  using C = Expand64<kR>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  float* h = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
+  const uint32_t ring_at = smem_u32(ring);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  // What comes before the wait reads the order of the rows, base and B, all complete
+  // when the first product's kernel began its own work.
+  const Rows rows{ws.tiles, ws.order};
+  const int4 head = rows.tile(0);
+  const int r = static_cast<int>(a.r), N = static_cast<int>(a.N), per_tile = (N - 1) / C::kUnit + 1;
+  const int64_t units = static_cast<int64_t>(a.y == a.base ? head.x : head.y) * per_tile;
+  const int64_t u0 = units * blockIdx.x / gridDim.x;
+  const int todo = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u0);
+  const Shares sh = shares_of(static_cast<int>((a.K + shrink_cols - 1) / shrink_cols), head.x, shrink_grid);
+
+  Walk f, now;
+  f.to(u0, per_tile);
+  now = f;
+  int left = todo;  // units not fetched yet
+  int4 ftile;
+  int base_row[C::kBases];
+  const uint16_t* fB;
+  const int base_chunk = threadIdx.x % C::kBaseChunks, base_row0 = threadIdx.x / C::kBaseChunks;
+  const int b_chunk = threadIdx.x % (kR / 8), b_col0 = threadIdx.x / (kR / 8);
+  constexpr int kBStep = C::kThreads / (kR / 8);  // columns whose rows of B the block copies at once
+  auto fetch_tile = [&] {
+    ftile = rows.tile(1 + f.t);
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < C::kBases; ++i) {
+        const int row = base_row0 + i * C::kBaseStep;
+        base_row[i] = row < ftile.z ? rows.row(ftile.y + row) : -1;
+      }
+    }
+    fB = a.B + static_cast<int64_t>(ftile.x) * N * r + b_col0 * r + b_chunk * 8;
+  };
+  if (left > 0) fetch_tile();
+  auto fetch = [&](uint32_t slot) {
+    if (left <= 0) return;
+    --left;
+    const int col = f.c * C::kUnit;
+    const uint32_t at = ring_at + slot;
+    if constexpr (kVec) {
+      const uint16_t* src = a.base + col + base_chunk * 8;
+      const bool in = col + base_chunk * 8 < N;
+#pragma unroll
+      for (int i = 0; i < C::kBases; ++i) {
+        const int row = base_row0 + i * C::kBaseStep;
+        if (in && base_row[i] >= 0)
+          cp_async16(at + row * (2 * C::kUnit) + ((base_chunk ^ (row & 1) << 2) << 4),
+                     src + base_row[i] * a.base_stride, true);
+      }
+    }
+    if (ftile.x >= 0) {
+      const uint16_t* src = fB + static_cast<int64_t>(col) * r;
+#pragma unroll
+      for (int i = 0; i < C::kBs; ++i) {
+        const int c = b_col0 + i * kBStep;
+        const bool real = b_chunk * 8 < r && col + c < N;
+        cp_async16(at + C::kBaseBytes + b_place<kR>(b_row(c), b_chunk), real ? src + i * kBStep * r : a.B, real);
+      }
+    }
+    if (f.next(per_tile) && left > 0) fetch_tile();
+  };
+#pragma unroll 1
+  for (int s = 0; s < C::kStages - 1; ++s) {
+    fetch(s * C::kStageBytes);
+    cp_commit();
+  }
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+
+  const int row0 = (warp & 3) * 16 + g;
+  Low<kR> low;
+  int4 tile;
+  uint16_t* y[2];
+  OddRows odd{reinterpret_cast<uint16_t*>(h) + warp * 16 * kOddRow, -1};
+  bool fresh = true;
+  uint32_t slot = 0, ahead = (C::kStages - 1) * C::kStageBytes;
+#pragma unroll 1
+  for (int u = 0; u < todo; ++u) {
+    cp_wait<C::kStages - 2>();
+    __syncthreads();
+    fetch(ahead);
+    cp_commit();
+    if (fresh) {
+      tile = rows.tile(1 + now.t);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        y[i] = row0 + 8 * i < tile.z ? a.y + rows.row(tile.y + row0 + 8 * i) * a.y_stride + 8 * q : nullptr;
+      if constexpr (!kVec) {
+        const int row = (warp & 3) * 16 + (lane & 15);
+        odd.m = row < tile.z ? rows.row(tile.y + row) : -1;
+      }
+      if (tile.x >= 0) {
+        add_shares<64, kR, 4>(h, a, ws.part, tile, head.z, sh.shares, threadIdx.x, C::kThreads);
+        __syncthreads();
+        low.load(h, row0, q);
+        if constexpr (!kVec) __syncthreads();  // the rows' stage lies there, too
+        // (the next tile's sums are written after the barrier of its first unit)
+      }
+    }
+    const int col0 = now.c * C::kUnit;
+    const uint8_t* stage = ring + slot;
+#pragma unroll
+    for (int step = 0; step < C::kUnit / 64; ++step) {
+      const int c0 = (warp >> 2) * (C::kUnit / 2) + step * 32;  // of the unit
+      const int col = col0 + c0;
+      float acc[4][4];
+      if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = row0 + 8 * i;
+          begin_with(acc, i, *reinterpret_cast<const uint4*>(stage + row * (2 * C::kUnit) +
+                                                             (((c0 / 8 + q) ^ (row & 1) << 2) << 4)));
+        }
+      } else {
+        odd.read(a, col, lane, acc);
+      }
+      if (tile.x >= 0) low.times(ring_at + slot + C::kBaseBytes + c0 * (2 * kR), acc, lane);
+      if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (y[i] != nullptr && col + 8 * q < N) *reinterpret_cast<uint4*>(y[i] + col) = rounded(acc, i);
+      } else {
+        odd.write(a, col, lane, acc);
+      }
+    }
+    fresh = now.next(per_tile);
+    ahead = slot;
+    slot += C::kStageBytes;
+    if (slot == C::kStages * C::kStageBytes) slot = 0;
+  }
+}
+
+bool sixteen_bytes(const LoraArgs& a) {
+  return a.N % 8 == 0 && a.base_stride % 8 == 0 && a.y_stride % 8 == 0 && aligned16(a.base) && aligned16(a.y);
+}
+
+template <int kR, bool kFew>
+cudaError_t launch_8(const Ctx& c, const LoraArgs& a, const Ws& ws) {
+  using S = Shrink8<kR>;
+  using E = Expand8<kR>;
   static SmemLimit lim;
-  cudaError_t e = raise_smem_limit(lim, shrink_kernel<kTile, kR>, c.device, C::kSmem);
+  cudaError_t e = raise_smem_limit(lim, shrink8_kernel<kR, kFew>, c.device, S::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t stages = (a.K + C::kCols - 1) / C::kCols, tiles = most_tiles(a.M, a.n);
-  const int fit = std::max(1, std::min(8, 220 * 1024 / C::kSmem));
-  const int64_t grid = std::min({int64_t{fit} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
-  e = launch_early(c, grid, kThreads, C::kSmem, shrink_kernel<kTile, kR>, a, ws);
+  const int64_t tiles = most_tiles(a.M, a.n), stages = (a.K - 1) / S::kCols + 1;
+  const int64_t grid = std::min({int64_t{S::kFit} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
+  e = launch_early(c, grid, kThreads, S::kSmem, shrink8_kernel<kR, kFew>, a, ws);
   if (e != cudaSuccess) return e;
-  const bool vec = a.N % 8 == 0 && a.base_stride % 8 == 0 && a.y_stride % 8 == 0 && aligned16(a.base) && aligned16(a.y);
-  const int64_t units = tiles * ((a.N + kUnit - 1) / kUnit);
-  const int64_t grid2 = std::min<int64_t>(units, int64_t{8} * c.sm_count);
-  return launch_early(c, grid2, kThreads, 0, vec ? expand_kernel<kTile, kR, true> : expand_kernel<kTile, kR, false>, a,
-                      ws, static_cast<int>(grid), int{C::kCols});
+  const int64_t units = tiles * ((a.N - 1) / kFewCols + 1);
+  const int64_t grid2 = std::min<int64_t>((units - 1) / kWarps + 1, E::kFit * c.sm_count);
+  const auto expand = [&](SmemLimit& limit, auto kern) {
+    const cudaError_t err = raise_smem_limit(limit, kern, c.device, E::kSmem);
+    return err != cudaSuccess ? err
+                              : launch_early(c, grid2, kThreads, E::kSmem, kern, a, ws, static_cast<int>(grid),
+                                             int{S::kCols});
+  };
+  static SmemLimit vec, odd;
+  return sixteen_bytes(a) ? expand(vec, expand8_kernel<kR, true, kFew>) : expand(odd, expand8_kernel<kR, false, kFew>);
 }
 
-template <int kTile>
-cudaError_t launch_ranks(const Ctx& c, const LoraArgs& a, const Ws& ws) {
-  if (a.r <= 16) return launch_products<kTile, 16>(c, a, ws);
-  if (a.r <= 32) return launch_products<kTile, 32>(c, a, ws);
-  if (a.r <= 64) return launch_products<kTile, 64>(c, a, ws);
-  return launch_products<kTile, 128>(c, a, ws);
+template <int kR>
+cudaError_t launch_64(const Ctx& c, const LoraArgs& a, const Ws& ws) {
+  using S = Shrink64<kR>;
+  using E = Expand64<kR>;
+  static SmemLimit lim;
+  cudaError_t e = raise_smem_limit(lim, shrink64_kernel<kR>, c.device, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = most_tiles(a.M, a.n), stages = (a.K - 1) / S::kCols + 1;
+  const int fit = std::min(8, 220 * 1024 / S::kSmem);
+  const int64_t grid = std::min({int64_t{fit} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
+  e = launch_early(c, grid, kThreads, S::kSmem, shrink64_kernel<kR>, a, ws);
+  if (e != cudaSuccess) return e;
+  const int64_t grid2 = std::min<int64_t>(tiles * ((a.N - 1) / E::kUnit + 1), E::kFit * c.sm_count);
+  const auto expand = [&](SmemLimit& limit, auto kern) {
+    const cudaError_t err = raise_smem_limit(limit, kern, c.device, E::kSmem);
+    return err != cudaSuccess ? err
+                              : launch_early(c, grid2, E::kThreads, E::kSmem, kern, a, ws, static_cast<int>(grid),
+                                             int{S::kCols});
+  };
+  static SmemLimit vec, odd;
+  return sixteen_bytes(a) ? expand(vec, expand64_kernel<kR, true>) : expand(odd, expand64_kernel<kR, false>);
+}
+
+template <int kR>
+cudaError_t launch_rank(const Ctx& c, const LoraArgs& a, const Ws& ws) {
+  if (a.M <= kFewRows) return launch_8<kR, true>(c, a, ws);
+  return tile_of(a.M) == kFewTile ? launch_8<kR, false>(c, a, ws) : launch_64<kR>(c, a, ws);
 }
 
 }  // namespace
@@ -384,16 +958,21 @@ cudaError_t launch_lora(const Ctx& c, const LoraArgs& a) {
   ws.order = reinterpret_cast<int32_t*>(p);
   p += round16(4 * a.M);
   ws.part = reinterpret_cast<float*>(p);
-  GroupArgs g{};
-  g.ids = a.adapter;
-  g.n = a.M;
-  g.E = static_cast<int>(a.n);
-  g.order = ws.order;
-  g.tiles = ws.tiles;
-  g.tile = tile_of(a.M);
-  const cudaError_t e = launch_group(c, g);
-  if (e != cudaSuccess) return e;
-  return tile_of(a.M) == 16 ? launch_ranks<16>(c, a, ws) : launch_ranks<64>(c, a, ws);
+  if (a.M > kFewRows) {
+    GroupArgs g{};
+    g.ids = a.adapter;
+    g.n = a.M;
+    g.E = static_cast<int>(a.n);
+    g.order = ws.order;
+    g.tiles = ws.tiles;
+    g.tile = tile_of(a.M);
+    const cudaError_t e = launch_group(c, g);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.r <= 16) return launch_rank<16>(c, a, ws);
+  if (a.r <= 32) return launch_rank<32>(c, a, ws);
+  if (a.r <= 64) return launch_rank<64>(c, a, ws);
+  return launch_rank<128>(c, a, ws);
 }
 
 }  // namespace wq
