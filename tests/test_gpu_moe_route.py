@@ -148,6 +148,32 @@ def test_nan_and_infinity(bf16):
         assert bool(d[3].isfinite().all())  # the ordinary row beside them
 
 
+def test_every_nan_comes_first():
+    """NaN of either sign and any payload, bf16 and float32."""
+    pay = np.array([0x7FC00000, 0xFFC00000, 0x7F800001, 0xFF800001, 0xFFFFFFFF, 0x7FFFFFFF], np.uint32)
+    x = logits(6, 64, 7)
+    for t in range(6):
+        x[t, 9 + t] = pay[t:t + 1].view(np.float32)[0]
+        x[t, 50] = pay[5 - t:6 - t].view(np.float32)[0]
+        x[t, 3] = np.inf
+    for t in (torch.from_numpy(x).cuda(), torch.from_numpy((x.view(np.uint32) >> 16 | 1).astype(np.uint16).view(np.int16)).cuda().view(torch.bfloat16)):
+        ids, _ = wq.moe_route(t, 3)
+        first = 3 if t.dtype == torch.float32 else None  # (bf16's infinity became a NaN here)
+        for i in range(6):
+            want = [9 + i, 50, 3] if first else [3, 9 + i, 50]
+            assert ids[i].tolist() == want, (t.dtype, i)
+
+
+def test_keys_that_differ_in_their_lowest_bits():
+    """Float32 logits that the expert's bits of a key cannot tell apart: among the chosen, at the border, and none."""
+    r = np.random.default_rng(11)
+    for E, k in ((20, 4), (64, 8), (256, 8), (1024, 32)):
+        x = r.standard_normal((40, E)).astype(np.float32)
+        x[::2] = (np.float32(1.0) + r.integers(0, 40, (20, E)).astype(np.float32) * np.float32(2.0 ** -23))
+        x[1::4] = -x[::4]
+        check(x, k, "softmax", True, 1.0, False, 3)
+
+
 def test_gradient_of_ids_that_are_none_or_twice():
     x = logits(3, 20, 8)
     ids = np.array([[3, -1, 40], [2, 2, 5], [-7, 1 << 30, -1]], np.int32)

@@ -5,9 +5,9 @@
 //
 // The ids are a few KB to a few hundred KB, so latency bounds it. A warp counts a
 // run of entries in its own row of counters (the lanes that share an id find each
-// other by a match, so nothing depends on the order of atomics), the rows and the
-// blocks are summed up, and the warp goes over its run once more and gives out
-// places. Few entries take one block; more take a cluster of 8 that exchange their
+// other by votes on its bits, so nothing depends on the order of atomics; the
+// instruction that matches whole numbers is far slower), the rows and the blocks are
+// summed up, and what was counted before an entry is its place. Few entries take one block; more take a cluster of 8 that exchange their
 // counts through distributed shared memory.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
@@ -44,6 +44,17 @@ __device__ int block_scan(int a, int b, int* warp_sum, int* total) {
   return before + x - a - b;
 }
 
+// The lanes whose number of `bits` bits is this lane's.
+__device__ __forceinline__ uint32_t lanes_with(uint32_t x, int bits) {
+  uint32_t same = 0xFFFFFFFFu;
+#pragma unroll 4
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t set = __ballot_sync(0xFFFFFFFFu, x >> b & 1);
+    same &= x >> b & 1 ? set : ~set;
+  }
+  return same;
+}
+
 template <int kBlocks>
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) group_kernel(const GroupArgs a) {
   extern __shared__ int32_t smem[];
@@ -56,40 +67,52 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) grou
   int32_t* tile0 = start + E1 + 1;      // [E1 + 1] tiles before the id's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = kBlocks > 1 ? static_cast<int>(cl::cluster_rank()) : 0;
+  const int64_t per = (a.n + kBlocks * kThreads - 1) / (kBlocks * kThreads) * 32;
+  const int64_t lo = (static_cast<int64_t>(rank) * kWarps + warp) * per, hi = lo + per < a.n ? lo + per : a.n;
   for (int i = threadIdx.x; i < kWarps * E1; i += kThreads) hist[i] = 0;
   cl::griddep_wait();
   cl::griddep_launch_dependents();
-  const int64_t per = (a.n + kBlocks * kThreads - 1) / (kBlocks * kThreads) * 32;
-  const int64_t lo = (static_cast<int64_t>(rank) * kWarps + warp) * per, hi = lo + per < a.n ? lo + per : a.n;
   int32_t* mine = hist + warp * E1;
-  int32_t id[kRun];
+  const int bits = 32 - __clz(E1);  // of E1, which stands for no entry
+  int32_t id[kRun], before[kRun];
   auto load = [&](int64_t i0) {
+    if (i0 >= hi) return;
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
+    for (int j = 0; j < kRun; ++j) {  // (without branches: a load behind one waits for the load before it)
       const int64_t i = i0 + 32 * j + lane;
-      id[j] = i < hi ? a.ids[i] : -2;
-      if (i < hi && (id[j] < 0 || id[j] >= a.E)) id[j] = a.E;
+      id[j] = a.ids[i < hi ? i : hi - 1];
+      if (id[j] < 0 || id[j] >= a.E) id[j] = a.E;
+      if (i >= hi) id[j] = E1;
     }
   };
-  __syncthreads();
-  for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRun) {
-    load(i0);
+  // counts the run's ids: before[j] of the same id come before this lane's
+  auto counted = [&](int64_t i0) {
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       if (i0 + 32 * j >= hi) break;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
-      if (id[j] >= 0 && lane == __ffs(same) - 1) mine[id[j]] += __popc(same);
+      const uint32_t same = lanes_with(id[j], bits), lower = same & ((1u << lane) - 1);
+      const int have = id[j] < E1 ? mine[id[j]] : 0;
+      before[j] = have + __popc(lower);
+      __syncwarp();
+      if (id[j] < E1 && lower == 0) mine[id[j]] = have + __popc(same);
       __syncwarp();
     }
+  };
+  load(lo);
+  __syncthreads();
+  for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRun) {
+    if (i0 > lo) load(i0);
+    counted(i0);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E1; e += kThreads) {
-    int run = 0;
-#pragma unroll 8
+    int c[kWarps], run = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) c[w] = hist[w * E1 + e];
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const int c = hist[w * E1 + e];
       hist[w * E1 + e] = run;
-      run += c;
+      run += c[w];
     }
     count[e] = run;
   }
@@ -119,8 +142,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) grou
   }
   if (kBlocks > 1) cl::cluster_arrive();  // this block reads no other's counts any more
   int total;
-  const int before = block_scan(all[0], all[1], warp_sum, &total);
-  int at = before;
+  int at = block_scan(all[0], all[1], warp_sum, &total);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int e = 2 * threadIdx.x + i;
@@ -155,22 +177,20 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) grou
   }
   if (kBlocks > 1) cl::cluster_wait();
   __syncthreads();
+  // (a run that the registers do not hold is counted once more, from the places given out before it)
+  const bool again = per > 32 * kRun;
   for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRun) {
-    if (per > 32 * kRun) load(i0);
+    if (again) {
+      load(i0);
+      counted(i0);
+    }
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      if (i0 + 32 * j >= hi) break;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
-      int place = 0;
-      if (id[j] >= 0) place = first[id[j]] + mine[id[j]] + __popc(same & ((1u << lane) - 1));
-      __syncwarp();
-      if (id[j] >= 0 && lane == __ffs(same) - 1) mine[id[j]] += __popc(same);
-      __syncwarp();
       const int64_t i = i0 + 32 * j + lane;
-      if (i < hi) {
-        if (a.slots != nullptr) a.slots[i] = id[j] < a.E ? place : -1;
-        if (a.order != nullptr) a.order[place] = static_cast<int32_t>(i);
-      }
+      if (i >= hi) continue;
+      const int place = first[id[j]] + (again ? 0 : mine[id[j]]) + before[j];
+      if (a.slots != nullptr) a.slots[i] = id[j] < a.E ? place : -1;
+      if (a.order != nullptr) a.order[place] = static_cast<int32_t>(i);
     }
   }
 }

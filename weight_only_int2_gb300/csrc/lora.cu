@@ -433,10 +433,8 @@ __device__ __forceinline__ void add_shares(float* h, const LoraArgs& a, const fl
       for (int j0 = 0; j0 < shares; j0 += kSums) {
         float4 v[kSums];
 #pragma unroll
-        for (int j = 0; j < kSums; ++j) {
-          if (j0 + j < shares) v[j] = __ldcg(reinterpret_cast<const float4*>(p));
-          p += stride;
-        }
+        for (int j = 0; j < kSums; ++j)  // (without branches: a load behind one waits for the load before it)
+          v[j] = __ldcg(reinterpret_cast<const float4*>(p + min(j0 + j, shares - 1) * stride));
 #pragma unroll
         for (int j = 0; j < kSums; ++j)
           if (j0 + j < shares) s.x += v[j].x, s.y += v[j].y, s.z += v[j].z, s.w += v[j].w;

@@ -5,6 +5,8 @@
 #include "wq_device.cuh"
 #include "wq_internal.h"
 
+#include <algorithm>
+
 namespace wq {
 namespace {
 
@@ -26,16 +28,23 @@ __device__ __forceinline__ float warp_max(float x) {
 // ---------------------------------------------------------------- router
 //
 // A warp per token; lane l holds the experts l, l + 32, .. as keys in the order of
-// the choice (larger logits first, NaN before all, 0.0 and -0.0 equal; 0 for -inf,
-// which is never chosen). A choice is two reductions of the warp: the largest key,
-// then the lowest expert that has it; only the lane that held it looks for its next.
-// Bound: a decode batch by the launch, many tokens by the issue of the choices.
+// the choice: larger logits first, NaN before all, 0.0 and -0.0 equal; 0 for -inf,
+// which is never chosen. The key's lowest bits make room for the expert (lower ones
+// are larger numbers), so that one reduction of the warp finds a choice, all keys
+// differ, and a lane sorts its own by minima and maxima alone; the lane whose largest
+// was chosen moves on to its next. A bf16 logit's key has those bits to spare. Two
+// float32 logits may differ in them alone: where neighbours among the chosen (or the
+// last one and one that was not) have equal keys but for the expert, the token is
+// done again by whole keys.
+// Bound: a decode batch by the launch, many tokens by the issue: 16384 rows of 256
+// float32 logits, 8 chosen, .. us (with two reductions and a search through the
+// lane's keys a choice 20.5 us).
 
+// (x + 0 is 0.0 for -0.0, and 0x7FFFFFFF for every NaN)
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return kAll;
-  const uint32_t b = __float_as_uint(x + 0.0f);
-  if (b == 0xFF800000u) return 0;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
+  const uint32_t key = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return key > 0x007FFFFFu ? key : 0u;  // -inf is 0x007FFFFF, the lowest
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   if (k == kAll) return __uint_as_float(0x7FC00000u);
@@ -46,6 +55,17 @@ template <bool kF32>
 __device__ __forceinline__ float logit(const void* row, int64_t e) {
   if constexpr (kF32) return static_cast<const float*>(row)[e];
   return bf16_bits_to_float(static_cast<const uint16_t*>(row)[e]);
+}
+
+// The lane's logits, -inf beyond the last (all loads on their way at once).
+template <bool kF32, int kPer>
+__device__ __forceinline__ void load_row(const void* row, int E, float (&x)[kPer]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = logit<kF32>(row, min(32 * i + lane, E - 1));
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (32 * i + lane >= E) x[i] = -INFINITY;
 }
 
 __device__ __forceinline__ float sigmoid(float x) {
@@ -69,9 +89,59 @@ __device__ __forceinline__ float chosen_weight(float x, bool held, float top, in
   return held ? p / sum : 0.0f;
 }
 
+// This token's choices by whole keys: lane j's expert, -1 if none is left.
+template <bool kF32, int kPer>
+__device__ __noinline__ int choose_exactly(const void* row, int E, int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[kPer];
+  {
+    float x[kPer];
+    load_row<kF32>(row, E, x);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = order_key(x[i]);
+  }
+  int id = -1;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    uint32_t mine = 0, at = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (key[i] > mine) mine = key[i], at = i;
+    const uint32_t best = __reduce_max_sync(kAll, mine);
+    if (best == 0) break;
+    const uint32_t e = __reduce_min_sync(kAll, mine == best ? 32u * at + lane : kAll);
+    if (lane == j) id = static_cast<int>(e);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (32u * i + lane == e) key[i] = 0;
+  }
+  return id;
+}
+
+// The larger keys first (Batcher's odd-even merge sort).
+template <int kPer, int kP = 1, int kK = 1>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[kPer]) {
+  if constexpr (kP < kPer) {
+#pragma unroll
+    for (int i = 0; i + kK < kPer; ++i) {
+      constexpr int kFirst = kK % kP;
+      if (i >= kFirst && (i - kFirst) % (2 * kK) < kK && i / (2 * kP) == (i + kK) / (2 * kP)) {
+        const uint32_t x = v[i], y = v[i + kK];
+        v[i] = max(x, y);
+        v[i + kK] = min(x, y);
+      }
+    }
+    if constexpr (kK > 1)
+      sort_down<kPer, kP, kK / 2>(v);
+    else
+      sort_down<kPer, 2 * kP, 2 * kP>(v);
+  }
+}
+
 template <bool kF32, int kPer>
 __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, int32_t* __restrict__ ids,
                                                          float* __restrict__ weights) {
+  constexpr uint32_t kExpert = 32 * kPer - 1;  // the bits of the expert
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   cl::griddep_wait();
@@ -79,48 +149,54 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, int3
   if (t >= a.T) return;
   const char* row = static_cast<const char*>(a.logits) + t * a.ld * (kF32 ? 4 : 2);
   const int E = static_cast<int>(a.E);
+  const bool over_all = a.score == WQ_SCORE_SOFTMAX && !a.renormalize;
   uint32_t key[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) key[i] = 32 * i + lane < E ? order_key(logit<kF32>(row, 32 * i + lane)) : 0u;
   float sum = 1.0f, top_all = 0.0f;
-  if (a.score == WQ_SCORE_SOFTMAX && !a.renormalize) {
-    uint32_t best = 0;
+  {
+    float x[kPer];
+    load_row<kF32>(row, E, x);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(kAll, best);
-    top_all = best != 0 ? key_value(best) : 0.0f;
-    sum = 0.0f;
+    for (int i = 0; i < kPer; ++i) key[i] = order_key(x[i]);
+    if (over_all) {
+      uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += key[i] != 0 ? expf(key_value(key[i]) - top_all) : 0.0f;
-    sum = warp_sum(sum);
+      for (int i = 0; i < kPer; ++i) best = max(best, key[i]);
+      best = __reduce_max_sync(kAll, best);
+      top_all = best != 0 ? key_value(best) : 0.0f;
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum += expf(x[i] - top_all);  // (exp(-inf) is 0)
+      sum = warp_sum(sum);
+    }
   }
-  uint32_t mine = 0;  // this lane's largest key not chosen yet
-  int at = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (key[i] > mine) mine = key[i], at = i;
-  uint32_t chosen = 0;
-  int id = -1;
+    if (key[i] != 0) key[i] = (key[i] & ~kExpert) | (kExpert - (32 * i + lane));
+  sort_down(key);
+  uint32_t chosen = 0, last = 0;
+  bool close = false;
   for (int j = 0; j < a.k; ++j) {
-    const uint32_t best = __reduce_max_sync(kAll, mine);
-    const uint32_t e = __reduce_min_sync(kAll, mine == best ? 32u * at + lane : kAll);
-    if (best != 0 && (e & 31) == lane) {
-      // (the key itself goes, then its lane's next largest, the first among equals)
-      mine = 0;
-      const int gone = at;
+    const uint32_t best = __reduce_max_sync(kAll, key[0]);
+    if (best == 0) break;
+    if (lane == j) chosen = best;
+    if (key[0] == best) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (i == gone) key[i] = 0;
-        if (key[i] > mine) mine = key[i], at = i;
-      }
+      for (int i = 0; i + 1 < kPer; ++i) key[i] = key[i + 1];
+      key[kPer - 1] = 0;
     }
-    if (lane == j && best != 0) chosen = best, id = static_cast<int>(e);
+    close |= (best ^ last) <= kExpert;
+    last = best;
+  }
+  int id = chosen != 0 ? static_cast<int>(kExpert - (chosen & kExpert)) : -1;
+  if constexpr (kF32) {
+    close |= (key[0] ^ last) <= kExpert && key[0] != 0;
+    if (__any_sync(kAll, close)) id = choose_exactly<kF32, kPer>(row, E, a.k);
   }
   const bool held = id >= 0;
-  const float x = held ? key_value(chosen) : 0.0f;
+  const float x = held ? logit<kF32>(row, id) : 0.0f;
   const float top = __shfl_sync(kAll, x, 0);
   float w;
-  if (a.score == WQ_SCORE_SOFTMAX && !a.renormalize)
+  if (over_all)
     w = held ? expf(x - top_all) / sum : 0.0f;
   else
     w = chosen_weight(x, held, top, a.score, a.renormalize != 0);
@@ -181,11 +257,9 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const RouteArgs a,
   float d;
   if (over_all) {
     float v[kPer], top = -INFINITY, sum = 0.0f;
+    load_row<kF32>(row, E, v);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      v[i] = 32 * i + lane < E ? logit<kF32>(row, 32 * i + lane) : -INFINITY;
-      top = fmaxf(top, v[i]);
-    }
+    for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);
     top = warp_max(top);
     if (top == -INFINITY) top = 0.0f;
 #pragma unroll
@@ -218,112 +292,242 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(const RouteArgs a,
 
 // ---------------------------------------------------------------- rows
 //
-// Bound: HBM; nothing but the rows is read or written. A thread has 16 bytes of a
-// token's row and goes over the token's choices: spread reads them once and writes k
-// times, combine has its k loads on their way at once, which many threads turn into
-// enough bytes in flight. Rows whose length is no multiple of 8 go value by value.
+// Bound: HBM; nothing but the rows is read or written. kLanes threads go along a
+// token's row, 8 values at a time, and over its
+// choices: spread reads a piece once and writes it k times, combine has its k loads
+// on their way at once. Few tokens are cut into parts, so that more SMs have work.
+// Measured for 8192 tokens of 8 choices of 5120: .. us; a thread a piece, flat over
+// all tokens, took 143 for combine (many short blocks).
 
-struct Place {
-  int64_t t;
-  int64_t c;
-};
-// This thread's token and place in its row of C pieces, flat over all tokens.
-__device__ __forceinline__ Place flat_place(int64_t C) {
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kThreads;
-  // (64-bit places are divided only where they are past 32 bits)
-  const int64_t t0 = u0 <= 0xFFFFFFFFll ? static_cast<uint32_t>(u0) / static_cast<uint32_t>(C) : u0 / C;
-  const uint32_t in = static_cast<uint32_t>(u0 - t0 * C) + threadIdx.x;
-  const uint32_t more = in / static_cast<uint32_t>(C);
-  return Place{t0 + more, static_cast<int64_t>(in - more * static_cast<uint32_t>(C))};
+constexpr int kRowThreads = 128;  // of a block, unless a token has more
+
+// 8 bf16 values.
+__device__ __forceinline__ void widen(const uint4& p, float (&v)[8]) {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 narrow(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int kVec>
-struct Piece;  // kVec bf16 values
-template <>
-struct Piece<8> {
-  using type = uint4;
-  __device__ static void widen(const uint4& p, float (&v)[8]) {
-    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+// Rows that do not begin at 16 bytes (kOdd) are written in whole pieces of 16 bytes,
+// and read by two of them and a shift; a warp takes the values at the row's ends one a
+// lane. (Value by value, 4096 tokens of 6 choices of 2049 took .. us.)
+//
+// Values i .. i + 7, whose 16-byte pieces both lie in the array, as two loads without
+// a branch (so that many are on their way at once) and a shift.
+struct Odd8 {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t i) {
+    const uint4* v = reinterpret_cast<const uint4*>(p) + (i >> 3);
+    a = v[0];
+    b = v[(i & 7) != 0];
   }
-  __device__ static uint4 narrow(const float (&v)[8]) {
-    uint32_t w[4];
+  __device__ __forceinline__ uint4 get(int64_t i) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t s[7], t[5];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&p);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int l = 0; l < 7; ++l) s[l] = i & 2 ? w[l + 1] : w[l];
+#pragma unroll
+    for (int l = 0; l < 5; ++l) t[l] = i & 4 ? s[l + 2] : s[l];
+    const int half = 16 * static_cast<int>(i & 1);
+    return make_uint4(__funnelshift_r(t[0], t[1], half), __funnelshift_r(t[1], t[2], half),
+                      __funnelshift_r(t[2], t[3], half), __funnelshift_r(t[3], t[4], half));
   }
 };
-template <>
-struct Piece<1> {
-  using type = uint16_t;
-  __device__ static void widen(const uint16_t& p, float (&v)[1]) { v[0] = bf16_bits_to_float(p); }
-  __device__ static uint16_t narrow(const float (&v)[1]) { return float_to_bf16_bits_rn(v[0]); }
+// A row of D that begins at value i of the array that is written: `head` values, then
+// `full` pieces, then at most 15 values.
+struct Ends {
+  int64_t D;
+  int head, full;
+  __device__ __forceinline__ Ends(int64_t i, int64_t D_) : D(D_) {
+    head = static_cast<int>(min(-i & 7, D));
+    full = static_cast<int>((D - head) / 8);
+  }
+  // One piece less where the last one's second load would pass the end of the array of
+  // n values that is read from value i on.
+  __device__ __forceinline__ void within(int64_t i, int64_t n) {
+    const int64_t at = i + head + 8 * (static_cast<int64_t>(full) - 1);
+    if (full > 0 && (at & 7) != 0 && (at >> 3) * 8 + 16 > n) --full;
+  }
+  // The value at an end that this lane takes, or -1.
+  __device__ __forceinline__ int64_t value(int lane) const {
+    const int64_t e = lane < 8 ? lane : head + 8 * static_cast<int64_t>(full) + lane - 8;
+    return (lane < 8 ? lane < head : e < D) ? e : -1;
+  }
 };
+constexpr int kOddBatch = 4;
 
 constexpr int kBatch = 8;  // choices whose rows are on their way at once
 
-template <int kVec>
-__global__ void __launch_bounds__(kThreads) spread_kernel(const ChoiceRows a, const uint16_t* __restrict__ x,
-                                                          int64_t x_stride, uint16_t* __restrict__ out) {
-  using V = typename Piece<kVec>::type;
-  const Place p = flat_place(a.D / kVec);
+// This thread's token, and its pieces: the first and the step.
+struct Along {
+  int64_t t;
+  int c, step;
+};
+template <int kLanes>
+constexpr int kBlock = kLanes > kRowThreads ? kLanes : kRowThreads;
+template <int kLanes>
+__device__ __forceinline__ Along along(int parts) {
+  const uint32_t part = blockIdx.x % parts, group = blockIdx.x / parts;
+  return Along{static_cast<int64_t>(group) * (kBlock<kLanes> / kLanes) + threadIdx.x / kLanes,
+               static_cast<int>(part * kLanes + threadIdx.x % kLanes), parts * kLanes};
+}
+
+template <bool kOdd, int kLanes>
+__global__ void __launch_bounds__(kRowThreads) spread_kernel(const ChoiceRows a, const uint16_t* __restrict__ x,
+                                                             int64_t x_stride, uint16_t* __restrict__ out, int parts) {
+  const Along p = along<kLanes>(parts);
   cl::griddep_wait();
   cl::griddep_launch_dependents();
   if (p.t >= a.T) return;
-  const V v = reinterpret_cast<const V*>(x + p.t * x_stride)[p.c];
+  const int64_t D = a.D, C = D / 8;
   const int32_t* slots = a.slots + p.t * a.k;
   for (int j0 = 0; j0 < a.k; j0 += kBatch) {
     int32_t s[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) s[j] = j0 + j < a.k ? slots[j0 + j] : -1;
+    for (int j = 0; j < kBatch; ++j) {
+      s[j] = slots[min(j0 + j, a.k - 1)];
+      if (j0 + j >= a.k || s[j] >= a.R) s[j] = -1;
+    }
+    if constexpr (kOdd) {
+      const int64_t from = p.t * x_stride;
+#pragma unroll 1
+      for (int j = j0; j < min(j0 + kBatch, a.k); ++j) {
+        const int64_t i = slots[j] * D;
+        if (i < 0 || slots[j] >= a.R) continue;
+        Ends ends(i, D);
+        ends.within(from, (a.T - 1) * x_stride + D);
+        const int64_t e = p.c < 32 ? ends.value(p.c) : -1;
+        if (e >= 0) out[i + e] = x[from + e];
+#pragma unroll 4
+        for (int c = p.c; c < ends.full; c += p.step) {
+          const int64_t at = ends.head + 8 * static_cast<int64_t>(c);
+          Odd8 v;
+          v.load(x, from + at);
+          *reinterpret_cast<uint4*>(out + i + at) = v.get(from + at);
+        }
+      }
+    } else {
+      for (int64_t c = p.c; c < C; c += p.step) {
+        const uint4 v = reinterpret_cast<const uint4*>(x + p.t * x_stride)[c];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      if (s[j] >= 0 && s[j] < a.R) reinterpret_cast<V*>(out + s[j] * a.D)[p.c] = v;
+        for (int j = 0; j < kBatch; ++j)
+          if (s[j] >= 0) reinterpret_cast<uint4*>(out + s[j] * D)[c] = v;
+      }
+    }
   }
 }
 
-template <int kVec>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const ChoiceRows a, const uint16_t* __restrict__ y,
-                                                           const uint16_t* residual, uint16_t* out) {
-  using P = Piece<kVec>;
-  using V = typename P::type;
-  const Place p = flat_place(a.D / kVec);
+template <bool kOdd, int kLanes>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const ChoiceRows a, const uint16_t* __restrict__ y,
+                                                              const uint16_t* residual, uint16_t* out, int parts) {
+  const Along p = along<kLanes>(parts);
   cl::griddep_wait();
   cl::griddep_launch_dependents();
   if (p.t >= a.T) return;
-  float acc[kVec] = {};
-  if (residual != nullptr) P::widen(reinterpret_cast<const V*>(residual + p.t * a.D)[p.c], acc);
-  const int64_t at = p.t * a.k;
-  for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-    int32_t s[kBatch];
-    float w[kBatch];
-    V v[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) s[j] = j0 + j < a.k ? a.slots[at + j0 + j] : -1;
+  const int64_t D = a.D, at = p.t * a.k, row = p.t * D;
+  int32_t s[kBatch];
+  float w[kBatch];
+  auto choices = [&](int j0) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      w[j] = 0.0f;
-      v[j] = V{};
-      if (s[j] < 0 || s[j] >= a.R) continue;
-      w[j] = a.weights != nullptr ? a.weights[at + j0 + j] : 1.0f;
-      v[j] = reinterpret_cast<const V*>(y + s[j] * a.D)[p.c];
+      s[j] = a.slots[at + min(j0 + j, a.k - 1)];
+      w[j] = 1.0f;
+    }
+    if (a.weights != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) w[j] = a.weights[at + min(j0 + j, a.k - 1)];
     }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      float f[kVec];
-      P::widen(v[j], f);
+    for (int j = 0; j < kBatch; ++j)
+      if (j0 + j >= a.k || s[j] >= a.R) s[j] = -1;
+  };
+  float acc[8];
+  auto add = [&](int j, const uint4& v) {
+    float f[8];
+    widen(v, f);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+  };
+  choices(0);
+  if constexpr (kOdd) {
+    Ends ends(row, D);
+    int full = ends.full;
+    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+      if (a.k > kBatch) choices(j0);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        Ends of(row, D);
+        of.within(max(s[j], 0) * D, a.R * D);
+        full = min(full, of.full);
+      }
+    }
+    ends.full = full;
+    const int64_t e = p.c < 32 ? ends.value(p.c) : -1;
+    if (e >= 0) {
+      float sum = residual != nullptr ? bf16_bits_to_float(residual[row + e]) : 0.0f;
+      for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+        if (a.k > kBatch) choices(j0);
+        uint16_t v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) v[j] = y[max(s[j], 0) * D + e];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (s[j] >= 0) sum = fmaf(w[j], bf16_bits_to_float(v[j]), sum);
+      }
+      out[row + e] = float_to_bf16_bits_rn(sum);
+    }
+#pragma unroll 1
+    for (int c = p.c; c < full; c += p.step) {
+      const int64_t i = ends.head + 8 * static_cast<int64_t>(c);
+      uint4 first = make_uint4(0, 0, 0, 0);
+      if (residual != nullptr) first = *reinterpret_cast<const uint4*>(residual + row + i);
+      widen(first, acc);
+      for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+        if (a.k > kBatch) choices(j0);
+#pragma unroll
+        for (int l = 0; l < kBatch; l += kOddBatch) {
+          Odd8 v[kOddBatch];
+#pragma unroll
+          for (int j = 0; j < kOddBatch; ++j) v[j].load(y, max(s[l + j], 0) * D + i);
+#pragma unroll
+          for (int j = 0; j < kOddBatch; ++j)
+            if (s[l + j] >= 0) add(l + j, v[j].get(s[l + j] * D + i));
+        }
+      }
+      *reinterpret_cast<uint4*>(out + row + i) = narrow(acc);
+    }
+  } else {
+    const int64_t C = D / 8;
+#pragma unroll 1
+    for (int64_t c = p.c; c < C; c += p.step) {
+      uint4 first = make_uint4(0, 0, 0, 0);
+      if (residual != nullptr) first = reinterpret_cast<const uint4*>(residual + row)[c];
+      widen(first, acc);
+      for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+        if (a.k > kBatch) choices(j0);
+        uint4 v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          v[j] = s[j] >= 0 ? reinterpret_cast<const uint4*>(y + s[j] * D)[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (s[j] >= 0) add(j, v[j]);
+      }
+      reinterpret_cast<uint4*>(out + row)[c] = narrow(acc);
     }
   }
-  reinterpret_cast<V*>(out + p.t * a.D)[p.c] = P::narrow(acc);
 }
 
 // The sums over the lanes of 8 numbers: lane l has that of number l / 4. Halves of
@@ -347,56 +551,91 @@ __device__ __forceinline__ float eight_sums(const float (&v)[8]) {
   return s + __shfl_xor_sync(kAll, s, 1);
 }
 
-// A block per token: dy's rows are written as y's are read, and the products with
-// dout are summed over the block in a fixed order.
-template <int kVec>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const ChoiceRows a, const uint16_t* __restrict__ dout,
-                                                                const uint16_t* __restrict__ y, uint16_t* dy,
-                                                                float* __restrict__ dweights) {
-  using P = Piece<kVec>;
-  using V = typename P::type;
-  __shared__ float part[kThreads / 32][kBatch];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int64_t t = blockIdx.x, at = t * a.k;
-  const int C = static_cast<int>(a.D / kVec);
+// dy's rows are written as y's are read; the products with dout are summed over a
+// token's threads in a fixed order.
+template <bool kOdd, int kLanes>
+__global__ void __launch_bounds__(kBlock<kLanes>, kOdd ? 1 : 768 / kBlock<kLanes>)
+    combine_grad_kernel(const ChoiceRows a, const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y,
+                        uint16_t* dy, float* __restrict__ dweights) {
+  constexpr int kGroupWarps = kLanes / 32;
+  __shared__ float part[kBlock<kLanes> / 32][kBatch];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Along p = along<kLanes>(1);
   cl::griddep_wait();
   cl::griddep_launch_dependents();
+  const bool real = p.t < a.T;  // (the block's barriers want every thread)
+  const int64_t t = real ? p.t : a.T - 1, at = t * a.k, D = a.D, C = real ? D / 8 : 0;
   for (int j0 = 0; j0 < a.k; j0 += kBatch) {
     int32_t s[kBatch];
     float w[kBatch], dot[kBatch] = {};
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      s[j] = j0 + j < a.k ? a.slots[at + j0 + j] : -1;
-      if (s[j] >= a.R) s[j] = -1;
-      w[j] = s[j] >= 0 ? a.weights[at + j0 + j] : 0.0f;
+      s[j] = a.slots[at + min(j0 + j, a.k - 1)];
+      w[j] = a.weights[at + min(j0 + j, a.k - 1)];
+      if (j0 + j >= a.k || s[j] >= a.R) s[j] = -1;
     }
-    for (int c = threadIdx.x; c < C; c += blockDim.x) {
-      float g[kVec];
-      V v[kBatch];
-      P::widen(reinterpret_cast<const V*>(dout + t * a.D)[c], g);
+    auto term = [&](int j, const uint4& yv, const float (&g)[8]) {
+      float f[8];
+      widen(yv, f);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) v[j] = s[j] >= 0 ? reinterpret_cast<const V*>(y + s[j] * a.D)[c] : V{};
+      for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = w[j] * g[i];
+      return narrow(f);
+    };
+    if constexpr (kOdd) {
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        if (s[j] < 0) continue;
-        float f[kVec];
-        P::widen(v[j], f);
+        if (s[j] < 0 || !real) continue;
+        const int64_t i = s[j] * D;  // y's and dy's pieces lie alike
+        Ends ends(i, D);
+        ends.within(t * D, a.T * D);
+        const int64_t e = p.c < 32 ? ends.value(p.c) : -1;
+        if (e >= 0) {
+          const float g = bf16_bits_to_float(dout[t * D + e]);
+          dot[j] = fmaf(g, bf16_bits_to_float(y[i + e]), dot[j]);
+          dy[i + e] = float_to_bf16_bits_rn(w[j] * g);
+        }
+#pragma unroll 2
+        for (int c = p.c; c < ends.full; c += kLanes) {
+          const int64_t l = ends.head + 8 * static_cast<int64_t>(c);
+          Odd8 v;
+          v.load(dout, t * D + l);
+          const uint4 yv = *reinterpret_cast<const uint4*>(y + i + l);
+          float g[8];
+          widen(v.get(t * D + l), g);
+          *reinterpret_cast<uint4*>(dy + i + l) = term(j, yv, g);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int64_t c = p.c; c < C; c += kLanes) {
+        float g[8];
+        uint4 v[kBatch];
+        widen(reinterpret_cast<const uint4*>(dout + t * D)[c], g);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+        for (int j = 0; j < kBatch; ++j)
+          v[j] = s[j] >= 0 ? reinterpret_cast<const uint4*>(y + s[j] * D)[c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) f[i] = w[j] * g[i];
-        reinterpret_cast<V*>(dy + s[j] * a.D)[c] = P::narrow(f);
+        for (int j = 0; j < kBatch; ++j)
+          if (s[j] >= 0) reinterpret_cast<uint4*>(dy + s[j] * D)[c] = term(j, v[j], g);
       }
     }
     const float sum = eight_sums(dot);
-    if ((lane & 3) == 0) part[warp][lane >> 2] = sum;
-    __syncthreads();
-    if (threadIdx.x < kBatch && j0 + static_cast<int>(threadIdx.x) < a.k) {
-      float d = 0.0f;
-      for (int i = 0; i < warps; ++i) d += part[i][threadIdx.x];
-      dweights[at + j0 + threadIdx.x] = d;
+    if constexpr (kGroupWarps == 1) {
+      if (real && (lane & 3) == 0 && j0 + (lane >> 2) < a.k) dweights[at + j0 + (lane >> 2)] = sum;
+    } else {
+      const int own = threadIdx.x % kLanes;
+      if ((lane & 3) == 0) part[warp][lane >> 2] = sum;
+      __syncthreads();
+      if (real && own < kBatch && j0 + own < a.k) {
+        float d = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kGroupWarps; ++i) d += part[threadIdx.x / kLanes * kGroupWarps + i][own];
+        dweights[at + j0 + own] = d;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -436,28 +675,57 @@ cudaError_t launch_moe_route_grad(const Ctx& c, const RouteArgs& a, const int32_
 }
 
 namespace {
-int64_t flat_grid(int64_t T, int64_t C) { return (T * C + kThreads - 1) / kThreads; }
+
+// How the rows go: in whole 16 bytes or not, threads a token (a warp for short
+// rows), parts a token is cut into, blocks.
+struct RowPlan {
+  bool odd;
+  int lanes, parts, threads;
+  int64_t grid;
+};
+RowPlan row_plan(int64_t T, int64_t D, int64_t stride, int lanes, int64_t cut_below) {
+  RowPlan p;
+  p.odd = D % 8 != 0 || stride % 8 != 0;
+  const int64_t C = std::max<int64_t>(D / 8, 1);
+  p.lanes = C <= 64 ? 32 : lanes;
+  p.threads = p.lanes < kRowThreads ? kRowThreads : p.lanes;
+  const int64_t groups = (T * p.lanes - 1) / p.threads + 1;
+  p.parts = groups < cut_below ? static_cast<int>((C - 1) / p.lanes + 1) : 1;
+  if (groups * p.parts > kMaxDim) p.parts = 1;
+  p.grid = groups * p.parts;
+  return p;
+}
+
 }  // namespace
 
+#define WQ_ROW_KERNEL(kern, p)                                                       \
+  ((p).lanes == 32 ? ((p).odd ? kern<true, 32> : kern<false, 32>)                    \
+                   : ((p).odd ? kern<true, kRowThreads> : kern<false, kRowThreads>))
+
 cudaError_t launch_moe_spread(const Ctx& c, const ChoiceRows& a, const uint16_t* x, int64_t x_stride, uint16_t* out) {
-  const bool vec = a.D % 8 == 0 && x_stride % 8 == 0;
-  const int64_t grid = flat_grid(a.T, vec ? a.D / 8 : a.D);
-  if (grid > kMaxDim) return cudaErrorInvalidConfiguration;
-  return launch_early(c, grid, kThreads, 0, vec ? spread_kernel<8> : spread_kernel<1>, a, x, x_stride, out);
+  // (a thread a piece: its k writes need no loop, 5 us of 122 for 8192 tokens of 8 choices of 5120)
+  const bool wide = a.D % 8 == 0 && x_stride % 8 == 0;
+  const RowPlan p = row_plan(a.T, a.D, x_stride, kRowThreads, wide ? kMaxDim : 4 * c.sm_count);
+  return launch_early(c, p.grid, p.threads, 0, WQ_ROW_KERNEL(spread_kernel, p), a, x, x_stride, out, p.parts);
 }
 
 cudaError_t launch_moe_combine(const Ctx& c, const ChoiceRows& a, const uint16_t* y, const uint16_t* residual,
                                uint16_t* out) {
-  const bool vec = a.D % 8 == 0;
-  const int64_t grid = flat_grid(a.T, vec ? a.D / 8 : a.D);
-  if (grid > kMaxDim) return cudaErrorInvalidConfiguration;
-  return launch_early(c, grid, kThreads, 0, vec ? combine_kernel<8> : combine_kernel<1>, a, y, residual, out);
+  const RowPlan p = row_plan(a.T, a.D, a.D, kRowThreads, 4 * c.sm_count);
+  return launch_early(c, p.grid, p.threads, 0, WQ_ROW_KERNEL(combine_kernel, p), a, y, residual, out, p.parts);
 }
 
 cudaError_t launch_moe_combine_grad(const Ctx& c, const ChoiceRows& a, const uint16_t* dout, const uint16_t* y,
                                     uint16_t* dy, float* dweights) {
-  return launch_early(c, a.T, kThreads, 0, a.D % 8 == 0 ? combine_grad_kernel<8> : combine_grad_kernel<1>, a, dout, y,
-                      dy, dweights);
+  // 128 threads a token: 4099 tokens of 6 choices of 2048 31 us (64: 31, 256: 36); few tokens of long rows 512 (64
+  // tokens of 8 choices of 5120 5.8 us, with 256 6.7, with 128 8.8)
+  if (a.T < 2 * c.sm_count && a.D > 2048) {
+    const RowPlan p = row_plan(a.T, a.D, a.D, 512, 0);
+    return launch_early(c, p.grid, p.threads, 0, p.odd ? combine_grad_kernel<true, 512> : combine_grad_kernel<false, 512>,
+                        a, dout, y, dy, dweights);
+  }
+  const RowPlan p = row_plan(a.T, a.D, a.D, kRowThreads, 0);
+  return launch_early(c, p.grid, p.threads, 0, WQ_ROW_KERNEL(combine_grad_kernel, p), a, dout, y, dy, dweights);
 }
 
 }  // namespace wq
