@@ -384,6 +384,39 @@ __device__ __forceinline__ Along along(int parts) {
                static_cast<int>(part * kLanes + threadIdx.x % kLanes), parts * kLanes};
 }
 
+// Writes the token's row to kBatch rows of out (-1: none).
+template <bool kOdd>
+__device__ __forceinline__ void spread_row(const ChoiceRows& a, const Along& p, const uint16_t* x, int64_t x_stride,
+                                           uint16_t* out, const int32_t (&s)[kBatch]) {
+  const int64_t D = a.D, from = p.t * x_stride;
+  if constexpr (kOdd) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (s[j] < 0) continue;
+      const int64_t i = s[j] * D;
+      Ends ends(i, D);
+      ends.within(from, (a.T - 1) * x_stride + D);
+      const int64_t e = p.c < 32 ? ends.value(p.c) : -1;
+      if (e >= 0) out[i + e] = x[from + e];
+#pragma unroll 2
+      for (int c = p.c; c < ends.full; c += p.step) {
+        const int64_t at = ends.head + 8 * static_cast<int64_t>(c);
+        Odd8 v;
+        v.load(x, from + at);
+        *reinterpret_cast<uint4*>(out + i + at) = v.get(from + at);
+      }
+    }
+  } else {
+    const int64_t C = D / 8;
+    for (int64_t c = p.c; c < C; c += p.step) {
+      const uint4 v = reinterpret_cast<const uint4*>(x + from)[c];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (s[j] >= 0) reinterpret_cast<uint4*>(out + s[j] * D)[c] = v;
+    }
+  }
+}
+
 template <bool kOdd, int kLanes>
 __global__ void __launch_bounds__(kRowThreads) spread_kernel(const ChoiceRows a, const uint16_t* __restrict__ x,
                                                              int64_t x_stride, uint16_t* __restrict__ out, int parts) {
@@ -391,7 +424,6 @@ __global__ void __launch_bounds__(kRowThreads) spread_kernel(const ChoiceRows a,
   cl::griddep_wait();
   cl::griddep_launch_dependents();
   if (p.t >= a.T) return;
-  const int64_t D = a.D, C = D / 8;
   const int32_t* slots = a.slots + p.t * a.k;
   for (int j0 = 0; j0 < a.k; j0 += kBatch) {
     int32_t s[kBatch];
@@ -400,32 +432,88 @@ __global__ void __launch_bounds__(kRowThreads) spread_kernel(const ChoiceRows a,
       s[j] = slots[min(j0 + j, a.k - 1)];
       if (j0 + j >= a.k || s[j] >= a.R) s[j] = -1;
     }
-    if constexpr (kOdd) {
-      const int64_t from = p.t * x_stride;
-#pragma unroll 1
-      for (int j = j0; j < min(j0 + kBatch, a.k); ++j) {
-        const int64_t i = slots[j] * D;
-        if (i < 0 || slots[j] >= a.R) continue;
-        Ends ends(i, D);
-        ends.within(from, (a.T - 1) * x_stride + D);
-        const int64_t e = p.c < 32 ? ends.value(p.c) : -1;
-        if (e >= 0) out[i + e] = x[from + e];
-#pragma unroll 4
-        for (int c = p.c; c < ends.full; c += p.step) {
-          const int64_t at = ends.head + 8 * static_cast<int64_t>(c);
-          Odd8 v;
-          v.load(x, from + at);
-          *reinterpret_cast<uint4*>(out + i + at) = v.get(from + at);
-        }
-      }
-    } else {
-      for (int64_t c = p.c; c < C; c += p.step) {
-        const uint4 v = reinterpret_cast<const uint4*>(x + p.t * x_stride)[c];
+    spread_row<kOdd>(a, p, x, x_stride, out, s);
+  }
+}
+
+__device__ __forceinline__ float eight_sums(const float (&v)[8]);
+
+// Few choices: a token's blocks find its places themselves, each the number of
+// choices that come before by (expert, choice), and one more block counts the
+// experts' (a launch less: 64 tokens of 8 choices of 5120 .. us, with one 5.2).
+constexpr int kFewChoices = 2048;
+
+template <bool kOdd>
+__global__ void __launch_bounds__(kRowThreads) sort_few_kernel(const ChoiceRows a, const int32_t* __restrict__ ids,
+                                                               int E, const uint16_t* __restrict__ x, int64_t x_stride,
+                                                               uint16_t* __restrict__ out, int32_t* slots,
+                                                               int32_t* __restrict__ offsets, int32_t* bad, int parts) {
+  __shared__ float part[2][kRowThreads / 32][kBatch];
+  __shared__ int count[kMaxGroups + 1];
+  const int n = static_cast<int>(a.T) * a.k, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool counts = blockIdx.x == gridDim.x - 1;
+  if (counts) {
+    for (int e = threadIdx.x; e <= E; e += kRowThreads) count[e] = 0;
+    __syncthreads();
+  }
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+  auto group_of = [&](int i) {  // ids outside [0, E) come last
+    const int id = ids[i];
+    return id < 0 || id >= E ? E : id;
+  };
+  if (counts) {
+    for (int i = threadIdx.x; i < n; i += kRowThreads) atomicAdd(&count[group_of(i)], 1);
+    __syncthreads();
+    if (warp == 0) {
+      int before = 0;
+      for (int e0 = 0; e0 <= E; e0 += 32) {
+        const int e = e0 + lane, c = e <= E ? count[e] : 0;
+        int sum = c;
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (s[j] >= 0) reinterpret_cast<uint4*>(out + s[j] * D)[c] = v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(kAll, sum, o);
+          if (lane >= o) sum += v;
+        }
+        if (e <= E) offsets[e] = before + sum - c;
+        before += __shfl_sync(kAll, sum, 31);
       }
+      if (lane == 0 && bad != nullptr && count[E] > 0) atomicAdd(bad, count[E]);
     }
+    return;
+  }
+  const Along p = along<kRowThreads>(parts);
+  const int own = static_cast<int>(p.t) * a.k;
+  for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+    // the (expert, choice) pairs as numbers
+    int key[kBatch], before[kBatch] = {};
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = own + min(j0 + j, a.k - 1);
+      key[j] = group_of(i) * kFewChoices + i;
+    }
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kRowThreads) {
+      const int other = group_of(i) * kFewChoices + i;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) before[j] += other < key[j];
+    }
+    float f[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) f[j] = static_cast<float>(before[j]);
+    const float sum = eight_sums(f);  // (at most 2048: exact)
+    float(&sums)[kRowThreads / 32][kBatch] = part[(j0 / kBatch) & 1];
+    if ((lane & 3) == 0) sums[warp][lane >> 2] = sum;
+    __syncthreads();
+    int32_t s[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      s[j] = static_cast<int32_t>((sums[0][j] + sums[1][j]) + (sums[2][j] + sums[3][j]));
+      if (key[j] >= E * kFewChoices) s[j] = -1;
+      if (p.c == j && j0 + j < a.k) slots[own + j0 + j] = s[j];
+      if (j0 + j >= a.k) s[j] = -1;
+    }
+    if (out != nullptr) spread_row<kOdd>(a, p, x, x_stride, out, s);
   }
 }
 
@@ -702,7 +790,24 @@ RowPlan row_plan(int64_t T, int64_t D, int64_t stride, int lanes, int64_t cut_be
   ((p).lanes == 32 ? ((p).odd ? kern<true, 32> : kern<false, 32>)                    \
                    : ((p).odd ? kern<true, kRowThreads> : kern<false, kRowThreads>))
 
-cudaError_t launch_moe_spread(const Ctx& c, const ChoiceRows& a, const uint16_t* x, int64_t x_stride, uint16_t* out) {
+cudaError_t launch_moe_sort(const Ctx& c, const ChoiceRows& a, const int32_t* ids, int64_t E, const uint16_t* x,
+                            int64_t x_stride, uint16_t* out, int32_t* offsets, int32_t* slots, int32_t* bad) {
+  const int64_t n = a.T * a.k;
+  if (n > 0 && n <= kFewChoices) {
+    const bool odd = a.D % 8 != 0 || x_stride % 8 != 0;
+    const int64_t parts = std::max<int64_t>(1, (a.D / 8 - 1) / kRowThreads + 1);
+    return launch_early(c, a.T * parts + 1, kRowThreads, 0, odd ? sort_few_kernel<true> : sort_few_kernel<false>, a, ids,
+                        static_cast<int>(E), x, x_stride, out, slots, offsets, bad, static_cast<int>(parts));
+  }
+  GroupArgs g{};
+  g.ids = ids;
+  g.n = n;
+  g.E = static_cast<int>(E);
+  g.slots = slots;
+  g.offsets = offsets;
+  g.bad = bad;
+  const cudaError_t e = launch_group(c, g);
+  if (e != cudaSuccess || out == nullptr || n == 0) return e;
   // (a thread a piece: its k writes need no loop, 5 us of 122 for 8192 tokens of 8 choices of 5120)
   const bool wide = a.D % 8 == 0 && x_stride % 8 == 0;
   const RowPlan p = row_plan(a.T, a.D, x_stride, kRowThreads, wide ? kMaxDim : 4 * c.sm_count);

@@ -105,18 +105,10 @@ wq_status moe_sort(const wq_bf16* x, int64_t x_stride, int64_t T, int64_t D, con
   WQ_OPT32(bad_count);
   Ctx c{};
   WQ_TRY(get_ctx(stream, &c));
-  GroupArgs g{};
-  g.ids = ids;
-  g.n = T * k;
-  g.E = static_cast<int>(E);
-  g.slots = slots;
-  g.offsets = offsets;
-  g.bad = bad_count;
+  const ChoiceRows r{slots, nullptr, T, T * k, rows ? D : 1, k};
   const std::lock_guard<std::mutex> order(launch_order());
-  WQ_TRY(launched(launch_group(c, g), "moe_sort launch"));
-  if (!rows || T == 0) return WQ_OK;
-  const ChoiceRows r{slots, nullptr, T, T * k, D, k};
-  return launched(launch_moe_spread(c, r, x, x_stride, out), "moe_sort launch");
+  return launched(launch_moe_sort(c, r, ids, E, x, rows ? x_stride : 1, out, offsets, slots, bad_count),
+                  "moe_sort launch");
 }
 
 wq_status moe_combine(const wq_bf16* y, int64_t R, const int32_t* slots, const float* weights,

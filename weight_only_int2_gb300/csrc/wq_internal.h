@@ -443,7 +443,9 @@ struct ChoiceRows {
   int64_t T, R, D;
   int k;
 };
-cudaError_t launch_moe_spread(const Ctx& c, const ChoiceRows& a, const uint16_t* x, int64_t x_stride, uint16_t* out);
+// a.slots is the slots written; x and out may be null (only slots and offsets)
+cudaError_t launch_moe_sort(const Ctx& c, const ChoiceRows& a, const int32_t* ids, int64_t E, const uint16_t* x,
+                            int64_t x_stride, uint16_t* out, int32_t* offsets, int32_t* slots, int32_t* bad);
 cudaError_t launch_moe_combine(const Ctx& c, const ChoiceRows& a, const uint16_t* y, const uint16_t* residual,
                                uint16_t* out);
 cudaError_t launch_moe_combine_grad(const Ctx& c, const ChoiceRows& a, const uint16_t* dout, const uint16_t* y,
