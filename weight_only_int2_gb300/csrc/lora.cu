@@ -265,7 +265,7 @@ struct Shrink64 {
   static constexpr int kCols = 64;  // of a stage
   static constexpr int kRowBytes = 2 * kCols;
   static constexpr int kChunks = kRowBytes / 16;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = kR == 128 ? 4 : 6;
   static constexpr int kStageBytes = (64 + kR) * kRowBytes;
   static constexpr int kSmem = kStages * kStageBytes;
   static constexpr int kStep = kThreads / kChunks;  // rows that the block copies at once
@@ -326,10 +326,10 @@ __global__ void __launch_bounds__(kThreads) shrink64_kernel(const LoraArgs a, co
     for (int s = first; s < last; ++s) {
       cp_wait<C::kStages - 2>();
       __syncthreads();
-      if (s + C::kStages - 1 < last) fetch(s + C::kStages - 1, (slot + C::kStages - 1) % C::kStages);
+      if (s + C::kStages - 1 < last) fetch(s + C::kStages - 1, slot == 0 ? C::kStages - 1 : slot - 1);
       cp_commit();
       const uint32_t at = ring_at + slot * C::kStageBytes;
-      slot = (slot + 1) % C::kStages;
+      slot = slot + 1 == C::kStages ? 0 : slot + 1;
 #pragma unroll
       for (int kk = 0; kk < C::kCols / 16; ++kk) {
         const int xr = warp * 16 + (lane & 15);
@@ -744,7 +744,7 @@ struct Expand64 {
   static constexpr int kBaseStep = kThreads / kBaseChunks;  // rows that the block copies at once
   static constexpr int kBases = 64 / kBaseStep;             // rows a thread copies
   static constexpr int kBs = kUnit * (kR / 8) / kThreads;   // pieces of B a thread copies
-  static constexpr int kFit = kR <= 16 ? 3 : (kR <= 64 ? 2 : 1);
+  static constexpr int kFit = kR <= 64 ? 2 : 1;
   static_assert(kFit * (kSmem + 1024) <= 228 * 1024, "");
 };
 
@@ -921,8 +921,7 @@ cudaError_t launch_64(const Ctx& c, const LoraArgs& a, const Ws& ws) {
   cudaError_t e = raise_smem_limit(lim, shrink64_kernel<kR>, c.device, S::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = most_tiles(a.M, a.n), stages = (a.K - 1) / S::kCols + 1;
-  const int fit = std::min(8, 220 * 1024 / S::kSmem);
-  const int64_t grid = std::min({int64_t{fit} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
+  const int64_t grid = std::min({int64_t{220 * 1024 / S::kSmem} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
   e = launch_early(c, grid, kThreads, S::kSmem, shrink64_kernel<kR>, a, ws);
   if (e != cudaSuccess) return e;
   const int64_t grid2 = std::min<int64_t>(tiles * ((a.N - 1) / E::kUnit + 1), E::kFit * c.sm_count);
