@@ -678,16 +678,19 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top_k:
 # ---------------------------------------------------------------- operators that pick weights by token
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_LOGIT_DTYPES = tuple(_LOGIT_TYPES)
 
 
 def _need_here(t: torch.Tensor, name: str) -> None:
     """A tensor on the current device: the call's kernels run there, on its current stream."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != _device():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_device()}")
+    dev = _device()
+    if at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
 
 
 def _need_at(t: torch.Tensor, name: str, dtype, shape=None) -> None:
@@ -700,12 +703,13 @@ def _need_matrix(t: torch.Tensor, name: str, shape, dtypes=(torch.bfloat16,)) ->
     _need_here(t, name)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must have shape {'two dimensions' if shape is None else tuple(shape)} (got {tuple(t.shape)})")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1 and rows > 0:
+    got, strides = t.shape, t.stride()
+    if len(got) != 2 or (shape is not None and got != shape):
+        raise ValueError(f"{name} must have {'two dimensions' if shape is None else f'shape {tuple(shape)}'} (got {tuple(got)})")
+    rows, cols = got
+    if cols > 1 and strides[1] != 1 and rows > 0:
         raise ValueError(f"each row of {name} must be contiguous")
-    return cols if rows <= 1 else t.stride(0)
+    return cols if rows <= 1 else strides[0]
 
 
 def _score(score: str) -> int:
@@ -721,12 +725,32 @@ def _or_new(out, name, dtype, shape, device) -> torch.Tensor:
     return out
 
 
+# A small call takes longer on the host than on the GPU, and most of that were the
+# checks: what passes these few comparisons passes the full checks, which are made
+# (and say what is wrong) only where something does not.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _plain(t, dtype, shape, dev) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous())
+
+
+def _tensors(*pairs) -> int:
+    """Tensors (with their names) on the GPU, the first on the current device, whose number is returned."""
+    for t, name in pairs:
+        if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+            _need_here(t, name)
+    _need_here(*pairs[0])
+    return pairs[0][0].get_device()
+
+
 def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", renormalize: bool = False,
               scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
     """The top_k experts of each token by its logits [T, E] (bf16 or float32, rows may be strided) and their weights:
     scale times the softmax or sigmoid score, divided by the chosen ones' sum with renormalize. Returns (ids [T, top_k]
     int32, weights [T, top_k] float32); an expert whose logit is -inf is never chosen (id -1, weight 0)."""
-    ld = _need_matrix(logits, "logits", None, tuple(_LOGIT_TYPES))
+    ld = _need_matrix(logits, "logits", None, _LOGIT_DTYPES)
     (T, E), dev = logits.shape, logits.device
     k = max(int(top_k), 0)
     ids = _or_new(ids, "ids", torch.int32, (T, k), dev)
@@ -740,13 +764,14 @@ def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tens
                    renormalize: bool = False, scale: float = 1.0, dlogits: torch.Tensor | None = None) -> torch.Tensor:
     """The gradient of moe_route's weights: dlogits [T, E] of the logits' type, from the ids that it returned and
     dweights [T, top_k] float32."""
-    ld = _need_matrix(logits, "logits", None, tuple(_LOGIT_TYPES))
+    ld = _need_matrix(logits, "logits", None, _LOGIT_DTYPES)
     T, E = logits.shape
     _need_at(ids, "ids", torch.int32)
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError(f"ids must have shape ({T}, top_k) (got {tuple(ids.shape)})")
     k = ids.shape[1]
-    _need_at(dweights, "dweights", torch.float32, (T, k))
+    if not _plain(dweights, _F32, ids.shape, _device()):
+        _need_at(dweights, "dweights", torch.float32, (T, k))
     dlogits = _or_new(dlogits, "dlogits", logits.dtype, (T, E), logits.device)
     _check(load().moe_route_grad(logits.data_ptr(), _LOGIT_TYPES[logits.dtype], ld, T, E, k, _score(score),
                                  1 if renormalize else 0, scale, ids.data_ptr(), dweights.data_ptr(),
@@ -762,20 +787,22 @@ def moe_sort(x: torch.Tensor | None, ids: torch.Tensor, E: int, out: torch.Tenso
     rows of out that no choice takes stay as they are. x None: out is None. The gradient of x is
     moe_combine(dout, slots)."""
     _need_at(ids, "ids", torch.int32)
-    if ids.dim() != 2:
-        raise ValueError(f"ids must be [T, k] (got {tuple(ids.shape)})")
-    (T, k), dev = ids.shape, ids.device
+    shape = ids.shape
+    if len(shape) != 2:
+        raise ValueError(f"ids must be [T, k] (got {tuple(shape)})")
+    (T, k), dev = shape, ids.device
     D = xs = 0
     if x is not None:
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x must be a tensor [T, D]")
         D = x.shape[1]
         xs = _need_matrix(x, "x", (T, D))
-        out = _or_new(out, "out", torch.bfloat16, (T * k, D), dev)
+        if out is None or not _plain(out, _BF16, (T * k, D), _device()):
+            out = _or_new(out, "out", torch.bfloat16, (T * k, D), dev)
     elif out is not None:
         raise ValueError("out is for a call with x")
     offsets = _or_new(offsets, "offsets", torch.int32, (E + 1,), dev)
-    slots = _or_new(slots, "slots", torch.int32, (T, k), dev)
+    slots = _or_new(slots, "slots", torch.int32, shape, dev)
     if bad_count is not None:
         _need_at(bad_count, "bad_count", torch.int32)
     _check(load().moe_sort(_ptr(x), xs, T, D, ids.data_ptr(), k, E, _ptr(out), offsets.data_ptr(), slots.data_ptr(),
@@ -783,18 +810,26 @@ def moe_sort(x: torch.Tensor | None, ids: torch.Tensor, E: int, out: torch.Tenso
     return out, offsets, slots
 
 
+def _rows_and_slots(y, slots):
+    dev = _tensors((y, "y"), (slots, "slots"))
+    ys, ss = y.shape, slots.shape
+    if not _plain(y, _BF16, ys, dev):
+        _need_at(y, "y", torch.bfloat16)
+    if not _plain(slots, _I32, ss, dev):
+        _need_at(slots, "slots", torch.int32)
+    if len(ys) != 2 or len(ss) != 2:
+        raise ValueError(f"y must be [R, D] and slots [T, k] (got {tuple(ys)} and {tuple(ss)})")
+    return ys, ss, dev
+
+
 def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """out[t] = (residual[t] +) sum_j weights[t, j] * y[slots[t, j]], [T, D] bf16: the choices' rows y [R, D] bf16
     back to their tokens (weights [T, k] float32; 1 without them). out may be residual itself."""
-    _need_at(y, "y", torch.bfloat16)
-    _need_at(slots, "slots", torch.int32)
-    if y.dim() != 2 or slots.dim() != 2:
-        raise ValueError(f"y must be [R, D] and slots [T, k] (got {tuple(y.shape)} and {tuple(slots.shape)})")
-    (R, D), (T, k) = y.shape, slots.shape
-    if weights is not None:
+    (R, D), (T, k), dev = _rows_and_slots(y, slots)
+    if weights is not None and not _plain(weights, _F32, (T, k), dev):
         _need_at(weights, "weights", torch.float32, (T, k))
-    if residual is not None:
+    if residual is not None and not _plain(residual, _BF16, (T, D), dev):
         _need_at(residual, "residual", torch.bfloat16, (T, D))
     out = _or_new(out, "out", torch.bfloat16, (T, D), y.device)
     _check(load().moe_combine(y.data_ptr(), R, slots.data_ptr(), _ptr(weights), _ptr(residual), T, D, k,
@@ -806,14 +841,13 @@ def moe_combine_grad(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, w
                      dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None):
     """The gradients of moe_combine from dout [T, D] bf16: dy [R, D] bf16 (rows that no choice names stay as they
     are) and dweights [T, k] float32. The residual's is dout itself."""
-    _need_at(y, "y", torch.bfloat16)
-    _need_at(slots, "slots", torch.int32)
-    if y.dim() != 2 or slots.dim() != 2:
-        raise ValueError(f"y must be [R, D] and slots [T, k] (got {tuple(y.shape)} and {tuple(slots.shape)})")
-    (R, D), (T, k) = y.shape, slots.shape
-    _need_at(dout, "dout", torch.bfloat16, (T, D))
-    _need_at(weights, "weights", torch.float32, (T, k))
-    dy = _or_new(dy, "dy", torch.bfloat16, (R, D), y.device)
+    (R, D), (T, k), dev = _rows_and_slots(y, slots)
+    if not _plain(dout, _BF16, (T, D), dev):
+        _need_at(dout, "dout", torch.bfloat16, (T, D))
+    if not _plain(weights, _F32, (T, k), dev):
+        _need_at(weights, "weights", torch.float32, (T, k))
+    if dy is None or not _plain(dy, _BF16, (R, D), dev):
+        dy = _or_new(dy, "dy", torch.bfloat16, (R, D), y.device)
     dweights = _or_new(dweights, "dweights", torch.float32, (T, k), y.device)
     _check(load().moe_combine_grad(dout.data_ptr(), y.data_ptr(), R, slots.data_ptr(), weights.data_ptr(), T, D, k,
                                    dy.data_ptr(), dweights.data_ptr(), _stream()), "moe_combine_grad")
@@ -831,24 +865,27 @@ def lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.
     """y[m] = base[m] + scale[a] * (x[m] . A[a]^T) . B[a]^T with a = adapter[m] (int32; -1: none, y[m] = base[m]).
     x [M, K], base and y [M, N] bf16 (rows may be strided; y may be base), A [n, r, K], B [n, N, r] bf16, scale [n]
     float32. base is the shared projection's output, such as wna16_gemm(x, ..)."""
-    _need_at(A, "A", torch.bfloat16)
-    _need_at(B, "B", torch.bfloat16)
-    if A.dim() != 3 or B.dim() != 3:
-        raise ValueError(f"A must be [n, r, K] and B [n, N, r] (got {tuple(A.shape)} and {tuple(B.shape)})")
-    (n, r, K), N = A.shape, B.shape[1]
-    if tuple(B.shape) != (n, N, r):
-        raise ValueError(f"B must have shape {(n, N, r)} (got {tuple(B.shape)})")
-    _need_at(adapter, "adapter", torch.int32)
-    M = adapter.shape[0]
-    _need(adapter, "adapter", torch.int32, (M,))
+    dev = _tensors((A, "A"), (B, "B"), (adapter, "adapter"))
+    As, Bs = A.shape, B.shape
+    if len(As) != 3 or len(Bs) != 3:
+        raise ValueError(f"A must be [n, r, K] and B [n, N, r] (got {tuple(As)} and {tuple(Bs)})")
+    n, r, K = As
+    N, M = Bs[1], adapter.shape[0] if adapter.dim() else 0
+    if not _plain(A, _BF16, As, dev):
+        _need_at(A, "A", torch.bfloat16)
+    if not _plain(B, _BF16, (n, N, r), dev):
+        _need_at(B, "B", torch.bfloat16, (n, N, r))
+    if not _plain(adapter, _I32, (M,), dev):
+        _need_at(adapter, "adapter", torch.int32, (M,))
     xs, bs = _need_matrix(x, "x", (M, K)), _need_matrix(base, "base", (M, N))
-    if scale is not None:
+    if scale is not None and not _plain(scale, _F32, (n,), dev):
         _need_at(scale, "scale", torch.float32, (n,))
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=base.device)
-    ys = _need_matrix(y, "y", (M, N))
-    if M <= 1 and y.data_ptr() == base.data_ptr():
-        ys = bs
+        y, ys = torch.empty((M, N), dtype=torch.bfloat16, device=base.device), N
+    else:
+        ys = _need_matrix(y, "y", (M, N))
+        if M <= 1 and y.data_ptr() == base.data_ptr():
+            ys = bs
     lib = load()
     if ws is None:
         ws = scratch(lora_workspace_bytes(M, n, r))
