@@ -523,7 +523,7 @@ struct Expand8 {
   static constexpr int kPieceBytes = kR == 16 ? 8 : 16;
   static constexpr int kBBytes = 8 * kPieces * kPieceBytes * 32;
   static constexpr int kStageBytes = kBBytes + 2 * 16 * 32;
-  static constexpr int kStages = kR == 16 ? 4 : (kR == 128 ? 2 : 3);
+  static constexpr int kStages = kR == 16 || kR == 128 ? 2 : 3;
   static constexpr int kWarpBytes = kStages * kStageBytes + 8 * kR * 4;
   static constexpr int kSmem = kWarps * kWarpBytes;
   static constexpr int kAll = kSmem + static_cast<int>(sizeof(Few)) + 1024;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
       }
       if (tile.x >= 0) {
         __syncwarp();
-        add_shares<8, kR, 8>(h, a, ws.part, tile, head.z, sh.shares, lane, 32);
+        add_shares<8, kR, 12>(h, a, ws.part, tile, head.z, sh.shares, lane, 32);
         __syncwarp();
 #pragma unroll
         for (int s = 0; s < kR / 16; ++s) {
