@@ -187,7 +187,8 @@ def test_binding_refuses_cpu_tensors():
 
 def test_the_workspace_holds_every_share_of_the_first_product():
     """The sizes behind lora_workspace_bytes, for any split of the rows into tiles: with G blocks, t tiles of at most
-    tile rows and s = min(32, max(1, G // t)) shares, the s * rows partial sums lie inside."""
+    tile rows and s = min(32, max(1, G // t)) shares, the s * rows partial sums lie inside, and with many rows two bf16
+    numbers for each value of each tile."""
     import weight_only_int2_gb300 as wq
 
     for M in (1, 2, 15, 16, 17, 100, 511, 512, 513, 4000, 70000):
@@ -196,7 +197,9 @@ def test_the_workspace_holds_every_share_of_the_first_product():
             for r in (8, 128):
                 have = wq.lora_workspace_bytes(M, n, r)
                 most = M // tile + min(M, n + 1)
-                head = -(-16 * (1 + most) // 16) * 16 + -(-4 * M // 16) * 16
+                head = 16 * (1 + most) + -(-4 * M // 16) * 16
+                if tile == 64 and r > 32:
+                    head += most * 64 * 128 * 4
                 for rows in {1, min(M, 7), M // 2 + 1, M}:
                     for groups in {1, min(n, rows)}:
                         per = -(-rows // groups)

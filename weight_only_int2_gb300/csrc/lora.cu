@@ -44,6 +44,7 @@ struct Ws {
   int4* tiles;     // as launch_group writes them
   int32_t* order;  // [M] the row at each place
   float* part;     // [shares][rows with an adapter][r]
+  uint4* low;      // many rows: x A^T as the second product's MMAs read it, [tiles][4][r / 16][2][32]
 };
 int64_t most_tiles(int64_t M, int64_t n) { return M / tile_of(M) + std::min(M, n + 1); }
 size_t part_bytes(int64_t M, int64_t r) {
@@ -51,6 +52,13 @@ size_t part_bytes(int64_t M, int64_t r) {
   return static_cast<size_t>(std::max(M, std::min(kMaxShares * M, int64_t{kMaxGrid} * tile_of(M)))) * r * 4;
 }
 size_t round16(size_t b) { return (b + 15) / 16 * 16; }
+// r as the kernels have it.
+constexpr int rank_of(int64_t r) { return r <= 16 ? 16 : (r <= 32 ? 32 : (r <= 64 ? 64 : 128)); }
+// Whether a kernel of its own adds up the shares of many rows (below).
+constexpr bool joined(int64_t r) { return r > 32; }
+size_t low_bytes(int64_t M, int64_t n, int64_t r) {
+  return tile_of(M) == 64 && joined(r) ? static_cast<size_t>(most_tiles(M, n)) * 64 * rank_of(r) * 4 : 0;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
   const int size = real ? 16 : 0;  // 0: zeros
@@ -358,8 +366,6 @@ __global__ void __launch_bounds__(kThreads) shrink64_kernel(const LoraArgs a, co
   }
 }
 
-// ---------------------------------------------------------------- y = base + (x A^T) B^T
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -371,6 +377,54 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   const float xh = __uint_as_float(hi << 16), yh = __uint_as_float(hi & 0xFFFF0000u);
   lo = pack2(fabsf(xh) < INFINITY ? x - xh : 0.0f, fabsf(yh) < INFINITY ? y - yh : 0.0f);
 }
+
+// Many rows, larger ranks: the shares added up in their order, scaled and written as
+// the MMAs of the second product read them, so that its blocks, which come to a tile
+// many times, find them ready (2049 rows, r 64, K 17408, 8 shares: 42 us for the call,
+// 47 where they added up the shares themselves; with r 16 the launch costs the 2 us
+// that it saves). A thread has two values of a row side by side; rows behind a tile's
+// last stay as they are.
+template <int kR>
+__global__ void __launch_bounds__(256) join_kernel(const LoraArgs a, const Ws ws, int shrink_grid, int shrink_cols) {
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+  const Rows rows{ws.tiles, ws.order};
+  const int4 head = rows.tile(0);
+  const int r = static_cast<int>(a.r);
+  const Shares sh = shares_of((static_cast<int>(a.K) - 1) / shrink_cols + 1, head.x, shrink_grid);
+  const int64_t stride = static_cast<int64_t>(head.z) * r, all = static_cast<int64_t>(head.x) * (32 * kR);
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < all; u += int64_t{256} * gridDim.x) {
+    const int t = static_cast<int>(u / (32 * kR)), pair = static_cast<int>(u % (32 * kR));
+    const int row = pair / (kR / 2), col = 2 * (pair % (kR / 2));
+    const int4 tile = rows.tile(1 + t);
+    if (row >= tile.z) continue;
+    float sx = 0.0f, sy = 0.0f;
+    if (col < r) {
+      const float* p = ws.part + (static_cast<int64_t>(tile.y) + row) * r + col;
+      for (int j0 = 0; j0 < sh.shares; j0 += 8) {
+        float2 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // (without branches: a load behind one waits for the load before it)
+          v[j] = __ldcg(reinterpret_cast<const float2*>(p + min(j0 + j, sh.shares - 1) * stride));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < sh.shares) sx += v[j].x, sy += v[j].y;
+      }
+      const float scale = a.scale != nullptr ? a.scale[tile.x] : 1.0f;
+      sx *= scale, sy *= scale;
+    }
+    uint32_t hi, lo;
+    split2(sx, sy, hi, lo);
+    // the lane and register that an MMA has the pair in
+    const int lane = (row & 7) * 4 + (col >> 1 & 3), reg = (row >> 3 & 1) + 2 * (col >> 3 & 1);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(ws.low) +
+                    ((((static_cast<int64_t>(t) * 4 + row / 16) * (kR / 16) + col / 16) * 2 * 32 + lane) * 4 + reg);
+    dst[0] = hi;
+    dst[32 * 4] = lo;
+  }
+}
+
+// ---------------------------------------------------------------- y = base + (x A^T) B^T
 
 // Where B's row of column c lies: the columns of MMA j of 32, which are 8 i + 2 j and
 // the next, one after another; and a piece of it, swizzled so that the 8 rows of an
@@ -385,16 +439,21 @@ __device__ __forceinline__ int b_row(int c) { return (c & ~31) + (c >> 1 & 3) * 
 // x A^T of 16 rows as the MMA's left operand, each value as two bf16 numbers.
 template <int kR>
 struct Low {
-  uint32_t hi[kR / 16][4], lo[kR / 16][4];
-  // h: float32 [rows][kR]; row: this thread's first
+  uint4 hi[kR / 16], lo[kR / 16];
+  // what the join wrote for these rows and this lane
+  __device__ __forceinline__ void load(const uint4* p) {
+#pragma unroll
+    for (int s = 0; s < kR / 16; ++s) hi[s] = __ldcg(p + 64 * s), lo[s] = __ldcg(p + 64 * s + 32);
+  }
+  // or h, float32 [rows][kR]; row: this thread's first
   __device__ __forceinline__ void load(const float* h, int row, int q) {
 #pragma unroll
     for (int s = 0; s < kR / 16; ++s) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = *reinterpret_cast<const float2*>(h + (row + 8 * (i & 1)) * kR + 16 * s + 8 * (i >> 1) + 2 * q);
-        split2(v.x, v.y, hi[s][i], lo[s][i]);
-      }
+      const float* p = h + row * kR + 16 * s + 2 * q;
+      split2(p[0], p[1], hi[s].x, lo[s].x);
+      split2(p[8 * kR], p[8 * kR + 1], hi[s].y, lo[s].y);
+      split2(p[8], p[9], hi[s].z, lo[s].z);
+      split2(p[8 * kR + 8], p[8 * kR + 9], hi[s].w, lo[s].w);
     }
   }
   // acc += x A^T B^T for 32 columns whose rows of B begin at `at`
@@ -405,10 +464,10 @@ struct Low {
       for (int j = 0; j < 4; j += 2) {
         uint32_t b[4];  // both halves of 16 values of r, for two MMAs
         ldmatrix4(b, at + b_place<kR>(j * 8 + (lane & 7) + (lane >> 4) * 8, 2 * s + (lane >> 3 & 1)));
-        mma_bf16_16816(acc[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], b[0], b[1]);
-        mma_bf16_16816(acc[j + 1], lo[s][0], lo[s][1], lo[s][2], lo[s][3], b[2], b[3]);
-        mma_bf16_16816(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], b[0], b[1]);
-        mma_bf16_16816(acc[j + 1], hi[s][0], hi[s][1], hi[s][2], hi[s][3], b[2], b[3]);
+        mma_bf16_16816(acc[j], lo[s].x, lo[s].y, lo[s].z, lo[s].w, b[0], b[1]);
+        mma_bf16_16816(acc[j + 1], lo[s].x, lo[s].y, lo[s].z, lo[s].w, b[2], b[3]);
+        mma_bf16_16816(acc[j], hi[s].x, hi[s].y, hi[s].z, hi[s].w, b[0], b[1]);
+        mma_bf16_16816(acc[j + 1], hi[s].x, hi[s].y, hi[s].z, hi[s].w, b[2], b[3]);
       }
     }
   }
@@ -737,9 +796,7 @@ struct Expand64 {
   static constexpr int kStages = 3;
   static constexpr int kBaseBytes = 64 * kUnit * 2;
   static constexpr int kStageBytes = kBaseBytes + kUnit * kR * 2;
-  static constexpr int kOddBytes = kWarps * 16 * kOddRow * 2;
-  static constexpr int kLow = 64 * kR * 4 > kOddBytes ? 64 * kR * 4 : kOddBytes;
-  static constexpr int kSmem = kStages * kStageBytes + kLow;
+  static constexpr int kSmem = kStages * kStageBytes + (joined(kR) ? 0 : 64 * kR * 4);
   static constexpr int kBaseChunks = kUnit / 8;             // 16-byte pieces of a row
   static constexpr int kBaseStep = kThreads / kBaseChunks;  // rows that the block copies at once
   static constexpr int kBases = 64 / kBaseStep;             // rows a thread copies
@@ -753,19 +810,19 @@ __global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
     expand64_kernel(const LoraArgs a, const Ws ws, int shrink_grid, int shrink_cols) {
   using C = Expand64<kR>;
   extern __shared__ __align__(128) uint8_t ring[];
-  float* h = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
+  __shared__ __align__(16) uint16_t odd_stage[kVec ? 8 : C::kWarps * 16 * kOddRow];
   const uint32_t ring_at = smem_u32(ring);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   // What comes before the wait reads the order of the rows, base and B, all complete
-  // when the first product's kernel began its own work.
+  // when the kernel before this one began its own work.
   const Rows rows{ws.tiles, ws.order};
   const int4 head = rows.tile(0);
   const int r = static_cast<int>(a.r), N = static_cast<int>(a.N), per_tile = (N - 1) / C::kUnit + 1;
   const int64_t units = static_cast<int64_t>(a.y == a.base ? head.x : head.y) * per_tile;
   const int64_t u0 = units * blockIdx.x / gridDim.x;
   const int todo = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u0);
-  const Shares sh = shares_of(static_cast<int>((a.K + shrink_cols - 1) / shrink_cols), head.x, shrink_grid);
 
+  const Shares sh = shares_of((static_cast<int>(a.K) - 1) / shrink_cols + 1, head.x, shrink_grid);
   Walk f, now;
   f.to(u0, per_tile);
   now = f;
@@ -827,7 +884,7 @@ __global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
   Low<kR> low;
   int4 tile;
   uint16_t* y[2];
-  OddRows odd{reinterpret_cast<uint16_t*>(h) + warp * 16 * kOddRow, -1};
+  OddRows odd{odd_stage + warp * 16 * kOddRow, -1};
   bool fresh = true;
   uint32_t slot = 0, ahead = (C::kStages - 1) * C::kStageBytes;
 #pragma unroll 1
@@ -846,11 +903,15 @@ __global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
         odd.m = row < tile.z ? rows.row(tile.y + row) : -1;
       }
       if (tile.x >= 0) {
-        add_shares<64, kR, 4>(h, a, ws.part, tile, head.z, sh.shares, threadIdx.x, C::kThreads);
-        __syncthreads();
-        low.load(h, row0, q);
-        if constexpr (!kVec) __syncthreads();  // the rows' stage lies there, too
-        // (the next tile's sums are written after the barrier of its first unit)
+        if constexpr (joined(kR)) {
+          low.load(ws.low + (static_cast<int64_t>(now.t) * 4 + (warp & 3)) * (kR / 16) * 64 + lane);
+        } else {
+          float* h = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
+          add_shares<64, kR, 4>(h, a, ws.part, tile, head.z, sh.shares, threadIdx.x, C::kThreads);
+          __syncthreads();
+          low.load(h, row0, q);
+          // (the next tile's sums are written after the barrier of its first unit)
+        }
       }
     }
     const int col0 = now.c * C::kUnit;
@@ -924,6 +985,11 @@ cudaError_t launch_64(const Ctx& c, const LoraArgs& a, const Ws& ws) {
   const int64_t grid = std::min({int64_t{220 * 1024 / S::kSmem} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
   e = launch_early(c, grid, kThreads, S::kSmem, shrink64_kernel<kR>, a, ws);
   if (e != cudaSuccess) return e;
+  if constexpr (joined(kR)) {
+    e = launch_early(c, std::min<int64_t>(tiles * (32 * kR / 256), 8 * c.sm_count), 256, 0, join_kernel<kR>, a, ws,
+                     static_cast<int>(grid), int{S::kCols});
+    if (e != cudaSuccess) return e;
+  }
   const int64_t grid2 = std::min<int64_t>(tiles * ((a.N - 1) / E::kUnit + 1), E::kFit * c.sm_count);
   const auto expand = [&](SmemLimit& limit, auto kern) {
     const cudaError_t err = raise_smem_limit(limit, kern, c.device, E::kSmem);
@@ -944,7 +1010,7 @@ cudaError_t launch_rank(const Ctx& c, const LoraArgs& a, const Ws& ws) {
 }  // namespace
 
 size_t lora_ws_bytes(int64_t M, int64_t n, int64_t r) {
-  return round16(16 * (1 + most_tiles(M, n))) + round16(4 * M) + part_bytes(M, r);
+  return round16(16 * (1 + most_tiles(M, n))) + round16(4 * M) + round16(part_bytes(M, r)) + low_bytes(M, n, r);
 }
 
 cudaError_t launch_lora(const Ctx& c, const LoraArgs& a) {
@@ -955,6 +1021,8 @@ cudaError_t launch_lora(const Ctx& c, const LoraArgs& a) {
   ws.order = reinterpret_cast<int32_t*>(p);
   p += round16(4 * a.M);
   ws.part = reinterpret_cast<float*>(p);
+  p += round16(part_bytes(a.M, a.r));
+  ws.low = reinterpret_cast<uint4*>(p);
   if (a.M > kFewRows) {
     GroupArgs g{};
     g.ids = a.adapter;
