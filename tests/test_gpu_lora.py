@@ -1,11 +1,10 @@
 """GPU checks of the low-rank adapters against the float64 oracle.
 
-Tolerance, per value: y's rounding 2^-8; the base's addition 2^-23 of its terms; the
-first product's K terms go 16 at a time into a float32 sum (each step at worst cut
-off, 2^-23), then at most 32 shares and 4 warps are added: (K / 16 + 40) 2^-23 of the
-terms' sizes, carried through B; its two bf16 numbers leave 2^-17, its scale 2^-24,
-and the second product has r / 8 + 2 such steps: 2^-17 + (r / 8 + 4) 2^-23 of its own
-terms' sizes."""
+Tolerance, per value: y's rounding 2^-8; the first product's K terms go 16 at a time
+into a float32 sum (each step at worst cut off, 2^-23), then at most 32 shares and 4
+warps are added: (K / 16 + 40) 2^-23 of the terms' sizes, carried through B; its two
+bf16 numbers leave 2^-17, its scale 2^-24; base begins the second product's sum, whose
+r / 8 steps are cut off likewise: (r / 8 + 4) 2^-23 of base's and the terms' sizes."""
 
 import threading
 
@@ -43,8 +42,8 @@ def ids_of(M, n, seed, none=0.15, each=1):
 
 
 def tolerance(want, first, second, base, K, r):
-    return (2.0 ** -8 * np.abs(want) + 2.0 ** -23 * (np.abs(base) + second) + (K / 16 + 40) * 2.0 ** -23 * first
-            + (2.0 ** -17 + (r / 8 + 4) * 2.0 ** -23) * second)
+    return (2.0 ** -8 * np.abs(want) + (K / 16 + 40) * 2.0 ** -23 * first + 2.0 ** -17 * second
+            + (r / 8 + 4) * 2.0 ** -23 * (np.abs(base) + second))
 
 
 def check(M, K, N, r, n, ids, scaled=True, base_wide=0, y_wide=0, x_wide=0, seed=0):
@@ -120,6 +119,17 @@ def test_infinite_and_nan_values(M):
     y = wq.lora_gemm(x, A, B, ids, base)
     assert bool((y[0] == float("inf")).all() and y[1].isnan().all() and (y[2] == float("inf")).all())
     assert torch.equal(y[3], base[3]) and bool(y[4:].isfinite().all())
+
+
+@pytest.mark.parametrize("M,N", [(5, 64), (5, 33), (700, 64), (700, 33)])
+def test_rows_without_an_adapter_are_copied_bit_by_bit(M, N):
+    """Every bf16 pattern (NaN payloads, infinities, -0.0) of base, beside rows with an adapter."""
+    K, r, n = 64, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    base = torch.randint(-2 ** 15, 2 ** 15, (M, N), generator=g, device="cuda", dtype=torch.int16).view(torch.bfloat16)
+    ids = torch.where(torch.arange(M, device="cuda") % 3 == 1, 1, -1).int()
+    y = wq.lora_gemm(rows((M, K), 1), rows((n, r, K), 2), rows((n, N, r), 3), ids, base)
+    assert torch.equal(y[ids < 0].view(torch.int16), base[ids < 0].view(torch.int16))
 
 
 def test_offsets_beyond_32_bits():

@@ -539,10 +539,13 @@ struct OddRows {
       begin_with(acc, i, make_uint4(p[0], p[1], p[2], p[3]));
     }
   }
-  __device__ __forceinline__ void write(const LoraArgs& a, int64_t col, int lane, const float (&acc)[4][4]) const {
+  // (without an adapter the stage holds what was read)
+  __device__ __forceinline__ void write(const LoraArgs& a, int64_t col, int lane, const float (&acc)[4][4],
+                                        bool adapted) const {
     const bool in = col + lane < a.N;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (!adapted) break;
       uint32_t* p = reinterpret_cast<uint32_t*>(stage + ((lane >> 2) + 8 * i) * kOddRow + 8 * (lane & 3));
       const uint4 v = rounded(acc, i);
       p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
@@ -726,9 +729,11 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
     const int col = now.c * kFewCols;
     // MMA j: its rows g and g + 8 are columns 8 g + 2 j and the next of y, its columns rows of y
     float acc[4][4];
+    uint4 was[2];  // base, as it is
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      uint4 v = make_uint4(0, 0, 0, 0);
+      uint4& v = was[i];
+      v = make_uint4(0, 0, 0, 0);
       if constexpr (kVec) {
         v = *reinterpret_cast<const uint4*>(own_base + slot + i * 512);
       } else if (base[i] != nullptr) {
@@ -769,9 +774,11 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (y[i] == nullptr) continue;
-      uint32_t o[4];
+      uint32_t o[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
+      if (tile.x >= 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = pack2(acc[j][i], acc[j][2 + i]);
+        for (int j = 0; j < 4; ++j) o[j] = pack2(acc[j][i], acc[j][2 + i]);
+      }
       if constexpr (kVec) {
         if (col + 8 * g < N) *reinterpret_cast<uint4*>(y[i] + col) = make_uint4(o[0], o[1], o[2], o[3]);
       } else {
@@ -934,10 +941,15 @@ __global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
       if (tile.x >= 0) low.times(ring_at + slot + C::kBaseBytes + c0 * (2 * kR), acc, lane);
       if constexpr (kVec) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (y[i] != nullptr && col + 8 * q < N) *reinterpret_cast<uint4*>(y[i] + col) = rounded(acc, i);
+        for (int i = 0; i < 2; ++i) {
+          if (y[i] == nullptr || col + 8 * q >= N) continue;
+          const int row = row0 + 8 * i;
+          *reinterpret_cast<uint4*>(y[i] + col) =
+              tile.x >= 0 ? rounded(acc, i)
+                          : *reinterpret_cast<const uint4*>(stage + row * (2 * C::kUnit) + (((c0 / 8 + q) ^ (row & 1) << 2) << 4));
+        }
       } else {
-        odd.write(a, col, lane, acc);
+        odd.write(a, col, lane, acc, tile.x >= 0);
       }
     }
     fresh = now.next(per_tile);
