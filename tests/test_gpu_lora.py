@@ -241,16 +241,29 @@ def test_same_bits_captured_on_another_stream_and_from_threads():
     assert not errors and wrong == [0] * len(jobs), (errors, wrong)
 
 
-def test_a_captured_call_with_other_adapters():
-    M, K, N, r, n = 48, 512, 264, 16, 12
-    x, A, B, base = rows((M, K), 1), rows((n, r, K), 2, K ** -0.5), rows((n, N, r), 3), rows((M, N), 4)
-    ids = dev(ids_of(M, n, 5))
-    wq.lora_gemm(x, A, B, ids, base)
+@pytest.mark.parametrize("M,r", [(48, 16), (48, 32), (200, 16), (700, 16), (700, 64)])
+def test_inputs_changed_between_calls(M, r):
+    """Every input is written anew before each call and each replay: what a call reads before the kernel in front of it
+    ends is what was there when the call began."""
+    K, N, n = 512, 264, 12
+    made = lambda seed: [rows((M, K), seed), rows((n, r, K), seed + 1, K ** -0.5), rows((n, N, r), seed + 2, r ** -0.5),  # noqa: E731
+                         dev(ids_of(M, n, seed + 3, none=0.2)), rows((M, N), seed + 4),
+                         torch.rand(n, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")]
+    use = made(0)
+    call = lambda t, **kw: wq.lora_gemm(t[0], t[1], t[2], t[3], t[4], scale=t[5], **kw)  # noqa: E731
+    call(use)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        y = wq.lora_gemm(x, A, B, ids, base)
-    for seed in range(5):
-        ids.copy_(dev(ids_of(M, n, 10 + seed, none=0.3 * seed)))
-        x.copy_(rows((M, K), 20 + seed))
-        graph.replay()
-        assert torch.equal(y, wq.lora_gemm(x, A, B, ids, base))
+        y = call(use)
+    sets = [made(10 * (i + 1)) for i in range(4)]
+    want = [call(t) for t in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for new, w in zip(sets, want):
+            for a, b in zip(use, new):
+                a.copy_(b)
+            got = call(use)
+            graph.replay()
+            again = y.clone()
+            in_place = call(use, y=use[4])
+            assert torch.equal(got, w) and torch.equal(again, w) and torch.equal(in_place, w)

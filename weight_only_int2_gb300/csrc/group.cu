@@ -8,7 +8,8 @@
 // other by votes on its bits, so nothing depends on the order of atomics; the
 // instruction that matches whole numbers is far slower), the rows and the blocks are
 // summed up, and what was counted before an entry is its place. Few entries take one block; more take a cluster of 8 that exchange their
-// counts through distributed shared memory.
+// counts through distributed shared memory. 65536 ids of 128 experts: about 7 us of a
+// sort's 121 (by matches 13).
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"

@@ -2,19 +2,24 @@
 //   base[m] + scale[a] (x[m] A[a]^T) B[a]^T,   a = adapter[m],
 // and base[m] for a row without an adapter.
 //
-// Three kernels. The rows are grouped by adapter into tiles (group.cu), so that every
-// A and B is read by few blocks. The first product contracts over K: a block takes a
-// tile and a share of K (as many shares as it takes to fill the GPU, a rule on the
-// number of tiles, which is on the device) through a ring of cp.async stages into
-// warp MMAs, and writes float32 partial sums. The second adds the shares up in their
-// order, scales, and takes a tile and a run of columns: x A^T stays in registers as
-// two bf16 numbers a value (2^-17 of itself; one would cost the sum bf16's 2^-9 once
-// more), B comes straight from memory in the MMA's layout, and base and y are read
-// and written 16 bytes a thread: the columns of four MMAs are dealt out so that a
-// thread holds 8 in a row.
+// Two products, with the rows grouped by adapter into tiles, so that every A and B is
+// read by few blocks (up to 128 rows each block groups them itself, more are grouped
+// by a launch before, group.cu). x A^T stays as two bf16 numbers a value on its way
+// into the second product (2^-17 of itself; one would cost the sum bf16's 2^-8 once
+// more), whose sums begin with base, float32 until y is rounded.
+//  - The first contracts over K: a block takes a tile and a share of K, as many shares
+//    as it takes to fill the GPU (a rule on the number of tiles, which is on the
+//    device), and writes float32 partial sums.
+//  - The second adds them up in their order, scales, and takes a tile and some of the
+//    columns; base and y are read and written 16 bytes a thread: the columns of four
+//    MMAs are dealt out so that a thread holds 8 in a row.
 //
-// Bound: HBM. With r up to 64 the MMAs take less time than base and y do; what a
-// decode batch reads is each adapter's A and B once.
+// Bound: HBM, where there is enough to read. 8192 rows, K 5120, N 17408, r 16, 658 MB:
+// 115 us, 5.7 TB/s (the second product 91 us of it; three blocks an SM instead of two
+// 145, since more places in base and y are open at once); r 64 146 us and r 128 270,
+// where the MMAs take as long as memory does (twice, for the two numbers a value). 64
+// rows of 41 adapters, 40 MB: 14.5 us, the chain rows -> order -> A, x -> sums -> B,
+// twice a launch. One row: 4.8 us.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
@@ -95,7 +100,7 @@ __device__ __forceinline__ Shares shares_of(int stages, int tiles, int grid) {
 // ---------------------------------------------------------------- rows by adapter
 
 // What both products know of the rows' order: as launch_group wrote it, or of few
-// rows in shared memory, found by the block itself (a launch less; 64 rows take ..).
+// rows in shared memory, found by the block itself (a launch less).
 struct Few {
   int key[kFewRows];      // (adapter, row) by row
   int id[kFewRows + 1];   // adapters by place; id[0]: none
