@@ -1,7 +1,8 @@
 """GB300 (sm_103a) weight-only quantized linear layers: WNA16 for 2..8-bit
 codes, W4A8, and the quantized-embedding gather, with the serving operators
 around them (paged key-value cache, decode attention, token log
-probabilities), behind the C ABI of libwq.so.
+probabilities), the router and rows of a mixture of experts with their gradients
+and low-rank adapters, behind the C ABI of libwq.so.
 
 The Python functions here marshal arguments into that ABI; all arithmetic runs
 in the library's CUDA kernels.
