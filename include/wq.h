@@ -495,7 +495,8 @@ size_t lora_workspace_bytes(int64_t M, int64_t n, int64_t r);
  *              N), 2-byte aligned: they may be columns of a fused projection (where
  *              both are 16-byte aligned and N and the strides multiples of 8, 16
  *              bytes are moved at a time). y may be base itself, with the same
- *              stride, and must not overlap anything else.
+ *              stride, and must not overlap anything else (columns beside base's or
+ *              x's in rows of the same stride do not; an overlap of these is refused).
  *  workspace   as kv_attn_decode's.
  * The result's bits do not depend on timing; a row's may depend on how many rows
  * each adapter has in the call. M >= 0 (M = 0 enqueues nothing). */

@@ -241,7 +241,7 @@ def test_same_bits_captured_on_another_stream_and_from_threads():
     assert not errors and wrong == [0] * len(jobs), (errors, wrong)
 
 
-@pytest.mark.parametrize("M,r", [(48, 16), (48, 32), (200, 16), (700, 16), (700, 64)])
+@pytest.mark.parametrize("M,r", [(48, 16), (48, 32), (200, 16), (700, 16), (700, 64), (1500, 16)])
 def test_inputs_changed_between_calls(M, r):
     """Every input is written anew before each call and each replay: what a call reads before the kernel in front of it
     ends is what was there when the call began."""

@@ -159,8 +159,8 @@ def test_combine_refusals(lib, p):
 def test_lora_refusals(lib, p):
     need = lib.lora_workspace_bytes(3, 2, 16)
     assert need > 0 and lib.lora_workspace_bytes(0, 2, 16) == 0 and lib.lora_workspace_bytes(3, 2, 256) == 0
-    ok = dict(x=p, xs=64, M=3, K=64, A=p, B=p, n=2, r=16, N=40, adapter=p, scale=None, base=p, bs=40, y=p + 4096, ys=40,
-              ws=p, wsb=need, stream=None)
+    ok = dict(x=p + 16384, xs=64, M=3, K=64, A=p, B=p, n=2, r=16, N=40, adapter=p, scale=None, base=p, bs=40, y=p + 4096,
+              ys=40, ws=p, wsb=need, stream=None)
     refused(lib, "lora_gemm", ok, [
         (dict(x=None), 1, "x is NULL"), (dict(x=p + 8), 1, "x is not 16"), (dict(xs=56), 1, "x_stride"), (dict(xs=68), 1, "x_stride"),
         (dict(M=-1), 1, "M must"), (dict(K=0), 1, "K must"), (dict(K=60), 1, "K must"), (dict(N=0), 1, "N must"),
@@ -169,8 +169,17 @@ def test_lora_refusals(lib, p):
         (dict(adapter=None), 1, "adapter is NULL"), (dict(adapter=p + 2), 1, "adapter is not 4"), (dict(scale=p + 2), 1, "scale is not 4"),
         (dict(base=None), 1, "base is NULL"), (dict(base=p + 1), 1, "base is not 2"), (dict(bs=39), 1, "base_stride"),
         (dict(y=None), 1, "y is NULL"), (dict(ys=39), 1, "y_stride"), (dict(y=p, ys=48), 1, "y is base"),
+        (dict(y=p + 2), 1, "y must be base"), (dict(y=p + 80), 1, "y must be base"), (dict(y=p + 80, ys=48), 1, "y must be base"),
+        (dict(bs=100, y=p + 78, ys=100), 1, "y must be base"), (dict(bs=100, y=p + 122, ys=100), 1, "y must be base"),
+        (dict(base=p + 80, bs=100, y=p + 202, ys=100), 1, "y must be base"), (dict(y=p + 16384), 1, "y must not overlap x"),
+        (dict(y=p + 16384 - 2), 1, "y must not overlap x"), (dict(y=p + 16384 + 2 * (2 * 64 + 63)), 1, "y must not overlap x"),
         (dict(ws=None), 1, "workspace is NULL"), (dict(wsb=need - 1), 1, "workspace too small"), (dict(ws=p + 8), 1, "workspace is not 16")])
     assert lib.lora_gemm(*{**ok, "M": 0, "x": None, "y": None}.values()) == 0
+    # side by side in one buffer, or one behind the other: the next check is reached
+    refused(lib, "lora_gemm", {**ok, "ws": None}, [
+        (kw, 1, "workspace is NULL") for kw in (dict(y=p), dict(y=p + 240), dict(base=p + 240, y=p), dict(bs=100, y=p + 80, ys=100),
+                                                dict(bs=100, y=p + 120, ys=100), dict(base=p + 80, bs=100, y=p, ys=100),
+                                                dict(xs=128, y=p + 16384 + 128, ys=128), dict(y=p + 16384 - 240))])
 
 
 def test_binding_refuses_cpu_tensors():

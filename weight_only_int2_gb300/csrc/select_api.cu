@@ -46,6 +46,19 @@ wq_status check_16bit(const void* p, const char* name) {
   return WQ_OK;
 }
 
+// Whether two 2-byte matrices of `rows` rows share a value; side by side in rows of
+// one stride (columns of one buffer) they do not.
+bool share_values(const void* p, int64_t p_stride, int64_t p_cols, const void* q, int64_t q_stride, int64_t q_cols,
+                  int64_t rows) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t a_end = a + 2 * ((rows - 1) * p_stride + p_cols), b_end = b + 2 * ((rows - 1) * q_stride + q_cols);
+  if (a >= b_end || b >= a_end) return false;
+  if (p_stride != q_stride || ((a ^ b) & 1) != 0) return true;
+  const int64_t apart = static_cast<int64_t>(a < b ? b - a : a - b) / 2 % p_stride;  // from the lower one's row
+  const int64_t lower = a < b ? p_cols : q_cols, higher = a < b ? q_cols : p_cols;
+  return apart < lower || apart + higher > p_stride;
+}
+
 }  // namespace
 }  // namespace wq
 
@@ -181,6 +194,9 @@ wq_status lora_gemm(const wq_bf16* x, int64_t x_stride, int64_t M, int64_t K, co
   if (y == base && y_stride != base_stride)
     return fail(WQ_EINVAL, "y is base: y_stride must be base_stride (got %lld and %lld)", (long long)y_stride,
                 (long long)base_stride);
+  if (y != base && share_values(base, base_stride, N, y, y_stride, N, M))
+    return fail(WQ_EINVAL, "y must be base or must not overlap it");
+  if (share_values(x, x_stride, K, y, y_stride, N, M)) return fail(WQ_EINVAL, "y must not overlap x");
   WQ_TRY(check_space(workspace, ws_bytes, lora_ws_bytes(M, n, r), "workspace"));
   Ctx c{};
   WQ_TRY(get_ctx(stream, &c));
