@@ -52,7 +52,8 @@ def f64(t):
 
 @pytest.mark.parametrize("T,k,E,out_of", [
     (1, 1, 1, 0), (1, 8, 128, 0), (3, 2, 4, 0.3), (64, 8, 128, 0), (64, 8, 1024, 0.1), (33, 1, 1, 0), (31, 32, 3, 0.5),
-    (100, 6, 7, 1.0), (1024, 8, 64, 0), (2048, 1, 1024, 0.2), (2731, 3, 256, 0.05), (1366, 6, 160, 0), (20000, 8, 1024, 0.1),
+    (100, 6, 7, 1.0), (1024, 8, 64, 0), (2048, 1, 1024, 0.2), (2731, 3, 256, 0.05), (1366, 6, 160, 0), (700, 4, 50, 0.1), (4096, 1, 1024, 0.1), (4097, 1, 8, 0),
+    (20000, 8, 1024, 0.1),
     (8193, 1, 1, 0.5), (70001, 2, 333, 0)])
 @pytest.mark.parametrize("skew", [False, True])
 def test_sort_places(T, k, E, out_of, skew):

@@ -445,7 +445,7 @@ __device__ __forceinline__ float eight_sums(const float (&v)[8]);
 // Few choices: a token's blocks find its places themselves, each the number of
 // choices that come before by (expert, choice), and one more block counts the
 // experts' (a launch less: 64 tokens of 8 choices of 5120 2.9 us, with one 5.2; 256
-// tokens 8.0, and 257 in two launches 10.5).
+// tokens 8.0, and 257 in two launches 9.6).
 constexpr int kFewChoices = 2048;
 
 template <bool kOdd>
