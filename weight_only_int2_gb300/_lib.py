@@ -859,12 +859,7 @@ def lora_workspace_bytes(M: int, n: int, r: int) -> int:
     return int(load().lora_workspace_bytes(M, n, r))
 
 
-def lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor, base: torch.Tensor,
-              scale: torch.Tensor | None = None, y: torch.Tensor | None = None,
-              ws: torch.Tensor | None = None) -> torch.Tensor:
-    """y[m] = base[m] + scale[a] * (x[m] . A[a]^T) . B[a]^T with a = adapter[m] (int32; -1: none, y[m] = base[m]).
-    x [M, K], base and y [M, N] bf16 (rows may be strided; y may be base), A [n, r, K], B [n, N, r] bf16, scale [n]
-    float32. base is the shared projection's output, such as wna16_gemm(x, ..)."""
+def _check_lora(x, A, B, adapter, base):
     dev = _tensors((A, "A"), (B, "B"), (adapter, "adapter"))
     As, Bs = A.shape, B.shape
     if len(As) != 3 or len(Bs) != 3:
@@ -878,6 +873,30 @@ def lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.
     if not _plain(adapter, _I32, (M,), dev):
         _need_at(adapter, "adapter", torch.int32, (M,))
     xs, bs = _need_matrix(x, "x", (M, K)), _need_matrix(base, "base", (M, N))
+    return n, r, K, N, M, xs, bs
+
+
+def lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.Tensor, base: torch.Tensor,
+              scale: torch.Tensor | None = None, y: torch.Tensor | None = None,
+              ws: torch.Tensor | None = None) -> torch.Tensor:
+    """y[m] = base[m] + scale[a] * (x[m] . A[a]^T) . B[a]^T with a = adapter[m] (int32; -1: none, y[m] = base[m]).
+    x [M, K], base and y [M, N] bf16 (rows may be strided; y may be base), A [n, r, K], B [n, N, r] bf16, scale [n]
+    float32. base is the shared projection's output, such as wna16_gemm(x, ..)."""
+    try:  # (as _plain and _need_matrix, in one go: this call has the most tensors)
+        (n, r, K), (_, N, _), (M,), dev = A.shape, B.shape, adapter.shape, _device()
+        (xs, x1), (bs, b1) = x.stride(), base.stride()
+        good = (A.dtype is _BF16 and B.dtype is _BF16 and x.dtype is _BF16 and base.dtype is _BF16 and adapter.dtype is _I32
+                and B.shape == (n, N, r) and x.shape == (M, K) and base.shape == (M, N) and x1 == 1 and b1 == 1 and M > 0
+                and A.get_device() == dev and B.get_device() == dev and x.get_device() == dev
+                and base.get_device() == dev and adapter.get_device() == dev and A.is_contiguous()
+                and B.is_contiguous() and adapter.is_contiguous())
+        if M == 1:
+            xs, bs = K, N
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        good = False
+    if not good:
+        n, r, K, N, M, xs, bs = _check_lora(x, A, B, adapter, base)
+        dev = _device()
     if scale is not None and not _plain(scale, _F32, (n,), dev):
         _need_at(scale, "scale", torch.float32, (n,))
     if y is None:
