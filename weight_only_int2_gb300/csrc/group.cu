@@ -7,9 +7,9 @@
 // run of entries in its own row of counters (the lanes that share an id find each
 // other by votes on its bits, so nothing depends on the order of atomics; the
 // instruction that matches whole numbers is far slower), the rows and the blocks are
-// summed up, and what was counted before an entry is its place. Few entries take one block; more take a cluster of 8 that exchange their
-// counts through distributed shared memory. 65536 ids of 128 experts: about 7 us of a
-// sort's 121 (by matches 13).
+// summed up, and what was counted before an entry is its place. Few entries take one
+// block; more take a cluster of 8 that exchange their counts through distributed
+// shared memory. 65536 ids of 128 experts: about 7 us of a sort's 121 (by matches 13).
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
@@ -158,7 +158,7 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) grou
     at += all[i];
   }
   if (a.tiles != nullptr && rank == 0) {
-    const int t0 = (all[0] + a.tile - 1) / a.tile, t1 = (all[1] + a.tile - 1) / a.tile;
+    const int t0 = all[0] / a.tile + (all[0] % a.tile != 0), t1 = all[1] / a.tile + (all[1] % a.tile != 0);
     int tiles;
     const int tb = block_scan(t0, t1, warp_sum, &tiles);
     if (2 * threadIdx.x < E1) tile0[2 * threadIdx.x] = tb;

@@ -85,8 +85,8 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&d)[4], uint32_t addr) {
                : "memory");
 }
 
-// How K is shared among blocks: `shares` of `per` stages each. (Shares are added up
-// 16 at a time: beyond 16 they have four stages at least.)
+// How K is shared among blocks: `shares` of `per` stages each. (Shares are added up a
+// few at a time: beyond 16 they have four stages at least.)
 struct Shares {
   int shares, per;
 };
