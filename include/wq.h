@@ -465,7 +465,8 @@ wq_status moe_sort(const wq_bf16* x, int64_t x_stride, int64_t T, int64_t D, con
  *   out[t] = (residual[t] +) sum_j weights[t, j] * y[slots[t, j]],
  * float32 in the order of j, rounded to bf16 once. A choice without a row adds
  * nothing, whatever its weight.
- *  y           [R, D] bf16.       weights  [T, k] float32, or NULL: all 1.
+ *  y           [R, D] bf16, R >= 1 (R = 0 is taken with T = 0).
+ *  weights     [T, k] float32, or NULL: all 1.
  *  residual    [T, D] bf16, or NULL; out may be residual itself.
  *  out         [T, D] bf16. */
 wq_status moe_combine(const wq_bf16* y, int64_t R, const int32_t* slots, const float* weights,

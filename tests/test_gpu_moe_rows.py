@@ -199,6 +199,17 @@ def test_no_tokens():
     assert not wq.moe_sort(None, ids, 9)[1].any()
 
 
+def test_no_tokens_from_the_sort_to_the_gradients():
+    ids = torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.empty((0, 4), device="cuda")
+    out, _, slots = wq.moe_sort(x, ids, 9)
+    assert wq.moe_combine(out, slots, w, x).shape == (0, 64)
+    dy, dw = wq.moe_combine_grad(x, out, slots, w)
+    assert dy.shape == (0, 64) and dw.shape == (0, 4)
+    assert wq.moe_combine(dy, slots).shape == (0, 64)
+
+
 def test_same_bits_every_time_and_on_another_stream():
     T, k, E, D = 3000, 6, 64, 512
     ids, x = dev(choices(T, k, E, 1, 0.1)), rows((T, D), 2)

@@ -156,6 +156,15 @@ def test_combine_refusals(lib, p):
     assert lib.moe_combine_grad(*{**ok, "T": 0, "y": None, "dy": None}.values()) == 0
 
 
+def test_no_tokens_after_a_sort_of_none(lib, p):
+    # what moe_sort gives for no tokens has no rows
+    assert lib.moe_combine(None, 0, None, None, None, 0, 64, 2, None, None) == 0
+    assert lib.moe_combine_grad(None, None, 0, None, None, 0, 64, 2, None, None, None) == 0
+    for n in (-1, 1 << 31):
+        assert lib.moe_combine(p, n, p, p, p, 0, 64, 2, p, None) == 1 and b"R must" in lib.wq_last_error()
+        assert lib.moe_combine_grad(p, p, n, p, p, 0, 64, 2, p, p, None) == 1 and b"R must" in lib.wq_last_error()
+
+
 def test_lora_refusals(lib, p):
     need = lib.lora_workspace_bytes(3, 2, 16)
     assert need > 0 and lib.lora_workspace_bytes(0, 2, 16) == 0 and lib.lora_workspace_bytes(3, 2, 256) == 0

@@ -21,6 +21,9 @@ wq_status check_experts(int64_t E) {
   return WQ_OK;
 }
 
+// R sorted rows: none only where no token is (what moe_sort gives for none).
+wq_status check_rows(int64_t R, int64_t T) { return R == 0 && T == 0 ? WQ_OK : check_size(R, "R"); }
+
 wq_status check_stride(int64_t stride, int64_t least, const char* name) {
   if (stride < least || stride > kMaxDim)
     return fail(WQ_EINVAL, "%s must be in %lld..2^31-1 (got %lld)", name, (long long)least, (long long)stride);
@@ -129,7 +132,7 @@ wq_status moe_combine(const wq_bf16* y, int64_t R, const int32_t* slots, const f
   clear_error();
   WQ_TRY(check_choices(T, k));
   WQ_TRY(check_size(D, "D"));
-  WQ_TRY(check_size(R, "R"));
+  WQ_TRY(check_rows(R, T));
   if (T == 0) return WQ_OK;
   WQ_PTR(y);
   WQ_PTR32(slots);
@@ -148,7 +151,7 @@ wq_status moe_combine_grad(const wq_bf16* dout, const wq_bf16* y, int64_t R, con
   clear_error();
   WQ_TRY(check_choices(T, k));
   WQ_TRY(check_size(D, "D"));
-  WQ_TRY(check_size(R, "R"));
+  WQ_TRY(check_rows(R, T));
   if (T == 0) return WQ_OK;
   WQ_PTR(dout);
   WQ_PTR(y);
