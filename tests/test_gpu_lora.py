@@ -267,3 +267,37 @@ def test_inputs_changed_between_calls(M, r):
             again = y.clone()
             in_place = call(use, y=use[4])
             assert torch.equal(got, w) and torch.equal(again, w) and torch.equal(in_place, w)
+
+
+@pytest.mark.parametrize("r", [40, 64, 96, 128])
+@pytest.mark.parametrize("M,K,N,n,base_wide,y_wide", [
+    (512, 64, 8, 1, 0, 0), (513, 128, 1000, 3, 0, 16), (700, 256, 333, 5, 3, 0), (900, 136, 72, 700, 8, 7), (2100, 72, 1416, 4, 64, 0)])
+def test_larger_ranks_of_many_rows(M, K, N, n, base_wide, y_wide, r):
+    check(M, K, N, r, n, ids_of(M, n, M + r, each=1 + M // 100), base_wide=base_wide, y_wide=y_wide, seed=M + r)
+
+
+@pytest.mark.parametrize("N", [200, 201])
+@pytest.mark.parametrize("r", [64, 128])
+def test_larger_ranks_of_out_of_range_infinite_and_other_inputs(N, r):
+    M, K, n = 700, 128, 3
+    ids = ids_of(M, n, M)
+    ids[::4] = np.resize(np.array([3, 1024, 2 ** 31 - 1, -2 ** 31, -2], np.int32), ids[::4].size)
+    check(M, K, N, r, n, ids, seed=N)
+    check(M, K, N, r, n, np.full(M, -1, np.int32), seed=N)
+    x, A, B = rows((M, K), 1), rows((n, r, K), 2).abs() + 0.1, rows((n, N, r), 3).abs() + 0.1
+    x[0], x[1, 5], x[2], x[3] = float("inf"), float("nan"), 1e38, float("nan")
+    base, ids = rows((M, N), 4), torch.zeros(M, dtype=torch.int32, device="cuda")
+    ids[3] = -1
+    y = wq.lora_gemm(x, A, B, ids, base)
+    assert bool((y[0] == float("inf")).all() and y[1].isnan().all() and (y[2] == float("inf")).all())
+    assert torch.equal(y[3], base[3]) and bool(y[4:].isfinite().all())
+    # the same bits again, on two streams at once
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for s in (one, two):
+            with torch.cuda.stream(s):
+                got.append(wq.lora_gemm(x, A, B, ids, base))
+        torch.cuda.synchronize()
+        assert all(torch.equal(v.view(torch.int16), y.view(torch.int16)) for v in got)

@@ -23,6 +23,7 @@
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
+#include "wq_tc.cuh"
 
 #include <cuda_bf16.h>
 
@@ -49,7 +50,7 @@ struct Ws {
   int4* tiles;     // as launch_group writes them
   int32_t* order;  // [M] the row at each place
   float* part;     // [shares][rows with an adapter][r]
-  uint4* low;      // many rows: x A^T as the second product's MMAs read it, [tiles][4][r / 16][2][32]
+  uint4* low;      // many rows: x A^T as the second product's MMAs read it, [tiles][r / 64][128][8]
 };
 int64_t most_tiles(int64_t M, int64_t n) { return M / tile_of(M) + std::min(M, n + 1); }
 size_t part_bytes(int64_t M, int64_t r) {
@@ -383,6 +384,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack2(fabsf(xh) < INFINITY ? x - xh : 0.0f, fabsf(yh) < INFINITY ? y - yh : 0.0f);
 }
 
+// Where the descriptors of the tensor cores have 16 bytes of a row of kRows: rows of 128
+// bytes, swizzled by their number; the ranks from 64 on lie behind all rows.
+template <int kRows>
+__device__ __forceinline__ uint32_t tile_place(int row, int chunk) {
+  return ((chunk >> 3) * kRows + row) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
 // Many rows, larger ranks: the shares added up in their order, scaled and written as
 // the MMAs of the second product read them, so that its blocks, which come to a tile
 // many times, find them ready (2049 rows, r 64, K 17408, 8 shares: 42 us for the call,
@@ -420,12 +428,10 @@ __global__ void __launch_bounds__(256) join_kernel(const LoraArgs a, const Ws ws
     }
     uint32_t hi, lo;
     split2(sx, sy, hi, lo);
-    // the lane and register that an MMA has the pair in
-    const int lane = (row & 7) * 4 + (col >> 1 & 3), reg = (row >> 3 & 1) + 2 * (col >> 3 & 1);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(ws.low) +
-                    ((((static_cast<int64_t>(t) * 4 + row / 16) * (kR / 16) + col / 16) * 2 * 32 + lane) * 4 + reg);
-    dst[0] = hi;
-    dst[32 * 4] = lo;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(ws.low + static_cast<int64_t>(t) * (64 * kR / 4)) +
+                   tile_place<128>(row / 16 * 32 + row % 16, col >> 3) + 2 * (col & 7);
+    *reinterpret_cast<uint32_t*>(dst) = hi;
+    *reinterpret_cast<uint32_t*>(dst + 16 * 128) = lo;  // (the 17th row from there is swizzled alike)
   }
 }
 
@@ -445,12 +451,7 @@ __device__ __forceinline__ int b_row(int c) { return (c & ~31) + (c >> 1 & 3) * 
 template <int kR>
 struct Low {
   uint4 hi[kR / 16], lo[kR / 16];
-  // what the join wrote for these rows and this lane
-  __device__ __forceinline__ void load(const uint4* p) {
-#pragma unroll
-    for (int s = 0; s < kR / 16; ++s) hi[s] = __ldcg(p + 64 * s), lo[s] = __ldcg(p + 64 * s + 32);
-  }
-  // or h, float32 [rows][kR]; row: this thread's first
+  // h: float32 [rows][kR]; row: this thread's first
   __device__ __forceinline__ void load(const float* h, int row, int q) {
 #pragma unroll
     for (int s = 0; s < kR / 16; ++s) {
@@ -804,16 +805,16 @@ template <int kR>
 struct Expand64 {
   static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kUnit = kR == 128 ? 64 : 128;  // columns of a stage
+  static constexpr int kUnit = 128;  // columns of a stage
   static constexpr int kStages = 3;
   static constexpr int kBaseBytes = 64 * kUnit * 2;
   static constexpr int kStageBytes = kBaseBytes + kUnit * kR * 2;
-  static constexpr int kSmem = kStages * kStageBytes + (joined(kR) ? 0 : 64 * kR * 4);
+  static constexpr int kSmem = kStages * kStageBytes + 64 * kR * 4;
   static constexpr int kBaseChunks = kUnit / 8;             // 16-byte pieces of a row
   static constexpr int kBaseStep = kThreads / kBaseChunks;  // rows that the block copies at once
   static constexpr int kBases = 64 / kBaseStep;             // rows a thread copies
   static constexpr int kBs = kUnit * (kR / 8) / kThreads;   // pieces of B a thread copies
-  static constexpr int kFit = kR <= 64 ? 2 : 1;
+  static constexpr int kFit = 2;
   static_assert(kFit * (kSmem + 1024) <= 228 * 1024, "");
 };
 
@@ -915,15 +916,11 @@ __global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
         odd.m = row < tile.z ? rows.row(tile.y + row) : -1;
       }
       if (tile.x >= 0) {
-        if constexpr (joined(kR)) {
-          low.load(ws.low + (static_cast<int64_t>(now.t) * 4 + (warp & 3)) * (kR / 16) * 64 + lane);
-        } else {
-          float* h = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
-          add_shares<64, kR, 4>(h, a, ws.part, tile, head.z, sh.shares, threadIdx.x, C::kThreads);
-          __syncthreads();
-          low.load(h, row0, q);
-          // (the next tile's sums are written after the barrier of its first unit)
-        }
+        float* h = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
+        add_shares<64, kR, 4>(h, a, ws.part, tile, head.z, sh.shares, threadIdx.x, C::kThreads);
+        __syncthreads();
+        low.load(h, row0, q);
+        // (the next tile's sums are written after the barrier of its first unit)
       }
     }
     const int col0 = now.c * C::kUnit;
@@ -964,6 +961,240 @@ __global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
   }
 }
 
+// Tiles of 64 rows, larger ranks: the same on the tcgen05 tensor cores. The two numbers
+// of a value are two of an MMA's 128 rows (16 rows' higher ones, their lower ones, the
+// next 16 ..), so that a warp finds both sums of its rows in its own lanes of tensor
+// memory, and reads them as its own MMAs would hold them: base, y and the order of the
+// columns are as above. What a block waits for (loads, MMAs, sums) the others on its SM
+// cover, or its 16 warps: 8192 rows, K 5120, N 17408: r 64 139 us (two blocks 140), r 128
+// 173 (two blocks of 8 warps and 64 columns 179); finishing a unit while the next one's
+// MMAs run, which costs a stage, 144 and 176; the numbers as separate MMAs of 64 rows
+// 144 and 189; by mma.sync 146 and 270. 2049 rows, K 17408, N 5120, r 64: 40.5 us and 42.
+template <int kR, bool kVec>
+struct ExpandMany {
+  static constexpr int kUnit = kR == 64 ? 64 : 128;  // columns of a stage
+  static constexpr int kFit = kR == 64 ? 3 : 1;
+  static constexpr int kStages = kR == 64 ? 3 : 4;
+  static constexpr int kWarps = kUnit / 8;  // 16 rows and 32 columns each
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kOdds = kVec ? 8 : kWarps * 16 * kOddRow;
+  static constexpr int kBaseBytes = kVec ? 64 * kUnit * 2 : 0;  // (rows at any address are read later)
+  static constexpr int kStageBytes = kBaseBytes + kUnit * kR * 2;
+  static constexpr int kLowBytes = 64 * kR * 4;
+  static constexpr int kSmem = 1024 + kLowBytes + kStages * kStageBytes;
+  static constexpr int kBaseChunks = kUnit / 8;             // 16-byte pieces of a row
+  static constexpr int kBaseStep = kThreads / kBaseChunks;  // rows that the block copies at once
+  static constexpr int kBases = 64 / kBaseStep;             // rows a thread copies
+  static constexpr int kBs = kUnit * (kR / 8) / kThreads;   // pieces of B a thread copies
+  static constexpr int kLows = kLowBytes / 16 / kThreads;   // and of x A^T
+  static_assert(kFit * kUnit <= 512 && kFit * (kSmem + 2 * kOdds + 1024 + 64) <= 228 * 1024, "");
+};
+
+// 16 lanes by 32 columns of tensor memory, as the sums of four MMAs of a warp's own.
+__device__ __forceinline__ void tmem_ld_sums(uint32_t at, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(at));
+}
+
+template <int kR, bool kVec>
+__global__ void __launch_bounds__(ExpandMany<kR, kVec>::kThreads, ExpandMany<kR, kVec>::kFit)
+    expand_many_kernel(const LoraArgs a, const Ws ws, unsigned* status) {
+  using C = ExpandMany<kR, kVec>;
+  extern __shared__ uint8_t smem[];
+  __shared__ __align__(16) uint16_t odd_stage[C::kOdds];
+  __shared__ uint64_t done;  // a unit's MMAs
+  __shared__ uint32_t tmem_at;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const uint32_t skip = -smem_u32(smem) & 1023;
+  uint4* const low = reinterpret_cast<uint4*>(smem + skip);
+  uint8_t* const ring = smem + skip + C::kLowBytes;
+  const uint32_t ring_at = smem_u32(ring);
+  if (threadIdx.x == 0) {
+    mbar_init(&done, 1);
+    fence_mbar_init();
+  }
+  // (before the next kernel may start, so that it cannot take the columns from a block that it then waits for)
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)),
+                 "r"(C::kUnit)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  // What comes before the wait reads the order of the rows, base and B, all complete
+  // when the kernel before this one began its own work.
+  const Rows rows{ws.tiles, ws.order};
+  const int4 head = rows.tile(0);
+  const int r = static_cast<int>(a.r), N = static_cast<int>(a.N), per_tile = (N - 1) / C::kUnit + 1;
+  const int64_t units = static_cast<int64_t>(a.y == a.base ? head.x : head.y) * per_tile;
+  const int64_t u0 = units * blockIdx.x / gridDim.x;
+  const int todo = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u0);
+
+  Walk f, now;
+  f.to(u0, per_tile);
+  now = f;
+  int left = todo;  // units not fetched yet
+  int4 ftile;
+  int base_row[C::kBases];
+  const uint16_t* fB;
+  const int base_chunk = threadIdx.x % C::kBaseChunks, base_row0 = threadIdx.x / C::kBaseChunks;
+  const int b_chunk = threadIdx.x % (kR / 8), b_col0 = threadIdx.x / (kR / 8);
+  constexpr int kBStep = C::kThreads / (kR / 8);  // columns whose rows of B the block copies at once
+  auto fetch_tile = [&] {
+    ftile = rows.tile(1 + f.t);
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < C::kBases; ++i) {
+        const int row = base_row0 + i * C::kBaseStep;
+        base_row[i] = row < ftile.z ? rows.row(ftile.y + row) : -1;
+      }
+    }
+    fB = a.B + static_cast<int64_t>(ftile.x) * N * r + b_col0 * r + b_chunk * 8;
+  };
+  if (left > 0) fetch_tile();
+  auto fetch = [&](uint32_t slot) {
+    if (left <= 0) return;
+    --left;
+    const int col = f.c * C::kUnit;
+    const uint32_t at = ring_at + slot;
+    if constexpr (kVec) {
+      const uint16_t* src = a.base + col + base_chunk * 8;
+      const bool in = col + base_chunk * 8 < N;
+#pragma unroll
+      for (int i = 0; i < C::kBases; ++i) {
+        const int row = base_row0 + i * C::kBaseStep;
+        if (in && base_row[i] >= 0)
+          cp_async16(at + row * (2 * C::kUnit) + ((base_chunk ^ (row & 1) << 2) << 4),
+                     src + base_row[i] * a.base_stride, true);
+      }
+    }
+    if (ftile.x >= 0) {
+      const uint16_t* src = fB + static_cast<int64_t>(col) * r;
+#pragma unroll
+      for (int i = 0; i < C::kBs; ++i) {
+        const int c = b_col0 + i * kBStep;
+        const bool real = b_chunk * 8 < r && col + c < N;
+        cp_async16(at + C::kBaseBytes + tile_place<C::kUnit>(b_row(c), b_chunk), real ? src + i * kBStep * r : a.B, real);
+      }
+    }
+    if (f.next(per_tile) && left > 0) fetch_tile();
+  };
+#pragma unroll 1
+  for (int s = 0; s < C::kStages - 1; ++s) {
+    fetch(s * C::kStageBytes);
+    cp_commit();
+  }
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+
+  const int row0 = (warp & 3) * 16 + g, c0 = (warp >> 2) * 32;  // of the unit
+  int4 tile;
+  uint16_t* y[2];
+  OddRows odd{odd_stage + warp * 16 * kOddRow, -1};
+  bool fresh = true, ok = true;
+  uint32_t slot = 0, ahead = (C::kStages - 1) * C::kStageBytes, parity = 0;
+  const uint64_t x_desc = tc::sw128_desc(smem_u32(low)), b_desc = tc::sw128_desc(ring_at + C::kBaseBytes);
+#pragma unroll 1
+  for (int u = 0; u < todo; ++u) {
+    cp_wait<C::kStages - 2>();
+    fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();  // (nothing reads the stage, the sums and x A^T of the unit before any more)
+    if (fresh) {
+      tile = rows.tile(1 + now.t);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        y[i] = row0 + 8 * i < tile.z ? a.y + rows.row(tile.y + row0 + 8 * i) * a.y_stride + 8 * q : nullptr;
+      if constexpr (!kVec) {
+        const int row = (warp & 3) * 16 + (lane & 15);
+        odd.m = row < tile.z ? rows.row(tile.y + row) : -1;
+      }
+      if (tile.x >= 0) {
+        const uint4* src = ws.low + static_cast<int64_t>(now.t) * (C::kLowBytes / 16) + threadIdx.x;
+        uint4 v[C::kLows];
+#pragma unroll
+        for (int i = 0; i < C::kLows; ++i) v[i] = __ldcg(src + i * C::kThreads);
+#pragma unroll
+        for (int i = 0; i < C::kLows; ++i) low[threadIdx.x + i * C::kThreads] = v[i];
+        fence_proxy_async_smem();
+        __syncthreads();
+      }
+    }
+    if (tile.x >= 0 && threadIdx.x == 0) {
+      tc::tc_fence_after();
+      const uint64_t b = b_desc + (slot >> 4);
+#pragma unroll
+      for (int i = 0; i < kR / 16; ++i) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem),
+            "l"(x_desc + (i / 4 * (128 * 128 / 16) + 2 * (i % 4))), "l"(b + (i / 4 * (C::kUnit * 128 / 16) + 2 * (i % 4))),
+            "r"(tc::make_idesc(128, C::kUnit)), "r"(i > 0 ? 1 : 0)
+            : "memory");
+      }
+      tc::umma_commit(&done);
+    }
+    fetch(ahead);
+    cp_commit();
+    const int col = now.c * C::kUnit + c0;
+    const uint8_t* stage = ring + slot;
+    float acc[4][4];
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = row0 + 8 * i;
+        begin_with(acc, i, *reinterpret_cast<const uint4*>(stage + row * (2 * C::kUnit) +
+                                                           (((c0 / 8 + q) ^ (row & 1) << 2) << 4)));
+      }
+    } else {
+      odd.read(a, col, lane, acc);
+    }
+    if (tile.x >= 0) {
+      if (ok) ok = mbar_wait_bounded(&done, parity);  // (after one wait that gave up without another)
+      parity ^= 1;
+      __syncwarp();
+      tc::tc_fence_after();
+      const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + c0;
+      uint32_t hi[16], lo[16];
+      tmem_ld_sums(at, hi);
+      tmem_ld_sums(at + (16u << 16), lo);
+      tc::tmem_wait_ld_all(hi);
+      tc::tmem_wait_ld_all(lo);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i >> 2][i & 3] += __uint_as_float(lo[i]) + __uint_as_float(hi[i]);
+    }
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (y[i] == nullptr || col + 8 * q >= N) continue;
+        const int row = row0 + 8 * i;
+        *reinterpret_cast<uint4*>(y[i] + col) =
+            tile.x >= 0 ? rounded(acc, i)
+                        : *reinterpret_cast<const uint4*>(stage + row * (2 * C::kUnit) + (((c0 / 8 + q) ^ (row & 1) << 2) << 4));
+      }
+    } else {
+      odd.write(a, col, lane, acc, tile.x >= 0);
+    }
+    fresh = now.next(per_tile);
+    ahead = slot;
+    slot = slot + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : slot + C::kStageBytes;
+  }
+  if (!ok) record_status(status, kStatusTimeout);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kUnit) : "memory");
+}
+
 bool sixteen_bytes(const LoraArgs& a) {
   return a.N % 8 == 0 && a.base_stride % 8 == 0 && a.y_stride % 8 == 0 && aligned16(a.base) && aligned16(a.y);
 }
@@ -994,7 +1225,6 @@ cudaError_t launch_8(const Ctx& c, const LoraArgs& a, const Ws& ws) {
 template <int kR>
 cudaError_t launch_64(const Ctx& c, const LoraArgs& a, const Ws& ws) {
   using S = Shrink64<kR>;
-  using E = Expand64<kR>;
   static SmemLimit lim;
   cudaError_t e = raise_smem_limit(lim, shrink64_kernel<kR>, c.device, S::kSmem);
   if (e != cudaSuccess) return e;
@@ -1002,20 +1232,29 @@ cudaError_t launch_64(const Ctx& c, const LoraArgs& a, const Ws& ws) {
   const int64_t grid = std::min({int64_t{220 * 1024 / S::kSmem} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
   e = launch_early(c, grid, kThreads, S::kSmem, shrink64_kernel<kR>, a, ws);
   if (e != cudaSuccess) return e;
+  static SmemLimit vec, odd;
   if constexpr (joined(kR)) {
     e = launch_early(c, std::min<int64_t>(tiles * (32 * kR / 256), 8 * c.sm_count), 256, 0, join_kernel<kR>, a, ws,
                      static_cast<int>(grid), int{S::kCols});
     if (e != cudaSuccess) return e;
+    const auto expand = [&](SmemLimit& limit, auto kern, auto E) {
+      const cudaError_t err = raise_smem_limit(limit, kern, c.device, E.kSmem);
+      const int64_t grid2 = std::min<int64_t>(tiles * ((a.N - 1) / E.kUnit + 1), E.kFit * c.sm_count);
+      return err != cudaSuccess ? err : launch_early(c, grid2, int{E.kThreads}, E.kSmem, kern, a, ws, c.status);
+    };
+    return sixteen_bytes(a) ? expand(vec, expand_many_kernel<kR, true>, ExpandMany<kR, true>{})
+                            : expand(odd, expand_many_kernel<kR, false>, ExpandMany<kR, false>{});
+  } else {
+    using E = Expand64<kR>;
+    const int64_t grid2 = std::min<int64_t>(tiles * ((a.N - 1) / E::kUnit + 1), E::kFit * c.sm_count);
+    const auto expand = [&](SmemLimit& limit, auto kern) {
+      const cudaError_t err = raise_smem_limit(limit, kern, c.device, E::kSmem);
+      return err != cudaSuccess ? err
+                                : launch_early(c, grid2, E::kThreads, E::kSmem, kern, a, ws, static_cast<int>(grid),
+                                               int{S::kCols});
+    };
+    return sixteen_bytes(a) ? expand(vec, expand64_kernel<kR, true>) : expand(odd, expand64_kernel<kR, false>);
   }
-  const int64_t grid2 = std::min<int64_t>(tiles * ((a.N - 1) / E::kUnit + 1), E::kFit * c.sm_count);
-  const auto expand = [&](SmemLimit& limit, auto kern) {
-    const cudaError_t err = raise_smem_limit(limit, kern, c.device, E::kSmem);
-    return err != cudaSuccess ? err
-                              : launch_early(c, grid2, E::kThreads, E::kSmem, kern, a, ws, static_cast<int>(grid),
-                                             int{S::kCols});
-  };
-  static SmemLimit vec, odd;
-  return sixteen_bytes(a) ? expand(vec, expand64_kernel<kR, true>) : expand(odd, expand64_kernel<kR, false>);
 }
 
 template <int kR>
