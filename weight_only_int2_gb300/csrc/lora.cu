@@ -16,10 +16,9 @@
 //
 // Bound: HBM, where there is enough to read. 8192 rows, K 5120, N 17408, r 16, 658 MB:
 // 115 us, 5.7 TB/s (the second product 91 us of it; three blocks an SM instead of two
-// 145, since more places in base and y are open at once); r 64 146 us and r 128 270,
-// where the MMAs take as long as memory does (twice, for the two numbers a value). 64
-// rows of 41 adapters, 40 MB: 14.5 us, the chain rows -> order -> A, x -> sums -> B,
-// twice a launch. One row: 4.8 us.
+// 145, since more places in base and y are open at once); r 64 144 us and r 128 171, both
+// products by tcgen05 there. 64 rows of 41 adapters, 40 MB: 14.5 us, the chain rows ->
+// order -> A, x -> sums -> B, twice a launch. One row: 4.8 us.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
 #include "wq_internal.h"
@@ -281,7 +280,7 @@ struct Shrink64 {
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kStages = kR == 128 ? 4 : 6;
   static constexpr int kStageBytes = (64 + kR) * kRowBytes;
-  static constexpr int kSmem = kStages * kStageBytes;
+  static constexpr int kSmem = kStages * kStageBytes + (joined(kR) ? 1024 : 0);
   static constexpr int kStep = kThreads / kChunks;  // rows that the block copies at once
   static constexpr int kXs = 64 / kStep;            // rows of x a thread copies
   static constexpr int kAs = kR / kStep;            // and of A
@@ -372,6 +371,148 @@ __global__ void __launch_bounds__(kThreads) shrink64_kernel(const LoraArgs a, co
   }
 }
 
+// 16 lanes by 32 columns of tensor memory, as the sums of four MMAs of a warp's own.
+__device__ __forceinline__ void tmem_ld_sums(uint32_t at, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(at));
+}
+
+// The same for larger ranks on the tcgen05 tensor cores: x's rows and A's lie in a stage
+// as the descriptors want them, the sums in tensor memory (8192 rows, r 128: 171 us for
+// the call, by mma.sync 179; 2049 rows, K 17408, r 64: 39 and 41.5; 512 rows of 60
+// adapters, r 64: 35 and 38).
+template <int kR>
+__global__ void __launch_bounds__(kThreads) shrink_many_kernel(const LoraArgs a, const Ws ws, unsigned* status) {
+  using C = Shrink64<kR>;
+  extern __shared__ uint8_t smem[];
+  __shared__ uint64_t done[C::kStages];  // a stage's MMAs
+  __shared__ uint32_t tmem_at;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t ring_at = (smem_u32(smem) + 1023) & ~1023u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&done[i], 1);
+    fence_mbar_init();
+  }
+  // (before the next kernel may start, so that it cannot take the columns from a block that it then waits for)
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(kR)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  cl::griddep_wait();
+  cl::griddep_launch_dependents();
+  const Rows rows{ws.tiles, ws.order};
+  const int4 head = rows.tile(0);
+  const int K = static_cast<int>(a.K), r = static_cast<int>(a.r), stages = (K - 1) / C::kCols + 1;
+  const Shares sh = shares_of(stages, head.x, gridDim.x);
+  const int chunk = threadIdx.x % C::kChunks, row0 = threadIdx.x / C::kChunks;
+  const int64_t units = static_cast<int64_t>(head.x) * sh.shares;
+  uint32_t slot = 0, parity = 0;  // of the next stage; bit i: of slot i
+  bool ok = true;
+  auto wait = [&](uint32_t i) {  // for the MMAs of slot i's stage (after one wait that gave up without another)
+    if (ok) ok = mbar_wait_bounded(&done[i], parity >> i & 1);
+    parity ^= 1u << i;
+  };
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int t = static_cast<int>(u / sh.shares), share = static_cast<int>(u - static_cast<int64_t>(t) * sh.shares);
+    const int4 tile = rows.tile(1 + t);
+    const int first = share * sh.per, last = min(first + sh.per, stages);
+    const uint16_t* src_x[C::kXs];
+#pragma unroll
+    for (int i = 0; i < C::kXs; ++i) {
+      const int row = row0 + i * C::kStep;
+      src_x[i] = row < tile.z ? a.x + rows.row(tile.y + row) * a.x_stride : nullptr;
+    }
+    const uint16_t* src_a = a.A + static_cast<int64_t>(tile.x) * r * K;
+    auto fetch = [&](int s, int slot) {
+      const int col = s * C::kCols + chunk * 8;  // (stages end below 2^31 + 2^6)
+      const bool in = col >= 0 && col < K;
+      const uint32_t at = ring_at + slot * C::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < C::kXs; ++i) {
+        const int row = row0 + i * C::kStep;
+        const bool real = in && src_x[i] != nullptr;
+        cp_async16(at + row * C::kRowBytes + ((chunk ^ (row & 7)) << 4), real ? src_x[i] + col : a.x, real);
+      }
+#pragma unroll
+      for (int i = 0; i < C::kAs; ++i) {
+        const int row = row0 + i * C::kStep;
+        const bool real = in && row < r;
+        cp_async16(at + (64 + row) * C::kRowBytes + ((chunk ^ (row & 7)) << 4),
+                   real ? src_a + static_cast<int64_t>(row) * K + col : a.A, real);
+      }
+    };
+    uint32_t into = slot;
+#pragma unroll 1
+    for (int s = 0; s < C::kStages - 1; ++s) {
+      if (first + s < last) fetch(first + s, into);
+      cp_commit();
+      into = into + 1 == C::kStages ? 0 : into + 1;
+    }
+#pragma unroll 1
+    for (int s = first; s < last; ++s) {
+      cp_wait<C::kStages - 2>();
+      fence_proxy_async_smem();
+      tc::tc_fence_before();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        tc::tc_fence_after();
+        const uint32_t at = ring_at + slot * C::kStageBytes;
+        const uint64_t x_desc = tc::sw128_desc(at), a_desc = tc::sw128_desc(at + 64 * C::kRowBytes);
+#pragma unroll
+        for (int k = 0; k < C::kCols / 16; ++k) {
+          asm volatile(
+              "{\n\t.reg .pred p;\n\t"
+              "setp.ne.b32 p, %4, 0;\n\t"
+              "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem),
+              "l"(x_desc + 2 * k), "l"(a_desc + 2 * k), "r"(tc::make_idesc(64, kR)), "r"(s > first || k > 0 ? 1 : 0)
+              : "memory");
+        }
+        tc::umma_commit(&done[slot]);
+      }
+      if (s > first) wait(into);  // the slot of the stage before
+      if (s + C::kStages - 1 < last) fetch(s + C::kStages - 1, into);
+      cp_commit();
+      into = slot;
+      slot = slot + 1 == C::kStages ? 0 : slot + 1;
+    }
+    wait(into);
+    __syncwarp();
+    tc::tc_fence_after();
+    float* part = ws.part + (static_cast<int64_t>(share) * head.z + tile.y) * r;
+    const int row = warp * 16 + (lane >> 2), q = 2 * (lane & 3);
+#pragma unroll
+    for (int c = 0; c < kR; c += 32) {
+      uint32_t v[16];
+      tmem_ld_sums(tmem + (static_cast<uint32_t>(warp) << 21) + c, v);
+      tc::tmem_wait_ld_all(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = c + j * 8 + q;
+        if (col >= r) break;
+        if (row < tile.z)
+          *reinterpret_cast<float2*>(part + row * r + col) = make_float2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]));
+        if (row + 8 < tile.z)
+          *reinterpret_cast<float2*>(part + (row + 8) * r + col) = make_float2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+      }
+    }
+  }
+  if (!ok) record_status(status, kStatusTimeout);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kR) : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -393,9 +534,9 @@ __device__ __forceinline__ uint32_t tile_place(int row, int chunk) {
 
 // Many rows, larger ranks: the shares added up in their order, scaled and written as
 // the MMAs of the second product read them, so that its blocks, which come to a tile
-// many times, find them ready (2049 rows, r 64, K 17408, 8 shares: 42 us for the call,
-// 47 where they added up the shares themselves; with r 16 the launch costs the 2 us
-// that it saves). A thread has two values of a row side by side; rows behind a tile's
+// many times, find them ready (2049 rows, r 64, K 17408, 8 shares, both products by
+// mma.sync: 42 us for the call, 47 where they added up the shares themselves; with r 16
+// the launch costs the 2 us that it saves). A thread has two values of a row side by side; rows behind a tile's
 // last stay as they are.
 template <int kR>
 __global__ void __launch_bounds__(256) join_kernel(const LoraArgs a, const Ws ws, int shrink_grid, int shrink_cols) {
@@ -965,16 +1106,17 @@ __global__ void __launch_bounds__(Expand64<kR>::kThreads, Expand64<kR>::kFit)
 // of a value are two of an MMA's 128 rows (16 rows' higher ones, their lower ones, the
 // next 16 ..), so that a warp finds both sums of its rows in its own lanes of tensor
 // memory, and reads them as its own MMAs would hold them: base, y and the order of the
-// columns are as above. What a block waits for (loads, MMAs, sums) the others on its SM
-// cover, or its 16 warps: 8192 rows, K 5120, N 17408: r 64 139 us (two blocks 140), r 128
-// 173 (two blocks of 8 warps and 64 columns 179); finishing a unit while the next one's
-// MMAs run, which costs a stage, 144 and 176; the numbers as separate MMAs of 64 rows
-// 144 and 189; by mma.sync 146 and 270. 2049 rows, K 17408, N 5120, r 64: 40.5 us and 42.
+// columns are as above. What a block waits for (loads, MMAs, sums) the other on its SM
+// covers, or its 16 warps. 8192 rows, K 5120, N 17408: r 64 144 us, r 128 171 (two blocks
+// of 8 warps and 64 columns 179); finishing a unit while the next one's MMAs run, which
+// costs a stage, 144 and 176; the numbers as separate MMAs of 64 rows 144 and 189; by
+// mma.sync 146 and 270. (Three blocks of r 64 take 139, but 207 where a block has to wait
+// for a place, since each has its part of the units from the start.)
 template <int kR, bool kVec>
 struct ExpandMany {
   static constexpr int kUnit = kR == 64 ? 64 : 128;  // columns of a stage
-  static constexpr int kFit = kR == 64 ? 3 : 1;
-  static constexpr int kStages = kR == 64 ? 3 : 4;
+  static constexpr int kFit = kR == 64 ? 2 : 1;
+  static constexpr int kStages = 4;
   static constexpr int kWarps = kUnit / 8;  // 16 rows and 32 columns each
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kOdds = kVec ? 8 : kWarps * 16 * kOddRow;
@@ -989,16 +1131,6 @@ struct ExpandMany {
   static constexpr int kLows = kLowBytes / 16 / kThreads;   // and of x A^T
   static_assert(kFit * kUnit <= 512 && kFit * (kSmem + 2 * kOdds + 1024 + 64) <= 228 * 1024, "");
 };
-
-// 16 lanes by 32 columns of tensor memory, as the sums of four MMAs of a warp's own.
-__device__ __forceinline__ void tmem_ld_sums(uint32_t at, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(at));
-}
 
 template <int kR, bool kVec>
 __global__ void __launch_bounds__(ExpandMany<kR, kVec>::kThreads, ExpandMany<kR, kVec>::kFit)
@@ -1226,11 +1358,16 @@ template <int kR>
 cudaError_t launch_64(const Ctx& c, const LoraArgs& a, const Ws& ws) {
   using S = Shrink64<kR>;
   static SmemLimit lim;
-  cudaError_t e = raise_smem_limit(lim, shrink64_kernel<kR>, c.device, S::kSmem);
-  if (e != cudaSuccess) return e;
   const int64_t tiles = most_tiles(a.M, a.n), stages = (a.K - 1) / S::kCols + 1;
   const int64_t grid = std::min({int64_t{220 * 1024 / S::kSmem} * c.sm_count, int64_t{kMaxGrid}, tiles * std::min<int64_t>(stages, kMaxShares)});
-  e = launch_early(c, grid, kThreads, S::kSmem, shrink64_kernel<kR>, a, ws);
+  cudaError_t e;
+  if constexpr (joined(kR)) {
+    e = raise_smem_limit(lim, shrink_many_kernel<kR>, c.device, S::kSmem);
+    if (e == cudaSuccess) e = launch_early(c, grid, kThreads, S::kSmem, shrink_many_kernel<kR>, a, ws, c.status);
+  } else {
+    e = raise_smem_limit(lim, shrink64_kernel<kR>, c.device, S::kSmem);
+    if (e == cudaSuccess) e = launch_early(c, grid, kThreads, S::kSmem, shrink64_kernel<kR>, a, ws);
+  }
   if (e != cudaSuccess) return e;
   static SmemLimit vec, odd;
   if constexpr (joined(kR)) {
