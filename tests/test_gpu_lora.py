@@ -301,3 +301,36 @@ def test_larger_ranks_of_out_of_range_infinite_and_other_inputs(N, r):
                 got.append(wq.lora_gemm(x, A, B, ids, base))
         torch.cuda.synchronize()
         assert all(torch.equal(v.view(torch.int16), y.view(torch.int16)) for v in got)
+
+
+@pytest.mark.parametrize("r", [64, 128])
+def test_larger_ranks_beside_a_quantized_layer_of_many_rows(r):
+    """A prompt's projection and its adapters, one after another in a stream, on two streams at once: both kinds of
+    kernel hold tensor memory."""
+    N, K, bits, M, n = 768, 1024, 6, 900, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 64, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    scales = ((torch.rand((N, K // 128), generator=g, device="cuda") + 0.5) / (32 * K ** 0.5)).bfloat16()
+    packed, s_dev = wq.wna16_repack(codes, scales, bits)
+    x, ids = rows((M, K), 2), ids_of(M, n, 3, each=50)
+    A, B, at = rows((n, r, K), 4, K ** -0.5), rows((n, 256, r), 5, r ** -0.5), dev(ids)
+    plain = wq.wna16_gemm(x, packed, s_dev, N, K, bits)
+
+    def layer():
+        y = wq.wna16_gemm(x, packed, s_dev, N, K, bits)
+        wq.lora_gemm(x, A, B, at, y[:, 512:], y=y[:, 512:])
+        return y
+
+    first_y = layer()
+    want, first, second = R.lora(f64(x), f64(A), f64(B), ids, f64(plain[:, 512:]))
+    assert torch.equal(first_y[:, :512], plain[:, :512])
+    assert np.all(np.abs(f64(first_y[:, 512:]) - want) <= tolerance(want, first, second, f64(plain[:, 512:]), K, r))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(layer())
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, first_y) for y in got)
