@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
         else
           cp_async16(at, from, real);
       };
-      if (r == kR && col + kFewCols <= N) {
+      if (r == kR && N - col >= kFewCols) {  // (col + 64 may be 2^31)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
 #pragma unroll
