@@ -17,7 +17,7 @@
 // Bound: HBM, where there is enough to read. 8192 rows, K 5120, N 17408, r 16, 658 MB:
 // 115 us, 5.7 TB/s (the second product 91 us of it; three blocks an SM instead of two
 // 145, since more places in base and y are open at once); r 64 144 us and r 128 171, both
-// products by tcgen05 there. 64 rows of 41 adapters, 40 MB: 14.5 us, the chain rows ->
+// products by tcgen05 there. 64 rows of 41 adapters, 40 MB: 14.1 us, the chain rows ->
 // order -> A, x -> sums -> B, twice a launch. One row: 4.8 us.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
@@ -69,10 +69,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
   const int size = real ? 16 : 0;  // 0: zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
-  const int size = real ? 8 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void cp_wait() {
@@ -110,7 +106,7 @@ struct Few {
 struct Rows {
   const int4* tiles;
   const int32_t* order;
-  // (past the first level cache, which may hold an earlier call's)
+  // (past the first level cache, as all that is read before the wait: nothing says that it holds no earlier call's)
   __device__ int4 tile(int i) const { return __ldcg(tiles + i); }
   __device__ int row(int i) const { return __ldcg(order + i); }
 };
@@ -725,12 +721,14 @@ struct Walk {
 // Tiles of 8 rows: a warp for itself, 64 columns at a time, without barriers. B, which
 // few rows use, is the left operand of four MMAs of 16 columns, dealt out so that a
 // lane's are 8 in a row of two rows of y; x A^T is the right one. A lane copies its
-// values of B and base itself into its own places of a ring of stages.
+// values of B and base itself into its own places of a ring of stages; of ranks up to
+// 16 it reads 8 bytes of a row, and the warp copies whole pieces of 16 (the copies of 8
+// go through the first level cache, which what is read before the wait must not).
 template <int kR>
 struct Expand8 {
-  static constexpr int kPieces = kR == 16 ? 1 : kR / 32;   // a lane's of a row of B
-  static constexpr int kPieceBytes = kR == 16 ? 8 : 16;
-  static constexpr int kBBytes = 8 * kPieces * kPieceBytes * 32;
+  static constexpr bool kShared = kR == 16;  // the warp's pieces
+  static constexpr int kPieces = kShared ? 1 : kR / 32;  // a lane's of a row of B
+  static constexpr int kBBytes = 64 * kR * 2;
   static constexpr int kStageBytes = kBBytes + 2 * 16 * 32;
   static constexpr int kStages = kR == 16 || kR == 128 ? 2 : 3;
   static constexpr int kWarpBytes = kStages * kStageBytes + 8 * kR * 4;
@@ -739,6 +737,9 @@ struct Expand8 {
   static constexpr int kFit = 228 * 1024 / kAll < 4 ? 228 * 1024 / kAll : 4;
 };
 constexpr int kFewCols = 64;
+// Rank 16: where the row of B of column c of 64 lies (the rows that a quarter of the
+// lanes reads at once are in different banks).
+__device__ __forceinline__ int b16_place(int c) { return (c ^ (c >> 3 & 3)) * 32; }
 
 template <int kR, bool kVec, bool kFew>
 __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
   extern __shared__ __align__(128) uint8_t ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   float* h = reinterpret_cast<float*>(ring + warp * C::kWarpBytes + C::kStages * C::kStageBytes);
-  const uint8_t* own_b = ring + warp * C::kWarpBytes + lane * C::kPieceBytes;
+  const uint8_t* own_b = ring + warp * C::kWarpBytes + (C::kShared ? 0 : lane * 16);
   const uint8_t* own_base = ring + warp * C::kWarpBytes + C::kBBytes + lane * 16;
   const uint32_t own_b_at = smem_u32(own_b), own_base_at = smem_u32(own_base);
   // What comes before the wait reads the order of the rows, base and B, all complete
@@ -783,14 +784,15 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
   int left = todo;  // units not fetched yet
   int4 ftile;
   const uint16_t *fB, *fbase[2];
-  // this lane's rows of y are 2 q and 2 q + 1, its columns 8 g .. 8 g + 7, its values of r 4 or 8 from here on
-  const int piece = (kR == 16 ? 4 : 8) * q;
+  // this lane's rows of y are 2 q and 2 q + 1, its columns 8 g .. 8 g + 7; what it copies of B begins at this column
+  // and value of r
+  const int b_col = C::kShared ? lane >> 1 : 8 * g, piece = C::kShared ? 8 * (lane & 1) : 8 * q;
   auto fetch_tile = [&] {
     ftile = rows.tile(1 + f.t);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       fbase[i] = 2 * q + i < ftile.z ? a.base + rows.row(ftile.y + 2 * q + i) * a.base_stride + 8 * g : nullptr;
-    fB = a.B + (static_cast<int64_t>(ftile.x) * N + 8 * g) * r + piece;
+    fB = a.B + (static_cast<int64_t>(ftile.x) * N + b_col) * r + piece;
   };
   if (left > 0) fetch_tile();
   auto fetch = [&](uint32_t slot) {
@@ -799,26 +801,27 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
     const int col = f.c * kFewCols;
     if (ftile.x >= 0) {
       const uint16_t* src = fB + static_cast<int64_t>(col) * r;
-      auto copy = [&](int j, int i, const uint16_t* from, bool real) {
-        const uint32_t at = own_b_at + slot + (j * C::kPieces + i) * (32 * C::kPieceBytes);
-        if constexpr (kR == 16)
-          cp_async8(at, from, real);
-        else
-          cp_async16(at, from, real);
-      };
-      if (r == kR && N - col >= kFewCols) {  // (col + 64 may be 2^31)
+      const bool whole = r == kR && N - col >= kFewCols;  // (col + 64 may be 2^31)
+      if constexpr (C::kShared) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool real = whole || (col + b_col + 16 * j < N && piece < r);
+          cp_async16(own_b_at + slot + b16_place(b_col + 16 * j) + 2 * piece, real ? src + 16 * j * r : a.B, real);
+        }
+      } else if (whole) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
 #pragma unroll
-          for (int i = 0; i < C::kPieces; ++i) copy(j, i, src + j * kR + 32 * i, true);
+          for (int i = 0; i < C::kPieces; ++i)
+            cp_async16(own_b_at + slot + (j * C::kPieces + i) * 512, src + j * kR + 32 * i, true);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
 #pragma unroll
           for (int i = 0; i < C::kPieces; ++i) {
-            const bool real = col + 8 * g + j < N && piece + 32 * i < r;
-            copy(j, i, real ? src + j * r + 32 * i : a.B, real);
+            const bool real = col + b_col + j < N && piece + 32 * i < r;
+            cp_async16(own_b_at + slot + (j * C::kPieces + i) * 512, real ? src + j * r + 32 * i : a.B, real);
           }
         }
       }
@@ -846,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
   uint32_t slot = 0, ahead = (C::kStages - 1) * C::kStageBytes;
 #pragma unroll 1
   for (int u = 0; u < todo; ++u) {
+    if constexpr (C::kShared) __syncwarp();  // (no lane reads the stage of the unit before any more)
     fetch(ahead);
     cp_commit();
     if (fresh) {
@@ -873,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
       }
     }
     cp_wait<C::kStages - 1>();
+    if constexpr (C::kShared) __syncwarp();  // (the other lanes' pieces)
     const int col = now.c * kFewCols;
     // MMA j: its rows g and g + 8 are columns 8 g + 2 j and the next of y, its columns rows of y
     float acc[4][4];
@@ -901,15 +906,15 @@ __global__ void __launch_bounds__(kThreads, Expand8<kR>::kFit)
       for (int i = 0; i < C::kPieces; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint8_t* at = own_b + slot + (2 * j * C::kPieces + i) * (32 * C::kPieceBytes);
-          if constexpr (kR == 16) {
-            const uint2 e = *reinterpret_cast<const uint2*>(at);
-            const uint2 o = *reinterpret_cast<const uint2*>(at + 32 * C::kPieceBytes);
+          if constexpr (C::kShared) {
+            const uint2 e = *reinterpret_cast<const uint2*>(own_b + slot + b16_place(8 * g + 2 * j) + 8 * q);
+            const uint2 o = *reinterpret_cast<const uint2*>(own_b + slot + b16_place(8 * g + 2 * j + 1) + 8 * q);
             mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, lo[0][0], lo[0][1]);
             mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, hi[0][0], hi[0][1]);
           } else {
+            const uint8_t* at = own_b + slot + (2 * j * C::kPieces + i) * 512;
             const uint4 e = *reinterpret_cast<const uint4*>(at);
-            const uint4 o = *reinterpret_cast<const uint4*>(at + C::kPieces * 32 * C::kPieceBytes);
+            const uint4 o = *reinterpret_cast<const uint4*>(at + C::kPieces * 512);
             mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, lo[2 * i][0], lo[2 * i][1]);
             mma_bf16_16816(acc[j], e.z, o.z, e.w, o.w, lo[2 * i + 1][0], lo[2 * i + 1][1]);
             mma_bf16_16816(acc[j], e.x, o.x, e.y, o.y, hi[2 * i][0], hi[2 * i][1]);
