@@ -908,6 +908,9 @@ def lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapter: torch.
     lib = load()
     if ws is None:
         ws = scratch(lora_workspace_bytes(M, n, r))
+    elif not (isinstance(ws, torch.Tensor) and ws.get_device() == dev and ws.is_contiguous()):
+        _need_here(ws, "ws")
+        raise ValueError("ws must be contiguous")
     _check(lib.lora_gemm(x.data_ptr(), xs, M, K, A.data_ptr(), B.data_ptr(), n, r, N, adapter.data_ptr(), _ptr(scale),
                          base.data_ptr(), bs, y.data_ptr(), ys, _ptr(ws), 0 if ws is None else
                          ws.numel() * ws.element_size(), _stream()), "lora_gemm")
