@@ -2,7 +2,8 @@
 the GPU: the rings of the tensor cores in steady state (more stages a share and units a
 block than a ring holds), 129 to 511 rows, and adapters rewritten between calls.
 
-The tolerance is that of tests/test_gpu_lora.py."""
+The tolerance is derived as in tests/test_gpu_lora.py; the two bf16 numbers of x A^T, the first
+below it and the second the rest rounded, leave 2^-16 of it."""
 
 import numpy as np
 import pytest
@@ -33,7 +34,7 @@ def definition(x, A, B, ids, base, scale):
 def near(y, x, A, B, ids, base, scale):
     want, first, second = definition(x, A, B, ids, base, scale)
     K, r = x.shape[1], A.shape[1]
-    tol = (2.0 ** -8 * want.abs() + (K / 16 + 40) * 2.0 ** -23 * first + 2.0 ** -17 * second
+    tol = (2.0 ** -8 * want.abs() + (K / 16 + 40) * 2.0 ** -23 * first + 2.0 ** -16 * second
            + (r / 8 + 4) * 2.0 ** -23 * (base.double().abs() + second))
     over = (y.double() - want).abs() - tol
     assert bool((over <= 0).all()), (float(over.max()), (over > 0).nonzero()[:4].tolist())

@@ -5,7 +5,7 @@
 // Two products, with the rows grouped by adapter into tiles, so that every A and B is
 // read by few blocks (up to 128 rows each block groups them itself, more are grouped
 // by a launch before, group.cu). x A^T stays as two bf16 numbers a value on its way
-// into the second product (2^-17 of itself; one would cost the sum bf16's 2^-8 once
+// into the second product (2^-16 of itself; one would cost the sum bf16's 2^-8 once
 // more), whose sums begin with base, float32 until y is rounded.
 //  - The first contracts over K: a block takes a tile and a share of K, as many shares
 //    as it takes to fill the GPU (a rule on the number of tiles, which is on the
@@ -513,12 +513,27 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-// Two values as pairs of bf16 numbers, whose sums are the values to 2^-17. (An
-// infinite value has no second number, so that it stays one.)
+// Two values as pairs of bf16 numbers of the values' own signs, neither of them 0 where the
+// value is not: an infinite value of B, or sums beyond float32's range, are infinite in both
+// products, or have the same sign in both, where a nearest number and its remainder gave NaN
+// (0 or a number of the other sign times infinity) and values next to the largest became
+// infinite. The first number is the largest below the value (of its size), the second the
+// rest rounded, so that the pair is the value to 2^-16 (or 2^-133). Nearest numbers, to
+// 2^-17, with the two products told apart where one is not finite took 1 to 14 % more of
+// a call of many rows. (x, y: results of sums, whose NaN is 0x7FFFFFFF.)
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack2(x, y);
-  const float xh = __uint_as_float(hi << 16), yh = __uint_as_float(hi & 0xFFFF0000u);
-  lo = pack2(fabsf(xh) < INFINITY ? x - xh : 0.0f, fabsf(yh) < INFINITY ? y - yh : 0.0f);
+  uint32_t first[2];
+  float rest[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float v = i == 0 ? x : y;
+    const uint32_t b = __float_as_uint(v), size = b & 0x7FFFFFFFu;
+    const uint32_t h = (b & 0x80000000u) | ((max(size, 0x00010001u) - 1) & 0xFFFF0000u);
+    first[i] = size != 0 ? h : 0u;
+    rest[i] = size != 0 ? copysignf(fmaxf(fabsf(v - __uint_as_float(h)), 0x1p-133f), v) : 0.0f;
+  }
+  hi = __byte_perm(first[0], first[1], 0x7632);
+  lo = pack2(rest[0], rest[1]);
 }
 
 // Where the descriptors of the tensor cores have 16 bytes of a row of kRows: rows of 128
