@@ -6,18 +6,20 @@
 // read by few blocks (up to 128 rows each block groups them itself, more are grouped
 // by a launch before, group.cu). x A^T stays as two bf16 numbers a value on its way
 // into the second product (2^-16 of itself; one would cost the sum bf16's 2^-8 once
-// more), whose sums begin with base, float32 until y is rounded.
+// more), whose float32 sums begin with base or have it added at their end (on tcgen05),
+// and are rounded once, to y.
 //  - The first contracts over K: a block takes a tile and a share of K, as many shares
 //    as it takes to fill the GPU (a rule on the number of tiles, which is on the
 //    device), and writes float32 partial sums.
-//  - The second adds them up in their order, scales, and takes a tile and some of the
-//    columns; base and y are read and written 16 bytes a thread: the columns of four
-//    MMAs are dealt out so that a thread holds 8 in a row.
+//  - The second adds them up in their order and scales (for larger ranks of many rows a
+//    launch between the two does), and takes a tile and some of the columns; base and y
+//    are read and written 16 bytes a thread: the columns of four MMAs are dealt out so
+//    that a thread holds 8 in a row.
 //
 // Bound: HBM, where there is enough to read. 8192 rows, K 5120, N 17408, r 16, 658 MB:
 // 115 us, 5.7 TB/s (the second product 91 us of it; three blocks an SM instead of two
 // 145, since more places in base and y are open at once); r 64 144 us and r 128 171, both
-// products by tcgen05 there. 64 rows of 41 adapters, 40 MB: 14.1 us, the chain rows ->
+// products by tcgen05 there. 64 rows of 41 adapters, 40 MB: 14.2 us, the chain rows ->
 // order -> A, x -> sums -> B, twice a launch. One row: 4.8 us.
 #include "wq_cluster.cuh"
 #include "wq_device.cuh"
@@ -38,7 +40,9 @@ constexpr int kMaxGrid = 1024;   // blocks of the first product
 
 // Rows of a tile. A decode batch has a few rows of each adapter: they are the 8
 // columns of an MMA, and A's or B's values its 16 rows. From kManyRows rows on tiles
-// are 64 rows, 16 a warp, and A's or B's values the columns.
+// are 64 rows, 16 a warp, and A's or B's values the columns. (512 rows, tiles of 8 and of
+// 64: r 16, 5 adapters 21.3 and 19.4 us; r 64, 5 adapters 25.8 and 20.3, 60 adapters 33.2
+// and 36.0; r 128, 5 adapters 38.7 and 24.0; r 16, 60 adapters 17.7 and 23.1.)
 constexpr int64_t kManyRows = 512;
 constexpr int kFewTile = 8;
 constexpr int tile_of(int64_t M) { return M < kManyRows ? kFewTile : 64; }
@@ -594,7 +598,8 @@ __global__ void __launch_bounds__(256) join_kernel(const LoraArgs a, const Ws ws
 // ldmatrix are in different banks.
 template <int kR>
 __device__ __forceinline__ uint32_t b_place(int row, int chunk) {
-  const int sw = kR == 16 ? row >> 2 & 1 : (kR == 32 ? row >> 1 & 3 : row & 7);
+  static_assert(kR == 16 || kR == 32, "larger ranks lie as tile_place has them");
+  const int sw = kR == 16 ? row >> 2 & 1 : row >> 1 & 3;
   return row * (2 * kR) + ((chunk ^ sw) << 4);
 }
 __device__ __forceinline__ int b_row(int c) { return (c & ~31) + (c >> 1 & 3) * 8 + (c >> 3 & 3) * 2 + (c & 1); }
