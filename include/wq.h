@@ -486,7 +486,7 @@ size_t lora_workspace_bytes(int64_t M, int64_t n, int64_t r);
 /* Low-rank adapters of many requests beside a linear layer: with a = adapter[m],
  *   y[m] = bf16(base[m] + scale[a] * (x[m] . A[a]^T) . B[a]^T),
  * and y[m] = base[m] for a row whose adapter is outside [0, n) (such as -1). Sums are
- * float32; x . A^T enters the second product to 2^-16 of itself (or 2^-133).
+ * float32; x . A^T enters the second product to 2^-16 of itself (or 2^-132).
  *  x           [M, K] bf16, rows x_stride elements apart (a multiple of 8, at least
  *              K); K a multiple of 8.
  *  A [n, r, K], B [n, N, r] bf16: 1 <= n <= 1024, r a multiple of 8 up to 128

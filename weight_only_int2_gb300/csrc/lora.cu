@@ -522,7 +522,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // products, or have the same sign in both, where a nearest number and its remainder gave NaN
 // (0 or a number of the other sign times infinity) and values next to the largest became
 // infinite. The first number is the largest below the value (of its size), the second the
-// rest rounded, so that the pair is the value to 2^-16 (or 2^-133). Nearest numbers, to
+// rest rounded, so that the pair is the value to 2^-16 (or 2^-132). Nearest numbers, to
 // 2^-17, with the two products told apart where one is not finite took 1 to 14 % more of
 // a call of many rows. (x, y: results of sums, whose NaN is 0x7FFFFFFF.)
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
